@@ -111,8 +111,8 @@ def draw(rng):
         else:
             dim, out = 128, out if kv == "bf16" else "bf16"
             seen = min(ctx, window + sinks + new) if window else ctx
-            heads = max(1, min(heads, 9 * 10 ** 8 // (group * new * seen)))
-            seqs = max(1, min(seqs, 9 * 10 ** 8 // (group * heads * new * seen), 2 ** 21 // (ctx * heads)))
+            heads = max(1, min(heads, 7 * 10 ** 8 // (group * new * seen)))
+            seqs = max(1, min(seqs, 7 * 10 ** 8 // (group * heads * new * seen), 2 ** 21 // (ctx * heads)))
         case = _attend("", op, kv, out, seqs, group, heads, dim, block, new_min, new,
                        max(ctx_min, new), ctx, window, sinks)
     del case["name"]
