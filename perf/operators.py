@@ -14,7 +14,7 @@ CODES = {"fp8": torch.float8_e4m3fn, "int8": torch.int8}
 QMAX = {"fp8": 448.0, "int8": 127.0}
 FLOATS = {"bf16": torch.bfloat16, "f32": torch.float32}
 BYTES = {"bf16": 2, "f32": 4, "fp8": 1, "int8": 1}
-MIN_SCALE = 2.0 ** -100
+MIN_SCALE = 2.0 ** -64
 
 
 # ------------------------------------------------------------------ cases
