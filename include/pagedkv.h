@@ -478,6 +478,109 @@ pkv_status paged_attention_prefill(const void* q, const int32_t* query_start,
                                    pkv_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* An 8-bit cache with one scale per block and head.                         */
+/* ------------------------------------------------------------------------ */
+/* K and V caches as above (FP8-E4M3 or INT8 codes), with k_scales / v_scales
+ * device float32 [num_blocks, scale_stride], scale_stride >= num_kv_heads:
+ * value = code * scales[block * scale_stride + kv_head].  The scales belong to
+ * the block: whoever copies a block (copy_blocks, swap_blocks) copies its row of
+ * scales too. */
+
+/* Append rows to such a cache, choosing the scales [TUT 3.1 symmetric
+ * quantisation, 4.2 append_token; TOPG 3.3].
+ *   k_new, v_new : device [num_tokens, num_kv_heads, head_dim], src_dtype (f32|bf16).
+ *   query_start  : device [num_seqs + 1] int32; sequence s owns rows
+ *                  query_start[s] .. query_start[s+1]-1 (n_s of them, 0 allowed),
+ *                  which are the LAST n_s tokens of its context.  NULL: one
+ *                  row per sequence, row s (none where context_lens[s] is 0).
+ *   block_tables : device [num_seqs, max_blocks_per_seq] int32; only the
+ *                  entries of the new tokens' blocks are read.
+ *   context_lens : device [num_seqs] int32, the new tokens included.
+ *   max_query_len : host upper bound of n_s (sizes the grid); 1 at most when
+ *                  query_start is NULL.
+ * For each block that new tokens fall into, each KV head, and K and V apart, with
+ * a = max |x| over those tokens' finite values and qmax = 448 (FP8) or 127 (INT8):
+ *   - the first of them is at offset 0 of the block: scale = max(a / qmax, 2^-64);
+ *   - else the block's stored scale s0 becomes s0 * 2^k with the least k >= 0 for
+ *     which a <= qmax * s0 * 2^k, and codes c at lower offsets become
+ *     round_half_even(c * 2^-k) (FP8: rounded to E4M3).  A stored scale that
+ *     is not finite or is below 2^-64 counts as unset: as the first case, older
+ *     codes left as they are.
+ *   - code = x / scale (IEEE float32) rounded half to even, saturating; a NaN
+ *     becomes the FP8 NaN code, or 0 in INT8.
+ * Rows outside every chunk, and blocks outside the new tokens', are not touched.
+ * Two sequences of one call must not append into the same block (share blocks by
+ * copy-on-write).  A bad query_start or context flags PKV_DEV_BAD_CONTEXT and
+ * skips the sequence, a bad block flags PKV_DEV_BAD_BLOCK and is skipped.
+ * head_dim a multiple of 16; block_size a power of two up to 4096; caches and rows
+ * 16-byte aligned. */
+pkv_status quantize_and_cache(const void* k_new, const void* v_new, const int32_t* query_start,
+                              const int32_t* block_tables, const int32_t* context_lens,
+                              void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                              int32_t num_seqs, int32_t num_tokens, int32_t max_query_len,
+                              int32_t num_kv_heads, int32_t head_dim, int32_t block_size,
+                              int64_t num_blocks, int32_t max_blocks_per_seq,
+                              int64_t scale_stride, int32_t src_dtype, int32_t cache_dtype,
+                              int32_t* device_status, pkv_stream_t stream);
+
+/* Read rows of a paged cache back [TUT 4.2 get_kv]: for each sequence s and
+ * i < n_s = row_start[s+1] - row_start[s], row row_start[s] + i of k_out / v_out
+ * becomes the cache row of position first_pos[s] + i.
+ *   row_start    : device [num_seqs + 1] int32, 0 <= row_start <= num_rows.
+ *   first_pos    : device [num_seqs] int32, or NULL for 0.
+ *   max_rows     : host upper bound of n_s (sizes the grid).
+ *   kv_dtype     : f32, bf16, fp8_e4m3 or int8.  8-bit codes are multiplied by
+ *                  their scale: k_scale / v_scale [num_blocks, scale_stride], or
+ *                  [num_kv_heads] with scale_stride 0.
+ *   k_out, v_out : device [num_rows, num_kv_heads, head_dim], out_dtype (f32 or
+ *                  bf16, one rounding of the float32 value).
+ * Positions must lie in the table (position < max_blocks_per_seq * block_size); a
+ * sequence that breaks a bound is skipped and flags PKV_DEV_BAD_CONTEXT, a
+ * bad block gives rows of 0 and flags PKV_DEV_BAD_BLOCK.  Other rows of the
+ * outputs are not written.  head_dim a multiple of 16. */
+pkv_status gather_cache(const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                        const int32_t* row_start, const int32_t* first_pos, int32_t num_seqs,
+                        int32_t num_rows, int32_t max_rows, int32_t num_kv_heads,
+                        int32_t head_dim, int32_t block_size, int64_t num_blocks,
+                        int32_t max_blocks_per_seq, int32_t kv_dtype, const float* k_scale,
+                        const float* v_scale, int64_t scale_stride, int32_t out_dtype,
+                        void* k_out, void* v_out, int32_t* device_status, pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Attention with a sliding window and sinks; scales per block.              */
+/* ------------------------------------------------------------------------ */
+/* Split-KV scratch of paged_attention_decode_window (0 when every query's
+ * visible tokens fit one partition), for the same arguments. */
+size_t paged_attention_window_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,
+                                              int32_t num_kv_heads, int32_t head_dim,
+                                              int32_t max_context_len, int32_t partition_tokens,
+                                              int32_t window, int32_t sinks);
+
+/* paged_attention_decode over part of the context, with more cache forms.
+ * Arguments as there, and:
+ *   window, sinks : with window > 0 the query (position p = context_lens[s] - 1)
+ *                  sees token t <= p when t > p - window or t < sinks; window = 0
+ *                  (then sinks = 0): the whole context.  Table entries of
+ *                  blocks without a visible token are not read, so their
+ *                  blocks may have been given back to the pool.
+ *   k_scale, v_scale, scale_stride : 8-bit caches; [num_blocks, scale_stride]
+ *                  scales per block and head, or [num_kv_heads] with
+ *                  scale_stride 0.  V scales count as at least 2^-100.
+ *   out, out_dtype : device [num_seqs, num_q_heads, head_dim], f32 or bf16.
+ *   partition_tokens : counted in visible tokens.
+ * Supported: bf16 caches with head_dim 64, 128 or 256; FP8 and INT8 caches with
+ * head_dim 128; num_q_heads / num_kv_heads <= 16; block_size a power of two in
+ * [8, 4096]; max_context_len <= 2^30. */
+pkv_status paged_attention_decode_window(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int64_t num_blocks, int32_t max_blocks_per_seq,
+    int32_t max_context_len, float scale, int32_t q_dtype, int32_t kv_dtype, const float* k_scale,
+    const float* v_scale, int64_t scale_stride, int32_t window, int32_t sinks, int32_t out_dtype,
+    void* out, void* workspace, size_t workspace_bytes, int32_t partition_tokens,
+    int32_t* device_status, pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* CUDA-graph decode step with batch-size buckets and padding.               */
 /* ------------------------------------------------------------------------ */
 /* A whole decode step - for every layer, reshape_and_cache of the new token

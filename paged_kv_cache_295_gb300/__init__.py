@@ -9,6 +9,7 @@ Names follow the C ABI in ``include/pagedkv.h``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import os
 
@@ -112,6 +113,14 @@ _SIGS = {
                                              I32, FL, I32, I32, P, P, P, I32, P, P]),
     "paged_attention_prefill": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32, I64,
                                       I32, I32, FL, I32, I32, I32, P, P, P, P, P]),
+    "quantize_and_cache": (I32, [P, P, P, P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I64, I32,
+                                 I64, I32, I32, P, P]),
+    "gather_cache": (I32, [P, P, P, P, P, I32, I32, I32, I32, I32, I32, I64, I32, I32, P, P, I64,
+                           I32, P, P, P, P]),
+    "paged_attention_window_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32, I32, I32]),
+    "paged_attention_decode_window": (I32, [P, P, P, P, P, I32, I32, I32, I32, I32, I64, I32, I32,
+                                            FL, I32, I32, P, P, I64, I32, I32, I32, P, P, SZ, I32,
+                                            P, P]),
     "pkv_test_force_decode_kernel": (I32, [I32]),
     "pkv_test_decode_stall": (I32, [C.c_uint32]),
     "pkv_copy_kernel": (I32, [P, P, SZ, P]),
@@ -401,9 +410,196 @@ def partition_tokens(num_seqs, num_q_heads, num_kv_heads, max_context_len, reque
 
 
 def workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
-                    partition=0) -> int:
+                    partition=0, window=None, sinks=0) -> int:
+    """Bytes of split-KV scratch of a decode call; with ``window`` (0: none) of a call
+    with a window, sinks or scales per block."""
+    if window is not None:
+        return int(library().paged_attention_window_workspace_bytes(
+            num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, partition, window,
+            sinks))
     return int(library().paged_attention_workspace_bytes(num_seqs, num_q_heads, num_kv_heads,
                                                          head_dim, max_context_len, partition))
+
+
+def _launch_on(stream, t, *others):
+    """Context in which a call allocates and launches: ``stream``, or the current stream
+    of the tensors' device.  All tensors are on one device."""
+    torch = _torch()
+    if t.device.type != "cuda":
+        raise ValueError("CUDA tensors are needed (no CPU path)")
+    for o in others:
+        if o is not None and o.device != t.device:
+            raise ValueError(f"tensors on {t.device} and {o.device}")
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"tensors on {t.device}, stream of {stream.device}")
+        return torch.cuda.stream(stream)
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _want(t, name, shape, dtypes):
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
+        raise ValueError(f"{name} must be {list(shape)} of {[str(d) for d in dtypes]}, got "
+                         f"{list(t.shape)} of {t.dtype}")
+
+
+def _caches(k_cache, v_cache):
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must be alike, [num_blocks, block_size, num_kv_heads, "
+                         "head_dim]")
+    return k_cache.shape
+
+
+def _block_scales(k_scale, v_scale, num_blocks, num_kv_heads):
+    """Floats between the scales of two blocks; 0 for one scale per head."""
+    torch = _torch()
+    if k_scale is None or v_scale is None:
+        raise ValueError("an 8-bit cache needs k_scale and v_scale")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t.dim() == 1:
+            _want(t, name, (num_kv_heads,), (torch.float32,))
+        elif (t.dim() != 2 or t.shape[0] != num_blocks or t.shape[1] < num_kv_heads
+              or t.dtype != torch.float32):
+            raise ValueError(f"{name} must be float32 [{num_kv_heads}] or [{num_blocks}, "
+                             f">= {num_kv_heads}], got {list(t.shape)} of {t.dtype}")
+    if k_scale.shape != v_scale.shape:
+        raise ValueError("k_scale and v_scale must be alike")
+    return 0 if k_scale.dim() == 1 else k_scale.shape[1]
+
+
+def quantize_and_cache(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables,
+                       context_lens, query_start=None, max_query_len=1, device_status=None,
+                       stream=None):
+    """Append rows ``[T, Hkv, D]`` to an 8-bit cache ``[NB, bs, Hkv, D]`` with float32 scales
+    ``[NB, >= Hkv]`` per block and head, choosing the scales of the blocks written.
+
+    Sequence ``s`` owns rows ``query_start[s] .. query_start[s + 1] - 1`` (int32 on the
+    device; None: one row per sequence), the last tokens of its context
+    ``context_lens[s]``; ``max_query_len`` is a host upper bound of a sequence's rows."""
+    torch = _torch()
+    nb, bs, hkv, d = _caches(k_cache, v_cache)
+    T, S = k_new.shape[0], context_lens.shape[0]
+    _want(k_new, "k_new", (T, hkv, d), (torch.float32, torch.bfloat16))
+    _want(v_new, "v_new", (T, hkv, d), (k_new.dtype,))
+    _want(context_lens, "context_lens", (S,), (torch.int32,))
+    _want(block_tables, "block_tables", (S, block_tables.shape[-1]), (torch.int32,))
+    if query_start is not None:
+        _want(query_start, "query_start", (S + 1,), (torch.int32,))
+    stride = _block_scales(k_scales, v_scales, nb, hkv)
+    if stride == 0:
+        raise ValueError("k_scales and v_scales must be [num_blocks, >= num_kv_heads]")
+    with _launch_on(stream, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables,
+                    context_lens, query_start, device_status):
+        st = library().quantize_and_cache(
+            _dev(k_new, "k_new"), _dev(v_new, "v_new"), _dev(query_start, "query_start"),
+            _dev(block_tables, "block_tables"), _dev(context_lens, "context_lens"),
+            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(k_scales, "k_scales"),
+            _dev(v_scales, "v_scales"), S, T, int(max_query_len), hkv, d, bs, nb,
+            block_tables.shape[1], stride, _dtype_code(k_new), _dtype_code(k_cache),
+            _dev(device_status, "device_status"), _stream(stream))
+    _check(st, "quantize_and_cache")
+
+
+def gather_cache(k_cache, v_cache, block_tables, row_start, num_rows, max_rows, first_pos=None,
+                 k_scale=None, v_scale=None, out_dtype=None, k_out=None, v_out=None,
+                 device_status=None, stream=None):
+    """Rows of a paged cache back as ``(k, v)``, each ``[num_rows, Hkv, D]``: row
+    ``row_start[s] + i`` is position ``first_pos[s] + i`` (None: ``i``) of sequence ``s``.
+
+    ``row_start`` int32 ``[S + 1]`` and ``first_pos`` int32 ``[S]`` on the device;
+    ``max_rows`` a host upper bound of a sequence's rows.  8-bit codes are multiplied by
+    ``k_scale`` / ``v_scale`` (``[Hkv]``, or ``[NB, >= Hkv]`` per block).  ``out_dtype``
+    float32 or bfloat16 (default: bfloat16, or that of ``k_out``)."""
+    torch = _torch()
+    nb, bs, hkv, d = _caches(k_cache, v_cache)
+    S = block_tables.shape[0]
+    _want(block_tables, "block_tables", (S, block_tables.shape[-1]), (torch.int32,))
+    _want(row_start, "row_start", (S + 1,), (torch.int32,))
+    if first_pos is not None:
+        _want(first_pos, "first_pos", (S,), (torch.int32,))
+    code = _dtype_code(k_cache)
+    stride = _block_scales(k_scale, v_scale, nb, hkv) if code in (FP8_E4M3, INT8) else 0
+    if out_dtype is None:
+        out_dtype = torch.bfloat16 if k_out is None else k_out.dtype
+    shape = (int(num_rows), hkv, d)
+    with _launch_on(stream, k_cache, v_cache, block_tables, row_start, first_pos, k_scale, v_scale,
+                    k_out, v_out, device_status):
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
+        if v_out is None:
+            v_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
+        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+            _want(t, name, shape, (out_dtype,))
+        st = library().gather_cache(
+            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(block_tables, "block_tables"),
+            _dev(row_start, "row_start"), _dev(first_pos, "first_pos"), S, shape[0], int(max_rows),
+            hkv, d, bs, nb, block_tables.shape[1], code, _dev(k_scale, "k_scale"),
+            _dev(v_scale, "v_scale"), stride, _dtype_code(k_out), _dev(k_out, "k_out"),
+            _dev(v_out, "v_out"), _dev(device_status, "device_status"), _stream(stream))
+    _check(st, "gather_cache")
+    return k_out, v_out
+
+
+def _windowed(out, out_dtype, k_scale, window, sinks) -> bool:
+    """Whether a call needs the form with a window, scales per block or another output type."""
+    torch = _torch()
+    if out is not None:
+        if out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
+        out_dtype = out.dtype
+    return bool(window or sinks or (k_scale is not None and k_scale.dim() == 2)
+                or out_dtype not in (None, torch.float32))
+
+
+def _attention_args(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale):
+    """Checks shared by the windowed decode and prefill calls; the scales' stride."""
+    torch = _torch()
+    nb, bs, hkv, d = _caches(k_cache, v_cache)
+    T, hq, _ = q.shape
+    S = context_lens.shape[0]
+    _want(q, "q", (T, hq, d), (torch.float32, torch.bfloat16))
+    _want(context_lens, "context_lens", (S,), (torch.int32,))
+    _want(block_tables, "block_tables", (S, block_tables.shape[-1]), (torch.int32,))
+    if _dtype_code(k_cache) in (FP8_E4M3, INT8):
+        return _block_scales(k_scale, v_scale, nb, hkv)
+    return 0
+
+
+def _attention_out(q, out, out_dtype):
+    torch = _torch()
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype or torch.float32, device=q.device)
+    _want(out, "out", q.shape, (torch.float32, torch.bfloat16))
+    return out
+
+
+def _decode_window(q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len, out,
+                   k_scale, v_scale, workspace, partition, device_status, stream, window, sinks,
+                   out_dtype):
+    torch = _torch()
+    stride = _attention_args(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale)
+    S, hq, d = q.shape
+    _want(context_lens, "context_lens", (S,), (torch.int32,))
+    nb, bs, hkv, _ = k_cache.shape
+    need = workspace_bytes(S, hq, hkv, d, max_context_len, partition, window, sinks)
+    with _launch_on(stream, q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, out,
+                    workspace, device_status):
+        out = _attention_out(q, out, out_dtype)
+        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        st = library().paged_attention_decode_window(
+            _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+            _dev(block_tables, "block_tables"), _dev(context_lens, "context_lens"), S, hq, hkv, d,
+            bs, nb, block_tables.shape[1], int(max_context_len), float(scale), _dtype_code(q),
+            _dtype_code(k_cache), _dev(k_scale, "k_scale"), _dev(v_scale, "v_scale"), stride,
+            int(window), int(sinks), _dtype_code(out), _dev(out, "out"),
+            _dev(workspace, "workspace"), ws_bytes, int(partition),
+            _dev(device_status, "device_status"), _stream(stream))
+    _check(st, "paged_attention_decode_window")
+    return out
 
 
 DECODE_KERNELS = {"auto": 0, "mma": 1, "simt": 2}
@@ -425,12 +621,23 @@ def stall_decode_for_test(nbytes: int = 0):
 
 def paged_attention_decode(q, k_cache, v_cache, block_tables, context_lens, scale,
                            max_context_len, out=None, k_scale=None, v_scale=None,
-                           workspace=None, partition=0, device_status=None, stream=None):
+                           workspace=None, partition=0, device_status=None, stream=None,
+                           window=0, sinks=0, out_dtype=None):
     """Decode attention; returns ``out [S, Hq, D]`` float32 (allocated if None).
 
     ``max_context_len`` is a host int (an upper bound of ``context_lens``).
     The split-KV workspace is allocated with torch when not given.
+
+    ``window`` > 0: the query sees the last ``window`` tokens and the first ``sinks``
+    ones.  ``k_scale`` / ``v_scale`` of an 8-bit cache: ``[Hkv]``, or ``[NB, >= Hkv]`` per
+    block.  ``out_dtype`` float32 or bfloat16.  Any of these takes
+    ``paged_attention_decode_window`` (whose shapes are narrower; its workspace is
+    ``workspace_bytes(..., window=window, sinks=sinks)``).
     """
+    if _windowed(out, out_dtype, k_scale, window, sinks):
+        return _decode_window(q, k_cache, v_cache, block_tables, context_lens, scale,
+                              max_context_len, out, k_scale, v_scale, workspace, partition,
+                              device_status, stream, window, sinks, out_dtype)
     torch = _torch()
     S, hq, d = q.shape
     nb, bs, hkv, _ = k_cache.shape

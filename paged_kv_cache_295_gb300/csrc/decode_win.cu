@@ -1,0 +1,159 @@
+// paged_attention_decode_window: argument checks, partition choice and the
+// launch of the windowed decode kernel (16-bit caches here, 8-bit ones in
+// decode_win_8bit.cu).
+#include <cmath>
+
+#include "decode_win_launch.cuh"
+
+namespace pkv {
+namespace {
+
+bool pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
+int ilog2(int64_t x) {
+  int l = 0;
+  while ((int64_t{1} << l) < x) ++l;
+  return l;
+}
+
+// Tokens of whole 32-token chunks a query can see: what the partitions are
+// sized for (16-token chunks need no more).
+int64_t visible_tokens(int32_t max_ctx, int32_t window, int32_t sinks) {
+  return 32 * max_visible_chunks(max_ctx, window, sinks, 32);
+}
+
+int32_t win_partition(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int64_t tokens,
+                      int32_t req) {
+  const int64_t t = tokens < INT32_MAX ? tokens : INT32_MAX;
+  return paged_attention_partition_tokens(num_seqs, num_q_heads, num_kv_heads,
+                                          static_cast<int32_t>(t), req);
+}
+
+template <int D>
+pkv_status launch16(const WinLaunch& a, const CUtensorMap& tk, const CUtensorMap& tv) {
+  constexpr int NW = D == 256 ? 2 : 4, STAGES = D == 64 ? 3 : 2;   // as launch_mma2
+  return a.q_f32 ? launch_win_shape<BF16, D, true, true, NW, STAGES, 16>(a, tk, tv)
+                 : launch_win_shape<BF16, D, false, true, NW, STAGES, 16>(a, tk, tv);
+}
+
+}  // namespace
+
+pkv_status launch_decode_win(const WinLaunch& a) {
+  CUtensorMap tk, tv;
+  if (!win_maps(a, &tk, &tv)) return PKV_ERR_CUDA;
+  switch (a.head_dim) {
+    case 64: return launch16<64>(a, tk, tv);
+    case 128: return launch16<128>(a, tk, tv);
+    default: return launch16<256>(a, tk, tv);
+  }
+}
+
+}  // namespace pkv
+
+extern "C" size_t paged_attention_window_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,
+                                                         int32_t num_kv_heads, int32_t head_dim,
+                                                         int32_t max_context_len,
+                                                         int32_t partition_tokens, int32_t window,
+                                                         int32_t sinks) {
+  if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      max_context_len < 0 || window < 0 || sinks < 0 || num_q_heads % num_kv_heads != 0)
+    return 0;
+  const int64_t tokens = pkv::visible_tokens(max_context_len, window, sinks);
+  const int32_t P =
+      pkv::win_partition(num_seqs, num_q_heads, num_kv_heads, tokens, partition_tokens);
+  if (P <= 0) return 0;
+  const int64_t parts = (tokens + P - 1) / P;
+  if (parts <= 1) return 0;
+  return static_cast<size_t>(num_seqs) * num_q_heads * parts * (head_dim + 2) * sizeof(float);
+}
+
+extern "C" pkv_status paged_attention_decode_window(
+    const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+    const int32_t* context_lens, int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int64_t num_blocks, int32_t max_blocks_per_seq,
+    int32_t max_context_len, float scale, int32_t q_dtype, int32_t kv_dtype, const float* k_scale,
+    const float* v_scale, int64_t scale_stride, int32_t window, int32_t sinks, int32_t out_dtype,
+    void* out, void* workspace, size_t workspace_bytes, int32_t partition_tokens,
+    int32_t* device_status, pkv_stream_t stream) {
+  using namespace pkv;
+  if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || num_blocks <= 0 ||
+      max_blocks_per_seq <= 0 || max_context_len < 0 || window < 0 || sinks < 0)
+    return PKV_ERR_INVALID_ARG;
+  if (num_q_heads % num_kv_heads != 0 || partition_tokens < 0 || partition_tokens % 64 != 0)
+    return PKV_ERR_INVALID_ARG;
+  if (sinks > 0 && window == 0) return PKV_ERR_INVALID_ARG;   // sinks add to a window
+  if (!std::isfinite(scale)) return PKV_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(max_context_len) > static_cast<int64_t>(max_blocks_per_seq) * block_size)
+    return PKV_ERR_INVALID_ARG;
+  const bool codes = kv_dtype == PKV_FP8_E4M3 || kv_dtype == PKV_INT8;
+  if (!codes && kv_dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
+  if (codes ? head_dim != 128 : (head_dim != 64 && head_dim != 128 && head_dim != 256))
+    return PKV_ERR_UNSUPPORTED;
+  if (q_dtype != PKV_F32 && q_dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
+  if (out_dtype != PKV_F32 && out_dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
+  const int G = num_q_heads / num_kv_heads;
+  if (G > 16 || !pow2(block_size) || block_size < 8 || block_size > 4096)
+    return PKV_ERR_UNSUPPORTED;
+  if (num_blocks > INT32_MAX || num_blocks * block_size > INT32_MAX ||
+      max_context_len > (1 << 30) || num_seqs > 65535 || num_kv_heads > 32767)
+    return PKV_ERR_UNSUPPORTED;
+  if (codes && scale_stride != 0 && scale_stride < num_kv_heads) return PKV_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PKV_OK;
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out ||
+      (codes && (!k_scale || !v_scale)))
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(block_tables) & 3u) ||
+      (reinterpret_cast<uintptr_t>(context_lens) & 3u))
+    return PKV_ERR_INVALID_ARG;
+  if (!encode_fn()) return PKV_ERR_CUDA;
+
+  const int64_t tokens = visible_tokens(max_context_len, window, sinks);
+  const int32_t P = win_partition(num_seqs, num_q_heads, num_kv_heads, tokens, partition_tokens);
+  if (P <= 0) return PKV_ERR_INVALID_ARG;
+  const int64_t parts = tokens > 0 ? (tokens + P - 1) / P : 1;
+  if (parts > 65535) return PKV_ERR_UNSUPPORTED;
+  const size_t need = paged_attention_window_workspace_bytes(
+      num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, P, window, sinks);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
+    return PKV_ERR_INVALID_ARG;
+
+  WinLaunch a{};
+  DecodeParams& p = a.w.p;
+  p.q = q;
+  p.k_cache = static_cast<const uint8_t*>(k_cache);
+  p.v_cache = static_cast<const uint8_t*>(v_cache);
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  float* ws = static_cast<float*>(workspace);
+  p.part_ml = need > 0 ? ws : nullptr;
+  p.part_o = need > 0 ? ws + static_cast<size_t>(num_seqs) * num_q_heads * parts * 2 : nullptr;
+  p.status = device_status;
+  p.num_kv_heads = num_kv_heads;
+  p.num_q_heads = num_q_heads;
+  p.bs_log2 = ilog2(block_size);
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.num_blocks = num_blocks;
+  p.partition_tokens = P;
+  p.max_parts = static_cast<int32_t>(parts);
+  p.q_is_bf16 = q_dtype == PKV_BF16;
+  p.qk_scale_log2 = scale * 1.4426950408889634f;
+  const int chl = codes ? 5 : 4;
+  a.w.out = out;
+  a.w.scale_stride = codes ? scale_stride : 0;
+  a.w.out_bf16 = out_dtype == PKV_BF16;
+  a.w.window = window;
+  a.w.sinks = sinks;
+  a.w.max_context_len = max_context_len;
+  a.w.box_log2 = p.bs_log2 < chl ? p.bs_log2 : chl;
+  a.w.head_split = G > 8 ? 2 : 1;
+  a.w.bits8 = codes;
+  a.num_seqs = num_seqs;
+  a.head_dim = head_dim;
+  a.kv_dtype = kv_dtype;
+  a.num_blocks = num_blocks;
+  a.q_f32 = q_dtype == PKV_F32;
+  a.stream = reinterpret_cast<cudaStream_t>(stream);
+  return codes ? launch_decode_win_8bit(a) : launch_decode_win(a);
+}

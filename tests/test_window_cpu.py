@@ -1,0 +1,181 @@
+"""Refusals of the block-scaled cache's and the windowed attention's calls (no GPU: every
+argument is checked before a launch), and pins of their oracle."""
+import ctypes as C
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import block_scaled as OB
+from oracle import attention as OA
+from tests import paged_cases as PC
+
+OK, INVALID, UNSUPPORTED = 0, 1, 5
+PTR = C.c_void_p(1 << 20)      # aligned, never dereferenced: the calls below are refused first
+
+
+def quantize(lib, **kw):
+    a = dict(k_new=PTR, v_new=PTR, qs=PTR, bt=PTR, ctx=PTR, kc=PTR, vc=PTR, ks=PTR, vs=PTR, S=2, T=8,
+             mq=4, hkv=2, d=64, bs=16, nb=10, mb=4, stride=2, src=1, dst=2)
+    a.update(kw)
+    return lib.library().quantize_and_cache(*a.values(), None, None)
+
+
+def gather(lib, **kw):
+    a = dict(kc=PTR, vc=PTR, bt=PTR, rs=PTR, fp=None, S=2, n=8, mx=4, hkv=2, d=64, bs=16, nb=10, mb=4,
+             kv=2, ks=PTR, vs=PTR, stride=2, out=1, ko=PTR, vo=PTR)
+    a.update(kw)
+    return lib.library().gather_cache(*a.values(), None, None)
+
+
+def decode(lib, **kw):
+    a = dict(q=PTR, kc=PTR, vc=PTR, bt=PTR, ctx=PTR, S=2, hq=8, hkv=2, d=128, bs=16, nb=10, mb=4, mx=64,
+             scale=0.1, qt=1, kv=1, ks=None, vs=None, stride=0, window=8, sinks=2, ot=0, out=PTR,
+             ws=None, wsb=0, part=0)
+    a.update(kw)
+    return lib.library().paged_attention_decode_window(*a.values(), None, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(S=-1), INVALID), (dict(T=-1), INVALID), (dict(hkv=0), INVALID), (dict(nb=0), INVALID),
+    (dict(mb=0), INVALID), (dict(stride=1), INVALID), (dict(mq=9), INVALID),
+    (dict(qs=None), INVALID), (dict(qs=None, mq=1, T=1), INVALID),
+    (dict(dst=1), UNSUPPORTED), (dict(dst=0), UNSUPPORTED), (dict(src=2), UNSUPPORTED),
+    (dict(d=72), UNSUPPORTED), (dict(bs=24), UNSUPPORTED), (dict(bs=8192), UNSUPPORTED),
+    (dict(S=65536, T=65536), UNSUPPORTED), (dict(mb=1 << 28), INVALID),
+    (dict(k_new=None), INVALID), (dict(v_new=None), INVALID), (dict(bt=None), INVALID),
+    (dict(ctx=None), INVALID), (dict(kc=None), INVALID), (dict(ks=None), INVALID),
+    (dict(vs=None), INVALID), (dict(k_new=C.c_void_p(8)), INVALID), (dict(kc=C.c_void_p(24)), INVALID),
+    (dict(bt=C.c_void_p(2)), INVALID), (dict(S=0), OK), (dict(mq=0), OK)])
+def test_quantize_refusals(lib, kw, want):
+    assert quantize(lib, **kw) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(S=-1), INVALID), (dict(n=-1, mx=-1), INVALID), (dict(mx=9), INVALID), (dict(hkv=0), INVALID),
+    (dict(kv=7), UNSUPPORTED), (dict(out=2), UNSUPPORTED), (dict(d=24), UNSUPPORTED),
+    (dict(bs=3), UNSUPPORTED), (dict(stride=1), INVALID), (dict(ks=None), INVALID),
+    (dict(kc=None), INVALID), (dict(rs=None), INVALID), (dict(ko=None), INVALID),
+    (dict(vo=C.c_void_p(4)), INVALID), (dict(rs=C.c_void_p(1)), INVALID),
+    (dict(S=0), OK), (dict(mx=0), OK)])
+def test_gather_refusals(lib, kw, want):
+    assert gather(lib, **kw) == want
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(window=0, sinks=1), INVALID),
+    (dict(hq=7), INVALID), (dict(part=100), INVALID), (dict(part=-64), INVALID),
+    (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID), (dict(mx=65), INVALID),
+    (dict(kv=0), UNSUPPORTED), (dict(d=96), UNSUPPORTED), (dict(kv=2, d=64, ks=PTR, vs=PTR), UNSUPPORTED),
+    (dict(qt=2), UNSUPPORTED), (dict(ot=3), UNSUPPORTED), (dict(hq=34), UNSUPPORTED),
+    (dict(bs=4, mx=16), UNSUPPORTED), (dict(bs=12, mx=48), UNSUPPORTED), (dict(nb=1 << 31), UNSUPPORTED),
+    (dict(kv=2), INVALID), (dict(kv=2, ks=PTR, vs=PTR, stride=1), INVALID),
+    (dict(q=None), INVALID), (dict(out=None), INVALID), (dict(out=C.c_void_p(8)), INVALID),
+    (dict(bt=C.c_void_p(2)), INVALID), (dict(S=0), OK)])
+def test_decode_refusals(lib, kw, want):
+    assert decode(lib, **kw) == want
+
+
+def test_workspace_covers_what_a_query_sees(lib):
+    w = lib.library().paged_attention_window_workspace_bytes
+    # 4 sinks and a window of 256 touch at most 1 + 9 chunks of 32 tokens
+    assert w(2, 8, 2, 128, 100000, 64, 256, 4) == 2 * 8 * 5 * 130 * 4
+    assert w(2, 8, 2, 128, 100000, 320, 256, 4) == 0
+    assert w(2, 8, 2, 128, 640, 64, 0, 0) == 2 * 8 * 10 * 130 * 4
+    assert w(2, 8, 2, 128, 640, 64, 10 ** 9, 10 ** 9) == 2 * 8 * 10 * 130 * 4
+    assert w(2, 7, 2, 128, 640, 64, 0, 0) == 0
+
+
+def test_python_refusals(lib):
+    nb, bs, hkv, d, S = 6, 16, 2, 128, 2
+    k8 = torch.zeros((nb, bs, hkv, d), dtype=torch.int8)
+    sc, ctx = torch.ones((nb, hkv)), torch.ones(S, dtype=torch.int32)
+    bt = torch.zeros((S, 3), dtype=torch.int32)
+    new = torch.zeros((S, hkv, d), dtype=torch.bfloat16)
+    q = torch.zeros((S, 4, d), dtype=torch.bfloat16)
+
+    def quant(**kw):
+        a = dict(k_new=new, v_new=new, k_cache=k8, v_cache=k8, k_scales=sc, v_scales=sc,
+                 block_tables=bt, context_lens=ctx)
+        a.update(kw)
+        lib.quantize_and_cache(**a)
+
+    def dec(**kw):
+        a = dict(q=q, k_cache=k8, v_cache=k8, block_tables=bt, context_lens=ctx, scale=0.1,
+                 max_context_len=48, k_scale=sc, v_scale=sc)
+        a.update(kw)
+        lib.paged_attention_decode(**a)
+
+    for kw in (dict(), dict(k_new=new[:, :1]), dict(v_new=new.float()), dict(k_new=new.half()),
+               dict(k_scales=sc[0]), dict(k_scales=sc[:3]), dict(v_scales=sc.double()),
+               dict(context_lens=ctx.long()), dict(block_tables=bt[:1]), dict(v_cache=k8[:3]),
+               dict(query_start=torch.zeros(S, dtype=torch.int32))):
+        with pytest.raises(ValueError):      # the first: no CPU path
+            quant(**kw)
+    for kw in (dict(), dict(k_scale=None), dict(v_scale=sc[0]), dict(k_scale=sc[:, :1], v_scale=sc[:, :1]),
+               dict(context_lens=ctx[:1]), dict(q=q.half()), dict(block_tables=bt.long()),
+               dict(out=torch.zeros((S, 4, d)), out_dtype=torch.bfloat16)):
+        with pytest.raises(ValueError):
+            dec(**kw)
+    rs = torch.zeros(S + 1, dtype=torch.int32)
+    for kw in (dict(), dict(row_start=rs[:2]), dict(row_start=rs.long()), dict(k_scale=None),
+               dict(first_pos=ctx[:1]), dict(block_tables=bt.long())):
+        a = dict(k_cache=k8, v_cache=k8, block_tables=bt, row_start=rs, num_rows=4, max_rows=2,
+                 k_scale=sc, v_scale=sc)
+        a.update(kw)
+        with pytest.raises(ValueError):
+            lib.gather_cache(**a)
+
+
+# ---- the oracle -------------------------------------------------------------------
+def test_oracle_visible():
+    assert OB.visible(5, 0, 0).tolist() == [0, 1, 2, 3, 4, 5]
+    assert OB.visible(9, 3, 2).tolist() == [0, 1, 7, 8, 9]
+    assert OB.visible(9, 1, 0).tolist() == [9]
+    assert OB.visible(3, 3, 2).tolist() == [0, 1, 2, 3]
+    assert OB.visible(0, 1, 4).tolist() == [0]
+
+
+def test_oracle_window_matches_masked_softmax():
+    rng = np.random.default_rng(0)
+    n, L, hq, hkv, d = 5, 40, 4, 2, 16
+    q, K, V = rng.standard_normal((n, hq, d)), rng.standard_normal((L, hkv, d)), rng.standard_normal((L, hkv, d))
+    pos = np.arange(L - n, L)
+    o, mag, _ = OB.attend(q, pos, K, V, 0.25, 8, 3)
+    k, v = (torch.from_numpy(np.repeat(x, hq // hkv, 1)) for x in (K, V))
+    z = torch.einsum("nhd,lhd->nhl", torch.from_numpy(q), k) * 0.25
+    i, j = torch.from_numpy(pos)[:, None, None], torch.arange(L)
+    z = z.masked_fill(~((j <= i) & ((i - j < 8) | (j < 3))), float("-inf"))
+    want = torch.einsum("nhl,lhd->nhd", z.softmax(-1), v)
+    assert np.abs(o - want.numpy()).max() < 1e-13
+    assert (mag >= np.abs(o) - 1e-15).all()
+
+
+@pytest.mark.parametrize("kv", ["fp8_e4m3", "int8"])
+def test_oracle_append(kv):
+    """Scale of a fresh block, growth by the least power of two, codes that move with it."""
+    case = PC.make(1, kv, [6], 1, 16, 4)
+    b0, b1 = case.tables[0]
+    x = np.zeros((6, 1, 16), dtype=np.float32)
+    x[:4, 0, 0], x[4:, 0, 0] = [1, 2, 3, 4], [1, 5]
+    q = OB.QMAX[kv]
+    OB.quantize_and_cache(x[:4], x[:4], [0, 4], case.tables, [4], case.k, case.v, case.ks, case.vs, "f32", kv)
+    assert case.ks[b0, 0] == np.float32(4) / q
+    OB.quantize_and_cache(x[4:5], x[4:5], [0, 1], case.tables, [5], case.k, case.v, case.ks, case.vs, "f32", kv)
+    assert case.ks[b1, 0] == np.float32(1) / q
+    c = OB.code_values(case.k[b1, 0, 0, 0], kv)
+    assert c == q
+    OB.quantize_and_cache(x[5:], x[5:], [0, 1], case.tables, [6], case.k, case.v, case.ks, case.vs, "f32", kv)
+    assert case.ks[b1, 0] == np.float32(1) / q * 8       # 5 <= 8
+    assert OB.code_values(case.k[b1, 0, 0, 0], kv) == (np.rint(c / 8) if kv == "int8" else c / 8)
+    assert OB.grown_scale(np.float32(1), np.float32(448), np.float32(448)) == (1, 0)
+    assert OB.grown_scale(np.float32(1), np.float32(449), np.float32(448)) == (2, 1)
+    y = OB.gather(case.k, case.ks, case.tables[0], 0, 6, kv)
+    assert np.abs(y - x).max() <= (5 / 127 * 2 if kv == "int8" else 5 * 2.0 ** -4)
+
+
+def test_oracle_gather_of_codes_is_the_static_dequant():
+    case = PC.make(2, "fp8_e4m3", [9], 2, 16, 4, scales="head")
+    y = OB.gather(case.k, case.ks, case.tables[0], 2, 5, "fp8_e4m3")
+    rows = OA.gather_sequence(case.k, case.tables[0], 9)[2:7]
+    assert np.array_equal(y.astype(np.float64), OA.fp8_dequant(rows, case.ks))
