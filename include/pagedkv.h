@@ -580,6 +580,22 @@ pkv_status paged_attention_decode_window(
     void* out, void* workspace, size_t workspace_bytes, int32_t partition_tokens,
     int32_t* device_status, pkv_stream_t stream);
 
+/* paged_attention_prefill with the same window, sinks, scales and output types:
+ * the query at position p (of a chunk's last n_s positions) sees token t <= p when
+ * t > p - window or t < sinks.  window > 0 needs causal = 1; sinks need a window.
+ * 8-bit caches carry the weights as one fp16 value (2^-11 relative), as
+ * paged_attention_prefill does, whatever the output type.  Table entries of blocks
+ * that no query of the chunk sees are not read.  max_context_len <= 2^30; shapes
+ * and errors otherwise as paged_attention_prefill. */
+pkv_status paged_attention_prefill_window(
+    const void* q, const int32_t* query_start, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, const int32_t* context_lens, int32_t num_seqs,
+    int32_t num_tokens, int32_t max_query_len, int32_t num_q_heads, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int64_t num_blocks, int32_t max_blocks_per_seq,
+    int32_t max_context_len, float scale, int32_t causal, int32_t q_dtype, int32_t kv_dtype,
+    const float* k_scale, const float* v_scale, int64_t scale_stride, int32_t window,
+    int32_t sinks, int32_t out_dtype, void* out, int32_t* device_status, pkv_stream_t stream);
+
 /* ------------------------------------------------------------------------ */
 /* CUDA-graph decode step with batch-size buckets and padding.               */
 /* ------------------------------------------------------------------------ */

@@ -121,6 +121,9 @@ _SIGS = {
     "paged_attention_decode_window": (I32, [P, P, P, P, P, I32, I32, I32, I32, I32, I64, I32, I32,
                                             FL, I32, I32, P, P, I64, I32, I32, I32, P, P, SZ, I32,
                                             P, P]),
+    "paged_attention_prefill_window": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32,
+                                             I64, I32, I32, FL, I32, I32, I32, P, P, I64, I32, I32,
+                                             I32, P, P, P]),
     "pkv_test_force_decode_kernel": (I32, [I32]),
     "pkv_test_decode_stall": (I32, [C.c_uint32]),
     "pkv_copy_kernel": (I32, [P, P, SZ, P]),
@@ -602,6 +605,30 @@ def _decode_window(q, k_cache, v_cache, block_tables, context_lens, scale, max_c
     return out
 
 
+def _prefill_window(q, query_start, k_cache, v_cache, block_tables, context_lens, scale,
+                    max_query_len, max_context_len, causal, out, k_scale, v_scale, device_status,
+                    stream, window, sinks, out_dtype):
+    torch = _torch()
+    stride = _attention_args(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale)
+    T, hq, d = q.shape
+    S = context_lens.shape[0]
+    _want(query_start, "query_start", (S + 1,), (torch.int32,))
+    nb, bs, hkv, _ = k_cache.shape
+    with _launch_on(stream, q, query_start, k_cache, v_cache, block_tables, context_lens, k_scale,
+                    v_scale, out, device_status):
+        out = _attention_out(q, out, out_dtype)
+        st = library().paged_attention_prefill_window(
+            _dev(q, "q"), _dev(query_start, "query_start"), _dev(k_cache, "k_cache"),
+            _dev(v_cache, "v_cache"), _dev(block_tables, "block_tables"),
+            _dev(context_lens, "context_lens"), S, T, int(max_query_len), hq, hkv, d, bs, nb,
+            block_tables.shape[1], int(max_context_len), float(scale), 1 if causal else 0,
+            _dtype_code(q), _dtype_code(k_cache), _dev(k_scale, "k_scale"),
+            _dev(v_scale, "v_scale"), stride, int(window), int(sinks), _dtype_code(out),
+            _dev(out, "out"), _dev(device_status, "device_status"), _stream(stream))
+    _check(st, "paged_attention_prefill_window")
+    return out
+
+
 DECODE_KERNELS = {"auto": 0, "mma": 1, "simt": 2}
 
 
@@ -708,11 +735,19 @@ def paged_attention_decode_noalloc(q, k_cache, v_cache, block_tables, context_le
 
 def paged_attention_prefill(q, query_start, k_cache, v_cache, block_tables, context_lens,
                             scale, max_query_len, max_context_len, causal=True, out=None,
-                            k_scale=None, v_scale=None, device_status=None, stream=None):
+                            k_scale=None, v_scale=None, device_status=None, stream=None,
+                            window=0, sinks=0, out_dtype=None):
     """Chunked prefill attention; returns ``out [T, Hq, D]`` float32 (allocated
     if None).  ``query_start`` is int32 ``[S + 1]`` on the device;
     ``max_query_len`` and ``max_context_len`` are host ints (upper bounds);
-    ``k_scale`` / ``v_scale`` (``[Hkv]`` float32) for an FP8 cache."""
+    ``k_scale`` / ``v_scale`` (``[Hkv]`` float32) for an FP8 cache.
+
+    ``window``, ``sinks``, scales ``[NB, >= Hkv]`` per block and ``out_dtype`` as in
+    ``paged_attention_decode``; any of them takes ``paged_attention_prefill_window``."""
+    if _windowed(out, out_dtype, k_scale, window, sinks):
+        return _prefill_window(q, query_start, k_cache, v_cache, block_tables, context_lens, scale,
+                               max_query_len, max_context_len, causal, out, k_scale, v_scale,
+                               device_status, stream, window, sinks, out_dtype)
     torch = _torch()
     T, hq, d = q.shape
     nb, bs, hkv, _ = k_cache.shape

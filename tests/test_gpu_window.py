@@ -2,6 +2,7 @@
 import numpy as np
 import pytest
 
+from oracle import block_scaled as OB
 from tests import gpu_cases as GC
 from tests import paged_cases as PC
 from tests.test_gpu_block_scaled import check_decode, decode
@@ -114,3 +115,142 @@ def test_two_graphs_share_a_workspace(lib):
         graphs[i].replay()
     torch.cuda.synchronize()
     assert all(torch.equal(a, b) for a, b in zip(outs, want))
+
+
+# ---- prefill ------------------------------------------------------------------
+def prefill(lib, case, new, q, scale, out="f32", status=None, causal=True, window=0, sinks=0, **kw):
+    import torch
+    d = case.device()
+    start = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    r = lib.paged_attention_prefill(
+        GC.to_torch(q, "bf16"), start, d["k"], d["v"], d["tables"], d["lens"], scale, max(new),
+        max(case.lens), causal=causal, k_scale=d.get("ks"), v_scale=d.get("vs"), window=window,
+        sinks=sinks, out_dtype=torch.bfloat16 if out == "bf16" else torch.float32,
+        device_status=status, **kw)
+    return r.float().cpu().numpy().astype(np.float64)
+
+
+def check_prefill(lib, case, new, hq, seed, out="f32", window=0, sinks=0, scale=None, causal=True,
+                  sample=9):
+    """Every chunk's first, last and some other rows against the definition."""
+    import torch
+    hkv, d = case.k.shape[2:]
+    scale = d ** -0.5 if scale is None else scale
+    q = PC.bf16_bits(np.random.default_rng(seed).standard_normal((sum(new), hq, d)))
+    q64 = GC.OA.to_f64(q, "bf16")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = prefill(lib, case, new, q, scale, out, status, causal, window, sinks)
+    assert int(status.item()) == 0
+    rng = np.random.default_rng(seed + 1)
+    row = worst = 0
+    for s, (c, n) in enumerate(zip(case.lens, new)):
+        if n == 0:
+            continue
+        pick = np.unique(np.r_[0, n - 1, rng.integers(0, n, sample)])
+        K, V = case.values(s)
+        pos = c - n + pick if causal else np.full(pick.shape, c - 1)
+        x = q64[row + pick]
+        o, mag, reach = OB.attend(x, pos, K, V, scale, window, sinks)
+        lim = PC.attention_bound(case, x, o, mag, reach, scale, False, out == "bf16",
+                                 case.kv == "bf16", min(c, window + sinks) if window else c)
+        worst = max(worst, float((np.abs(got[row + pick] - o) / lim).max()))
+        row += n
+    assert worst <= 1.0, worst
+    return got
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3", "int8"])
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (64, 0), (33, 4), (100, 64), (200, 129),
+                                          (300, 16), (5000, 4)])
+def test_prefill(lib, kv, window, sinks):
+    """Chunks of one token to several query tiles, with and without a prefix; windows below
+    and above the chunk's and the tile's length; group sizes that do and do not divide 128."""
+    for bs, hq, hkv in ((16, 2, 2), (64, 8, 1), (8, 6, 2)):
+        lens = [1, 300, 641, 130, 700]
+        new = [1, 300, 130, 0, 257]
+        case = PC.make(11 * bs + window, kv, lens, hkv, 128, bs, stride=hkv + 1)
+        check_prefill(lib, case, new, hq, 12, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3", "int8"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("bs,hq,hkv", [(16, 4, 4), (128, 16, 1), (32, 3, 1), (256, 5, 1)])
+def test_prefill_block_scales_and_outputs(lib, kv, out, bs, hq, hkv):
+    """The whole context and windows, causal or (without a window) not, either output type,
+    scales of blocks that differ a lot, negative and zero logit scales."""
+    lens, new = [257, 64, 500], [257, 3, 140]
+    case = PC.make(bs, kv, lens, hkv, 128, bs, spread=1.5)
+    if kv != "bf16":
+        case.ks = np.minimum(case.ks, np.float32(8.0 / OB.QMAX[kv]))
+    check_prefill(lib, case, new, hq, 13, out=out)
+    check_prefill(lib, case, new, hq, 14, out=out, causal=False)
+    check_prefill(lib, case, new, hq, 15, out=out, window=77, sinks=3, scale=-0.1)
+    check_prefill(lib, case, new, hq, 16, out=out, window=70, sinks=0, scale=0.0)
+    if kv != "bf16":   # one scale per head
+        case = PC.make(bs, kv, lens, hkv, 128, bs, scales="head")
+        check_prefill(lib, case, new, hq, 17, out=out, window=90, sinks=70)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+def test_prefill_hidden_blocks_are_not_read(lib, kv):
+    """Hidden rows hold NaN and hidden blocks' table entries anything."""
+    import torch
+    bs, window, sinks = 16, 90, 20
+    lens, new = [700, 400, 333], [200, 1, 130]
+    case = PC.make(3, kv, lens, 2, 128, bs)
+    for s, (c, n) in enumerate(zip(lens, new)):
+        low = c - n - window + 1
+        for t in range(sinks, max(sinks, low)):
+            for x in (case.k, case.v):
+                x[case.tables[s][t // bs], t % bs] = GC.POISON[kv][1]
+        for b in range(-(-c // bs)):
+            if b * bs >= sinks and (b + 1) * bs <= low:
+                case.tables[s][b] = -5 if b % 2 else 10 ** 8
+    real = case.tables.copy()
+    case.tables = np.where((real < 0) | (real >= case.k.shape[0]), 0, real).astype(np.int32)
+    hold = case.values
+    kept = case.tables
+    case.tables = real
+    case.values = lambda s, *a: _values_with(case, kept, hold, s)
+    check_prefill(lib, case, new, 4, 5, window=window, sinks=sinks)
+
+
+def _values_with(case, tables, values, s):
+    """The sequence's rows with the hidden blocks' entries replaced and their NaN as 0."""
+    real, case.tables = case.tables, tables
+    K, V = values(s)
+    case.tables = real
+    return np.nan_to_num(K), np.nan_to_num(V)
+
+
+def test_prefill_flags(lib):
+    import torch
+    case = PC.make(6, "bf16", [100, 50, 20], 2, 128, 16)
+    new = [30, 50, 20]
+    q = PC.bf16_bits(np.random.default_rng(1).standard_normal((100, 4, 128)))
+    ok = prefill(lib, case, new, q, 0.1, window=30, sinks=4)
+    case.lens = [100, 49, 20]              # shorter than its chunk: rows of 0
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = prefill(lib, case, new, q, 0.1, status=status, window=30, sinks=4)
+    assert int(status.item()) == lib.DEV_BAD_CONTEXT
+    assert (got[30:80] == 0).all() and np.array_equal(got[:30], ok[:30]) and np.array_equal(got[80:], ok[80:])
+    case = PC.make(6, "bf16", [100, 50, 20], 2, 128, 16)
+    case.tables[0, 4] = 10 ** 7            # tokens 64..79, inside the first chunk's windows
+    status.zero_()
+    got = prefill(lib, case, new, q, 0.1, status=status, window=30, sinks=4)
+    assert int(status.item()) == lib.DEV_BAD_BLOCK and np.array_equal(got[30:], ok[30:])
+
+
+def test_prefill_equals_decode_rows(lib):
+    """The last token of each chunk is the decode query of that context."""
+    for kv in ("bf16", "fp8_e4m3"):
+        case = PC.make(21, kv, [300, 77, 1], 2, 128, 16)
+        new = [40, 77, 1]
+        q = PC.bf16_bits(np.random.default_rng(2).standard_normal((sum(new), 8, 128)))
+        last = np.cumsum(new) - 1
+        for w, s in ((50, 4), (1000, 0)):
+            a = prefill(lib, case, new, q, 0.09, out="bf16", window=w, sinks=s)[last]
+            b = decode(lib, case, q[last], "bf16", 0.09, "bf16", window=w, sinks=s)
+            # both round to bf16: two half steps, and fp16 weights on 8-bit caches
+            A = max(float(np.abs(case.values(i)[1]).max()) for i in range(3))
+            assert np.abs(a - b).max() <= (2 * 2.0 ** -8 + 4 * 2.0 ** -11) * A

@@ -179,3 +179,25 @@ def test_oracle_gather_of_codes_is_the_static_dequant():
     y = OB.gather(case.k, case.ks, case.tables[0], 2, 5, "fp8_e4m3")
     rows = OA.gather_sequence(case.k, case.tables[0], 9)[2:7]
     assert np.array_equal(y.astype(np.float64), OA.fp8_dequant(rows, case.ks))
+
+
+def prefill(lib, **kw):
+    a = dict(q=PTR, qs=PTR, kc=PTR, vc=PTR, bt=PTR, ctx=PTR, S=2, T=8, mq=4, hq=8, hkv=2, d=128, bs=16,
+             nb=10, mb=4, mx=64, scale=0.1, causal=1, qt=1, kv=1, ks=None, vs=None, stride=0, window=8,
+             sinks=2, ot=0, out=PTR)
+    a.update(kw)
+    return lib.library().paged_attention_prefill_window(*a.values(), None, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(window=-1), INVALID), (dict(sinks=-1), INVALID), (dict(window=0), INVALID),
+    (dict(causal=0), INVALID), (dict(causal=2), INVALID), (dict(hq=7), INVALID),
+    (dict(scale=float("nan")), INVALID), (dict(mx=65), INVALID), (dict(mq=9), INVALID),
+    (dict(mb=1 << 28), INVALID), (dict(kv=0), UNSUPPORTED), (dict(qt=0), UNSUPPORTED),
+    (dict(d=64), UNSUPPORTED), (dict(ot=2), UNSUPPORTED), (dict(hq=34), UNSUPPORTED),
+    (dict(bs=4, mx=16), UNSUPPORTED), (dict(nb=1 << 31), UNSUPPORTED), (dict(kv=3), INVALID),
+    (dict(kv=3, ks=PTR, vs=PTR, stride=1), INVALID), (dict(q=None), INVALID), (dict(qs=None), INVALID),
+    (dict(out=C.c_void_p(4)), INVALID), (dict(qs=C.c_void_p(2)), INVALID), (dict(S=0), OK),
+    (dict(mq=0), OK)])
+def test_prefill_refusals(lib, kw, want):
+    assert prefill(lib, **kw) == want
