@@ -9,7 +9,6 @@ Names follow the C ABI in ``include/pagedkv.h``.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes as C
 import os
 
@@ -424,27 +423,62 @@ def workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_l
                                                          head_dim, max_context_len, partition))
 
 
-def _launch_on(stream, t, *others):
-    """Context in which a call allocates and launches: ``stream``, or the current stream
-    of the tensors' device.  All tensors are on one device."""
+# The calls below are made once per layer and step, so their checks are kept to a few
+# attribute reads: a call takes about 10 us of host time, launch included.
+_CODE_OF = {}
+
+
+def _code_of(dtype) -> int:
+    if not _CODE_OF:
+        torch = _torch()
+        _CODE_OF.update({torch.float32: F32, torch.bfloat16: BF16, torch.uint8: FP8_E4M3,
+                         torch.float8_e4m3fn: FP8_E4M3, torch.int8: INT8})
+    code = _CODE_OF.get(dtype)
+    if code is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    return code
+
+
+def _elsewhere(t, stream):
+    """None if the call runs on the current stream of the tensor's device and that device is
+    current; else the context that makes it so."""
     torch = _torch()
-    if t.device.type != "cuda":
+    dev = t.get_device()
+    if dev < 0:
         raise ValueError("CUDA tensors are needed (no CPU path)")
-    for o in others:
-        if o is not None and o.device != t.device:
-            raise ValueError(f"tensors on {t.device} and {o.device}")
     if stream is not None:
-        if stream.device != t.device:
-            raise ValueError(f"tensors on {t.device}, stream of {stream.device}")
+        if stream.device_index != dev:
+            raise ValueError(f"tensors on cuda:{dev}, stream of cuda:{stream.device_index}")
         return torch.cuda.stream(stream)
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
 
 
-def _want(t, name, shape, dtypes):
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
-        raise ValueError(f"{name} must be {list(shape)} of {[str(d) for d in dtypes]}, got "
+def _current_stream(dev):
+    torch = _torch()
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _ptrs(dev, **tensors):
+    """Device pointers (None for None) of contiguous tensors on device ``dev``, by name."""
+    out = []
+    for name, t in tensors.items():
+        if t is None:
+            out.append(None)
+        elif t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, the call on cuda:{dev}")
+        elif not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        else:
+            out.append(t.data_ptr())
+    return out
+
+
+def _want(t, name, shape, *codes):
+    """Shape and element type (as pkv_dtype codes, or torch dtypes) of an argument."""
+    if t.shape != shape or (t.dtype not in codes and _CODE_OF.get(t.dtype) not in codes):
+        raise ValueError(f"{name} must be {list(shape)} of "
+                         f"{[DTYPE_NAMES.get(c, c) if type(c) is int else c for c in codes]}, got "
                          f"{list(t.shape)} of {t.dtype}")
 
 
@@ -455,21 +489,30 @@ def _caches(k_cache, v_cache):
     return k_cache.shape
 
 
+def _tables(block_tables, context_lens, num_seqs):
+    i32 = _torch().int32
+    if block_tables.dim() != 2 or block_tables.shape[0] != num_seqs or block_tables.dtype != i32:
+        raise ValueError(f"block_tables must be int32 [{num_seqs}, max_blocks], got "
+                         f"{list(block_tables.shape)} of {block_tables.dtype}")
+    if context_lens is not None:
+        _want(context_lens, "context_lens", (num_seqs,), i32)
+    return block_tables.shape[1]
+
+
 def _block_scales(k_scale, v_scale, num_blocks, num_kv_heads):
     """Floats between the scales of two blocks; 0 for one scale per head."""
-    torch = _torch()
     if k_scale is None or v_scale is None:
         raise ValueError("an 8-bit cache needs k_scale and v_scale")
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t.dim() == 1:
-            _want(t, name, (num_kv_heads,), (torch.float32,))
-        elif (t.dim() != 2 or t.shape[0] != num_blocks or t.shape[1] < num_kv_heads
-              or t.dtype != torch.float32):
-            raise ValueError(f"{name} must be float32 [{num_kv_heads}] or [{num_blocks}, "
-                             f">= {num_kv_heads}], got {list(t.shape)} of {t.dtype}")
-    if k_scale.shape != v_scale.shape:
-        raise ValueError("k_scale and v_scale must be alike")
-    return 0 if k_scale.dim() == 1 else k_scale.shape[1]
+    f32 = _torch().float32
+    shape = k_scale.shape
+    per_head = len(shape) == 1
+    if v_scale.shape != shape or k_scale.dtype != f32 or v_scale.dtype != f32 or (
+            shape[0] != num_kv_heads if per_head else
+            len(shape) != 2 or shape[0] != num_blocks or shape[1] < num_kv_heads):
+        raise ValueError(f"k_scale and v_scale must be float32 [{num_kv_heads}] or [{num_blocks}, "
+                         f">= {num_kv_heads}], both alike, got {list(shape)} of {k_scale.dtype} and "
+                         f"{list(v_scale.shape)} of {v_scale.dtype}")
+    return 0 if per_head else shape[1]
 
 
 def quantize_and_cache(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables,
@@ -484,25 +527,29 @@ def quantize_and_cache(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block
     torch = _torch()
     nb, bs, hkv, d = _caches(k_cache, v_cache)
     T, S = k_new.shape[0], context_lens.shape[0]
-    _want(k_new, "k_new", (T, hkv, d), (torch.float32, torch.bfloat16))
-    _want(v_new, "v_new", (T, hkv, d), (k_new.dtype,))
-    _want(context_lens, "context_lens", (S,), (torch.int32,))
-    _want(block_tables, "block_tables", (S, block_tables.shape[-1]), (torch.int32,))
+    src, dst = _code_of(k_new.dtype), _code_of(k_cache.dtype)
+    _want(k_new, "k_new", (T, hkv, d), F32, BF16)
+    _want(v_new, "v_new", (T, hkv, d), src)
+    mb = _tables(block_tables, context_lens, S)
     if query_start is not None:
-        _want(query_start, "query_start", (S + 1,), (torch.int32,))
+        _want(query_start, "query_start", (S + 1,), torch.int32)
     stride = _block_scales(k_scales, v_scales, nb, hkv)
     if stride == 0:
         raise ValueError("k_scales and v_scales must be [num_blocks, >= num_kv_heads]")
-    with _launch_on(stream, k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables,
-                    context_lens, query_start, device_status):
-        st = library().quantize_and_cache(
-            _dev(k_new, "k_new"), _dev(v_new, "v_new"), _dev(query_start, "query_start"),
-            _dev(block_tables, "block_tables"), _dev(context_lens, "context_lens"),
-            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(k_scales, "k_scales"),
-            _dev(v_scales, "v_scales"), S, T, int(max_query_len), hkv, d, bs, nb,
-            block_tables.shape[1], stride, _dtype_code(k_new), _dtype_code(k_cache),
-            _dev(device_status, "device_status"), _stream(stream))
-    _check(st, "quantize_and_cache")
+    place = _elsewhere(k_new, stream)
+    if place is not None:
+        with place:
+            return quantize_and_cache(k_new, v_new, k_cache, v_cache, k_scales, v_scales,
+                                      block_tables, context_lens, query_start, max_query_len,
+                                      device_status)
+    dev = k_new.get_device()
+    ptrs = _ptrs(dev, k_new=k_new, v_new=v_new, query_start=query_start, block_tables=block_tables,
+                 context_lens=context_lens, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
+                 v_scales=v_scales)
+    status = _ptrs(dev, device_status=device_status)[0] if device_status is not None else None
+    _check(library().quantize_and_cache(*ptrs, S, T, int(max_query_len), hkv, d, bs, nb, mb, stride,
+                                        src, dst, status, _current_stream(dev)),
+           "quantize_and_cache")
 
 
 def gather_cache(k_cache, v_cache, block_tables, row_start, num_rows, max_rows, first_pos=None,
@@ -518,30 +565,39 @@ def gather_cache(k_cache, v_cache, block_tables, row_start, num_rows, max_rows, 
     torch = _torch()
     nb, bs, hkv, d = _caches(k_cache, v_cache)
     S = block_tables.shape[0]
-    _want(block_tables, "block_tables", (S, block_tables.shape[-1]), (torch.int32,))
-    _want(row_start, "row_start", (S + 1,), (torch.int32,))
+    mb = _tables(block_tables, None, S)
+    _want(row_start, "row_start", (S + 1,), torch.int32)
     if first_pos is not None:
-        _want(first_pos, "first_pos", (S,), (torch.int32,))
-    code = _dtype_code(k_cache)
-    stride = _block_scales(k_scale, v_scale, nb, hkv) if code in (FP8_E4M3, INT8) else 0
+        _want(first_pos, "first_pos", (S,), torch.int32)
+    code = _code_of(k_cache.dtype)
+    stride = 0
+    if code in (FP8_E4M3, INT8):
+        stride = _block_scales(k_scale, v_scale, nb, hkv)
+    else:
+        k_scale = v_scale = None
+    place = _elsewhere(k_cache, stream)
+    if place is not None:
+        with place:
+            return gather_cache(k_cache, v_cache, block_tables, row_start, num_rows, max_rows,
+                                first_pos, k_scale, v_scale, out_dtype, k_out, v_out, device_status)
     if out_dtype is None:
         out_dtype = torch.bfloat16 if k_out is None else k_out.dtype
     shape = (int(num_rows), hkv, d)
-    with _launch_on(stream, k_cache, v_cache, block_tables, row_start, first_pos, k_scale, v_scale,
-                    k_out, v_out, device_status):
-        if k_out is None:
-            k_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
-        if v_out is None:
-            v_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
-        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-            _want(t, name, shape, (out_dtype,))
-        st = library().gather_cache(
-            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(block_tables, "block_tables"),
-            _dev(row_start, "row_start"), _dev(first_pos, "first_pos"), S, shape[0], int(max_rows),
-            hkv, d, bs, nb, block_tables.shape[1], code, _dev(k_scale, "k_scale"),
-            _dev(v_scale, "v_scale"), stride, _dtype_code(k_out), _dev(k_out, "k_out"),
-            _dev(v_out, "v_out"), _dev(device_status, "device_status"), _stream(stream))
-    _check(st, "gather_cache")
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
+    out_code = _code_of(out_dtype)
+    _want(k_out, "k_out", shape, out_code)
+    _want(v_out, "v_out", shape, out_code)
+    dev = k_cache.get_device()
+    kc, vc, bt, rs, fp, ks, vs, ko, vo, status = _ptrs(
+        dev, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, row_start=row_start,
+        first_pos=first_pos, k_scale=k_scale, v_scale=v_scale, k_out=k_out, v_out=v_out,
+        device_status=device_status)
+    _check(library().gather_cache(kc, vc, bt, rs, fp, S, shape[0], int(max_rows), hkv, d, bs, nb, mb,
+                                  code, ks, vs, stride, out_code, ko, vo, status,
+                                  _current_stream(dev)), "gather_cache")
     return k_out, v_out
 
 
@@ -553,28 +609,31 @@ def _windowed(out, out_dtype, k_scale, window, sinks) -> bool:
             raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
         out_dtype = out.dtype
     return bool(window or sinks or (k_scale is not None and k_scale.dim() == 2)
-                or out_dtype not in (None, torch.float32))
+                or (out_dtype is not None and out_dtype != torch.float32))
 
 
 def _attention_args(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale):
-    """Checks shared by the windowed decode and prefill calls; the scales' stride."""
-    torch = _torch()
+    """Checks shared by the windowed decode and prefill calls.  Returns S, Hq, Hkv, D, block size,
+    blocks, table width, the codes of q and of the cache, the scales and their stride."""
     nb, bs, hkv, d = _caches(k_cache, v_cache)
     T, hq, _ = q.shape
     S = context_lens.shape[0]
-    _want(q, "q", (T, hq, d), (torch.float32, torch.bfloat16))
-    _want(context_lens, "context_lens", (S,), (torch.int32,))
-    _want(block_tables, "block_tables", (S, block_tables.shape[-1]), (torch.int32,))
-    if _dtype_code(k_cache) in (FP8_E4M3, INT8):
-        return _block_scales(k_scale, v_scale, nb, hkv)
-    return 0
+    q_code, kv_code = _code_of(q.dtype), _code_of(k_cache.dtype)
+    _want(q, "q", (T, hq, d), F32, BF16)
+    mb = _tables(block_tables, context_lens, S)
+    stride = 0
+    if kv_code in (FP8_E4M3, INT8):
+        stride = _block_scales(k_scale, v_scale, nb, hkv)
+    else:
+        k_scale = v_scale = None
+    return S, hq, hkv, d, bs, nb, mb, q_code, kv_code, k_scale, v_scale, stride
 
 
 def _attention_out(q, out, out_dtype):
     torch = _torch()
     if out is None:
         out = torch.empty(q.shape, dtype=out_dtype or torch.float32, device=q.device)
-    _want(out, "out", q.shape, (torch.float32, torch.bfloat16))
+    _want(out, "out", q.shape, F32, BF16)
     return out
 
 
@@ -582,26 +641,33 @@ def _decode_window(q, k_cache, v_cache, block_tables, context_lens, scale, max_c
                    k_scale, v_scale, workspace, partition, device_status, stream, window, sinks,
                    out_dtype):
     torch = _torch()
-    stride = _attention_args(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale)
-    S, hq, d = q.shape
-    _want(context_lens, "context_lens", (S,), (torch.int32,))
-    nb, bs, hkv, _ = k_cache.shape
-    need = workspace_bytes(S, hq, hkv, d, max_context_len, partition, window, sinks)
-    with _launch_on(stream, q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, out,
-                    workspace, device_status):
-        out = _attention_out(q, out, out_dtype)
-        if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = library().paged_attention_decode_window(
-            _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
-            _dev(block_tables, "block_tables"), _dev(context_lens, "context_lens"), S, hq, hkv, d,
-            bs, nb, block_tables.shape[1], int(max_context_len), float(scale), _dtype_code(q),
-            _dtype_code(k_cache), _dev(k_scale, "k_scale"), _dev(v_scale, "v_scale"), stride,
-            int(window), int(sinks), _dtype_code(out), _dev(out, "out"),
-            _dev(workspace, "workspace"), ws_bytes, int(partition),
-            _dev(device_status, "device_status"), _stream(stream))
-    _check(st, "paged_attention_decode_window")
+    S, hq, hkv, d, bs, nb, mb, q_code, kv_code, k_scale, v_scale, stride = _attention_args(
+        q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale)
+    if q.shape[0] != S:
+        raise ValueError(f"q must hold one row per sequence: {q.shape[0]} rows, {S} contexts")
+    place = _elsewhere(q, stream)
+    if place is not None:
+        with place:
+            return _decode_window(q, k_cache, v_cache, block_tables, context_lens, scale,
+                                  max_context_len, out, k_scale, v_scale, workspace, partition,
+                                  device_status, None, window, sinks, out_dtype)
+    out = _attention_out(q, out, out_dtype)
+    lib = library()
+    need = lib.paged_attention_window_workspace_bytes(S, hq, hkv, d, max_context_len, partition,
+                                                      window, sinks)
+    ws_bytes = 0 if workspace is None else workspace.nbytes
+    if need > ws_bytes:
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        ws_bytes = need
+    dev = q.get_device()
+    qp, kc, vc, bt, cl, ks, vs, op, ws, status = _ptrs(
+        dev, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
+        context_lens=context_lens, k_scale=k_scale, v_scale=v_scale, out=out, workspace=workspace,
+        device_status=device_status)
+    _check(lib.paged_attention_decode_window(
+        qp, kc, vc, bt, cl, S, hq, hkv, d, bs, nb, mb, int(max_context_len), float(scale), q_code,
+        kv_code, ks, vs, stride, int(window), int(sinks), _code_of(out.dtype), op, ws, ws_bytes,
+        int(partition), status, _current_stream(dev)), "paged_attention_decode_window")
     return out
 
 
@@ -609,23 +675,26 @@ def _prefill_window(q, query_start, k_cache, v_cache, block_tables, context_lens
                     max_query_len, max_context_len, causal, out, k_scale, v_scale, device_status,
                     stream, window, sinks, out_dtype):
     torch = _torch()
-    stride = _attention_args(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale)
-    T, hq, d = q.shape
-    S = context_lens.shape[0]
-    _want(query_start, "query_start", (S + 1,), (torch.int32,))
-    nb, bs, hkv, _ = k_cache.shape
-    with _launch_on(stream, q, query_start, k_cache, v_cache, block_tables, context_lens, k_scale,
-                    v_scale, out, device_status):
-        out = _attention_out(q, out, out_dtype)
-        st = library().paged_attention_prefill_window(
-            _dev(q, "q"), _dev(query_start, "query_start"), _dev(k_cache, "k_cache"),
-            _dev(v_cache, "v_cache"), _dev(block_tables, "block_tables"),
-            _dev(context_lens, "context_lens"), S, T, int(max_query_len), hq, hkv, d, bs, nb,
-            block_tables.shape[1], int(max_context_len), float(scale), 1 if causal else 0,
-            _dtype_code(q), _dtype_code(k_cache), _dev(k_scale, "k_scale"),
-            _dev(v_scale, "v_scale"), stride, int(window), int(sinks), _dtype_code(out),
-            _dev(out, "out"), _dev(device_status, "device_status"), _stream(stream))
-    _check(st, "paged_attention_prefill_window")
+    S, hq, hkv, d, bs, nb, mb, q_code, kv_code, k_scale, v_scale, stride = _attention_args(
+        q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale)
+    _want(query_start, "query_start", (S + 1,), torch.int32)
+    place = _elsewhere(q, stream)
+    if place is not None:
+        with place:
+            return _prefill_window(q, query_start, k_cache, v_cache, block_tables, context_lens,
+                                   scale, max_query_len, max_context_len, causal, out, k_scale,
+                                   v_scale, device_status, None, window, sinks, out_dtype)
+    out = _attention_out(q, out, out_dtype)
+    dev = q.get_device()
+    qp, qs, kc, vc, bt, cl, ks, vs, op, status = _ptrs(
+        dev, q=q, query_start=query_start, k_cache=k_cache, v_cache=v_cache,
+        block_tables=block_tables, context_lens=context_lens, k_scale=k_scale, v_scale=v_scale,
+        out=out, device_status=device_status)
+    _check(library().paged_attention_prefill_window(
+        qp, qs, kc, vc, bt, cl, S, q.shape[0], int(max_query_len), hq, hkv, d, bs, nb, mb,
+        int(max_context_len), float(scale), 1 if causal else 0, q_code, kv_code, ks, vs, stride,
+        int(window), int(sinks), _code_of(out.dtype), op, status, _current_stream(dev)),
+        "paged_attention_prefill_window")
     return out
 
 
@@ -794,6 +863,8 @@ class DecodeGraph:
                  device_status=None):
         torch = _torch()
         e = engine
+        if getattr(e, "scales", None) is not None:
+            raise ValueError("decode graphs take one scale per head, not block scales")
         dev = e.storage.device
         self.buckets = sorted(int(b) for b in buckets)
         B, L = self.buckets[-1], e.num_layers
