@@ -15,13 +15,17 @@
 // code is rescaled exactly unless it becomes subnormal, and the INT8 rounding
 // errors of successive growths are halved by each later one, so a value is
 // never more than one step of its final scale off, however often its block grew.
+#include <type_traits>
+
 #include "common.cuh"
 #include "quant.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kQThreads = 256;
+constexpr int kQThreads = 128;
+constexpr int kGThreads = 256;
+constexpr int kQGrid = 8;
 constexpr float kMinScale = 5.421010862427522e-20f;   // 2^-64
 
 template <typename Q>
@@ -81,18 +85,120 @@ __device__ __forceinline__ Chunk load_chunk(const QuantParams& p, int s) {
   return c;
 }
 
-// One team of T threads per (sequence, touched block, head, K or V); a CTA holds
-// 256 / T teams.  Each thread takes 16-element segments of the new rows.
+// 8 consecutive elements of a row, as loaded.  kHeld of them per thread stay in
+// registers between the maximum and the codes, and as many of the next head's.
+template <typename Src>
+struct Vec8;
+template <>
+struct Vec8<__nv_bfloat16> {
+  static constexpr int kHeld = 8;
+  uint32_t w[4];
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
+  }
+  __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
+  // Elements 2i and 2i + 1, negated.
+  __device__ __forceinline__ float2 neg2(int i) const {
+    const uint32_t n = w[i] ^ 0x80008000u;
+    return make_float2(bf16_lo(n), bf16_hi(n));
+  }
+  // The largest |x| so far as two bf16 halves (NaN stays), and as a float32's bits.
+  __device__ __forceinline__ uint32_t top(uint32_t m) const {
+    __nv_bfloat162 t = *reinterpret_cast<const __nv_bfloat162*>(&m);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      t = __hmax2_nan(t, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+    return *reinterpret_cast<const uint32_t*>(&t);
+  }
+  static __device__ __forceinline__ uint32_t top_bits(uint32_t m) {
+    m &= 0x7FFF7FFFu;
+    return max(m & 0xFFFFu, m >> 16) << 16;
+  }
+};
+template <>
+struct Vec8<float> {
+  static constexpr int kHeld = 4;
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const float* p) {
+    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 0;
+  }
+  __device__ __forceinline__ float2 neg2(int i) const {
+    return make_float2(-__uint_as_float(w[2 * i]), -__uint_as_float(w[2 * i + 1]));
+  }
+  __device__ __forceinline__ uint32_t top(uint32_t m) const {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+    return m;
+  }
+  static __device__ __forceinline__ uint32_t top_bits(uint32_t m) { return m; }
+};
+
+// x / s rounded to nearest, for two finite x given as -x, without a divide per
+// element, by Markstein's theorem ("Computation of elementary functions on the IBM
+// RISC System/6000 processor", 1990): with r = 1 / s rounded to nearest and q within
+// one ulp of x / s, q - (q s - x) r, whose residual one fma gives exactly, is x / s
+// rounded to nearest.  x r is within two ulps, so one step makes it faithful and a
+// second one exact.  s >= 2^-64 keeps the residuals of every quotient that rounds to
+// a non-zero code in the normal range; the sign of a zero x is kept.
+__device__ __forceinline__ float2 quotient2(float2 neg_x, float2 s, float2 neg_r) {
+  float2 q = __fmul2_rn(neg_x, neg_r);
+  q = __ffma2_rn(__ffma2_rn(q, s, neg_x), neg_r, q);
+  return __ffma2_rn(__ffma2_rn(q, s, neg_x), neg_r, q);
+}
+
+// Codes of 8 elements; FINITE: none is an infinity or NaN.
+template <typename Src, typename Q, bool FINITE>
+__device__ __forceinline__ uint2 codes8(const Vec8<Src>& v, float s, float r) {
+  uint32_t w[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    float q[4];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float2 n = v.neg2(2 * k + e);
+      const float2 y = FINITE ? quotient2(n, make_float2(s, s), make_float2(-r, -r))
+                              : make_float2(__fdiv_rn(-n.x, s), __fdiv_rn(-n.y, s));
+      q[2 * e] = y.x;
+      q[2 * e + 1] = y.y;
+    }
+    if constexpr (FINITE && std::is_same<Q, INT8>::value) {
+      // |q| < 127.5: adding 1.5 * 2^23 leaves round-half-even(q) in the low byte
+      uint32_t u[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) u[e] = __float_as_uint(q[e] + 12582912.f);
+      w[k] = __byte_perm(__byte_perm(u[0], u[1], 0x0040), __byte_perm(u[2], u[3], 0x0040), 0x5410);
+    } else {
+      w[k] = quant4<Q>(q);
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// A team of T threads takes one (head, K or V) of one sequence's touched block
+// at a time; a CTA of 128 / T teams walks a share of the block's 2 Hkv of them, so
+// the lookups (context, table) are paid once, and loads the next one's rows
+// before it computes the current one's codes.  Rows are read once, unless a block
+// holds more than T * kHeld vectors (T = 128: block_size * head_dim above 8,192
+// for bf16): the rest is then read again, from L2.  Bound by HBM: 2 or 4 bytes
+// read and 1 written per element.
 template <typename Src, typename Q, int T>
-__global__ void __launch_bounds__(kQThreads) quantize_kernel(const QuantParams p) {
+__global__ void __launch_bounds__(kQThreads, 8) quantize_kernel(const QuantParams p) {
   constexpr int U = kQThreads / T;
-  __shared__ float red[kQThreads / 32];
+  constexpr int kHeld = Vec8<Src>::kHeld;
+  __shared__ uint32_t red[2][kQThreads / 32];
   grid_dependency_wait();
   allow_dependents();
   const int s = blockIdx.y;
   const int i = blockIdx.x / p.head_groups;   // touched block of the sequence
   const int team = threadIdx.x / T, t = threadIdx.x % T;
-  const int unit = (blockIdx.x % p.head_groups) * U + team;   // head, then K | V
   const Chunk c = load_chunk(p, s);
   if (c.bad) {
     if (blockIdx.x == 0 && threadIdx.x == 0) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
@@ -103,87 +209,157 @@ __global__ void __launch_bounds__(kQThreads) quantize_kernel(const QuantParams p
   const int lb = (first >> p.bs_log2) + i;
   if ((static_cast<int64_t>(lb) << p.bs_log2) >= c.ctx) return;
   const int bs = 1 << p.bs_log2;
-  const int pos0 = max(first, lb << p.bs_log2), pos1 = min(c.ctx, (lb + 1) << p.bs_log2);
+  const int pos0 = max(first, lb << p.bs_log2);
+  const int pos1 = static_cast<int>(min(static_cast<int64_t>(c.ctx), (static_cast<int64_t>(lb) + 1) << p.bs_log2));
   const int off = pos0 & (bs - 1);
   const int32_t blk = __ldg(p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq + lb);
+  const int vecs = p.segs * 2;   // 8-element vectors per row
+  const int items = (pos1 - pos0) * vecs;
+  const int units = 2 * p.num_kv_heads;
+  const int64_t row = static_cast<int64_t>(p.num_kv_heads) * vecs;   // vectors per token
+  const int64_t src0 = (static_cast<int64_t>(c.q0) + pos0 - first) * row;
+  // this thread's vectors t, t + T, ...: offsets within a head's rows, -1 past the end
+  int rel[kHeld];
+#pragma unroll
+  for (int k = 0; k < kHeld; ++k) {
+    const int it = t + k * T;
+    rel[k] = it < items ? static_cast<int>((it / vecs) * row) + it % vecs : -1;
+  }
+  const int step = p.head_groups * U;
+  auto head_of = [&](int unit) { return unit >= p.num_kv_heads ? unit - p.num_kv_heads : unit; };
+  auto rows_of = [&](int unit) {   // K of every head, then V
+    return static_cast<const Src*>(unit >= p.num_kv_heads ? p.v_new : p.k_new) +
+           (src0 + head_of(unit) * vecs) * 8;
+  };
+  auto load = [&](Vec8<Src>(&v)[kHeld], int unit) {
+    const Src* src = unit < units ? rows_of(unit) : nullptr;
+#pragma unroll
+    for (int k = 0; k < kHeld; ++k) {
+      v[k].zero();
+      if (src && rel[k] >= 0) v[k].load(src + static_cast<int64_t>(rel[k]) * 8);
+    }
+  };
+  Vec8<Src> held[kHeld];
+  const int u_first = (blockIdx.x % p.head_groups) * U;
+  load(held, u_first + team);
   if (blk < 0 || blk >= p.num_blocks) {   // the same for the whole CTA
-    if (threadIdx.x == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
+    if (threadIdx.x == 0 && blockIdx.x % p.head_groups == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
     return;
   }
-  const bool live = unit < 2 * p.num_kv_heads;
-  const int head = live ? unit >> 1 : 0;
-  const bool is_v = unit & 1;
-  const Src* src = static_cast<const Src*>(is_v ? p.v_new : p.k_new) +
-                   (static_cast<int64_t>(c.q0 + pos0 - first) * p.num_kv_heads + head) *
-                       (p.segs * 16);
-  const int64_t src_row = static_cast<int64_t>(p.num_kv_heads) * p.segs * 16;
-  const int items = live ? (pos1 - pos0) * p.segs : 0;
-
-  float a = 0.f;
-  for (int it = t; it < items; it += T) {
-    float x[16];
-    load16<Src>(src + (it / p.segs) * src_row + (it % p.segs) * 16, x);
+  int turn = 0;
+  // the team's maximum; buf: one of red's halves, by turns
+  auto team_max = [&](uint32_t x, uint32_t* buf) {
+    x = __reduce_max_sync(0xffffffffu, x);
+    if (T > 32) {
+      if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
+      __syncthreads();
 #pragma unroll
-    for (int e = 0; e < 16; ++e) {
-      const float v = fabsf(x[e]);
-      a = v <= 3.402823466e38f ? fmaxf(a, v) : a;   // finite values only
+      for (int w = 0; w < T / 32; ++w) x = max(x, buf[team * (T / 32) + w]);
     }
-  }
-  float* sp = (is_v ? p.v_scales : p.k_scales) + blk * p.scale_stride + head;
-  const float s0 = live && off > 0 ? *sp : 0.f;
+    return x;
+  };
+  auto work = [&](Vec8<Src>(&v)[kHeld], int unit) {
+    const bool live = unit < units;
+    const bool is_v = unit >= p.num_kv_heads;
+    const int head = live ? head_of(unit) : 0;
+    const Src* src = rows_of(live ? unit : 0);
+    float* sp = (is_v ? p.v_scales : p.k_scales) + blk * p.scale_stride + head;
+    const float s0 = live && off > 0 ? *sp : 0.f;
+    uint32_t m = 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-  if (T > 32) {
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = a;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < T / 32; ++w) a = fmaxf(a, red[team * (T / 32) + w]);
-  } else {
-    __syncwarp();
-  }
-  if (!live) return;
-  constexpr float kQ = CodeRange<Q>::kMax;
-  float sc, shrink = 1.f;
-  if (off == 0 || !(s0 >= kMinScale) || s0 > 3.402823466e38f) {
-    sc = fmaxf(__fdiv_rn(a, kQ), kMinScale);
-  } else {
-    sc = s0;
-    while (a > kQ * sc) {
-      sc *= 2.f;
-      shrink *= 0.5f;
-    }
-  }
-  if (t == 0) *sp = sc;
-  uint4* cache = reinterpret_cast<uint4*>(is_v ? p.v_cache : p.k_cache) +
-                 ((static_cast<int64_t>(blk) << p.bs_log2) * p.num_kv_heads + head) * p.segs;
-  const int64_t row = static_cast<int64_t>(p.num_kv_heads) * p.segs;
-  if (shrink < 1.f) {   // the scale grew: the block's older codes move to it
-    for (int it = t; it < off * p.segs; it += T) {
-      uint4* at = cache + (it / p.segs) * row + it % p.segs;
-      float x[16];
-      decode16<Q>(*at, x);
-      uint32_t w[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        float q[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) q[e] = x[4 * k + e] * shrink;
-        w[k] = quant4<Q>(q);
+    for (int k = 0; k < kHeld; ++k) m = v[k].top(m);
+    if (live)
+      for (int it = t + kHeld * T; it < items; it += T) {
+        Vec8<Src> y;
+        y.load(src + ((it / vecs) * row + it % vecs) * 8);
+        m = y.top(m);
       }
-      *at = make_uint4(w[0], w[1], w[2], w[3]);
+    m = team_max(Vec8<Src>::top_bits(m), red[turn]);
+    const bool finite = m < 0x7F800000u;
+    if (T > 32 ? __syncthreads_or(!finite) : !finite) {   // rare: the maximum of the finite values
+      uint32_t f = 0;
+      for (int it = t; live && it < items; it += T) {
+        Vec8<Src> y;
+        y.load(src + ((it / vecs) * row + it % vecs) * 8);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 n = y.neg2(e);
+          const uint32_t b0 = __float_as_uint(n.x) & 0x7FFFFFFFu, b1 = __float_as_uint(n.y) & 0x7FFFFFFFu;
+          if (b0 < 0x7F800000u) f = max(f, b0);
+          if (b1 < 0x7F800000u) f = max(f, b1);
+        }
+      }
+      m = team_max(f, red[turn ^ 1]);
+      if (T > 32) __syncthreads();
     }
+    turn ^= 1;
+    if (!live) return;
+    const float a = __uint_as_float(m);
+    constexpr float kQ = CodeRange<Q>::kMax;
+    float sc, shrink = 1.f;
+    if (off == 0 || !(s0 >= kMinScale) || s0 > 3.402823466e38f) {
+      sc = fmaxf(__fdiv_rn(a, kQ), kMinScale);
+    } else {
+      sc = s0;
+      while (a > kQ * sc) {   // ends: a is finite
+        sc *= 2.f;
+        shrink *= 0.5f;
+      }
+    }
+    if (t == 0) *sp = sc;
+    uint2* cache = reinterpret_cast<uint2*>(is_v ? p.v_cache : p.k_cache) +
+                   (static_cast<int64_t>(blk) << p.bs_log2) * row + head * vecs;
+    if (shrink < 1.f) {   // the scale grew: the block's older codes move to it
+      uint4* old = reinterpret_cast<uint4*>(cache);
+      for (int it = t; it < off * p.segs; it += T) {
+        uint4* at = old + (it / p.segs) * (row / 2) + it % p.segs;
+        float x[16];
+        decode16<Q>(*at, x);
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float q[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) q[e] = x[4 * k + e] * shrink;
+          w[k] = quant4<Q>(q);
+        }
+        *at = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+    }
+    cache += off * row;
+    if (finite) {
+      const float r = __frcp_rn(sc);
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k)
+        if (rel[k] >= 0) cache[rel[k]] = codes8<Src, Q, true>(v[k], sc, r);
+      for (int it = t + kHeld * T; it < items; it += T) {
+        Vec8<Src> y;
+        y.load(src + ((it / vecs) * row + it % vecs) * 8);
+        cache[(it / vecs) * row + it % vecs] = codes8<Src, Q, true>(y, sc, r);
+      }
+    } else {
+      for (int it = t; it < items; it += T) {
+        Vec8<Src> y;
+        y.load(src + ((it / vecs) * row + it % vecs) * 8);
+        cache[(it / vecs) * row + it % vecs] = codes8<Src, Q, false>(y, sc, 0.f);
+      }
+    }
+  };
+  for (int u = u_first; u < units; u += step) {   // uniform over the CTA
+    work(held, u + team);
+    load(held, u + step + team);
   }
-  for (int it = t; it < items; it += T)
-    cache[(off + it / p.segs) * row + it % p.segs] =
-        quant16<Src, Q>(src + (it / p.segs) * src_row + (it % p.segs) * 16, sc);
 }
 
 template <typename Src, typename Q, int T>
 cudaError_t launch_quantize(QuantParams& p, int num_seqs, cudaStream_t st) {
   constexpr int U = kQThreads / T;
-  p.head_groups = (2 * p.num_kv_heads + U - 1) / U;
   const int bs = 1 << p.bs_log2;
   const int64_t touched = (static_cast<int64_t>(p.max_query_len) + bs - 2) / bs + 1;
+  // CTAs per block: one, or more while the grid has fewer than kQGrid CTAs per SM
+  const int64_t most = (2 * p.num_kv_heads + U - 1) / U;
+  const int64_t want = (kQGrid * device_sm_count() + touched * num_seqs - 1) / (touched * num_seqs);
+  p.head_groups = static_cast<int32_t>(want < most ? want : most);
   const int64_t x = touched * p.head_groups;
   if (x > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   return launch_pdl(quantize_kernel<Src, Q, T>, dim3(static_cast<unsigned>(x), num_seqs),
@@ -193,11 +369,11 @@ cudaError_t launch_quantize(QuantParams& p, int num_seqs, cudaStream_t st) {
 template <typename Src, typename Q>
 cudaError_t pick_team(QuantParams& p, int num_seqs, cudaStream_t st) {
   const int bs = 1 << p.bs_log2;
-  const int64_t items = static_cast<int64_t>(p.max_query_len < bs ? p.max_query_len : bs) * p.segs;
-  if (items <= 128) return launch_quantize<Src, Q, 32>(p, num_seqs, st);
-  if (items <= 256) return launch_quantize<Src, Q, 64>(p, num_seqs, st);
-  if (items <= 512) return launch_quantize<Src, Q, 128>(p, num_seqs, st);
-  return launch_quantize<Src, Q, 256>(p, num_seqs, st);
+  const int64_t items = static_cast<int64_t>(p.max_query_len < bs ? p.max_query_len : bs) * p.segs * 2;
+  constexpr int kHeld = Vec8<Src>::kHeld;
+  if (items <= 32 * kHeld) return launch_quantize<Src, Q, 32>(p, num_seqs, st);
+  if (items <= 64 * kHeld) return launch_quantize<Src, Q, 64>(p, num_seqs, st);
+  return launch_quantize<Src, Q, 128>(p, num_seqs, st);
 }
 
 // ---- read-back ---------------------------------------------------------------
@@ -223,14 +399,6 @@ struct GatherParams {
   int32_t tile_rows;            // rows per CTA
 };
 
-template <typename KV>
-__device__ __forceinline__ void load_values16(const uint8_t* row, int seg, float* x) {
-  constexpr int V = KV::kBytes;   // 16-byte vectors per segment
-  const uint4* v = reinterpret_cast<const uint4*>(row) + seg * V;
-#pragma unroll
-  for (int i = 0; i < V; ++i) decode16<KV>(__ldg(v + i), x + i * KV::kPerVec);
-}
-
 __device__ __forceinline__ void store16(float* out, const float* x) {
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -249,15 +417,19 @@ __device__ __forceinline__ void store16(__nv_bfloat16* out, const float* x) {
 }
 
 // One CTA per (tile of a sequence's rows, sequence); a thread takes 16-element
-// segments, K and V of the same place.
+// segments, K and V of the same place, kGHeld of them at a time: their table
+// entries, then their codes and scales, are each one round trip.  Bound by HBM: one
+// byte read and two (bf16) or four written per element.
+constexpr int kGHeld = 2;
+
 template <typename KV, typename Out>
-__global__ void __launch_bounds__(kQThreads) gather_kernel(const GatherParams p) {
+__global__ void __launch_bounds__(kGThreads) gather_kernel(const GatherParams p) {
   grid_dependency_wait();
   allow_dependents();
   const int s = blockIdx.y;
   const int r0 = __ldg(p.row_start + s), r1 = __ldg(p.row_start + s + 1);
   const int64_t pos0 = p.first_pos ? __ldg(p.first_pos + s) : 0;
-  const int n = r1 - r0;
+  const int64_t n = static_cast<int64_t>(r1) - r0;
   const int64_t cap = static_cast<int64_t>(p.max_blocks_per_seq) << p.bs_log2;
   if (r0 < 0 || n < 0 || r1 > p.num_rows || n > p.max_rows || pos0 < 0 || pos0 + n > cap) {
     if (blockIdx.x == 0 && threadIdx.x == 0) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
@@ -267,35 +439,61 @@ __global__ void __launch_bounds__(kQThreads) gather_kernel(const GatherParams p)
   if (tile >= n) return;
   const int rows = static_cast<int>(min(static_cast<int64_t>(p.tile_rows), n - tile));
   const int per_row = p.num_kv_heads * p.segs;
+  const int items = rows * per_row;
   const int32_t* bt = p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq;
-  for (int64_t it = threadIdx.x; it < static_cast<int64_t>(rows) * per_row; it += kQThreads) {
-    const int r = static_cast<int>(it / per_row), hs = static_cast<int>(it % per_row);
-    const int head = hs / p.segs;
-    const int64_t pos = pos0 + tile + r;
-    const int32_t blk = __ldg(bt + (pos >> p.bs_log2));
-    float k[16], v[16];
-    if (blk >= 0 && blk < p.num_blocks) {
-      const int64_t slot = (static_cast<int64_t>(blk) << p.bs_log2) + (pos & ((1 << p.bs_log2) - 1));
-      const int64_t row = slot * per_row * 16 * KV::kBytes;
-      load_values16<KV>(p.k_cache + row, hs, k);
-      load_values16<KV>(p.v_cache + row, hs, v);
-      if (KV::kBytes == 1) {
-        const int64_t at = p.scale_stride ? blk * p.scale_stride + head : head;
-        const float ks = __ldg(p.k_scale + at), vs = __ldg(p.v_scale + at);
+  constexpr int V = KV::kBytes;   // 16-byte vectors per segment
+  for (int it0 = threadIdx.x; it0 < items; it0 += kGThreads * kGHeld) {
+    int32_t blk[kGHeld];
+    int64_t pos[kGHeld];
+    int hs[kGHeld];
+#pragma unroll
+    for (int k = 0; k < kGHeld; ++k) {
+      const int it = it0 + k * kGThreads;
+      const int r = it / per_row;
+      hs[k] = it - r * per_row;
+      pos[k] = pos0 + tile + r;
+      blk[k] = it < items ? __ldg(bt + (pos[k] >> p.bs_log2)) : 0;
+    }
+    uint4 kc[kGHeld][V], vc[kGHeld][V];
+    float ks[kGHeld], vs[kGHeld];
+#pragma unroll
+    for (int k = 0; k < kGHeld; ++k) {
+      const bool ok = it0 + k * kGThreads < items && blk[k] >= 0 && blk[k] < p.num_blocks;
+      if (it0 + k * kGThreads < items && !ok) flag_status(p.status, PKV_DEV_BAD_BLOCK);
+      const int64_t slot = (static_cast<int64_t>(blk[k]) << p.bs_log2) + (pos[k] & ((1 << p.bs_log2) - 1));
+      const int64_t at = (slot * per_row + hs[k]) * V;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        kc[k][i] = ok ? __ldg(reinterpret_cast<const uint4*>(p.k_cache) + at + i) : make_uint4(0, 0, 0, 0);
+        vc[k][i] = ok ? __ldg(reinterpret_cast<const uint4*>(p.v_cache) + at + i) : make_uint4(0, 0, 0, 0);
+      }
+      if (V == 1) {
+        const int64_t sc = p.scale_stride ? blk[k] * p.scale_stride + hs[k] / p.segs : hs[k] / p.segs;
+        ks[k] = ok ? __ldg(p.k_scale + sc) : 0.f;
+        vs[k] = ok ? __ldg(p.v_scale + sc) : 0.f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kGHeld; ++k) {
+      const int it = it0 + k * kGThreads;
+      if (it >= items) break;
+      const int64_t o = ((r0 + tile) * per_row + it) * 16;
+      float x[16], y[16];
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        decode16<KV>(kc[k][i], x + i * KV::kPerVec);
+        decode16<KV>(vc[k][i], y + i * KV::kPerVec);
+      }
+      if (V == 1) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          k[e] *= ks;
-          v[e] *= vs;
+          x[e] *= ks[k];
+          y[e] *= vs[k];
         }
       }
-    } else {
-      flag_status(p.status, PKV_DEV_BAD_BLOCK);
-#pragma unroll
-      for (int e = 0; e < 16; ++e) k[e] = v[e] = 0.f;
+      store16(static_cast<Out*>(p.k_out) + o, x);
+      store16(static_cast<Out*>(p.v_out) + o, y);
     }
-    const int64_t o = ((r0 + tile + r) * per_row + hs) * 16;
-    store16(static_cast<Out*>(p.k_out) + o, k);
-    store16(static_cast<Out*>(p.v_out) + o, v);
   }
 }
 
@@ -413,11 +611,11 @@ extern "C" pkv_status gather_cache(
   p.bs_log2 = ilog2(block_size);
   p.max_blocks_per_seq = max_blocks_per_seq;
   const int per_row = num_kv_heads * p.segs;
-  p.tile_rows = per_row >= 4 * kQThreads ? 1 : (4 * kQThreads) / per_row;
+  p.tile_rows = per_row >= 4 * kGThreads ? 1 : (4 * kGThreads) / per_row;
   const int64_t tiles = (static_cast<int64_t>(max_rows) + p.tile_rows - 1) / p.tile_rows;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto launch = [&](auto kern) {
-    return launch_pdl(kern, dim3(static_cast<unsigned>(tiles), num_seqs), dim3(kQThreads), 0, st, p);
+    return launch_pdl(kern, dim3(static_cast<unsigned>(tiles), num_seqs), dim3(kGThreads), 0, st, p);
   };
   auto pick = [&](auto tag) {
     using KV = decltype(tag);

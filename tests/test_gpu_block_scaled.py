@@ -101,6 +101,7 @@ def test_append_special_values(lib, kv, src):
     case = PC.make(9, kv, lens, hkv, d, bs, spread=0.1)
     x = rows(10, sum(new), hkv, d, "f32")
     x[:, 0] = 0.0
+    x[::2, 0, ::3] = -0.0
     x[3, 1, 5], x[4, 1, 6], x[5, 1, 7] = np.nan, np.inf, -np.inf
     x[17, 1] = np.nan                       # a continued block, one row with no finite value
     x[0, 2, 0], x[18, 2, 1] = 3.3e38, -3.3e38
