@@ -78,42 +78,7 @@ struct PrefillParams {
   float qk_scale_log2;
   const float* k_scale;          // FP8 caches: [num_kv_heads] dequant scales
   const float* v_scale;
-  // WIN kernels only: `out` is unused, the output goes to win_out
-  void* win_out;                 // [T, Hq, D], f32 or bf16
-  int64_t scale_stride;          // 8-bit caches: floats between blocks' scales; 0: one per head
-  int32_t out_bf16;
-  int32_t window;                // 0: none
-  int32_t sinks;
 };
-
-// WIN kernels.  A query at position q sees key t <= q with t > q - window or
-// t < sinks.  A CTA's list of key tiles is the sinks' tiles and then the tiles
-// from its first query's window on; tile B skips the list's tiles between the
-// sinks and its own first window.  All scalars of the list:
-struct PfList {
-  int ns;        // list entries 0 .. ns - 1 are key tiles 0 .. ns - 1
-  int base;      // entry j >= ns is key tile j - ns + base
-  int low;       // first key of tile A's first window: older keys are hidden (but sinks)
-  int skip0, nskip;   // tile B leaves out entries skip0 .. skip0 + nskip - 1
-  __device__ __forceinline__ int key0(int j) const { return (j < ns ? j : j - ns + base) * kPfKeys; }
-  __device__ __forceinline__ bool skips(int t, int j) const {
-    return t == 1 && j >= skip0 && j < skip0 + nskip;
-  }
-  // How many entries tile t has worked through before entry j.
-  __device__ __forceinline__ int count(int t, int j) const {
-    return t == 1 && j >= skip0 + nskip ? j - nskip : j;
-  }
-};
-
-// 8-bit caches of WIN kernels: what 8 consecutive keys of a stage share.
-struct PfScale {
-  float kf;    // K scale * logit scale * log2(e)
-  float vs;    // V scale
-  float lv;    // log2 vs
-  float pad;
-};
-// Smallest V scale (2^-100): keeps log2 vs, and p = w / vs < 2^108, finite.
-constexpr float kPfMinVScale = 7.888609052210118e-31f;
 
 // 2^x with the MUFU instruction (relative error about 2^-22; 2^-inf = +0,
 // results below 2^-126 flush to 0, which only drops terms that small).
@@ -172,11 +137,7 @@ struct PfLayout {
 
 // KIND: 0 bf16 cache; 1 FP8-E4M3 codes; 2 INT8 codes.  Both 8-bit kinds take
 // the widening path (FP8 below means "8-bit codes").
-// WIN: keys limited to a window and sinks (PfList), 8-bit caches with a scale per
-// block and head (or per head), output in f32 or bf16.  For 8-bit caches the
-// running reference m follows max(logit + log2 vs), so the weights w = p vs that
-// enter P V stay below 2^8 whatever the blocks' scales; l sums p itself.
-template <int STAGES, int KIND, bool WIN = false>
+template <int STAGES, int KIND>
 __global__ void __launch_bounds__(kPfThreads, 1)
     paged_prefill_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
                             const __grid_constant__ CUtensorMap tmap_v, const PrefillParams p) {
@@ -194,8 +155,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   __shared__ __align__(8) uint64_t s_full[2], s_free[2], q_ready[2], p_full[2], o_done[2], drain[2];
   __shared__ __align__(8) uint64_t raw_full[2][kPfRawBufs];   // FP8: [K | V][buffer] landed
   __shared__ uint64_t key_mask[STAGES];   // per stage: keys with cache data
-  constexpr bool BS = WIN && FP8;
-  __shared__ __align__(16) PfScale key_scale[BS ? STAGES : 1][8];   // per 8 keys of a stage
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
   __shared__ int seq_sh;
@@ -254,55 +213,15 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const int ntok = min(2 * TQ, n - tok0);
     for (int i = tid; i < ntok * G * kPfD; i += kPfThreads) {
       const int t = i / (G * kPfD), r = i % (G * kPfD);
-      const int64_t at = (static_cast<int64_t>(q0 + tok0 + t) * p.num_q_heads + g * G) * kPfD + r;
-      if constexpr (WIN) {
-        if (p.out_bf16)
-          static_cast<__nv_bfloat16*>(p.win_out)[at] = __float2bfloat16_rn(0.f);
-        else
-          static_cast<float*>(p.win_out)[at] = 0.f;
-      } else {
-        p.out[at] = 0.f;
-      }
+      p.out[(static_cast<int64_t>(q0 + tok0 + t) * p.num_q_heads + g * G) * kPfD + r] = 0.f;
     }
     return;
   }
   // key tiles each query tile needs (causal: up to its last token's position)
   const int end_a = min(tok0 + TQ, n), end_b = min(tok0 + 2 * TQ, n);
-  int nt_a = ((p.causal ? ctx - n + end_a : ctx) + kPfKeys - 1) / kPfKeys;
-  int nt_b = has_b ? ((p.causal ? ctx - n + end_b : ctx) + kPfKeys - 1) / kPfKeys : 0;
-  PfList ls = {0, 0, 0, 0, 0};
-  if constexpr (WIN) {   // entries of the list instead of key tiles
-    if (p.window > 0) {
-      const int first_a = ctx - n + tok0;
-      const int sink_tiles = (min(p.sinks, ctx) + kPfKeys - 1) / kPfKeys;
-      ls.low = max(0, first_a - p.window + 1);
-      ls.base = ls.low / kPfKeys;
-      ls.ns = min(sink_tiles, ls.base);
-      nt_a += ls.ns - ls.base;
-      if (has_b) {
-        nt_b += ls.ns - ls.base;
-        ls.skip0 = sink_tiles > ls.base ? sink_tiles : ls.ns;   // (then ns = base)
-        ls.nskip = max(0, max(0, first_a + TQ - p.window + 1) / kPfKeys - ls.base + ls.ns - ls.skip0);
-      }
-    }
-  }
+  const int nt_a = ((p.causal ? ctx - n + end_a : ctx) + kPfKeys - 1) / kPfKeys;
+  const int nt_b = has_b ? ((p.causal ? ctx - n + end_b : ctx) + kPfKeys - 1) / kPfKeys : 0;
   const int ntiles = max(nt_a, nt_b);
-  auto key0 = [&](int j) { return WIN ? ls.key0(j) : j * kPfKeys; };
-  // a box of keys some query of the CTA may see
-  auto box_seen = [&](int kb, int rows) {
-    if constexpr (WIN) return kb < ctx && (kb < p.sinks || kb + rows > ls.low);
-    return kb < ctx;
-  };
-  // keys of the tile at k0 that no query of the CTA sees, as a mask to clear
-  auto hidden = [&](int k0) -> uint64_t {
-    if constexpr (WIN) {
-      const int lo = min(max(ls.low - k0, 0), kPfKeys), sk = min(max(p.sinks - k0, 0), kPfKeys);
-      const uint64_t below = lo >= 64 ? ~0ull : (1ull << lo) - 1ull;
-      const uint64_t sink = sk >= 64 ? ~0ull : (1ull << sk) - 1ull;
-      return below & ~sink;
-    }
-    return 0;
-  };
   const int32_t* bt_row = p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq;
 
   if (tid == 0) {
@@ -353,10 +272,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     const int bx = lane >> 1, hh = lane & 1;
     for (int j = 0; j < ntiles; ++j) {
       const int st = j % STAGES;
-      const int k0 = key0(j);
+      const int k0 = j * kPfKeys;
       const int kb = k0 + bx * box_rows;
       int32_t blk = -1;
-      if (bx < nbox && box_seen(kb, box_rows)) {
+      if (bx < nbox && kb < ctx) {
         const int32_t b = __ldg(bt_row + (kb >> p.bs_log2));
         blk = (b >= 0 && b < p.num_blocks) ? b : -2;
       }
@@ -380,7 +299,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
             const uint64_t run = rows >= 64 ? ~0ull : ((1ull << rows) - 1ull);
             m |= run << (i * box_rows);
           }
-          key_mask[st] = m & ~hidden(k0);
+          key_mask[st] = m;
         }
         mbar_arrive_expect_tx(bar, static_cast<uint32_t>(__popc(valid)) * 2u * box_rows * 128u);
       }
@@ -405,13 +324,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // Looked up one tile ahead of its copy, so the table load's latency
       // overlaps the widening of the tile in between.
       auto lookup = [&](int jj) -> int32_t {
-        const int kb = key0(jj) + lane * box_rows;
-        if (jj >= ntiles || lane >= nbox || !box_seen(kb, box_rows)) return -1;
+        const int kb = jj * kPfKeys + lane * box_rows;
+        if (jj >= ntiles || lane >= nbox || kb >= ctx) return -1;
         const int32_t b = __ldg(bt_row + (kb >> p.bs_log2));
         return (b >= 0 && b < p.num_blocks) ? b : -2;
       };
       auto issue_raw = [&](int jj, int32_t blk) -> uint32_t {   // bit i: box i has data
-        const int kb = key0(jj) + lane * box_rows;
+        const int kb = jj * kPfKeys + lane * box_rows;
         const uint32_t valid = __ballot_sync(0xffffffffu, blk >= 0);
         if (!is_v && __ballot_sync(0xffffffffu, blk == -2) && !flagged) {
           if (lane == 0) flag_status(p.status, PKV_DEV_BAD_BLOCK);
@@ -430,24 +349,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // valids[i]: the boxes of tile j + i that have data (a window that moves
       // with j, so it stays in registers)
       uint32_t valids[kPfRawBufs];
-      // BS, warp 8: lane i keeps the scales of box i of tiles j .. j + kPfRawBufs - 1,
-      // loaded when the tile's copy is issued and published with its key mask
-      PfScale scales[BS ? kPfRawBufs : 1];
-      auto load_scales = [&](int32_t blk) {
-        PfScale e = {0.f, 1.f, 0.f, 0.f};
-        if (BS && !is_v && blk >= 0) {
-          const int64_t at = static_cast<int64_t>(blk) * p.scale_stride + g;
-          e.kf = p.qk_scale_log2 * __ldg(p.k_scale + at);
-          e.vs = fmaxf(__ldg(p.v_scale + at), kPfMinVScale);
-        }
-        return e;
-      };
 #pragma unroll
-      for (int b = 0; b < kPfRawBufs; ++b) {
-        const int32_t blk = lookup(b);
-        valids[b] = b < ntiles ? issue_raw(b, blk) : 0u;
-        if constexpr (BS) scales[b] = load_scales(blk);
-      }
+      for (int b = 0; b < kPfRawBufs; ++b) valids[b] = b < ntiles ? issue_raw(b, lookup(b)) : 0u;
       // Four codes -> two f16x2.  E4M3: exact.  INT8: code + 1152 (one XOR and
       // two PRMT): in K it adds the same 1152 * sum(q) to every logit of a row,
       // which its softmax cancels.  V takes the offset off again (two HSUB2 per
@@ -467,7 +370,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       for (int u = 0; u < 8; ++u) unit_off[u] = static_cast<uint32_t>((u ^ (lane & 7)) << 4);
       for (int j = 0; j < ntiles; ++j) {
         const int st = j % STAGES;
-        const int k0 = key0(j);
+        const int k0 = j * kPfKeys;
         const int32_t next_blk = lookup(j + kPfRawBufs);   // used after this tile's widening
         if (j >= STAGES) {
           bool ok = true;
@@ -524,13 +427,6 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           widen_tile(std::true_type{});
         else
           widen_tile(std::false_type{});
-        if constexpr (BS) {
-          if (!is_v && lane < nbox) {   // box `lane` covers box_rows / 8 of the tile's 8-key groups
-            PfScale e = scales[0];
-            e.lv = __log2f(e.vs);
-            for (int u = 0; u < box_rows / 8; ++u) key_scale[st][lane * (box_rows / 8) + u] = e;
-          }
-        }
         fence_proxy_async();   // the stage's generic writes before the MMAs' reads; the
         __syncwarp();          // raw buffer's reads before the next copy into it
         if (lane == 0) {
@@ -542,17 +438,13 @@ __global__ void __launch_bounds__(kPfThreads, 1)
               const uint64_t run = rows >= 64 ? ~0ull : ((1ull << rows) - 1ull);
               m |= run << (i * box_rows);
             }
-            key_mask[st] = m & ~hidden(k0);
+            key_mask[st] = m;
           }
           mbar_arrive(smem_u32(is_v ? &full_v[st] : &full[st]));
         }
 #pragma unroll
-        for (int b = 0; b + 1 < kPfRawBufs; ++b) {
-          valids[b] = valids[b + 1];
-          if constexpr (BS) scales[b] = scales[b + 1];
-        }
+        for (int b = 0; b + 1 < kPfRawBufs; ++b) valids[b] = valids[b + 1];
         valids[kPfRawBufs - 1] = j + kPfRawBufs < ntiles ? issue_raw(j + kPfRawBufs, next_blk) : 0u;
-        if constexpr (BS) scales[kPfRawBufs - 1] = load_scales(next_blk);
       }
     }
   } else if (warp == 9) {
@@ -568,10 +460,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         bool ok = true;
         for (int t = 0; t < 2; ++t) {
           if (j >= (t == 0 ? nt_a : nt_b)) continue;
-          if (WIN && ls.skips(t, j)) continue;
-          const int jt = WIN ? ls.count(t, j) : j;   // entries this query tile has done
-          const bool ready = jt == 0 ? tc_wait(smem_u32(&q_ready[t]), 0, abort_flag)
-                                     : tc_wait(smem_u32(&s_free[t]), (jt - 1) & 1, abort_flag);
+          const bool ready = j == 0 ? tc_wait(smem_u32(&q_ready[t]), 0, abort_flag)
+                                    : tc_wait(smem_u32(&s_free[t]), (j - 1) & 1, abort_flag);
           if (!ready) {
             ok = false;
             break;
@@ -608,9 +498,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         bool ok = true;
         for (int t = 0; t < 2; ++t) {
           if (j >= (t == 0 ? nt_a : nt_b)) continue;
-          if (WIN && ls.skips(t, j)) continue;
-          const int jt = WIN ? ls.count(t, j) : j;
-          if (!tc_wait(smem_u32(&p_full[t]), jt & 1, abort_flag)) {
+          if (!tc_wait(smem_u32(&p_full[t]), j & 1, abort_flag)) {
             ok = false;
             break;
           }
@@ -621,7 +509,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
 #pragma unroll
           for (int kk = 0; kk < kPfKeys / 16; ++kk) {
             const uint64_t bdesc = vd + ((kk * 2048) >> 4);
-            tc_mma(dO, pd + ((kk * 32) >> 4), bdesc, idesc_pv, (jt > 0 || kk > 0));
+            tc_mma(dO, pd + ((kk * 32) >> 4), bdesc, idesc_pv, (j > 0 || kk > 0));
             if constexpr (!FP8) tc_mma(dO, pd + ((LY::kPPart + kk * 32) >> 4), bdesc, idesc_pv, 1);
           }
           tc_commit(smem_u32(&o_done[t]));
@@ -647,12 +535,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     // exact for every element within 2^-24 of that max (a bf16 has 8
     // significant bits).  The logit scale takes 2^-qsh back.
     float q_unscale = 1.f;
-    float q_offset = 0.f;
     {   // this row of Q_t (token tok0 + t*TQ + r/G, head g*G + r%G; 0 past the
         // chunk) into TMEM, bf16 pairs per column (fp16 for FP8 caches): the A
         // operand of every QK
       float w[64];
-      float qs = 0.f;
       const uint4* src = reinterpret_cast<const uint4*>(
           p.q + (static_cast<int64_t>(q0 + tok0 + t * TQ + tl) * p.num_q_heads + g * G + r % G) *
                     kPfD);
@@ -678,21 +564,12 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const uint4 v = row_ok ? src[i] : make_uint4(0, 0, 0, 0);
         const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {   // FP8 caches: the scaled bf16 pair as an fp16 pair
+        for (int e = 0; e < 4; ++e)   // FP8 caches: the scaled bf16 pair as an fp16 pair
           w[4 * i + e] = __uint_as_float(
               FP8 ? pack_f16(qmul * __uint_as_float(x[e] << 16),
                              qmul * __uint_as_float(x[e] & 0xFFFF0000u))
                   : x[e]);
-          if constexpr (BS && I8) {   // q as the MMA sees it
-            const uint32_t b = __float_as_uint(w[4 * i + e]);
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&b));
-            qs += f.x + f.y;
-          }
-        }
       }
-      // INT8 codes enter Q K^T as code + 1152: with a scale per block the offset no
-      // longer cancels in the softmax, so it is taken off each logit
-      if constexpr (BS && I8) q_offset = 1152.f * qs;
       tc_st32(tQ + lane_q, w);
       tc_st32(tQ + lane_q + 32, w + 32);
       tc_fence_before();
@@ -701,19 +578,16 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     }
     const int qpos = ctx - n + tok0 + t * TQ + tl;      // this row's position
     const int last = p.causal ? qpos : ctx - 1;         // last key it sees
-    const float sl2 = FP8 && !BS ? p.qk_scale_log2 * __ldg(p.k_scale + g) * q_unscale : p.qk_scale_log2;
+    const float sl2 = FP8 ? p.qk_scale_log2 * __ldg(p.k_scale + g) * q_unscale : p.qk_scale_log2;
     const bool pos_scale = sl2 > 0.f;
-    const int row_low = WIN && p.window > 0 ? qpos - p.window + 1 : 0;   // first key of its window
     uint8_t* pb = sm + LY::kP + t * LY::pbuf(FP8);
     float m = -CUDART_INF_F, l = 0.f;                   // m in scaled (log2) units
     bool alive = true;
     for (int j = 0; j < my_nt && alive; ++j) {
-      if (WIN && ls.skips(t, j)) continue;
-      const int jt = WIN ? ls.count(t, j) : j;
-      const int k0 = key0(j);
+      const int k0 = j * kPfKeys;
       // S(j) ready implies the stage's copies landed; waiting on the stage's
       // barrier as well makes the producer's key mask for it visible here.
-      if (!tc_wait(smem_u32(&s_full[t]), jt & 1, abort_flag) ||
+      if (!tc_wait(smem_u32(&s_full[t]), j & 1, abort_flag) ||
           !tc_wait(smem_u32(&full[j % STAGES]), (j / STAGES) & 1, abort_flag))
         alive = false;
       if (!__all_sync(0xffffffffu, alive)) break;
@@ -722,25 +596,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const int lim = last - k0 + 1;
       uint64_t rmask = lim >= kPfKeys ? ~0ull : (lim <= 0 ? 0ull : ((1ull << lim) - 1ull));
       rmask = row_ok ? (rmask & vmask) : 0ull;
-      if constexpr (WIN) {
-        const int lo = row_low - k0;   // keys below it are hidden, but for the sinks
-        if (lo > 0) {
-          const int sk = p.sinks - k0;
-          const uint64_t below = lo >= kPfKeys ? ~0ull : (1ull << lo) - 1ull;
-          const uint64_t sink = sk >= kPfKeys ? ~0ull : (sk <= 0 ? 0ull : (1ull << sk) - 1ull);
-          rmask &= ~below | sink;
-        }
-      }
-      bool pos = pos_scale;
-      float kf[BS ? 8 : 1];   // logit factors of the 8-key groups
-      if constexpr (BS) {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          kf[u] = key_scale[j % STAGES][u].kf * q_unscale;
-          pos = pos && kf[u] > 0.f;
-        }
-      }
-      const bool dense = pos && __all_sync(0xffffffffu, rmask == ~0ull);
+      const bool dense = pos_scale && __all_sync(0xffffffffu, rmask == ~0ull);
       tc_fence_after();
       float sv[kPfKeys];
       pf_ld64(tS + lane_q, sv);
@@ -748,27 +604,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       __syncwarp();
       if ((lane & 31) == 0) mbar_arrive(smem_u32(&s_free[t]));
       float mt;
-      if constexpr (BS) {
-        // (s - q_offset) kf per 8-key group; the reference follows logit + log2 vs
-        mt = -CUDART_INF_F;
-        if (dense) {
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const float a = pf_max3(sv[8 * u], sv[8 * u + 1], sv[8 * u + 2]);
-            const float b = pf_max3(sv[8 * u + 3], sv[8 * u + 4], sv[8 * u + 5]);
-            const float c = fmaxf(sv[8 * u + 6], sv[8 * u + 7]);
-            mt = fmaxf(mt, fmaf(pf_max3(a, b, c) - q_offset, kf[u], key_scale[j % STAGES][u].lv));
-          }
-        } else {
-          const uint32_t mlo = static_cast<uint32_t>(rmask), mhi = static_cast<uint32_t>(rmask >> 32);
-#pragma unroll
-          for (int c = 0; c < kPfKeys; ++c) {
-            const bool ok = ((c < 32 ? mlo : mhi) >> (c & 31)) & 1u;
-            sv[c] = ok ? (sv[c] - q_offset) * kf[c >> 3] : -CUDART_INF_F;
-            mt = fmaxf(mt, sv[c] + key_scale[j % STAGES][c >> 3].lv);
-          }
-        }
-      } else if (dense) {   // warp-uniform: nothing masked; max of the raw logits, then scale
+      if (dense) {   // warp-uniform: nothing masked; max of the raw logits, then scale
         static_assert(kPfKeys % 4 == 0, "two three-input max chains");
         float ma = sv[0], mb = sv[1];
 #pragma unroll
@@ -804,14 +640,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       const float2 nmu = make_float2(-mu, -mu);
       float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
       if (dense) {
-        float2 s2 = make_float2(sl2, sl2), nm = nmu;
+        const float2 s2 = make_float2(sl2, sl2);
 #pragma unroll
         for (int c = 0; c < kPfKeys; c += 2) {
-          if constexpr (BS) {
-            s2 = make_float2(kf[c >> 3], kf[c >> 3]);
-            if constexpr (I8) nm.x = nm.y = fmaf(-q_offset, kf[c >> 3], -mu);
-          }
-          const float2 x = __ffma2_rn(make_float2(sv[c], sv[c + 1]), s2, nm);
+          const float2 x = __ffma2_rn(make_float2(sv[c], sv[c + 1]), s2, nmu);
           sv[c] = pf_ex2(x.x);
           sv[c + 1] = pf_ex2(x.y);
           ls[(c >> 1) & 1] = __fadd2_rn(ls[(c >> 1) & 1], make_float2(sv[c], sv[c + 1]));
@@ -826,17 +658,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         }
       }
       l = l * alpha + ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y));
-      if constexpr (BS) {   // the weights p vs; l has taken p
-#pragma unroll
-        for (int c = 0; c < kPfKeys; c += 2) {
-          const float vs = key_scale[j % STAGES][c >> 3].vs;
-          const float2 w = __fmul2_rn(make_float2(sv[c], sv[c + 1]), make_float2(vs, vs));
-          sv[c] = w.x;
-          sv[c + 1] = w.y;
-        }
-      }
       // PV(j-1) must be finished before P is overwritten and before O is scaled
-      if (jt >= 1 && !tc_wait(smem_u32(&o_done[t]), (jt - 1) & 1, abort_flag)) alive = false;
+      if (j >= 1 && !tc_wait(smem_u32(&o_done[t]), (j - 1) & 1, abort_flag)) alive = false;
       if (!__all_sync(0xffffffffu, alive)) break;
       // P for the MMA.  16-bit caches: bf16 hi part, then what it left (about
       // 2^-17 relative together; bf16 alone would cost up to 2.7e-3 on N(0,1)
@@ -895,31 +718,20 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       if (lane == 0) mbar_arrive(smem_u32(&p_full[t]));
     }
     // epilogue: this warp's O rows / l
-    const int done = WIN ? (my_nt > 0 ? ls.count(t, my_nt) : 0) : my_nt;
     const bool ok = alive && my_nt > 0 &&
-                    tc_wait(smem_u32(&o_done[t]), (done - 1) & 1, abort_flag);
+                    tc_wait(smem_u32(&o_done[t]), (my_nt - 1) & 1, abort_flag);
     if (__all_sync(0xffffffffu, ok)) {   // warp-uniform: the TMEM load is warp-wide
       tc_fence_after();
       // 1 / l, times the V scale for 8-bit caches
-      const float vsc = FP8 && !BS ? __ldg(p.v_scale + g) : 1.f;
+      const float vsc = FP8 ? __ldg(p.v_scale + g) : 1.f;
       const float inv = l > 0.f ? vsc / l : 0.f;
-      const int64_t at = (static_cast<int64_t>(q0 + tok0 + t * TQ + tl) * p.num_q_heads + g * G +
-                          r % G) * kPfD;
-      float* orow = (WIN ? static_cast<float*>(p.win_out) : p.out) + at;
+      float* orow = p.out + (static_cast<int64_t>(q0 + tok0 + t * TQ + tl) * p.num_q_heads +
+                             g * G + r % G) * kPfD;
 #pragma unroll
       for (int c = 0; c < kPfD; c += 32) {
         float o[32];
         tc_ld32(tO + lane_q + c, o);
-        if (WIN && p.out_bf16) {
-          if (row_ok) {
-            __nv_bfloat16* hrow = static_cast<__nv_bfloat16*>(p.win_out) + at;
-#pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              *reinterpret_cast<uint4*>(hrow + c + e) = make_uint4(
-                  pack_bf16(o[e] * inv, o[e + 1] * inv), pack_bf16(o[e + 2] * inv, o[e + 3] * inv),
-                  pack_bf16(o[e + 4] * inv, o[e + 5] * inv), pack_bf16(o[e + 6] * inv, o[e + 7] * inv));
-          }
-        } else if (row_ok) {
+        if (row_ok) {
 #pragma unroll
           for (int e = 0; e < 32; e += 4)
             *reinterpret_cast<float4*>(orow + c + e) =

@@ -2,7 +2,7 @@
 // the tcgen05 prefill kernel with a window, sinks and scales per block.
 #include <cmath>
 
-#include "prefill_tc.cuh"
+#include "prefill_win.cuh"
 #include "tmap.cuh"
 
 namespace pkv {
@@ -57,7 +57,8 @@ extern "C" pkv_status paged_attention_prefill_window(
     return PKV_ERR_INVALID_ARG;
   if (!encode_fn()) return PKV_ERR_CUDA;
 
-  PrefillParams p{};
+  PrefillWinParams w{};
+  PrefillParams& p = w.p;
   p.q = static_cast<const __nv_bfloat16*>(q);
   p.query_start = query_start;
   p.block_tables = block_tables;
@@ -76,11 +77,11 @@ extern "C" pkv_status paged_attention_prefill_window(
   p.qk_scale_log2 = scale * 1.4426950408889634f;
   p.k_scale = codes ? k_scale : nullptr;
   p.v_scale = codes ? v_scale : nullptr;
-  p.win_out = out;
-  p.scale_stride = codes ? scale_stride : 0;
-  p.out_bf16 = out_dtype == PKV_BF16;
-  p.window = window;
-  p.sinks = sinks;
+  w.out = out;
+  w.scale_stride = codes ? scale_stride : 0;
+  w.out_bf16 = out_dtype == PKV_BF16;
+  w.window = window;
+  w.sinks = sinks;
 
   CUtensorMap tk, tv;
   const int64_t rows = num_blocks * block_size;
@@ -90,15 +91,17 @@ extern "C" pkv_status paged_attention_prefill_window(
 
   const int pairs = (max_query_len + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens);
   const dim3 grid(pairs, num_kv_heads, num_seqs);
-  auto launch = [&](auto kern, size_t smem) {
+  auto launch = [&](auto kern, int threads, size_t smem) {
     if (!opt_in_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem)))
       return PKV_ERR_CUDA;
-    kern<<<grid, kPfThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(tk, tv, p);
+    kern<<<grid, threads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(tk, tv, w);
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
   };
+  const size_t smem8 = PwLayout::bytes(kPfStagesFp8, true);
   if (kv_dtype == PKV_FP8_E4M3)
-    return launch(paged_prefill_tc_kernel<kPfStagesFp8, 1, true>, PfLayout::bytes(kPfStagesFp8, true));
+    return launch(paged_prefill_win_kernel<kPfStagesFp8, 1>, kPwThreads8, smem8);
   if (kv_dtype == PKV_INT8)
-    return launch(paged_prefill_tc_kernel<kPfStagesFp8, 2, true>, PfLayout::bytes(kPfStagesFp8, true));
-  return launch(paged_prefill_tc_kernel<kPfStages, 0, true>, PfLayout::bytes(kPfStages, false));
+    return launch(paged_prefill_win_kernel<kPfStagesFp8, 2>, kPwThreads8, smem8);
+  return launch(paged_prefill_win_kernel<kPfStages, 0>, kPfThreads,
+                PwLayout::bytes(kPfStages, false));
 }

@@ -96,8 +96,8 @@ def attention_bound(case, q, out, mag, reach, scale, q_f32, out_bf16, hi_lo, lon
 
     z: 24 float32 steps on sum |q k| (the k-steps' additions, the scales' products, the
     exponent's argument), and q's split where q is float32 (bf16 hi + lo 2^-16, fp16 2^-22).
-    p: hi + lo (bf16 2^-16, fp16 2^-22) or one fp16 (2^-11); ex2.approx and the V scale's
-    product 2^-21.  Sums: a float32 step for each 16 tokens and 24 for warps and partitions.
+    p: hi + lo (bf16 2^-16, fp16 2^-22) or one value (bf16 2^-8, fp16 2^-11); ex2.approx and
+    the V scale's product 2^-21.  Sums: a float32 step for each 16 tokens and 24 for warps and partitions.
     These act on numerator and denominator alike: twice their sum times A.
 
     8-bit caches: an fp16 weight below 2^-14 is off by up to 2^-25 where the largest weight
@@ -118,6 +118,6 @@ def attention_bound(case, q, out, mag, reach, scale, q_f32, out_bf16, hi_lo, lon
         if case.kv == "int8" and not hi_lo:
             dz = dz + 16 * 2.0 ** -23 * scale * 1279 * ks * np.abs(q).sum(-1)
             extra += 2 * steps * 2.0 ** -23 * 1279 * vs
-    e_p = (2.0 ** -22 if codes else 2.0 ** -16) if hi_lo else 2.0 ** -11
+    e_p = (2.0 ** -22 if codes else 2.0 ** -16) if hi_lo else 2.0 ** (-11 if codes else -8)
     e = 2 * (dz[..., None] + e_p + 2.0 ** -21 + steps * 2.0 ** -23) * mag + extra
     return e + (2.0 ** -8 if out_bf16 else 2.0 ** -23) * (np.abs(out) + e)
