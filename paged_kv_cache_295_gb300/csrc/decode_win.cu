@@ -21,11 +21,54 @@ int64_t visible_tokens(int32_t max_ctx, int32_t window, int32_t sinks) {
   return 32 * max_visible_chunks(max_ctx, window, sinks, 32);
 }
 
+// Tokens per partition.  `tokens` is what the longest query can see; token_bytes the K and V
+// bytes of one token and head.  With n partitions a launch has heads * n CTAs of about
+// tokens / n tokens, three to an SM, and is estimated (us) as
+//   3, and 2 more for the merging kernel if n > 1
+//   + per full wave of CTA slots: 1 + len * slots * token_bytes / HBM bandwidth
+//   + the last, partial wave: 1 + len * the same rate times how full it is, but at least
+//     the rate of a CTA alone, which its two-stage rings bound (48 KB/us).
+// The n with the least estimate is taken.  Measured (bf16, GQA-8, 64 x 8 heads, window 1024):
+// 1 partition of 1,120 tokens 57.2 us (1.1 waves), 2 of 576 52; 4 x 8 heads: 17.1 us with
+// one, 8.6 with nine; one sequence, window 4096: 50.3 with one, 9.6 with 33.
+int32_t auto_win_partition(int64_t heads, int64_t tokens, int token_bytes) {
+  const double slots = 3.0 * device_sm_count();
+  const double full = slots * token_bytes / 6.6e6, alone = token_bytes / 4.8e4;
+  int32_t best = 4096;
+  double least = 1e30;
+  int32_t before = 0;
+  for (int64_t n = 1; n <= 64; ++n) {
+    int64_t len = ((tokens + n - 1) / n + 63) / 64 * 64;
+    if (len < 64) len = 64;
+    if (len > 4096 || len == before) continue;   // 4096: the box table's room
+    before = static_cast<int32_t>(len);
+    const int64_t parts = (tokens + len - 1) / len;
+    const double waves = static_cast<double>(heads) * parts / slots;
+    const double whole = static_cast<double>(static_cast<int64_t>(waves)), rest = waves - whole;
+    double t = (parts > 1 ? 5.0 : 3.0) + whole * (1.0 + len * full);
+    if (rest > 0) t += 1.0 + len * (rest * full > alone ? rest * full : alone);
+    if (t < least) {
+      least = t;
+      best = static_cast<int32_t>(len);
+    }
+  }
+  return best;
+}
+
 int32_t win_partition(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int64_t tokens,
-                      int32_t req) {
-  const int64_t t = tokens < INT32_MAX ? tokens : INT32_MAX;
-  return paged_attention_partition_tokens(num_seqs, num_q_heads, num_kv_heads,
-                                          static_cast<int32_t>(t), req);
+                      int token_bytes, int32_t req) {
+  if (req < 0 || req % 64 != 0) return 0;
+  if (req > 0) return req;
+  const int split = num_q_heads / num_kv_heads > 8 ? 2 : 1;
+  return auto_win_partition(static_cast<int64_t>(num_seqs) * num_kv_heads * split, tokens,
+                            token_bytes);
+}
+
+size_t window_scratch(int32_t num_seqs, int32_t num_q_heads, int32_t head_dim, int64_t tokens,
+                      int32_t P) {
+  const int64_t parts = P > 0 ? (tokens + P - 1) / P : 0;
+  if (parts <= 1) return 0;
+  return static_cast<size_t>(num_seqs) * num_q_heads * parts * (head_dim + 2) * sizeof(float);
 }
 
 template <int D>
@@ -57,13 +100,16 @@ extern "C" size_t paged_attention_window_workspace_bytes(int32_t num_seqs, int32
   if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       max_context_len < 0 || window < 0 || sinks < 0 || num_q_heads % num_kv_heads != 0)
     return 0;
+  // enough for a 16-bit and for an 8-bit cache, whose partitions may differ
   const int64_t tokens = pkv::visible_tokens(max_context_len, window, sinks);
-  const int32_t P =
-      pkv::win_partition(num_seqs, num_q_heads, num_kv_heads, tokens, partition_tokens);
-  if (P <= 0) return 0;
-  const int64_t parts = (tokens + P - 1) / P;
-  if (parts <= 1) return 0;
-  return static_cast<size_t>(num_seqs) * num_q_heads * parts * (head_dim + 2) * sizeof(float);
+  size_t most = 0;
+  for (int bytes = 1; bytes <= 2; ++bytes) {
+    const int32_t P = pkv::win_partition(num_seqs, num_q_heads, num_kv_heads, tokens,
+                                         2 * head_dim * bytes, partition_tokens);
+    const size_t need = pkv::window_scratch(num_seqs, num_q_heads, head_dim, tokens, P);
+    if (need > most) most = need;
+  }
+  return most;
 }
 
 extern "C" pkv_status paged_attention_decode_window(
@@ -108,12 +154,12 @@ extern "C" pkv_status paged_attention_decode_window(
   if (!encode_fn()) return PKV_ERR_CUDA;
 
   const int64_t tokens = visible_tokens(max_context_len, window, sinks);
-  const int32_t P = win_partition(num_seqs, num_q_heads, num_kv_heads, tokens, partition_tokens);
+  const int32_t P = win_partition(num_seqs, num_q_heads, num_kv_heads, tokens,
+                                  2 * head_dim * (codes ? 1 : 2), partition_tokens);
   if (P <= 0) return PKV_ERR_INVALID_ARG;
   const int64_t parts = tokens > 0 ? (tokens + P - 1) / P : 1;
   if (parts > 65535) return PKV_ERR_UNSUPPORTED;
-  const size_t need = paged_attention_window_workspace_bytes(
-      num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, P, window, sinks);
+  const size_t need = window_scratch(num_seqs, num_q_heads, head_dim, tokens, P);
   if (need > 0 && (!workspace || workspace_bytes < need || !aligned16(workspace)))
     return PKV_ERR_INVALID_ARG;
 
