@@ -48,7 +48,30 @@ struct WinParams {
   int32_t box_log2;       // log2 of the rows per TMA box: min(block_size, CH)
   int32_t head_split;     // CTAs per KV head: 1, or 2 for groups of 9 to 16 heads
   int32_t bits8;          // CH of the cache type: 32 when set, else 16
+  int32_t cluster;        // the partitions of a sequence and head are one cluster
 };
+
+// Up to 8 partitions of a sequence and KV head run as one thread-block cluster, which
+// merges them through distributed shared memory: no scratch in HBM and no second kernel.
+constexpr int kWinCluster = 8;
+
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {   // exited CTAs are not waited for
+  asm volatile("barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// The same shared-memory address in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t cluster_map(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float cluster_ld(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];\n" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
 
 // What one sequence's query sees, in chunks of CH tokens.
 struct Visible {
@@ -115,7 +138,7 @@ struct WinSmem {
   static constexpr int kBoxes = Base::kBoxes;
   static constexpr int kBoxBytes = Base::kBoxBytes;
   static constexpr int kWarpBytes = STAGES * kStageBytes + kScratch;
-  static_assert(STAGES * kStageBytes >= 8 * (D + 3) * 4, "combine area fits a warp ring");
+  static_assert(STAGES * kStageBytes >= 2 * 8 * (D + 3) * 4, "two combine areas fit a warp ring");
   static constexpr int kEntry = KV::kBytes == 1 ? 16 : 4;   // bytes per box entry
   static size_t bytes(int boxes) {
     return 1024 + static_cast<size_t>(NW) * kWarpBytes + static_cast<size_t>(boxes) * kEntry;
@@ -609,6 +632,8 @@ __global__ void __launch_bounds__(NW * 32)
   __syncthreads();
 
   const bool single = nparts == 1;
+  // this partition's result for the cluster: [8][D] o, m[8], l[8], behind warp 0's own
+  float* cres = reinterpret_cast<float*>(smem) + 8 * (D + 2);
   for (int i = threadIdx.x; i < G * D; i += NW * 32) {
     const int h = i / D, d = i % D;
     float M = -CUDART_INF_F;
@@ -626,6 +651,12 @@ __global__ void __launch_bounds__(NW * 32)
     const int64_t sh = static_cast<int64_t>(s) * p.num_q_heads + hq0 + h;
     if (single) {
       put_out(wp, sh * D + d, O / L);
+    } else if (wp.cluster) {
+      cres[i] = O;
+      if (d == 0) {
+        cres[8 * D + h] = M;
+        cres[8 * D + 8 + h] = L;
+      }
     } else {
       const int64_t pi = sh * p.max_parts + part;
       p.part_o[pi * D + d] = O;
@@ -635,6 +666,33 @@ __global__ void __launch_bounds__(NW * 32)
       }
     }
   }
+  if (single || !wp.cluster) return;
+  // Every CTA of the cluster that has tokens merges a share of the outputs; the others
+  // have left.  None leaves before all have read.
+  cluster_arrive();
+  cluster_wait();
+  const uint32_t cres_a = smem_u32(cres);
+  for (int i = part * (NW * 32) + static_cast<int>(threadIdx.x); i < G * D; i += nparts * NW * 32) {
+    const int h = i / D;
+    float m[kWinCluster], M = -CUDART_INF_F;
+#pragma unroll
+    for (int r = 0; r < kWinCluster; ++r) {
+      m[r] = r < nparts ? cluster_ld(cluster_map(cres_a + 4 * (8 * D + h), r)) : -CUDART_INF_F;
+      M = fmaxf(M, m[r]);
+    }
+    float L = 0.f, O = 0.f;
+#pragma unroll
+    for (int r = 0; r < kWinCluster; ++r) {
+      if (r < nparts) {
+        const float c = exp2f(m[r] - M);
+        L = fmaf(cluster_ld(cluster_map(cres_a + 4 * (8 * D + 8 + h), r)), c, L);
+        O = fmaf(cluster_ld(cluster_map(cres_a + 4 * i, r)), c, O);
+      }
+    }
+    put_out(wp, (static_cast<int64_t>(s) * p.num_q_heads + hq0) * D + i, O / L);
+  }
+  cluster_arrive();
+  cluster_wait();
 }
 
 // Merges the partitions' (m, l, o): one warp per (sequence, query head), as

@@ -18,9 +18,22 @@ pkv_status launch_win_shape(const WinLaunch& a, const CUtensorMap& tk, const CUt
   if (!opt_in_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem)))
     return PKV_ERR_CUDA;
   const dim3 grid(w.p.num_kv_heads * w.head_split, w.p.max_parts, a.num_seqs);
-  if (launch_pdl(kern, grid, dim3(NW * 32), smem, a.stream, tk, tv, w) != cudaSuccess)
-    return PKV_ERR_CUDA;
-  if (w.p.max_parts > 1 &&
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(NW * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = a.stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = w.cluster ? w.p.max_parts : 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = w.cluster ? 2 : 1;
+  if (cudaLaunchKernelEx(&cfg, kern, tk, tv, w) != cudaSuccess) return PKV_ERR_CUDA;
+  if (w.p.max_parts > 1 && !w.cluster &&
       launch_pdl(paged_decode_win_reduce_kernel<D>, dim3(a.num_seqs * w.p.num_q_heads), dim3(32), 0,
                  a.stream, w) != cudaSuccess)
     return PKV_ERR_CUDA;

@@ -35,6 +35,18 @@ def test_decode_split(lib, kv, q_type):
         check_decode(lib, case, 8, 10, q_type=q_type, out="bf16", window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("kv,d", [("bf16", 64), ("bf16", 128), ("bf16", 256), ("fp8_e4m3", 128)])
+def test_decode_clusters(lib, kv, d):
+    """Two to eight partitions merged within a cluster, sequences with fewer than the most, and
+    more partitions than a cluster takes."""
+    case = PC.make(17, kv, [1, 64, 130, 520, 0, 300], 2, d, 16)
+    for part, parts in ((64, 9), (128, 5), (192, 3), (320, 2), (576, 1)):
+        scratch = lib.workspace_bytes(6, 20, 2, d, 520, part, window=0)
+        assert (scratch > 0) == (parts > 8)
+        check_decode(lib, case, 20, 18, out="f32", window=10 ** 6, partition=part)
+    check_decode(lib, case, 6, 19, out="bf16", window=200, sinks=30, partition=64)
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3", "int8"])
 def test_hidden_blocks_are_not_read(lib, kv):
     """Table entries of blocks without a visible token may be anything, and hidden rows NaN."""
@@ -93,7 +105,9 @@ def test_two_graphs_share_a_workspace(lib):
     import torch
     case = PC.make(8, "bf16", [900, 500], 2, 128, 16)
     d = case.device()
-    ws = torch.empty(lib.workspace_bytes(2, 8, 2, 128, 900, 64, window=0), dtype=torch.uint8, device="cuda")
+    need = lib.workspace_bytes(2, 8, 2, 128, 900, 64, window=0)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
     qs = [torch.randn((2, 8, 128), device="cuda").to(torch.bfloat16) for _ in range(2)]
     outs = [torch.zeros((2, 8, 128), device="cuda") for _ in range(2)]
     wins = [(300, 4), (700, 0)]

@@ -78,8 +78,10 @@ def test_decode_refusals(lib, kw, want):
 
 def test_workspace_covers_what_a_query_sees(lib):
     w = lib.library().paged_attention_window_workspace_bytes
-    # 4 sinks and a window of 256 touch at most 1 + 9 chunks of 32 tokens
-    assert w(2, 8, 2, 128, 100000, 64, 256, 4) == 2 * 8 * 5 * 130 * 4
+    # 4 sinks and a window of 512 touch at most 1 + 17 chunks of 32 tokens
+    assert w(2, 8, 2, 128, 100000, 64, 512, 4) == 2 * 8 * 9 * 130 * 4
+    assert w(2, 8, 2, 128, 100000, 128, 512, 4) == 0      # few CTAs, up to 8 partitions: none
+    assert w(200, 8, 2, 128, 100000, 128, 512, 4) == 200 * 8 * 5 * 130 * 4
     assert w(2, 8, 2, 128, 100000, 320, 256, 4) == 0
     assert w(2, 8, 2, 128, 640, 64, 0, 0) == 2 * 8 * 10 * 130 * 4
     assert w(2, 8, 2, 128, 640, 64, 10 ** 9, 10 ** 9) == 2 * 8 * 10 * 130 * 4
