@@ -565,9 +565,13 @@ size_t paged_attention_window_workspace_bytes(int32_t num_seqs, int32_t num_q_he
  *                  blocks may have been given back to the pool.
  *   k_scale, v_scale, scale_stride : 8-bit caches; [num_blocks, scale_stride]
  *                  scales per block and head, or [num_kv_heads] with
- *                  scale_stride 0.  V scales count as at least 2^-100.
+ *                  scale_stride 0.  K scales are not negative; V scales count
+ *                  as at least 2^-100.
  *   out, out_dtype : device [num_seqs, num_q_heads, head_dim], f32 or bf16.
  *   partition_tokens : counted in visible tokens.
+ *   workspace    : calls whose kernels may overlap on the GPU need one each.
+ *                  Small grids merge their partitions within thread-block
+ *                  clusters and need none.
  * Supported: bf16 caches with head_dim 64, 128 or 256; FP8 and INT8 caches with
  * head_dim 128; num_q_heads / num_kv_heads <= 16; block_size a power of two in
  * [8, 4096]; max_context_len <= 2^30. */

@@ -359,9 +359,15 @@ class Pool:
 # ---------------------------------------------------------------------------
 # Device calls (torch tensors in, async on the current stream).
 # ---------------------------------------------------------------------------
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t) -> int:
@@ -455,22 +461,23 @@ def _elsewhere(t, stream):
 
 def _current_stream(dev):
     torch = _torch()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # no stream object made
     return raw(dev) if raw else torch.cuda.current_stream(dev).cuda_stream
 
 
-def _ptrs(dev, **tensors):
-    """Device pointers (None for None) of contiguous tensors on device ``dev``, by name."""
+def _ptrs(dev, names, *tensors):
+    """Device pointers (None for None) of contiguous tensors on device ``dev``; ``names``:
+    theirs, in one string."""
     out = []
-    for name, t in tensors.items():
+    for t in tensors:
         if t is None:
             out.append(None)
-        elif t.get_device() != dev:
-            raise ValueError(f"{name} is on {t.device}, the call on cuda:{dev}")
-        elif not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        else:
+        elif t.get_device() == dev and t.is_contiguous():
             out.append(t.data_ptr())
+        else:
+            name = names.split()[len(out)]
+            raise ValueError(f"{name} must be contiguous" if t.get_device() == dev else
+                             f"{name} is on {t.device}, the call on cuda:{dev}")
     return out
 
 
@@ -543,11 +550,11 @@ def quantize_and_cache(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block
                                       block_tables, context_lens, query_start, max_query_len,
                                       device_status)
     dev = k_new.get_device()
-    ptrs = _ptrs(dev, k_new=k_new, v_new=v_new, query_start=query_start, block_tables=block_tables,
-                 context_lens=context_lens, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales,
-                 v_scales=v_scales)
-    status = _ptrs(dev, device_status=device_status)[0] if device_status is not None else None
-    _check(library().quantize_and_cache(*ptrs, S, T, int(max_query_len), hkv, d, bs, nb, mb, stride,
+    kn, vn, qs, bt, cl, kc, vc, ks, vs, status = _ptrs(
+        dev, "k_new v_new query_start block_tables context_lens k_cache v_cache k_scales v_scales "
+        "device_status", k_new, v_new, query_start, block_tables, context_lens, k_cache, v_cache,
+        k_scales, v_scales, device_status)
+    _check(library().quantize_and_cache(kn, vn, qs, bt, cl, kc, vc, ks, vs, S, T, int(max_query_len), hkv, d, bs, nb, mb, stride,
                                         src, dst, status, _current_stream(dev)),
            "quantize_and_cache")
 
@@ -592,9 +599,9 @@ def gather_cache(k_cache, v_cache, block_tables, row_start, num_rows, max_rows, 
     _want(v_out, "v_out", shape, out_code)
     dev = k_cache.get_device()
     kc, vc, bt, rs, fp, ks, vs, ko, vo, status = _ptrs(
-        dev, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables, row_start=row_start,
-        first_pos=first_pos, k_scale=k_scale, v_scale=v_scale, k_out=k_out, v_out=v_out,
-        device_status=device_status)
+        dev, "k_cache v_cache block_tables row_start first_pos k_scale v_scale k_out v_out "
+        "device_status", k_cache, v_cache, block_tables, row_start, first_pos, k_scale, v_scale,
+        k_out, v_out, device_status)
     _check(library().gather_cache(kc, vc, bt, rs, fp, S, shape[0], int(max_rows), hkv, d, bs, nb, mb,
                                   code, ks, vs, stride, out_code, ko, vo, status,
                                   _current_stream(dev)), "gather_cache")
@@ -661,9 +668,9 @@ def _decode_window(q, k_cache, v_cache, block_tables, context_lens, scale, max_c
         ws_bytes = need
     dev = q.get_device()
     qp, kc, vc, bt, cl, ks, vs, op, ws, status = _ptrs(
-        dev, q=q, k_cache=k_cache, v_cache=v_cache, block_tables=block_tables,
-        context_lens=context_lens, k_scale=k_scale, v_scale=v_scale, out=out, workspace=workspace,
-        device_status=device_status)
+        dev, "q k_cache v_cache block_tables context_lens k_scale v_scale out workspace "
+        "device_status", q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, out,
+        workspace, device_status)
     _check(lib.paged_attention_decode_window(
         qp, kc, vc, bt, cl, S, hq, hkv, d, bs, nb, mb, int(max_context_len), float(scale), q_code,
         kv_code, ks, vs, stride, int(window), int(sinks), _code_of(out.dtype), op, ws, ws_bytes,
@@ -687,9 +694,9 @@ def _prefill_window(q, query_start, k_cache, v_cache, block_tables, context_lens
     out = _attention_out(q, out, out_dtype)
     dev = q.get_device()
     qp, qs, kc, vc, bt, cl, ks, vs, op, status = _ptrs(
-        dev, q=q, query_start=query_start, k_cache=k_cache, v_cache=v_cache,
-        block_tables=block_tables, context_lens=context_lens, k_scale=k_scale, v_scale=v_scale,
-        out=out, device_status=device_status)
+        dev, "q query_start k_cache v_cache block_tables context_lens k_scale v_scale out "
+        "device_status", q, query_start, k_cache, v_cache, block_tables, context_lens, k_scale,
+        v_scale, out, device_status)
     _check(library().paged_attention_prefill_window(
         qp, qs, kc, vc, bt, cl, S, q.shape[0], int(max_query_len), hq, hkv, d, bs, nb, mb,
         int(max_context_len), float(scale), 1 if causal else 0, q_code, kv_code, ks, vs, stride,

@@ -220,8 +220,9 @@ __global__ void __launch_bounds__(NW * 32)
           row = (b << p.bs_log2) + (t & ((1 << p.bs_log2) - 1));
           if (F8) {
             const int64_t at = static_cast<int64_t>(b) * wp.scale_stride + g;
-            e.y = p.qk_scale_log2 * __ldg(p.k_scale + at);
-            e.z = fmaxf(__ldg(p.v_scale + at), kMinVScale);
+            // past L1, whose line may be older than the append before this launch
+            e.y = p.qk_scale_log2 * __ldcg(p.k_scale + at);
+            e.z = fmaxf(__ldcg(p.v_scale + at), kMinVScale);
             e.w = __log2f(e.z);
           }
         }

@@ -20,6 +20,10 @@
 #include "common.cuh"
 #include "quant.cuh"
 
+// Codes and scales that an earlier kernel may have written are read past L1 (__ldcg):
+// with programmatic launches a kernel's CTAs share an SM with the writer's, whose own
+// loads may have left older lines there.
+
 namespace pkv {
 namespace {
 
@@ -264,7 +268,7 @@ __global__ void __launch_bounds__(kQThreads, 8) quantize_kernel(const QuantParam
     const int head = live ? head_of(unit) : 0;
     const Src* src = rows_of(live ? unit : 0);
     float* sp = (is_v ? p.v_scales : p.k_scales) + blk * p.scale_stride + head;
-    const float s0 = live && off > 0 ? *sp : 0.f;
+    const float s0 = live && off > 0 ? __ldcg(sp) : 0.f;
     uint32_t m = 0;
 #pragma unroll
     for (int k = 0; k < kHeld; ++k) m = v[k].top(m);
@@ -314,7 +318,7 @@ __global__ void __launch_bounds__(kQThreads, 8) quantize_kernel(const QuantParam
       for (int it = t; it < off * p.segs; it += T) {
         uint4* at = old + (it / p.segs) * (row / 2) + it % p.segs;
         float x[16];
-        decode16<Q>(*at, x);
+        decode16<Q>(__ldcg(at), x);
         uint32_t w[4];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -399,31 +403,83 @@ struct GatherParams {
   int32_t tile_rows;            // rows per CTA
 };
 
-__device__ __forceinline__ void store16(float* out, const float* x) {
+// E elements of a cache row, as loaded, and as values.
+template <typename KV, int E>
+struct Piece {
+  static constexpr int kWords = E * KV::kBytes / 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void zero() {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    reinterpret_cast<float4*>(out)[i] =
-        make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+    for (int i = 0; i < kWords; ++i) w[i] = 0;
+  }
+  // Past L1, whose lines may be older than what the kernel before this one wrote.
+  __device__ __forceinline__ void load(const uint8_t* p) {
+    if constexpr (kWords == 1) {
+      w[0] = __ldcg(reinterpret_cast<const uint32_t*>(p));
+    } else if constexpr (kWords == 2) {
+      const uint2 v = __ldcg(reinterpret_cast<const uint2*>(p));
+      w[0] = v.x;
+      w[1] = v.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords / 4; ++i) {
+        const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p) + i);
+        w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+      }
+    }
+  }
+  __device__ __forceinline__ void values(float scale, float* x) const {
+    if constexpr (KV::kBytes == 4) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) x[i] = __uint_as_float(w[i]);
+    } else if constexpr (KV::kBytes == 2) {
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i) {
+        x[2 * i] = bf16_lo(w[i]);
+        x[2 * i + 1] = bf16_hi(w[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E / 4; ++i) {
+        if constexpr (std::is_same<KV, FP8>::value) {
+          const float2 a = e4m3x2_to_float2(static_cast<uint16_t>(w[i] & 0xFFFFu));
+          const float2 b = e4m3x2_to_float2(static_cast<uint16_t>(w[i] >> 16));
+          x[4 * i] = a.x; x[4 * i + 1] = a.y; x[4 * i + 2] = b.x; x[4 * i + 3] = b.y;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            x[4 * i + e] = static_cast<float>(static_cast<int8_t>((w[i] >> (8 * e)) & 0xFFu));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < E; ++i) x[i] *= scale;
+    }
+  }
+};
+
+__device__ __forceinline__ void store_piece(float* out, const float* x) {
+  *reinterpret_cast<float4*>(out) = make_float4(x[0], x[1], x[2], x[3]);
 }
-__device__ __forceinline__ void store16(__nv_bfloat16* out, const float* x) {
-  uint32_t w[8];
+__device__ __forceinline__ void store_piece(__nv_bfloat16* out, const float* x) {
+  uint32_t w[4];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 4; ++i) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
     w[i] = *reinterpret_cast<const uint32_t*>(&h);
   }
-  reinterpret_cast<uint4*>(out)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-  reinterpret_cast<uint4*>(out)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// One CTA per (tile of a sequence's rows, sequence); a thread takes 16-element
-// segments, K and V of the same place, kGHeld of them at a time: their table
-// entries, then their codes and scales, are each one round trip.  Bound by HBM: one
-// byte read and two (bf16) or four written per element.
+// One CTA per (tile of a sequence's rows, sequence); a thread takes pieces of 16 output
+// bytes (so that a warp's stores are whole lines; pieces of 16 elements, stored as two
+// halves, took 39.5 us where these take 35), K and V of the same place, kGHeld at a
+// time.  Bound by HBM: one byte read and two (bf16) or four written per element.
 constexpr int kGHeld = 2;
+constexpr int kGTile = 4;
 
 template <typename KV, typename Out>
 __global__ void __launch_bounds__(kGThreads) gather_kernel(const GatherParams p) {
+  constexpr int E = 16 / sizeof(Out);
   grid_dependency_wait();
   allow_dependents();
   const int s = blockIdx.y;
@@ -438,61 +494,56 @@ __global__ void __launch_bounds__(kGThreads) gather_kernel(const GatherParams p)
   const int64_t tile = static_cast<int64_t>(blockIdx.x) * p.tile_rows;
   if (tile >= n) return;
   const int rows = static_cast<int>(min(static_cast<int64_t>(p.tile_rows), n - tile));
-  const int per_row = p.num_kv_heads * p.segs;
-  const int items = rows * per_row;
+  const uint32_t per_head = p.segs * (16 / E), per_row = p.num_kv_heads * per_head;
   const int32_t* bt = p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq;
-  constexpr int V = KV::kBytes;   // 16-byte vectors per segment
-  for (int it0 = threadIdx.x; it0 < items; it0 += kGThreads * kGHeld) {
-    int32_t blk[kGHeld];
-    int64_t pos[kGHeld];
-    int hs[kGHeld];
-#pragma unroll
-    for (int k = 0; k < kGHeld; ++k) {
-      const int it = it0 + k * kGThreads;
-      const int r = it / per_row;
-      hs[k] = it - r * per_row;
-      pos[k] = pos0 + tile + r;
-      blk[k] = it < items ? __ldg(bt + (pos[k] >> p.bs_log2)) : 0;
-    }
-    uint4 kc[kGHeld][V], vc[kGHeld][V];
+  // this thread's place, row r and piece c of the row, and its step of kGThreads pieces
+  const uint32_t dr = kGThreads / per_row, dc = kGThreads % per_row;
+  int r = threadIdx.x / per_row;
+  uint32_t c = threadIdx.x % per_row;
+  while (r < rows) {
+    Piece<KV, E> k[kGHeld], v[kGHeld];
     float ks[kGHeld], vs[kGHeld];
+    int64_t out[kGHeld];
 #pragma unroll
-    for (int k = 0; k < kGHeld; ++k) {
-      const bool ok = it0 + k * kGThreads < items && blk[k] >= 0 && blk[k] < p.num_blocks;
-      if (it0 + k * kGThreads < items && !ok) flag_status(p.status, PKV_DEV_BAD_BLOCK);
-      const int64_t slot = (static_cast<int64_t>(blk[k]) << p.bs_log2) + (pos[k] & ((1 << p.bs_log2) - 1));
-      const int64_t at = (slot * per_row + hs[k]) * V;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        kc[k][i] = ok ? __ldg(reinterpret_cast<const uint4*>(p.k_cache) + at + i) : make_uint4(0, 0, 0, 0);
-        vc[k][i] = ok ? __ldg(reinterpret_cast<const uint4*>(p.v_cache) + at + i) : make_uint4(0, 0, 0, 0);
-      }
-      if (V == 1) {
-        const int64_t sc = p.scale_stride ? blk[k] * p.scale_stride + hs[k] / p.segs : hs[k] / p.segs;
-        ks[k] = ok ? __ldg(p.k_scale + sc) : 0.f;
-        vs[k] = ok ? __ldg(p.v_scale + sc) : 0.f;
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kGHeld; ++k) {
-      const int it = it0 + k * kGThreads;
-      if (it >= items) break;
-      const int64_t o = ((r0 + tile) * per_row + it) * 16;
-      float x[16], y[16];
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        decode16<KV>(kc[k][i], x + i * KV::kPerVec);
-        decode16<KV>(vc[k][i], y + i * KV::kPerVec);
-      }
-      if (V == 1) {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          x[e] *= ks[k];
-          y[e] *= vs[k];
+    for (int i = 0; i < kGHeld; ++i) {
+      out[i] = -1;
+      ks[i] = vs[i] = 0.f;
+      k[i].zero();
+      v[i].zero();
+      if (r < rows) {
+        out[i] = ((r0 + tile + r) * per_row + c) * E;
+        const int64_t pos = pos0 + tile + r;
+        const int32_t blk = __ldg(bt + (pos >> p.bs_log2));
+        if (blk >= 0 && blk < p.num_blocks) {
+          const int64_t slot =
+              (static_cast<int64_t>(blk) << p.bs_log2) + (pos & ((1 << p.bs_log2) - 1));
+          const int64_t at = (slot * per_row + c) * (E * KV::kBytes);
+          k[i].load(p.k_cache + at);
+          v[i].load(p.v_cache + at);
+          if (KV::kBytes == 1) {
+            const int64_t sc = blk * p.scale_stride + c / per_head;   // stride 0: per head
+            ks[i] = __ldcg(p.k_scale + sc);
+            vs[i] = __ldcg(p.v_scale + sc);
+          }
+        } else {
+          flag_status(p.status, PKV_DEV_BAD_BLOCK);
         }
       }
-      store16(static_cast<Out*>(p.k_out) + o, x);
-      store16(static_cast<Out*>(p.v_out) + o, y);
+      r += dr;
+      c += dc;
+      if (c >= per_row) {
+        c -= per_row;
+        ++r;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kGHeld; ++i) {
+      if (out[i] < 0) continue;
+      float x[E];
+      k[i].values(ks[i], x);
+      store_piece(static_cast<Out*>(p.k_out) + out[i], x);
+      v[i].values(vs[i], x);
+      store_piece(static_cast<Out*>(p.v_out) + out[i], x);
     }
   }
 }
@@ -525,9 +576,10 @@ extern "C" pkv_status quantize_and_cache(
   if (num_blocks > INT32_MAX || num_seqs > 65535 || num_kv_heads > 65535 || head_dim > 65536)
     return PKV_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(max_blocks_per_seq) * block_size > INT32_MAX) return PKV_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PKV_OK;
   if (max_query_len > num_tokens) return PKV_ERR_INVALID_ARG;
   if (!query_start && (max_query_len > 1 || num_tokens < num_seqs)) return PKV_ERR_INVALID_ARG;
-  if (num_seqs == 0 || max_query_len == 0) return PKV_OK;
+  if (max_query_len == 0) return PKV_OK;
   if (!k_new || !v_new || !block_tables || !context_lens || !k_cache || !v_cache || !k_scales ||
       !v_scales)
     return PKV_ERR_INVALID_ARG;
@@ -610,8 +662,9 @@ extern "C" pkv_status gather_cache(
   p.segs = head_dim / 16;
   p.bs_log2 = ilog2(block_size);
   p.max_blocks_per_seq = max_blocks_per_seq;
-  const int per_row = num_kv_heads * p.segs;
-  p.tile_rows = per_row >= 4 * kGThreads ? 1 : (4 * kGThreads) / per_row;
+  // a tile of about kGTile pieces per thread
+  const int64_t per_row = static_cast<int64_t>(num_kv_heads) * p.segs * (out_dtype == PKV_F32 ? 4 : 2);
+  p.tile_rows = per_row >= kGTile * kGThreads ? 1 : static_cast<int32_t>(kGTile * kGThreads / per_row);
   const int64_t tiles = (static_cast<int64_t>(max_rows) + p.tile_rows - 1) / p.tile_rows;
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
   auto launch = [&](auto kern) {
