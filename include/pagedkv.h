@@ -566,7 +566,7 @@ size_t paged_attention_window_workspace_bytes(int32_t num_seqs, int32_t num_q_he
  *   k_scale, v_scale, scale_stride : 8-bit caches; [num_blocks, scale_stride]
  *                  scales per block and head, or [num_kv_heads] with
  *                  scale_stride 0.  K scales are not negative; V scales count
- *                  as at least 2^-100.
+ *                  as at least 2^-80.
  *   out, out_dtype : device [num_seqs, num_q_heads, head_dim], f32 or bf16.
  *   partition_tokens : counted in visible tokens.
  *   workspace    : calls whose kernels may overlap on the GPU need one each.

@@ -21,21 +21,22 @@
 //  * Tokens the query does not see score -inf and their rows are zeroed in
 //    shared memory, so whatever those slots hold reaches no product.
 //  * 8-bit caches: the running reference m follows max_t(c q.K_t + log2 vs), so
-//    the weights w = p vs that enter the PV product stay below 2^8 whatever the
+//    the weights w = p vs that enter the PV product stay below 2^15 whatever the
 //    scales of the blocks; the sum takes p itself.
-//  * P in 16 bits is hi + lo (bf16 caches: 2^-17; 8-bit caches with HL: fp16
-//    hi + lo, 2^-22) for float32 outputs; 8-bit caches with a bf16 output
-//    (HL false) carry w as one fp16 (2^-12), a sixteenth of the output's own
-//    rounding.  INT8 codes keep their offset of 1152 only there (see
-//    decode_mma2.cuh); with HL they are widened exactly.
+//  * The weights enter P V as 16-bit parts: for a float32 output three of bf16
+//    (2^-24; the third costs 2 % of the time) or, on 8-bit caches (HL), two of
+//    fp16 (2^-22); for a bf16 output two of bf16, or one of fp16 (2^-11, an
+//    eighth of the output's own rounding).  INT8 codes keep their offset of
+//    1152 only in the last case (see decode_mma2.cuh), else they are widened
+//    exactly.
 #pragma once
 
 #include "decode_mma2.cuh"
 
 namespace pkv {
 
-// Smallest V scale (2^-100): keeps log2 vs, and p = w / vs < 2^108, finite.
-constexpr float kMinVScale = 7.888609052210118e-31f;
+// Smallest V scale (2^-80): keeps log2 vs, and p = w / vs <= 2^95 and its sums, finite.
+constexpr float kMinVScale = 8.271806125530277e-25f;
 
 struct WinParams {
   DecodeParams p;         // partition_tokens: a multiple of CH; out: unused
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(NW * 32)
           if (F8) {
             const int64_t at = static_cast<int64_t>(b) * wp.scale_stride + g;
             // past L1, whose line may be older than the append before this launch
-            e.y = p.qk_scale_log2 * __ldcg(p.k_scale + at);
+            e.y = fabsf(p.qk_scale_log2) * __ldcg(p.k_scale + at);
             e.z = fmaxf(__ldcg(p.v_scale + at), kMinVScale);
             e.w = __log2f(e.z);
           }
@@ -277,6 +278,10 @@ __global__ void __launch_bounds__(NW * 32)
   for (int st = 0; st < STAGES - 1; ++st) issue(st);
 
   // ---- q^T as B fragments (decode_mma2.cuh: the dimension map of each cache type) --------
+  // A negative logit scale is folded into q and a zero one raised to the smallest normal, so
+  // that the factors below are positive and a masked -inf stays -inf under them.
+  constexpr float kTiny = 1.17549435e-38f;
+  const float qsign = p.qk_scale_log2 < 0.f ? -1.f : 1.f;
   uint32_t qb[KSTEPS][2];
   uint32_t qblo[QF32 ? KSTEPS : 1][2];
   float q_unscale = 1.f;
@@ -290,13 +295,13 @@ __global__ void __launch_bounds__(NW * 32)
       if (real) {
         if (QF32) {
           const float2 v = *reinterpret_cast<const float2*>(static_cast<const float*>(p.q) + row * D + col);
-          x0 = v.x;
-          x1 = v.y;
+          x0 = qsign * v.x;
+          x1 = qsign * v.y;
         } else {
           const uint32_t v = *reinterpret_cast<const uint32_t*>(
               static_cast<const __nv_bfloat16*>(p.q) + row * D + col);
-          x0 = bf16_lo(v);
-          x1 = bf16_hi(v);
+          x0 = qsign * bf16_lo(v);
+          x1 = qsign * bf16_hi(v);
         }
       }
     };
@@ -352,7 +357,8 @@ __global__ void __launch_bounds__(NW * 32)
       qsum1 = kI8Bias * __shfl_sync(0xffffffffu, qs, 8 * tig + 4);
     }
   }
-  const float sl2 = p.qk_scale_log2;   // 16-bit caches
+  const float sl2 = fmaxf(fabsf(p.qk_scale_log2), kTiny);   // 16-bit caches
+  const bool third = !F8 && !wp.out_bf16;   // P in three bf16 parts
 
   for (int it = 0; it < my_n; ++it) {
     issue(it + STAGES - 1);
@@ -432,33 +438,31 @@ __global__ void __launch_bounds__(NW * 32)
         if (QF32) mma_bf16(sacc[0], a, qblo[QF32 ? ks : 0][0], qblo[QF32 ? ks : 0][1]);
       }
     }
-    // ---- scaled logits (log2 units), masked; vs and log2 vs of the row groups -------------
-    float vsc[RT][2], mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
+    // ---- the chunk's largest logit (log2 units; 8-bit caches: + log2 vs) -------------------
+    // Tokens the query does not see become -inf.  Rows 16rt + 8hf + gid share one box, hence
+    // one logit factor fs and one V scale.
+    float fs[RT][2], vsc[RT][2], mx0 = -CUDART_INF_F, mx1 = -CUDART_INF_F;
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {   // rows 16rt + 8hf + gid: one box
-        float lv = 0.f;
-        if (F8) {
-          const float4 e = ents8[e0 + ((16 * rt + 8 * hf) >> wp.box_log2)];
-          const float f = e.y * q_unscale;
-          vsc[rt][hf] = e.z;
-          lv = e.w;
-          if (BIAS) {
-            sacc[rt][2 * hf] -= qsum0;
-            sacc[rt][2 * hf + 1] -= qsum1;
-          }
-          sacc[rt][2 * hf] *= f;
-          sacc[rt][2 * hf + 1] *= f;
-        } else {
-          vsc[rt][hf] = 1.f;
-          sacc[rt][2 * hf] *= sl2;
-          sacc[rt][2 * hf + 1] *= sl2;
+      for (int hf = 0; hf < 2; ++hf) {
+        if (BIAS) {
+          sacc[rt][2 * hf] -= qsum0;
+          sacc[rt][2 * hf + 1] -= qsum1;
         }
         if (partial && !sees(t0 + 16 * rt + 8 * hf + gid))
           sacc[rt][2 * hf] = sacc[rt][2 * hf + 1] = -CUDART_INF_F;
-        mx0 = fmaxf(mx0, sacc[rt][2 * hf] + lv);
-        mx1 = fmaxf(mx1, sacc[rt][2 * hf + 1] + lv);
+        if (F8) {
+          const float4 e = ents8[e0 + ((16 * rt + 8 * hf) >> wp.box_log2)];
+          fs[rt][hf] = fmaxf(e.y * q_unscale, kTiny);
+          vsc[rt][hf] = e.z;
+          mx0 = fmaxf(mx0, fmaf(sacc[rt][2 * hf], fs[rt][hf], e.w));
+          mx1 = fmaxf(mx1, fmaf(sacc[rt][2 * hf + 1], fs[rt][hf], e.w));
+        } else {
+          fs[rt][hf] = sl2;
+          mx0 = fmaxf(mx0, sacc[rt][2 * hf]);
+          mx1 = fmaxf(mx1, sacc[rt][2 * hf + 1]);
+        }
       }
     }
 #pragma unroll
@@ -466,10 +470,17 @@ __global__ void __launch_bounds__(NW * 32)
       mx0 = fmaxf(mx0, __shfl_xor_sync(0xffffffffu, mx0, off));
       mx1 = fmaxf(mx1, __shfl_xor_sync(0xffffffffu, mx1, off));
     }
-    // lazy rescale: the reference moves only by more than 2^kLazyLog2
-    const bool up0 = mx0 > m0 + kLazyLog2, up1 = mx1 > m1 + kLazyLog2;
+    if (!F8) {   // sl2 > 0: the max of the scaled logits
+      mx0 *= sl2;
+      mx1 *= sl2;
+    }
+    // Lazy rescale: the reference moves only when a weight would exceed 2^(kUp + kLazyLog2).
+    // 8-bit caches set it kUp = 7 below the maximum, so that fp16 weights (at most 2^15) and
+    // their lo parts stay clear of its smallest step.
+    constexpr float kUp = F8 ? 7.f : 0.f;
+    const bool up0 = mx0 > m0 + (kUp + kLazyLog2), up1 = mx1 > m1 + (kUp + kLazyLog2);
     if (__any_sync(0xffffffffu, up0 || up1)) {
-      const float mn0 = up0 ? mx0 : m0, mn1 = up1 ? mx1 : m1;
+      const float mn0 = up0 ? mx0 - kUp : m0, mn1 = up1 ? mx1 - kUp : m1;
       const float a0 = up0 ? fast_ex2(m0 - mn0) : 1.f;
       const float a1 = up1 ? fast_ex2(m1 - mn1) : 1.f;
       l0 *= a0;
@@ -493,7 +504,8 @@ __global__ void __launch_bounds__(NW * 32)
     for (int rt = 0; rt < RT; ++rt) {
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        float p0 = fast_ex2(sacc[rt][2 * hf] - m0), p1 = fast_ex2(sacc[rt][2 * hf + 1] - m1);
+        float p0 = fast_ex2(fmaf(sacc[rt][2 * hf], fs[rt][hf], -m0));
+        float p1 = fast_ex2(fmaf(sacc[rt][2 * hf + 1], fs[rt][hf], -m1));
         l0 += p0;
         l1 += p1;
         if (F8) {
@@ -516,13 +528,18 @@ __global__ void __launch_bounds__(NW * 32)
           ps0 += h0;
           ps1 += h1;
         }
-        if (HL)
-          *reinterpret_cast<uint32_t*>(at + CH * 16) =
-              F8 ? pack_f16(p0 - h0, p1 - h1) : pack_bf16(p0 - h0, p1 - h1);
+        if (HL) {
+          const uint32_t lo = F8 ? pack_f16(p0 - h0, p1 - h1) : pack_bf16(p0 - h0, p1 - h1);
+          *reinterpret_cast<uint32_t*>(at + CH * 16) = lo;
+          if (!F8 && third)
+            *reinterpret_cast<uint32_t*>(at + 2 * CH * 16) =
+                pack_bf16(p0 - h0 - bf16_lo(lo), p1 - h1 - bf16_hi(lo));
+        }
       }
     }
     __syncwarp();
     uint32_t pb0[RT], pb1[RT], pl0[RT], pl1[RT];   // k-steps' hi and lo fragments
+    uint32_t pt0 = 0, pt1 = 0;                     // 16-bit caches: the third part's
     {
       uint32_t r0, r1, r2, r3;
       ldsm_x4_t(smem_u32(scratch) + lane * 16, r0, r1, r2, r3);
@@ -541,6 +558,11 @@ __global__ void __launch_bounds__(NW * 32)
       } else {
         pl0[0] = r2;
         pl1[0] = r3;
+        if (third) {
+          ldsm_x4_t(smem_u32(scratch) + 512 + lane * 16, r0, r1, r2, r3);   // rows 32 .. 47
+          pt0 = r0;
+          pt1 = r1;
+        }
       }
     }
 
@@ -591,6 +613,7 @@ __global__ void __launch_bounds__(NW * 32)
         ldsm_x4_t(vb_a + hh * SM::kBoxBytes + swz(r, u), a[0], a[1], a[2], a[3]);
         mma_bf16(o[mt], a, pb0[0], pb1[0]);
         mma_bf16(o[mt], a, pl0[0], pl1[0]);
+        if (third) mma_bf16(o[mt], a, pt0, pt1);
       }
     }
     __syncwarp();   // every lane is done with this stage before it is refilled

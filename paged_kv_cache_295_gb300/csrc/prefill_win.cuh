@@ -73,8 +73,8 @@ struct PfScale {
   float lv;    // log2 vs
   float pad;
 };
-// Smallest V scale (2^-100): keeps log2 vs, and p = w / vs < 2^108, finite.
-constexpr float kPfMinVScale = 7.888609052210118e-31f;
+// Smallest V scale (2^-80): keeps log2 vs, and p = w / vs < 2^88, finite.
+constexpr float kPfMinVScale = 8.271806125530277e-25f;
 
 struct PwLayout {
   // [Q_A][Q_B] 32 KB each (two halves of 64 dims); [8-bit only: raw tiles, K x4 then

@@ -101,7 +101,8 @@ def attention_bound(case, q, out, mag, reach, scale, q_f32, out_bf16, hi_lo, lon
     These act on numerator and denominator alike: twice their sum times A.
 
     8-bit caches: an fp16 weight below 2^-14 is off by up to 2^-25 where the largest weight
-    is at least 1, that is by 2^-25 max(vs) in p |v| per unit code: 2^-25 qmax max(vs) a token.
+    is at least 1, that is by 2^-25 max(vs) in p |v| per unit code: 2^-25 qmax max(vs) a token
+    (in decode the largest weight is at least 2^7, which only makes this smaller).
 
     INT8 with one fp16 weight (no hi + lo) carries code + 1152 (at most 1279) in both
     products: 16 float32 steps on sum |q| 1279 ks in z, and a step for each 16 tokens, twice
