@@ -27,9 +27,8 @@
 namespace pkv {
 namespace {
 
-constexpr int kQThreads = 128;
 constexpr int kGThreads = 256;
-constexpr int kQGrid = 8;
+constexpr int kQWarps = 28;   // warps of the append per SM (72 registers; 32 would spill)
 constexpr float kMinScale = 5.421010862427522e-20f;   // 2^-64
 
 template <typename Q>
@@ -187,17 +186,20 @@ __device__ __forceinline__ uint2 codes8(const Vec8<Src>& v, float s, float r) {
 }
 
 // A team of T threads takes one (head, K or V) of one sequence's touched block
-// at a time; a CTA of 128 / T teams walks a share of the block's 2 Hkv of them, so
-// the lookups (context, table) are paid once, and loads the next one's rows
-// before it computes the current one's codes.  Rows are read once, unless a block
-// holds more than T * kHeld vectors (T = 128: block_size * head_dim above 8,192
-// for bf16): the rest is then read again, from L2.  Bound by HBM: 2 or 4 bytes
-// read and 1 written per element.
+// at a time; a CTA (128 threads, or one larger team) walks a share of the block's
+// 2 Hkv of them, so the lookups (context, table) are paid once.  Rows are read
+// once, unless a block holds more than T * kHeld vectors (T = 512: block_size *
+// head_dim above 32,768 for bf16): the rest is then read again, from L2.  Bound by
+// HBM: 2 or 4 bytes read and 1 written per element.
+template <int T>
+constexpr int kQThreads = T > 128 ? T : 128;
+
 template <typename Src, typename Q, int T>
-__global__ void __launch_bounds__(kQThreads, 8) quantize_kernel(const QuantParams p) {
-  constexpr int U = kQThreads / T;
+__global__ void __launch_bounds__(kQThreads<T>, (kQWarps * 32) / kQThreads<T>)
+    quantize_kernel(const QuantParams p) {
+  constexpr int U = kQThreads<T> / T;
   constexpr int kHeld = Vec8<Src>::kHeld;
-  __shared__ uint32_t red[2][kQThreads / 32];
+  __shared__ uint32_t red[2][kQThreads<T> / 32];
   grid_dependency_wait();
   allow_dependents();
   const int s = blockIdx.y;
@@ -224,11 +226,21 @@ __global__ void __launch_bounds__(kQThreads, 8) quantize_kernel(const QuantParam
   const int64_t src0 = (static_cast<int64_t>(c.q0) + pos0 - first) * row;
   // this thread's vectors t, t + T, ...: offsets within a head's rows, -1 past the end
   int rel[kHeld];
+  {
+    int r = t / vecs, v = t - r * vecs;   // row and vector of the row, advanced by T vectors
+    const int dr = T / vecs, dv = T - dr * vecs;
 #pragma unroll
-  for (int k = 0; k < kHeld; ++k) {
-    const int it = t + k * T;
-    rel[k] = it < items ? static_cast<int>((it / vecs) * row) + it % vecs : -1;
+    for (int k = 0; k < kHeld; ++k) {
+      rel[k] = t + k * T < items ? r * static_cast<int>(row) + v : -1;
+      r += dr;
+      v += dv;
+      if (v >= vecs) {
+        v -= vecs;
+        ++r;
+      }
+    }
   }
+  const bool whole = items >= kHeld * T;   // every thread holds kHeld vectors
   const int step = p.head_groups * U;
   auto head_of = [&](int unit) { return unit >= p.num_kv_heads ? unit - p.num_kv_heads : unit; };
   auto rows_of = [&](int unit) {   // K of every head, then V
@@ -236,11 +248,16 @@ __global__ void __launch_bounds__(kQThreads, 8) quantize_kernel(const QuantParam
            (src0 + head_of(unit) * vecs) * 8;
   };
   auto load = [&](Vec8<Src>(&v)[kHeld], int unit) {
-    const Src* src = unit < units ? rows_of(unit) : nullptr;
+    const Src* src = rows_of(unit < units ? unit : 0);
+    if (whole && unit < units) {
 #pragma unroll
-    for (int k = 0; k < kHeld; ++k) {
-      v[k].zero();
-      if (src && rel[k] >= 0) v[k].load(src + static_cast<int64_t>(rel[k]) * 8);
+      for (int k = 0; k < kHeld; ++k) v[k].load(src + static_cast<int64_t>(rel[k]) * 8);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kHeld; ++k) {
+        v[k].zero();
+        if (unit < units && rel[k] >= 0) v[k].load(src + static_cast<int64_t>(rel[k]) * 8);
+      }
     }
   };
   Vec8<Src> held[kHeld];
@@ -253,7 +270,7 @@ __global__ void __launch_bounds__(kQThreads, 8) quantize_kernel(const QuantParam
   int turn = 0;
   // the team's maximum; buf: one of red's halves, by turns
   auto team_max = [&](uint32_t x, uint32_t* buf) {
-    x = __reduce_max_sync(0xffffffffu, x);
+    x = __reduce_max_sync(T < 32 ? 0xFFFFu << (threadIdx.x & 16) : 0xffffffffu, x);
     if (T > 32) {
       if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
       __syncthreads();
@@ -280,7 +297,8 @@ __global__ void __launch_bounds__(kQThreads, 8) quantize_kernel(const QuantParam
       }
     m = team_max(Vec8<Src>::top_bits(m), red[turn]);
     const bool finite = m < 0x7F800000u;
-    if (T > 32 ? __syncthreads_or(!finite) : !finite) {   // rare: the maximum of the finite values
+    // rare: the maximum of the finite values; every team of the CTA takes part
+    if (T > 32 && U > 1 ? __syncthreads_or(!finite) : !finite) {
       uint32_t f = 0;
       for (int it = t; live && it < items; it += T) {
         Vec8<Src> y;
@@ -333,9 +351,14 @@ __global__ void __launch_bounds__(kQThreads, 8) quantize_kernel(const QuantParam
     cache += off * row;
     if (finite) {
       const float r = __frcp_rn(sc);
+      if (whole) {
 #pragma unroll
-      for (int k = 0; k < kHeld; ++k)
-        if (rel[k] >= 0) cache[rel[k]] = codes8<Src, Q, true>(v[k], sc, r);
+        for (int k = 0; k < kHeld; ++k) cache[rel[k]] = codes8<Src, Q, true>(v[k], sc, r);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kHeld; ++k)
+          if (rel[k] >= 0) cache[rel[k]] = codes8<Src, Q, true>(v[k], sc, r);
+      }
       for (int it = t + kHeld * T; it < items; it += T) {
         Vec8<Src> y;
         y.load(src + ((it / vecs) * row + it % vecs) * 8);
@@ -357,17 +380,21 @@ __global__ void __launch_bounds__(kQThreads, 8) quantize_kernel(const QuantParam
 
 template <typename Src, typename Q, int T>
 cudaError_t launch_quantize(QuantParams& p, int num_seqs, cudaStream_t st) {
-  constexpr int U = kQThreads / T;
+  constexpr int U = kQThreads<T> / T;
   const int bs = 1 << p.bs_log2;
   const int64_t touched = (static_cast<int64_t>(p.max_query_len) + bs - 2) / bs + 1;
-  // CTAs per block: one, or more while the grid has fewer than kQGrid CTAs per SM
+  // CTAs per block: as many as make up to two whole waves, at least one.  A partial wave
+  // costs its whole length: 8,192 tokens x 32 heads took 38.2 us with three CTAs per block
+  // (1.5 waves) and take 34.6 with two or four; 64 x 128 tokens x 8 heads 16.9 with one
+  // (half a wave) and 13.3 with two.
   const int64_t most = (2 * p.num_kv_heads + U - 1) / U;
-  const int64_t want = (kQGrid * device_sm_count() + touched * num_seqs - 1) / (touched * num_seqs);
-  p.head_groups = static_cast<int32_t>(want < most ? want : most);
+  const int64_t waves =
+      2 * (kQWarps * 32 / kQThreads<T>) * static_cast<int64_t>(device_sm_count()) / (touched * num_seqs);
+  p.head_groups = static_cast<int32_t>(waves < 1 ? 1 : (waves < most ? waves : most));
   const int64_t x = touched * p.head_groups;
   if (x > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   return launch_pdl(quantize_kernel<Src, Q, T>, dim3(static_cast<unsigned>(x), num_seqs),
-                    dim3(kQThreads), 0, st, p);
+                    dim3(kQThreads<T>), 0, st, p);
 }
 
 template <typename Src, typename Q>
@@ -375,9 +402,12 @@ cudaError_t pick_team(QuantParams& p, int num_seqs, cudaStream_t st) {
   const int bs = 1 << p.bs_log2;
   const int64_t items = static_cast<int64_t>(p.max_query_len < bs ? p.max_query_len : bs) * p.segs * 2;
   constexpr int kHeld = Vec8<Src>::kHeld;
+  if (items <= 16 * kHeld) return launch_quantize<Src, Q, 16>(p, num_seqs, st);
   if (items <= 32 * kHeld) return launch_quantize<Src, Q, 32>(p, num_seqs, st);
   if (items <= 64 * kHeld) return launch_quantize<Src, Q, 64>(p, num_seqs, st);
-  return launch_quantize<Src, Q, 128>(p, num_seqs, st);
+  if (items <= 128 * kHeld) return launch_quantize<Src, Q, 128>(p, num_seqs, st);
+  if (items <= 256 * kHeld) return launch_quantize<Src, Q, 256>(p, num_seqs, st);
+  return launch_quantize<Src, Q, 512>(p, num_seqs, st);
 }
 
 // ---- read-back ---------------------------------------------------------------
