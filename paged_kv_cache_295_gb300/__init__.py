@@ -429,97 +429,39 @@ def workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_l
                                                          head_dim, max_context_len, partition))
 
 
-# The calls below are made once per layer and step, so their checks are kept to a few
-# attribute reads: a call takes about 10 us of host time, launch included.
-_CODE_OF = {}
+_ext = None
 
 
-def _code_of(dtype) -> int:
-    if not _CODE_OF:
-        torch = _torch()
-        _CODE_OF.update({torch.float32: F32, torch.bfloat16: BF16, torch.uint8: FP8_E4M3,
-                         torch.float8_e4m3fn: FP8_E4M3, torch.int8: INT8})
-    code = _CODE_OF.get(dtype)
-    if code is None:
-        raise ValueError(f"unsupported dtype {dtype}")
-    return code
+def _binding():
+    """``_pkv_torch.so``: the calls below with tensors as arguments (checks, allocation and the
+    call of the C ABI in one step); raises if it has not been built."""
+    global _ext
+    if _ext is None:
+        _torch()
+        library()
+        try:
+            from . import _pkv_torch
+        except ImportError as e:
+            raise RuntimeError("_pkv_torch.so not built: run "
+                               "paged_kv_cache_295_gb300._build.build_library()") from e
+        _ext = _pkv_torch
+    return _ext
 
 
-def _elsewhere(t, stream):
-    """None if the call runs on the current stream of the tensor's device and that device is
-    current; else the context that makes it so."""
-    torch = _torch()
-    dev = t.get_device()
-    if dev < 0:
+def _on_stream(stream, t):
+    """Context in which a call allocates and launches on ``stream``."""
+    if not t.is_cuda:
         raise ValueError("CUDA tensors are needed (no CPU path)")
-    if stream is not None:
-        if stream.device_index != dev:
-            raise ValueError(f"tensors on cuda:{dev}, stream of cuda:{stream.device_index}")
-        return torch.cuda.stream(stream)
-    return None if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+    if stream.device != t.device:
+        raise ValueError(f"tensors on {t.device}, stream of {stream.device}")
+    return _torch().cuda.stream(stream)
 
 
-def _current_stream(dev):
-    torch = _torch()
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)   # no stream object made
-    return raw(dev) if raw else torch.cuda.current_stream(dev).cuda_stream
-
-
-def _ptrs(dev, names, *tensors):
-    """Device pointers (None for None) of contiguous tensors on device ``dev``; ``names``:
-    theirs, in one string."""
-    out = []
-    for t in tensors:
-        if t is None:
-            out.append(None)
-        elif t.get_device() == dev and t.is_contiguous():
-            out.append(t.data_ptr())
-        else:
-            name = names.split()[len(out)]
-            raise ValueError(f"{name} must be contiguous" if t.get_device() == dev else
-                             f"{name} is on {t.device}, the call on cuda:{dev}")
-    return out
-
-
-def _want(t, name, shape, *codes):
-    """Shape and element type (as pkv_dtype codes, or torch dtypes) of an argument."""
-    if t.shape != shape or (t.dtype not in codes and _CODE_OF.get(t.dtype) not in codes):
-        raise ValueError(f"{name} must be {list(shape)} of "
-                         f"{[DTYPE_NAMES.get(c, c) if type(c) is int else c for c in codes]}, got "
-                         f"{list(t.shape)} of {t.dtype}")
-
-
-def _caches(k_cache, v_cache):
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache must be alike, [num_blocks, block_size, num_kv_heads, "
-                         "head_dim]")
-    return k_cache.shape
-
-
-def _tables(block_tables, context_lens, num_seqs):
-    i32 = _torch().int32
-    if block_tables.dim() != 2 or block_tables.shape[0] != num_seqs or block_tables.dtype != i32:
-        raise ValueError(f"block_tables must be int32 [{num_seqs}, max_blocks], got "
-                         f"{list(block_tables.shape)} of {block_tables.dtype}")
-    if context_lens is not None:
-        _want(context_lens, "context_lens", (num_seqs,), i32)
-    return block_tables.shape[1]
-
-
-def _block_scales(k_scale, v_scale, num_blocks, num_kv_heads):
-    """Floats between the scales of two blocks; 0 for one scale per head."""
-    if k_scale is None or v_scale is None:
-        raise ValueError("an 8-bit cache needs k_scale and v_scale")
-    f32 = _torch().float32
-    shape = k_scale.shape
-    per_head = len(shape) == 1
-    if v_scale.shape != shape or k_scale.dtype != f32 or v_scale.dtype != f32 or (
-            shape[0] != num_kv_heads if per_head else
-            len(shape) != 2 or shape[0] != num_blocks or shape[1] < num_kv_heads):
-        raise ValueError(f"k_scale and v_scale must be float32 [{num_kv_heads}] or [{num_blocks}, "
-                         f">= {num_kv_heads}], both alike, got {list(shape)} of {k_scale.dtype} and "
-                         f"{list(v_scale.shape)} of {v_scale.dtype}")
-    return 0 if per_head else shape[1]
+def _done(r, where):
+    """The result of a binding call, or its status as an exception."""
+    if type(r) is int:
+        _check(r, where)
+    return r
 
 
 def quantize_and_cache(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables,
@@ -531,32 +473,14 @@ def quantize_and_cache(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block
     Sequence ``s`` owns rows ``query_start[s] .. query_start[s + 1] - 1`` (int32 on the
     device; None: one row per sequence), the last tokens of its context
     ``context_lens[s]``; ``max_query_len`` is a host upper bound of a sequence's rows."""
-    torch = _torch()
-    nb, bs, hkv, d = _caches(k_cache, v_cache)
-    T, S = k_new.shape[0], context_lens.shape[0]
-    src, dst = _code_of(k_new.dtype), _code_of(k_cache.dtype)
-    _want(k_new, "k_new", (T, hkv, d), F32, BF16)
-    _want(v_new, "v_new", (T, hkv, d), src)
-    mb = _tables(block_tables, context_lens, S)
-    if query_start is not None:
-        _want(query_start, "query_start", (S + 1,), torch.int32)
-    stride = _block_scales(k_scales, v_scales, nb, hkv)
-    if stride == 0:
-        raise ValueError("k_scales and v_scales must be [num_blocks, >= num_kv_heads]")
-    place = _elsewhere(k_new, stream)
-    if place is not None:
-        with place:
+    if stream is not None:
+        with _on_stream(stream, k_new):
             return quantize_and_cache(k_new, v_new, k_cache, v_cache, k_scales, v_scales,
                                       block_tables, context_lens, query_start, max_query_len,
                                       device_status)
-    dev = k_new.get_device()
-    kn, vn, qs, bt, cl, kc, vc, ks, vs, status = _ptrs(
-        dev, "k_new v_new query_start block_tables context_lens k_cache v_cache k_scales v_scales "
-        "device_status", k_new, v_new, query_start, block_tables, context_lens, k_cache, v_cache,
-        k_scales, v_scales, device_status)
-    _check(library().quantize_and_cache(kn, vn, qs, bt, cl, kc, vc, ks, vs, S, T, int(max_query_len), hkv, d, bs, nb, mb, stride,
-                                        src, dst, status, _current_stream(dev)),
-           "quantize_and_cache")
+    _done(_binding().quantize_and_cache(k_new, v_new, k_cache, v_cache, k_scales, v_scales,
+                                        block_tables, context_lens, query_start, max_query_len,
+                                        device_status), "quantize_and_cache")
 
 
 def gather_cache(k_cache, v_cache, block_tables, row_start, num_rows, max_rows, first_pos=None,
@@ -569,140 +493,51 @@ def gather_cache(k_cache, v_cache, block_tables, row_start, num_rows, max_rows, 
     ``max_rows`` a host upper bound of a sequence's rows.  8-bit codes are multiplied by
     ``k_scale`` / ``v_scale`` (``[Hkv]``, or ``[NB, >= Hkv]`` per block).  ``out_dtype``
     float32 or bfloat16 (default: bfloat16, or that of ``k_out``)."""
-    torch = _torch()
-    nb, bs, hkv, d = _caches(k_cache, v_cache)
-    S = block_tables.shape[0]
-    mb = _tables(block_tables, None, S)
-    _want(row_start, "row_start", (S + 1,), torch.int32)
-    if first_pos is not None:
-        _want(first_pos, "first_pos", (S,), torch.int32)
-    code = _code_of(k_cache.dtype)
-    stride = 0
-    if code in (FP8_E4M3, INT8):
-        stride = _block_scales(k_scale, v_scale, nb, hkv)
-    else:
-        k_scale = v_scale = None
-    place = _elsewhere(k_cache, stream)
-    if place is not None:
-        with place:
+    if stream is not None:
+        with _on_stream(stream, k_cache):
             return gather_cache(k_cache, v_cache, block_tables, row_start, num_rows, max_rows,
                                 first_pos, k_scale, v_scale, out_dtype, k_out, v_out, device_status)
-    if out_dtype is None:
-        out_dtype = torch.bfloat16 if k_out is None else k_out.dtype
-    shape = (int(num_rows), hkv, d)
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
-    out_code = _code_of(out_dtype)
-    _want(k_out, "k_out", shape, out_code)
-    _want(v_out, "v_out", shape, out_code)
-    dev = k_cache.get_device()
-    kc, vc, bt, rs, fp, ks, vs, ko, vo, status = _ptrs(
-        dev, "k_cache v_cache block_tables row_start first_pos k_scale v_scale k_out v_out "
-        "device_status", k_cache, v_cache, block_tables, row_start, first_pos, k_scale, v_scale,
-        k_out, v_out, device_status)
-    _check(library().gather_cache(kc, vc, bt, rs, fp, S, shape[0], int(max_rows), hkv, d, bs, nb, mb,
-                                  code, ks, vs, stride, out_code, ko, vo, status,
-                                  _current_stream(dev)), "gather_cache")
-    return k_out, v_out
+    return _done(_binding().gather_cache(k_cache, v_cache, block_tables, row_start, num_rows,
+                                         max_rows, first_pos, k_scale, v_scale, out_dtype, k_out,
+                                         v_out, device_status), "gather_cache")
 
 
 def _windowed(out, out_dtype, k_scale, window, sinks) -> bool:
     """Whether a call needs the form with a window, scales per block or another output type."""
-    torch = _torch()
-    if out is not None:
-        if out_dtype is not None and out.dtype != out_dtype:
-            raise ValueError(f"out is {out.dtype}, out_dtype {out_dtype}")
-        out_dtype = out.dtype
-    return bool(window or sinks or (k_scale is not None and k_scale.dim() == 2)
-                or (out_dtype is not None and out_dtype != torch.float32))
-
-
-def _attention_args(q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale):
-    """Checks shared by the windowed decode and prefill calls.  Returns S, Hq, Hkv, D, block size,
-    blocks, table width, the codes of q and of the cache, the scales and their stride."""
-    nb, bs, hkv, d = _caches(k_cache, v_cache)
-    T, hq, _ = q.shape
-    S = context_lens.shape[0]
-    q_code, kv_code = _code_of(q.dtype), _code_of(k_cache.dtype)
-    _want(q, "q", (T, hq, d), F32, BF16)
-    mb = _tables(block_tables, context_lens, S)
-    stride = 0
-    if kv_code in (FP8_E4M3, INT8):
-        stride = _block_scales(k_scale, v_scale, nb, hkv)
-    else:
-        k_scale = v_scale = None
-    return S, hq, hkv, d, bs, nb, mb, q_code, kv_code, k_scale, v_scale, stride
-
-
-def _attention_out(q, out, out_dtype):
-    torch = _torch()
-    if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype or torch.float32, device=q.device)
-    _want(out, "out", q.shape, F32, BF16)
-    return out
+    if window or sinks:
+        return True
+    f32 = _torch().float32
+    return bool((k_scale is not None and k_scale.dim() == 2)
+                or (out is not None and out.dtype != f32)
+                or (out_dtype is not None and out_dtype != f32))
 
 
 def _decode_window(q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len, out,
                    k_scale, v_scale, workspace, partition, device_status, stream, window, sinks,
                    out_dtype):
-    torch = _torch()
-    S, hq, hkv, d, bs, nb, mb, q_code, kv_code, k_scale, v_scale, stride = _attention_args(
-        q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale)
-    if q.shape[0] != S:
-        raise ValueError(f"q must hold one row per sequence: {q.shape[0]} rows, {S} contexts")
-    place = _elsewhere(q, stream)
-    if place is not None:
-        with place:
+    if stream is not None:
+        with _on_stream(stream, q):
             return _decode_window(q, k_cache, v_cache, block_tables, context_lens, scale,
                                   max_context_len, out, k_scale, v_scale, workspace, partition,
                                   device_status, None, window, sinks, out_dtype)
-    out = _attention_out(q, out, out_dtype)
-    lib = library()
-    need = lib.paged_attention_window_workspace_bytes(S, hq, hkv, d, max_context_len, partition,
-                                                      window, sinks)
-    ws_bytes = 0 if workspace is None else workspace.nbytes
-    if need > ws_bytes:
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        ws_bytes = need
-    dev = q.get_device()
-    qp, kc, vc, bt, cl, ks, vs, op, ws, status = _ptrs(
-        dev, "q k_cache v_cache block_tables context_lens k_scale v_scale out workspace "
-        "device_status", q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, out,
-        workspace, device_status)
-    _check(lib.paged_attention_decode_window(
-        qp, kc, vc, bt, cl, S, hq, hkv, d, bs, nb, mb, int(max_context_len), float(scale), q_code,
-        kv_code, ks, vs, stride, int(window), int(sinks), _code_of(out.dtype), op, ws, ws_bytes,
-        int(partition), status, _current_stream(dev)), "paged_attention_decode_window")
-    return out
+    return _done(_binding().decode_window(
+        q, k_cache, v_cache, block_tables, context_lens, scale, max_context_len, out, k_scale,
+        v_scale, workspace, partition, device_status, window, sinks, out_dtype),
+        "paged_attention_decode_window")
 
 
 def _prefill_window(q, query_start, k_cache, v_cache, block_tables, context_lens, scale,
                     max_query_len, max_context_len, causal, out, k_scale, v_scale, device_status,
                     stream, window, sinks, out_dtype):
-    torch = _torch()
-    S, hq, hkv, d, bs, nb, mb, q_code, kv_code, k_scale, v_scale, stride = _attention_args(
-        q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale)
-    _want(query_start, "query_start", (S + 1,), torch.int32)
-    place = _elsewhere(q, stream)
-    if place is not None:
-        with place:
+    if stream is not None:
+        with _on_stream(stream, q):
             return _prefill_window(q, query_start, k_cache, v_cache, block_tables, context_lens,
                                    scale, max_query_len, max_context_len, causal, out, k_scale,
                                    v_scale, device_status, None, window, sinks, out_dtype)
-    out = _attention_out(q, out, out_dtype)
-    dev = q.get_device()
-    qp, qs, kc, vc, bt, cl, ks, vs, op, status = _ptrs(
-        dev, "q query_start k_cache v_cache block_tables context_lens k_scale v_scale out "
-        "device_status", q, query_start, k_cache, v_cache, block_tables, context_lens, k_scale,
-        v_scale, out, device_status)
-    _check(library().paged_attention_prefill_window(
-        qp, qs, kc, vc, bt, cl, S, q.shape[0], int(max_query_len), hq, hkv, d, bs, nb, mb,
-        int(max_context_len), float(scale), 1 if causal else 0, q_code, kv_code, ks, vs, stride,
-        int(window), int(sinks), _code_of(out.dtype), op, status, _current_stream(dev)),
+    return _done(_binding().prefill_window(
+        q, query_start, k_cache, v_cache, block_tables, context_lens, scale, max_query_len,
+        max_context_len, causal, out, k_scale, v_scale, device_status, window, sinks, out_dtype),
         "paged_attention_prefill_window")
-    return out
 
 
 DECODE_KERNELS = {"auto": 0, "mma": 1, "simt": 2}

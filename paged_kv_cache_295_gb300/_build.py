@@ -1,8 +1,9 @@
-"""In-tree build of libpagedkv.so for sm_103a with nvcc (no cmake, no torch).
+"""In-tree build of libpagedkv.so for sm_103a with nvcc (no cmake, no torch), and of
+_pkv_torch.so, the Python entry points that take torch tensors (g++, torch's headers).
 
 Each translation unit compiles in parallel into ``_build/``; the shared
-library lands next to this file.  A rebuild happens when any source or header
-is newer than the library.
+libraries land next to this file.  A rebuild happens when any source or header
+is newer than a library.
 """
 from __future__ import annotations
 
@@ -11,6 +12,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +20,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
+BINDING_SRC = os.path.join(CSRC, "binding", "torch_binding.cpp")
+BINDING = os.path.join(PKG, "_pkv_torch.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -36,14 +40,14 @@ def sources():
     cu = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     cpp = sorted(glob.glob(os.path.join(CSRC, "*.cpp")))
     deps = cu + cpp + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + \
-        sorted(glob.glob(os.path.join(INCLUDE, "*.h")))
+        sorted(glob.glob(os.path.join(INCLUDE, "*.h"))) + [BINDING_SRC]
     return cu, cpp, deps
 
 
 def stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return any(os.path.getmtime(f) > t for f in sources()[2] + [__file__])
 
 
@@ -54,8 +58,29 @@ def _run(cmd):
     return r.stdout + r.stderr
 
 
+def binding_commands():
+    """Compile and link commands of the torch binding."""
+    import torch
+    root = os.path.dirname(os.path.abspath(torch.__file__))
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    obj = os.path.join(BUILD, "torch_binding.cpp.o")
+    cxx = os.environ.get("CXX", "g++")
+    compile_ = [cxx, *CXX_FLAGS, "-I" + sysconfig.get_paths()["include"],
+                *(f"-isystem{os.path.join(root, 'include', d)}"
+                  for d in ("", os.path.join("torch", "csrc", "api", "include"))),
+                f"-isystem{os.path.join(cuda, 'include')}",
+                f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+                "-c", BINDING_SRC, "-o", obj]
+    lib = os.path.join(root, "lib")
+    # torch's libraries are loaded by then: only their names are needed
+    link = [cxx, "-shared", "-o", BINDING + ".tmp", obj, f"-L{PKG}", "-lpagedkv", f"-L{lib}",
+            "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    return compile_, link
+
+
 def build_library(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile every CUDA / C++ unit for sm_103a and link ``libpagedkv.so``."""
+    """Compile every CUDA / C++ unit for sm_103a and link ``libpagedkv.so``, then the torch
+    binding against it."""
     if not force and not stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -69,14 +94,18 @@ def build_library(force: bool = False, verbose_ptxas: bool = False) -> str:
     for src in cpp:
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
         jobs.append([os.environ.get("CXX", "g++"), *CXX_FLAGS, "-c", src, "-o", obj])
+    bind, bind_link = binding_commands()
+    jobs.append(bind)
     logs = []
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
         for out in ex.map(_run, jobs):
             logs.append(out)
-    objs = [j[-1] for j in jobs]
+    objs = [j[-1] for j in jobs[:-1]]
     tmp = LIB + ".tmp"
     _run([nv, *ARCH, "-shared", "-o", tmp, *objs])
     os.replace(tmp, LIB)
+    _run(bind_link)
+    os.replace(BINDING + ".tmp", BINDING)
     if verbose_ptxas:
         with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
             f.write("\n".join(logs))

@@ -119,6 +119,15 @@ def test_python_refusals(lib):
                dict(out=torch.zeros((S, 4, d)), out_dtype=torch.bfloat16)):
         with pytest.raises(ValueError):
             dec(**kw)
+    for kw in (dict(k_new=None), dict(k_cache=3), dict(max_query_len="a"), dict(max_query_len=1 << 40)):
+        with pytest.raises(ValueError):
+            quant(**kw)
+    for kw in (dict(scale="x"), dict(window=1.5), dict(window=1 << 33), dict(out_dtype=torch.float16),
+               dict(out_dtype="bf16"), dict(workspace=7)):
+        with pytest.raises((ValueError, TypeError)):
+            dec(**kw)
+    with pytest.raises(ValueError):
+        lib._binding().decode_window(q)
     rs = torch.zeros(S + 1, dtype=torch.int32)
     for kw in (dict(), dict(row_start=rs[:2]), dict(row_start=rs.long()), dict(k_scale=None),
                dict(first_pos=ctx[:1]), dict(block_tables=bt.long())):
