@@ -24,18 +24,25 @@ int64_t visible_tokens(int32_t max_ctx, int32_t window, int32_t sinks) {
 // Tokens per partition.  `tokens` is what the longest query can see; token_bytes the K and V
 // bytes of one token and head.  With n partitions a launch has heads * n CTAs of about
 // tokens / n tokens, three to an SM, and is estimated (us) as
-//   3, and 2 more for the merging kernel if n > 1
+//   3, and for merging 1.5 more within a cluster, 2 by a second kernel
 //   + per full wave of CTA slots: 1 + len * slots * token_bytes / HBM bandwidth
-//   + the last, partial wave: 1 + len * the same rate times how full it is, but at least
-//     the rate of a CTA alone, which its two-stage rings bound (48 KB/us).
+//   + the last, partial wave: 1 + len * the root of the squares of that rate times how full
+//     the wave is and of the rate of a CTA alone, which its two-stage rings bound (42 KB/us).
 // The n with the least estimate is taken.  Measured (bf16, GQA-8, 64 x 8 heads, window 1024):
-// 1 partition of 1,120 tokens 57.2 us (1.1 waves), 2 of 576 52; 4 x 8 heads: 17.1 us with
-// one, 8.6 with nine; one sequence, window 4096: 50.3 with one, 9.6 with 33.
+// one partition 57.6 us (1.1 waves), two of 576 and 512 57.4, of 704 and 384 53.0; 16 x 8
+// heads, GQA-4: 20.3 with one, 17.1 with three; 4 x 8 heads: 18.6 with one, 8.7 with six;
+// one sequence, window 4096: 56.9 with two, 10.1 with 33.
 int32_t auto_win_partition(int64_t heads, int64_t tokens, int token_bytes) {
   const double slots = 3.0 * device_sm_count();
-  const double full = slots * token_bytes / 6.6e6, alone = token_bytes / 4.8e4;
+  const double full = slots * token_bytes / 6.6e6, alone = token_bytes / 4.2e4;
   int32_t best = 4096;
   double least = 1e30;
+  auto consider = [&](int64_t len, double t) {
+    if (t < least) {
+      least = t;
+      best = static_cast<int32_t>(len);
+    }
+  };
   int32_t before = 0;
   for (int64_t n = 1; n <= 64; ++n) {
     int64_t len = ((tokens + n - 1) / n + 63) / 64 * 64;
@@ -45,12 +52,15 @@ int32_t auto_win_partition(int64_t heads, int64_t tokens, int token_bytes) {
     const int64_t parts = (tokens + len - 1) / len;
     const double waves = static_cast<double>(heads) * parts / slots;
     const double whole = static_cast<double>(static_cast<int64_t>(waves)), rest = waves - whole;
-    double t = (parts > 1 ? 5.0 : 3.0) + whole * (1.0 + len * full);
-    if (rest > 0) t += 1.0 + len * (rest * full > alone ? rest * full : alone);
-    if (t < least) {
-      least = t;
-      best = static_cast<int32_t>(len);
-    }
+    const double merge = parts <= 1 ? 0 : parts <= kWinCluster && heads * parts <= slots ? 1.5 : 2;
+    double t = 3.0 + merge + whole * (1.0 + len * full);
+    if (rest > 0) t += 1.0 + len * std::sqrt(rest * full * rest * full + alone * alone);
+    consider(len, t);
+    // The same number of partitions with a last one of about 40 %: past one wave the short
+    // ones fill the slots that equal ones would leave empty at the end.
+    const int64_t longer = (tokens * 10 / (10 * n - 6) + 63) / 64 * 64, last = tokens - (n - 1) * longer;
+    if (n > 1 && waves > 1 && longer <= 4096 && last > 0)
+      consider(longer, 5.0 + waves + heads * tokens / slots * full + last * alone);
   }
   return best;
 }
