@@ -589,7 +589,9 @@ pkv_status paged_attention_decode_window(
  * t > p - window or t < sinks.  window > 0 needs causal = 1; sinks need a window.
  * 8-bit caches carry the weights as one fp16 value (2^-11 relative), as
  * paged_attention_prefill does, whatever the output type.  Table entries of blocks
- * that no query of the chunk sees are not read.  max_context_len <= 2^30; shapes
+ * that no query of the chunk sees are not read.  A key that a query does not see, but
+ * another one of the same work tile (up to 256 query rows) does, has weight 0 there; a V
+ * value of it that is not finite gives NaN.  max_context_len <= 2^30; shapes
  * and errors otherwise as paged_attention_prefill. */
 pkv_status paged_attention_prefill_window(
     const void* q, const int32_t* query_start, const void* k_cache, const void* v_cache,

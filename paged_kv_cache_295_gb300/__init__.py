@@ -402,6 +402,7 @@ def _stream(stream):
 def reshape_and_cache(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale=None,
                       v_scale=None, device_status=None, stream=None):
     """Append token rows ``[T, Hkv, D]`` into one layer's ``[NB, bs, Hkv, D]`` cache."""
+    _per_head(k_scale, v_scale, "reshape_and_cache")
     T, hkv, d = k_new.shape
     nb, bs = k_cache.shape[0], k_cache.shape[1]
     st = library().reshape_and_cache(
@@ -502,12 +503,22 @@ def gather_cache(k_cache, v_cache, block_tables, row_start, num_rows, max_rows, 
                                          v_out, device_status), "gather_cache")
 
 
+def _block_scales(scale) -> bool:
+    """Whether these are scales per block; ``[1, Hkv]`` reads the same as ``[Hkv]``."""
+    return scale is not None and scale.dim() == 2 and scale.shape[0] != 1
+
+
+def _per_head(k_scale, v_scale, where):
+    if _block_scales(k_scale) or _block_scales(v_scale):
+        raise ValueError(f"{where} takes one scale per head, not scales per block")
+
+
 def _windowed(out, out_dtype, k_scale, window, sinks) -> bool:
     """Whether a call needs the form with a window, scales per block or another output type."""
     if window or sinks:
         return True
     f32 = _torch().float32
-    return bool((k_scale is not None and k_scale.dim() == 2)
+    return bool(_block_scales(k_scale)
                 or (out is not None and out.dtype != f32)
                 or (out_dtype is not None and out_dtype != f32))
 
@@ -604,6 +615,7 @@ def paged_attention_decode_append(q, k_new, v_new, slot_mapping, k_cache, v_cach
     """``reshape_and_cache`` of one new token per sequence (``k_new`` / ``v_new``
     ``[S, Hkv, D]``, ``slot_mapping`` int64 ``[S]``, each the slot of position
     ``context_lens[s] - 1``) and ``paged_attention_decode``, as one call."""
+    _per_head(k_scale, v_scale, "paged_attention_decode_append")
     torch = _torch()
     S, hq, d = q.shape
     nb, bs, hkv, _ = k_cache.shape
@@ -632,6 +644,7 @@ def paged_attention_decode_noalloc(q, k_cache, v_cache, block_tables, context_le
                                    device_status=None, stream=None):
     """``paged_attention_decode`` into a caller-owned ``out`` with the library's
     built-in split-KV scratch (no device allocation by the library or here)."""
+    _per_head(k_scale, v_scale, "paged_attention_decode_noalloc")
     S, hq, d = q.shape
     nb, bs, hkv, _ = k_cache.shape
     st = library().paged_attention_decode_noalloc(

@@ -168,6 +168,14 @@ at::ScalarType out_type(PyObject* dtype, const Tensor& out, at::ScalarType other
   return out.defined() ? out.scalar_type() : otherwise;
 }
 
+// The status word: an int32 on the device, or None.
+const Tensor& status_word(PyObject* o) {
+  const Tensor& t = tensor(o, "device_status", true);
+  if (t.defined() && (t.scalar_type() != at::kInt || t.numel() < 1))
+    refuse("device_status must be Int with at least one element, got " + show(t));
+  return t;
+}
+
 void arity(Py_ssize_t n, Py_ssize_t wanted) {
   if (n != wanted) refuse("wrong number of arguments");
 }
@@ -182,7 +190,7 @@ PyObject* do_quantize(PyObject* const* a, Py_ssize_t na) {
                &vc = tensor(a[3], "v_cache"), &ks = tensor(a[4], "k_scales"),
                &vs = tensor(a[5], "v_scales"), &bt = tensor(a[6], "block_tables"),
                &cl = tensor(a[7], "context_lens"), &qs = tensor(a[8], "query_start", true),
-               &st = tensor(a[10], "device_status", true);
+               &st = status_word(a[10]);
   const int32_t max_query = integer32(a[9], "max_query_len");
   const Cache c = cache_of(kc, vc);
   if (kn.dim() != 3 || cl.dim() != 1) refuse("k_new must be [T, heads, dim] and context_lens [S]");
@@ -218,7 +226,7 @@ PyObject* do_gather(PyObject* const* a, Py_ssize_t na) {
   arity(na, 13);
   const Tensor &kc = tensor(a[0], "k_cache"), &vc = tensor(a[1], "v_cache"),
                &bt = tensor(a[2], "block_tables"), &rs = tensor(a[3], "row_start"),
-               &fp = tensor(a[6], "first_pos", true), &st = tensor(a[12], "device_status", true);
+               &fp = tensor(a[6], "first_pos", true), &st = status_word(a[12]);
   const int64_t rows = integer32(a[4], "num_rows");
   const int32_t max_rows = integer32(a[5], "max_rows");
   const Cache c = cache_of(kc, vc);
@@ -309,7 +317,7 @@ PyObject* do_decode(PyObject* const* a, Py_ssize_t na) {
   const float scale = real(a[5], "scale");
   const int32_t max_ctx = integer32(a[6], "max_context_len"), part = integer32(a[11], "partition"),
                 window = integer32(a[13], "window"), sinks = integer32(a[14], "sinks");
-  const Tensor& st = tensor(a[12], "device_status", true);
+  const Tensor& st = status_word(a[12]);
   const at::Device dev = cuda_device(p.q);
   const c10::cuda::CUDAGuard guard(dev);
   Tensor out = attention_out(p, tensor(a[7], "out", true), a[15]), ws = tensor(a[10], "workspace", true);
@@ -345,7 +353,7 @@ PyObject* do_prefill(PyObject* const* a, Py_ssize_t na) {
   Tensor ks = tensor(a[11], "k_scale", true), vs = tensor(a[12], "v_scale", true);
   const Attention p(a[0], a[2], a[3], a[4], a[5], ks, vs);
   if (!is_codes(p.c.code)) ks = vs = Tensor();
-  const Tensor &qs = tensor(a[1], "query_start"), &st = tensor(a[13], "device_status", true);
+  const Tensor &qs = tensor(a[1], "query_start"), &st = status_word(a[13]);
   want(qs, "query_start", {p.S + 1}, {at::kInt});
   const float scale = real(a[6], "scale");
   const int32_t max_query = integer32(a[7], "max_query_len"), max_ctx = integer32(a[8], "max_context_len"),

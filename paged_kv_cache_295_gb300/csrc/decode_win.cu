@@ -160,7 +160,8 @@ extern "C" pkv_status paged_attention_decode_window(
   if (G > 16 || !pow2(block_size) || block_size < 8 || block_size > 4096)
     return PKV_ERR_UNSUPPORTED;
   if (num_blocks > INT32_MAX || num_blocks * block_size > INT32_MAX ||
-      max_context_len > (1 << 30) || num_seqs > 65535 || num_kv_heads > 32767)
+      max_context_len > (1 << 30) || num_seqs > 65535 || num_kv_heads > 32767 ||
+      static_cast<int64_t>(num_seqs) * num_q_heads > INT32_MAX)
     return PKV_ERR_UNSUPPORTED;
   if (codes && scale_stride != 0 && scale_stride < num_kv_heads) return PKV_ERR_INVALID_ARG;
   if (num_seqs == 0) return PKV_OK;

@@ -395,3 +395,124 @@ def test_other_stream(lib):
     kb, vb = lib.gather_cache(dev["k"], dev["v"], dev["tables"], start, 150, 100, stream=st, **kw)
     st.synchronize()
     assert torch.equal(a, b) and torch.equal(ka, kb) and torch.equal(va, vb)
+
+
+def test_empty_batches(lib):
+    """No sequence, and sequences without rows: nothing is written, outputs are empty or 0."""
+    import torch
+    nb, bs, hkv, d = 4, 16, 2, 128
+    cache = torch.full((nb, bs, hkv, d), 5, dtype=torch.int8, device="cuda")
+    sc = torch.ones((nb, hkv), device="cuda")
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    rows = torch.zeros((0, hkv, d), device="cuda")
+    kw = {"k_scale": sc, "v_scale": sc}
+    q = torch.zeros((0, 4, d), dtype=torch.bfloat16, device="cuda")
+    for S, start in ((0, i32(0)), (2, i32(0, 0, 0))):
+        bt = torch.zeros((S, 2), dtype=torch.int32, device="cuda")
+        lens = torch.zeros(S, dtype=torch.int32, device="cuda")
+        lib.quantize_and_cache(rows, rows, cache, cache, sc, sc, bt, lens, query_start=start,
+                               max_query_len=0)
+        k, v = lib.gather_cache(cache, cache, bt, start, 0, 0, **kw)
+        assert k.shape == v.shape == (0, hkv, d)
+        assert lib.paged_attention_prefill(q, start, cache, cache, bt, lens, 0.1, 0, 0, **kw).shape == (0, 4, d)
+        qs = torch.ones((S, 4, d), dtype=torch.bfloat16, device="cuda")
+        out = lib.paged_attention_decode(qs, cache, cache, bt, lens, 0.1, 0, **kw)
+        assert out.shape == (S, 4, d) and (out == 0).all()
+    assert (cache == 5).all() and (sc == 1).all()
+
+
+def test_requantise_chain(lib):
+    """Rows read back and appended to another cache at once, call after call with new rows in
+    the same buffers: each call sees what the one before it wrote."""
+    import torch
+    nb, bs, hkv, d, n = 40, 16, 8, 128, 600
+    torch.manual_seed(3)
+    xs = [torch.randn((n, hkv, d), device="cuda") * (i + 1) for i in range(20)]
+    bt = torch.randperm(nb, device="cuda").to(torch.int32)[None, :38].contiguous()
+    lens, start = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([n], [0, n]))
+    new = lambda dt: (torch.zeros((nb, bs, hkv, d), dtype=dt, device="cuda"),
+                      torch.zeros((nb, hkv), device="cuda"))
+
+    def step(x, c, e, buf, wait):
+        sync = torch.cuda.synchronize if wait else (lambda: None)
+        lib.quantize_and_cache(x, x, c[0], c[2], c[1], c[3], bt, lens, start, n)
+        sync()
+        lib.gather_cache(c[0], c[2], bt, start, n, n, k_scale=c[1], v_scale=c[3], k_out=buf[0], v_out=buf[1])
+        sync()
+        lib.quantize_and_cache(buf[0], buf[1], e[0], e[2], e[1], e[3], bt, lens, start, n)
+        sync()
+        return lib.gather_cache(e[0], e[2], bt, start, n, n, k_scale=e[1], v_scale=e[3],
+                                out_dtype=torch.float32)[0]
+    runs = []
+    for wait in (True, False):
+        c, e = new(torch.int8) + new(torch.int8), new(torch.uint8) + new(torch.uint8)
+        buf = [torch.zeros((n, hkv, d), device="cuda") for _ in range(2)]
+        runs.append([step(x, c, e, buf, wait) for x in xs])
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(*runs))
+
+
+@pytest.mark.parametrize("kv", ["int8", "bf16"])
+def test_blocks_past_32_bit_offsets(lib, kv):
+    """Blocks beyond 4 GiB of a cache give what the same blocks of a small cache give."""
+    import torch
+    bs, hkv, d, S, n = 64, 8, 128, 3, 200
+    size = 1 if kv == "int8" else 2
+    nb = (1 << 32) // (bs * hkv * d * size) + 64
+    dt = torch.int8 if kv == "int8" else torch.bfloat16
+    big = [torch.empty((nb, bs, hkv, d), dtype=dt, device="cuda") for _ in range(2)]
+    far = torch.arange(nb - 16, nb - 16 + 4 * S, device="cuda").to(torch.int32).view(S, 4)
+    near = (far - (nb - 16)).contiguous()
+    torch.manual_seed(5)
+    small = [torch.randint(-127, 128, (16, bs, hkv, d), device="cuda").to(dt) for _ in range(2)]
+    for b, s in zip(big, small):
+        b[nb - 16:] = s
+    lens = torch.full((S,), n, dtype=torch.int32, device="cuda")
+    start = torch.arange(0, S * 30 + 1, 30, device="cuda").to(torch.int32)
+    q = torch.randn((S * 30, 16, d), device="cuda").to(torch.bfloat16)
+    res = []
+    for (k, v), bt, blocks in ((big, far, nb), (small, near, 16)):
+        kw = {}
+        if kv == "int8":
+            kw = {w: torch.zeros((blocks, hkv), device="cuda") for w in ("k_scale", "v_scale")}
+            torch.manual_seed(6)
+            for x in kw.values():
+                x[-16:] = torch.rand((16, hkv), device="cuda") + 0.5
+            torch.manual_seed(7)
+            x = torch.randn((S * 30, hkv, d), device="cuda") * 90
+            lib.quantize_and_cache(x, x, k, v, kw["k_scale"], kw["v_scale"], bt, lens, start, 30)
+        first = lens - 100
+        rows = torch.arange(0, S * 100 + 1, 100, device="cuda").to(torch.int32)
+        r = list(lib.gather_cache(k, v, bt, rows, S * 100, 100, first_pos=first, **kw))
+        r.append(lib.paged_attention_decode(q[:S].contiguous(), k, v, bt, lens, 0.01, n, window=90, **kw))
+        r.append(lib.paged_attention_prefill(q, start, k, v, bt, lens, 0.01, 30, n, window=90, **kw))
+        res.append(r)
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+
+
+def test_two_streams_at_once(lib):
+    """Calls on two streams, each with its own buffers, as one after the other."""
+    import torch
+    kv, bs, d, hkv = "fp8_e4m3", 16, 128, 4
+    case = PC.make(96, kv, [700, 333, 12], hkv, d, bs)
+    q = torch.randn((3, 16, d), device="cuda").to(torch.bfloat16)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    devs = [case.device() for _ in range(2)]
+    x = torch.randn((3, hkv, d), device="cuda") * 3
+    torch.cuda.synchronize()
+
+    def step(dev, st):
+        lib.quantize_and_cache(x, x, dev["k"], dev["v"], dev["ks"], dev["vs"], dev["tables"], dev["lens"],
+                               stream=st)
+        return lib.paged_attention_decode(q, dev["k"], dev["v"], dev["tables"], dev["lens"], 0.08, 700,
+                                          k_scale=dev["ks"], v_scale=dev["vs"], partition=64, stream=st)
+    ref = case.device()
+    torch.cuda.synchronize()
+    want = [step(ref, torch.cuda.current_stream()) for _ in range(8)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i in range(2):
+            got[i].append(step(devs[i], streams[i]))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for g in got for a, b in zip(g, want))

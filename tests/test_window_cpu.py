@@ -212,3 +212,41 @@ def prefill(lib, **kw):
     (dict(mq=0), OK)])
 def test_prefill_refusals(lib, kw, want):
     assert prefill(lib, **kw) == want
+
+
+def test_sizes_past_32_bits_are_refused(lib):
+    """Places within a block, and sequences times heads, are 32-bit in the kernels."""
+    assert quantize(lib, bs=4096, hkv=4096, d=1024, stride=4096, mb=4) == UNSUPPORTED
+    assert decode(lib, S=65535, hq=32767 * 2, hkv=32767) == UNSUPPORTED
+
+
+def test_status_word_is_checked(lib):
+    k8 = torch.zeros((4, 16, 2, 128), dtype=torch.int8)
+    sc, n = torch.ones((4, 2)), torch.ones(1, dtype=torch.int32)
+    bt, rows = torch.zeros((1, 2), dtype=torch.int32), torch.zeros((1, 2, 128))
+    start = torch.zeros(2, dtype=torch.int32)
+    q = torch.zeros((1, 4, 128), dtype=torch.bfloat16)
+    for bad in (torch.zeros(1, dtype=torch.uint8), torch.zeros(0, dtype=torch.int32)):
+        kw = dict(device_status=bad)
+        for call in (lambda: lib.quantize_and_cache(rows, rows, k8, k8, sc, sc, bt, n, **kw),
+                     lambda: lib.gather_cache(k8, k8, bt, start, 1, 1, k_scale=sc, v_scale=sc, **kw),
+                     lambda: lib.paged_attention_decode(q, k8, k8, bt, n, 0.1, 32, k_scale=sc, v_scale=sc,
+                                                        **kw),
+                     lambda: lib.paged_attention_prefill(q, start, k8, k8, bt, n, 0.1, 1, 32, k_scale=sc,
+                                                         v_scale=sc, **kw)):
+            with pytest.raises(ValueError, match="device_status"):
+                call()
+
+
+def test_calls_with_one_scale_per_head_refuse_block_scales(lib):
+    k8 = torch.zeros((4, 16, 2, 128), dtype=torch.int8)
+    sc, n = torch.ones((4, 2)), torch.ones(1, dtype=torch.int32)
+    bt, rows = torch.zeros((1, 2), dtype=torch.int32), torch.zeros((1, 2, 128))
+    slots = torch.zeros(1, dtype=torch.int64)
+    q, out = torch.zeros((1, 4, 128), dtype=torch.bfloat16), torch.zeros((1, 4, 128))
+    kw = dict(k_scale=sc, v_scale=sc)
+    for call in (lambda: lib.reshape_and_cache(rows, rows, slots, k8, k8, **kw),
+                 lambda: lib.paged_attention_decode_append(q, rows, rows, slots, k8, k8, bt, n, 0.1, 32, **kw),
+                 lambda: lib.paged_attention_decode_noalloc(q, k8, k8, bt, n, 0.1, 32, out, **kw)):
+        with pytest.raises(ValueError, match="per head"):
+            call()
