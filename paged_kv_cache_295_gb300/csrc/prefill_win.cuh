@@ -16,25 +16,25 @@
 // this one's softmax is still at its exponentials, and with P out of shared memory
 // the softmax stores it in two instructions.
 //
-// What bounds it (clock64 trace, two query tiles of 128 rows, steady state): the
-// softmax chain of a key tile (S load 370 cycles, max 270, exponentials 820, P
-// store, barriers), about 2,300 cycles for f32 outputs, next to about 2,100 of MMA
-// issue (16 QK at N = 64 and 16 PV).  So: bf16 outputs carry P as one bf16 value (8 PV
-// fewer; its 2^-8 is the size of the output's own rounding), waits read the timer only
-// when they do not succeed at once, and 8-bit tiles are widened by four warps of their
-// own, which halves the time a tile waits for its codes.
+// What bounds it (clock64 trace, two query tiles of 128 rows, steady state): the chain of a
+// key tile in the softmax warps - look at the barriers (over 100 cycles each, so two are
+// asked together), S load 110, maximum 260, exponentials 500, P store 200 to 600 - next to the
+// MMAs, which hold both issuers for 1,200 cycles a key tile; and, on 8-bit caches, instruction
+// fetch: the roles' loops together overrun the instruction cache.  So: the issuers' code is
+// uniform (pw_elect); bf16 outputs carry P as one bf16 value (8 PV fewer; its 2^-8 is the size
+// of the output's own rounding); a mask is built only for tiles that cut some row of the warp;
+// 8-bit tiles are widened by four warps of their own.
 //
 // 8-bit caches: the running reference m follows max(logit + log2 vs), so the weights
 // w = p vs that enter P V stay below 2^8 whatever the blocks' scales; l sums p itself.
 // Each row of q is scaled by a power of two into fp16's range; weights are one fp16
-// value (2^-11).  INT8 K codes enter as code + 1152; the offset is taken off each logit
-// (1152 times the row's sum of q), V codes are widened exactly.
+// value (2^-11).  Codes are widened to fp16 exactly.
 //
 // Measured, chunks of 512 tokens at contexts up to 4,096: 16 x 32 heads, bf16, window 1,024,
-// f32 output 207 us (580 TFLOP/s, 47 % of the tensor pipe's cycles); 16 x 8 heads GQA-4, fp8,
-// no window, bf16 output 326 (800 TFLOP/s, 35 %).  Three ragged chunks of up to 700 tokens, 8
-// heads GQA-8, window 4,096, bf16 output: 145 (870 TFLOP/s).  Every CTA has about 10 us of Q
-// loading, first copies and epilogue besides its key tiles, of which a window leaves few.
+// f32 output 196 us (615 TFLOP/s); 16 x 8 heads GQA-4, fp8, no window, bf16 output 284 (920
+// TFLOP/s).  Three ragged chunks of up to 700 tokens, 8 heads GQA-8, window 4,096, bf16
+// output: 123 (1,020 TFLOP/s).  Every CTA has about 10 us of setup, Q, first copies and epilogue
+// besides its key tiles, of which a window leaves few.
 //
 // Every wait is bounded (2 s) and gives up when another role has given up; TMEM is
 // released before the CTA exits.
@@ -121,6 +121,25 @@ __device__ __forceinline__ bool pw_wait(uint32_t bar, uint32_t parity, volatile 
   }
 }
 
+// The same for a whole warp.
+__device__ __forceinline__ bool pw_wait_all(uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  return __all_sync(0xffffffffu, pw_wait(bar, parity, abort_flag));
+}
+
+// Whether two phases are complete, asked together: a look at a barrier takes over 100 cycles,
+// however long ago its phase completed.
+__device__ __forceinline__ bool pw_test2(uint32_t bar_a, uint32_t par_a, uint32_t bar_b, uint32_t par_b) {
+  uint32_t a, b;
+  asm volatile(
+      "{\n .reg .pred p, q;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%2], %3;\n"
+      " mbarrier.test_wait.parity.shared::cta.b64 q, [%4], %5;\n"
+      " selp.u32 %0, 1, 0, p;\n selp.u32 %1, 1, 0, q;\n}\n"
+      : "=r"(a), "=r"(b)
+      : "r"(bar_a), "r"(par_a), "r"(bar_b), "r"(par_b)
+      : "memory");
+  return (a & b) != 0;
+}
+
 // 32 registers to 32 TMEM columns of this warp's lanes, without the wait.
 __device__ __forceinline__ void pw_st32(uint32_t taddr, const uint32_t* v) {
   asm volatile(
@@ -137,6 +156,15 @@ __device__ __forceinline__ void pw_st_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;\n" ::: "memory");
 }
 
+// One lane of the warp, the same each time; the compiler knows its code uniform, with `warp`,
+// the TMEM base and the lengths shuffled, and keeps descriptors and barriers in uniform
+// registers: the three measured cases took 192, 126 and 287 us, with `lane == 0` 209, 146 and 322.
+__device__ __forceinline__ bool pw_elect() {
+  uint32_t e = 0;
+  asm volatile("{\n .reg .b32 x;\n .reg .pred p;\n elect.sync x|p, 0xffffffff;\n @p mov.s32 %0, 1;\n}\n"
+               : "+r"(e));
+  return e != 0;
+}
 // Bits lo .. of a 64-key mask below key `n` of the tile.
 __device__ __forceinline__ uint64_t pw_below(int n) {
   return n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1ull);
@@ -173,7 +201,28 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
   const uint32_t sma = smem_u32(sm);
   volatile int* abort_flag = &abort_sh;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  if (tid == kThreads - 1) {   // while the others read the lengths
+    for (int st = 0; st < STAGES; ++st) {
+      mbar_init(smem_u32(&full[st]), C8 ? 2 : 1);     // K in the stage, key mask and scales
+      mbar_init(smem_u32(&full_v[st]), C8 ? 2 : 1);   // V in the stage
+      mbar_init(smem_u32(&empty[st]), 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(smem_u32(&s_full[t]), 1);
+      mbar_init(smem_u32(&s_free[t]), 4);
+      mbar_init(smem_u32(&q_ready[t]), 4);
+      mbar_init(smem_u32(&p_full[t]), 4);
+      mbar_init(smem_u32(&o_done[t]), 1);
+      mbar_init(smem_u32(&drain[t]), 1);
+    }
+    for (int i = 0; i < 2 * kPfRawBufs; ++i) {
+      mbar_init(smem_u32(&raw_full[i / kPfRawBufs][i % kPfRawBufs]), 1);
+      mbar_init(smem_u32(&raw_free[i / kPfRawBufs][i % kPfRawBufs]), 2);
+    }
+    abort_sh = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+  }
   // Work order (prefill_tc.cuh): KV heads fastest, then the pairs of a sequence, latest
   // first, then the sequences by context length, longest first.  The batch's lengths
   // and starts are read in one round trip.
@@ -211,6 +260,10 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
     q1 = __ldg(p.query_start + s + 1);
     ctx = __ldg(p.context_lens + s);
   }
+  s = __shfl_sync(0xffffffffu, s, 0);
+  q0 = __shfl_sync(0xffffffffu, q0, 0);
+  q1 = __shfl_sync(0xffffffffu, q1, 0);
+  ctx = __shfl_sync(0xffffffffu, ctx, 0);
   if (q0 < 0 || q1 < q0 || q1 > p.num_tokens) {   // rows outside q / out: touch nothing
     if (pair == 0 && g == 0 && tid == 0) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
     return;
@@ -270,27 +323,6 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
   };
   const int32_t* bt_row = p.block_tables + static_cast<int64_t>(s) * p.max_blocks_per_seq;
 
-  if (tid == 0) {
-    for (int st = 0; st < STAGES; ++st) {
-      mbar_init(smem_u32(&full[st]), C8 ? 2 : 1);     // K in the stage, key mask and scales
-      mbar_init(smem_u32(&full_v[st]), C8 ? 2 : 1);   // V in the stage
-      mbar_init(smem_u32(&empty[st]), 1);
-    }
-    for (int t = 0; t < 2; ++t) {
-      mbar_init(smem_u32(&s_full[t]), 1);
-      mbar_init(smem_u32(&s_free[t]), 4);
-      mbar_init(smem_u32(&q_ready[t]), 4);
-      mbar_init(smem_u32(&p_full[t]), 4);
-      mbar_init(smem_u32(&o_done[t]), 1);
-      mbar_init(smem_u32(&drain[t]), 1);
-    }
-    for (int i = 0; i < 2 * kPfRawBufs; ++i) {
-      mbar_init(smem_u32(&raw_full[i / kPfRawBufs][i % kPfRawBufs]), 1);
-      mbar_init(smem_u32(&raw_free[i / kPfRawBufs][i % kPfRawBufs]), 2);
-    }
-    abort_sh = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
-  }
   if (warp == 0) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;\n" ::"r"(
                      smem_u32(&tmem_base_sh))
@@ -302,10 +334,17 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
   __syncthreads();
   tc_fence_after();
   // TMEM: query tile t's P at columns 256t + [0, 64), S at 256t + 64, O at 256t + 128
-  const uint32_t tm = tmem_base_sh;
+  const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base_sh, 0);
 
   // 8-bit caches launch 512 threads of 128 registers; the softmax warps take 168 and the
   // others 88 (256 x 168 + 256 x 88 = 512 x 128).
+  // The issuing roles: one lane's code on bf16 caches (123 us on the three ragged chunks named
+  // above, 130 as a whole warp's), a whole warp's on 8-bit ones (284 us on the fp8 chunks, 292
+  // as one lane's).
+  auto issuer = [&] { return !C8 || pw_elect(); };
+  auto issuer_wait = [&](uint32_t bar, uint32_t parity) {
+    return C8 ? pw_wait_all(bar, parity, abort_flag) : pw_wait(bar, parity, abort_flag);
+  };
   if (warp >= 8) {
   if constexpr (C8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
   if (warp == 8 || warp == 11) {
@@ -336,9 +375,7 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
         const uint32_t valid = __ballot_sync(0xffffffffu, blk >= 0) & 0xFFFFu;   // bit i: box i
         report(blk);
         if (j >= STAGES) {
-          bool ok = true;
-          if (lane == 0) ok = pw_wait(smem_u32(&empty[st]), ((j / STAGES) - 1) & 1, abort_flag);
-          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+          if (!pw_wait_all(smem_u32(&empty[st]), ((j / STAGES) - 1) & 1, abort_flag)) break;
         }
         const uint32_t bar = smem_u32(is_v ? &full_v[st] : &full[st]);
         if (lane == 0) {
@@ -388,10 +425,8 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
         report(blk);
         const PfScale e = {fabsf(p.qk_scale_log2) * ks, vs, __log2f(vs), 0.f};
         if (j >= kPfRawBufs) {
-          bool ok = true;
-          if (lane == 0)
-            ok = pw_wait(smem_u32(&raw_free[is_v ? 1 : 0][rb]), ((j / kPfRawBufs) - 1) & 1, abort_flag);
-          if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+          if (!pw_wait_all(smem_u32(&raw_free[is_v ? 1 : 0][rb]), ((j / kPfRawBufs) - 1) & 1, abort_flag))
+            break;
         }
         if (!is_v && lane < nbox)
           for (int u = 0; u < box_rows / 8; ++u) raw_scale[rb][lane * (box_rows / 8) + u] = e;
@@ -412,30 +447,32 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
     // ---------------------------- QK issuer ------------------------------------
     // Key tiles in order, query tile A then B: once the stage has landed and the S
     // columns are free (the softmax has loaded the previous S).
-    if (lane == 0) {
+    if (C8 || pw_elect()) {
       const uint32_t idesc_qk = tc_idesc(kPfRows, kPfKeys, false, false, !C8);
       const uint64_t qd[2] = {tc_desc(sma, 0, 1024), tc_desc(sma + LY::kQ, 0, 1024)};
       for (int j = 0; j < ntiles; ++j) {
-        if (!pw_wait(smem_u32(&full[j % STAGES]), (j / STAGES) & 1, abort_flag)) break;
+        if (!issuer_wait(smem_u32(&full[j % STAGES]), (j / STAGES) & 1)) break;
         const uint64_t kd = tc_desc(sma + kRing + (j % STAGES) * kStage, 0, 1024);
         bool ok = true;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (j >= (t == 0 ? nt_a : nt_b) || ls.skips(t, j)) continue;
           const int jt = ls.count(t, j);   // entries this query tile has done
-          ok = jt == 0 ? pw_wait(smem_u32(&q_ready[t]), 0, abort_flag)
-                       : pw_wait(smem_u32(&s_free[t]), (jt - 1) & 1, abort_flag);
+          ok = jt == 0 ? issuer_wait(smem_u32(&q_ready[t]), 0)
+                       : issuer_wait(smem_u32(&s_free[t]), (jt - 1) & 1);
           if (!ok) break;
           tc_fence_after();
+          if (issuer()) {
 #pragma unroll
-          for (int ks = 0; ks < kPfD / 16; ++ks)   // 16 dims: half ks / 4, 32 bytes each
-            tc_mma(tm + 256 * t + kPfKeys, qd[t] + (((ks >> 2) * LY::kQHalf + (ks & 3) * 32) >> 4),
-                   kd + (((ks >> 2) * kKVHalf + (ks & 3) * 32) >> 4), idesc_qk, ks > 0);
-          tc_commit(smem_u32(&s_full[t]));
+            for (int ks = 0; ks < kPfD / 16; ++ks)   // 16 dims: half ks / 4, 32 bytes each
+              tc_mma(tm + 256 * t + kPfKeys, qd[t] + (((ks >> 2) * LY::kQHalf + (ks & 3) * 32) >> 4),
+                     kd + (((ks >> 2) * kKVHalf + (ks & 3) * 32) >> 4), idesc_qk, ks > 0);
+            tc_commit(smem_u32(&s_full[t]));
+          }
         }
         if (!ok) break;
       }
-      tc_commit(smem_u32(&drain[0]));   // its MMAs finish before TMEM is released
+      if (issuer()) tc_commit(smem_u32(&drain[0]));   // its MMAs finish before TMEM is released
       volatile int no_abort = 0;
       pw_wait(smem_u32(&drain[0]), 0, &no_abort);
     }
@@ -443,11 +480,11 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
     // ---------------------------- PV issuer ------------------------------------
     // Query tile A then B of each key tile, once its P is written; then the stage is
     // released (its QK finished before its P could be written).
-    if (lane == 0) {
+    if (C8 || pw_elect()) {
       const uint32_t idesc_pv = tc_idesc(kPfRows, kPfD, false, true, !C8);
       const bool lo = !C8 && !wp.out_bf16;
       for (int j = 0; j < ntiles; ++j) {
-        if (!pw_wait(smem_u32(&full_v[j % STAGES]), (j / STAGES) & 1, abort_flag)) break;
+        if (!issuer_wait(smem_u32(&full_v[j % STAGES]), (j / STAGES) & 1)) break;
         const uint64_t vd =
             tc_desc(sma + kRing + (j % STAGES) * kStage + 2 * kKVHalf, kKVHalf, 1024);
         bool ok = true;
@@ -455,36 +492,43 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
         for (int t = 0; t < 2; ++t) {
           if (j >= (t == 0 ? nt_a : nt_b) || ls.skips(t, j)) continue;
           const int jt = ls.count(t, j);
-          ok = pw_wait(smem_u32(&p_full[t]), jt & 1, abort_flag);
+          ok = issuer_wait(smem_u32(&p_full[t]), jt & 1);
           if (!ok) break;
           tc_fence_after();
           const uint32_t dO = tm + 256 * t + 2 * kPfKeys;
+          if (issuer()) {
 #pragma unroll
-          for (int kk = 0; kk < kPfKeys / 16; ++kk) {
-            const uint64_t bdesc = vd + ((kk * 2048) >> 4);
-            tc_mma_ts(dO, tm + 256 * t + 8 * kk, bdesc, idesc_pv, (jt > 0 || kk > 0));
-            if (lo) tc_mma_ts(dO, tm + 256 * t + 32 + 8 * kk, bdesc, idesc_pv, 1);
+            for (int kk = 0; kk < kPfKeys / 16; ++kk) {
+              const uint64_t bdesc = vd + ((kk * 2048) >> 4);
+              tc_mma_ts(dO, tm + 256 * t + 8 * kk, bdesc, idesc_pv, (jt > 0 || kk > 0));
+              if (lo) tc_mma_ts(dO, tm + 256 * t + 32 + 8 * kk, bdesc, idesc_pv, 1);
+            }
+            tc_commit(smem_u32(&o_done[t]));
           }
-          tc_commit(smem_u32(&o_done[t]));
         }
         if (!ok) break;
-        tc_commit(smem_u32(&empty[j % STAGES]));
+        if (issuer()) tc_commit(smem_u32(&empty[j % STAGES]));
       }
-      tc_commit(smem_u32(&drain[1]));
+      if (issuer()) tc_commit(smem_u32(&drain[1]));
       volatile int no_abort = 0;
       pw_wait(smem_u32(&drain[1]), 0, &no_abort);
     }
   } else if (C8 && warp >= 12) {
     // ---------------- widening: warps 12, 13 K; 14, 15 V; 32 rows each ----------------
-    // A lane widens one row's 128 codes to fp16 (exact for E4M3 and, in V, INT8) into
-    // the stage's two swizzled halves.  Lane = row and one 16-byte chunk per step spread
-    // each step's loads and stores evenly over the banks; all loads precede the stores.
+    // A lane widens one row's 128 codes to fp16 (exactly) into the stage's two swizzled
+    // halves.  Lane = row and one 16-byte chunk per step spread each step's loads and stores
+    // evenly over the banks; loads precede the stores.
     const bool is_v = warp >= 14;
     const int r0 = (warp & 1) * 32;
     const uint8_t* raw = sm + LY::raw() + (is_v ? kPfRawBufs * kRawTile : 0) + (r0 + lane) * 128;
-    uint32_t off[8];   // where 16-byte unit u sits in a row = lane (mod 8)
+    // Units per pass.  The roles' loops together overrun the instruction cache, which slows
+    // the softmax warps: INT8, whose widening is the longer code, takes 1,300 ns a key tile with
+    // one unit a pass and 1,780 with eight; E4M3 1,245 and 1,200.
+    constexpr int kStep = I8 ? 1 : 8;
+    uint32_t offs[8];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) off[u] = static_cast<uint32_t>((u ^ (lane & 7)) << 4);
+    for (int u = 0; u < 8; ++u) offs[u] = static_cast<uint32_t>((u ^ (lane & 7)) << 4);
+    auto off = [&](int u) -> uint32_t { return kStep == 8 ? offs[u & 7] : static_cast<uint32_t>((u ^ (lane & 7)) << 4); };
     for (int j = 0; j < ntiles; ++j) {
       const int st = j % STAGES, rb = j % kPfRawBufs;
       bool ok = pw_wait(smem_u32(&raw_full[is_v ? 1 : 0][rb]), (j / kPfRawBufs) & 1, abort_flag);
@@ -493,32 +537,35 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
       if (!__all_sync(0xffffffffu, ok)) break;
       const uint8_t* src = raw + rb * kRawTile;
       uint8_t* dst = sm + kRing + st * kStage + (is_v ? 2 * kKVHalf : 0) + (r0 + lane) * 128;
-      uint4 cs[8];
-#pragma unroll
-      for (int u = 0; u < 8; ++u) cs[u] = *reinterpret_cast<const uint4*>(src + off[u]);
       if (warp == 12) {
         if (lane < 8) key_scale[st][lane] = raw_scale[rb][lane];
         if (lane == 0) key_mask[st] = raw_mask[rb];
       }
+#pragma unroll 1
+      for (int u0 = 0; u0 < 8; u0 += kStep) {
+        uint4 cs[kStep];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        uint32_t h[8];
-        const uint32_t w[4] = {cs[u].x, cs[u].y, cs[u].z, cs[u].w};
+        for (int v = 0; v < kStep; ++v) cs[v] = *reinterpret_cast<const uint4*>(src + off(u0 + v));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          if constexpr (I8)
-            s8x4_to_f16x2x2_biased(w[e], h[2 * e], h[2 * e + 1]);
-          else
-            e4m3x4_to_f16x2x2(w[e], h[2 * e], h[2 * e + 1]);
+        for (int v = 0; v < kStep; ++v) {
+          uint32_t h[8];
+          const uint32_t w[4] = {cs[v].x, cs[v].y, cs[v].z, cs[v].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (I8)
+              s8x4_to_f16x2x2_biased(w[e], h[2 * e], h[2 * e + 1]);
+            else
+              e4m3x4_to_f16x2x2(w[e], h[2 * e], h[2 * e + 1]);
+          }
+          if constexpr (I8) {   // code + 1152 - 1152: the code, exactly
+#pragma unroll
+            for (int e = 0; e < 8; ++e) h[e] = hsub2_u32(h[e], 0x64806480u);
+          }
+          uint8_t* half = dst + ((u0 + v) >> 2) * kKVHalf;
+          const int uu = 2 * ((u0 + v) & 3);
+          *reinterpret_cast<uint4*>(half + off(uu)) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(half + off(uu + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
         }
-        if (I8 && is_v) {   // code + 1152 - 1152: the code, exactly
-#pragma unroll
-          for (int e = 0; e < 8; ++e) h[e] = hsub2_u32(h[e], 0x64806480u);
-        }
-        uint8_t* half = dst + (u >> 2) * kKVHalf;
-        const int uu = 2 * (u & 3);
-        *reinterpret_cast<uint4*>(half + off[uu]) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(half + off[uu + 1]) = make_uint4(h[4], h[5], h[6], h[7]);
       }
       fence_proxy_async();   // the stage's writes before the MMAs' reads, the raw buffer's
       __syncwarp();          // reads before the next copy into it
@@ -546,7 +593,6 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
       return (static_cast<int64_t>(q0 + tok) * p.num_q_heads + g * G + row - tk * G) * kPfD;
     };
     float q_unscale = 1.f;   // 8-bit caches: the row of q went to fp16 times 1 / q_unscale
-    float q_offset = 0.f;    // INT8: 1152 * the row's sum of that
     {
       // The warp's 32 rows of Q_t into shared memory (two halves of 64 dims, K-major, 128B
       // swizzle).  Pass i takes rows 2i and 2i + 1, 16 lanes x 16 bytes each, so that every
@@ -579,25 +625,12 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
           const int ex = mb >= 0x0080u ? static_cast<int>(mb >> 7) - 127 : 0;
           const int qsh = min(max(14 - ex, -126), 126);
           const float qmul = __uint_as_float(static_cast<uint32_t>(127 + qsh) << 23);
-          float qs = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            x[e] = pack_f16(qmul * bf16_lo(x[e]), qmul * bf16_hi(x[e]));
-            if constexpr (I8) {   // q as the MMA sees it
-              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[e]));
-              qs += f.x + f.y;
-            }
-          }
+          for (int e = 0; e < 4; ++e) x[e] = pack_f16(qmul * bf16_lo(x[e]), qmul * bf16_hi(x[e]));
           v[i] = make_uint4(x[0], x[1], x[2], x[3]);
-          // thread `lane` keeps row w0 + lane's factors: pass lane / 2, half-warp lane % 2
+          // thread `lane` keeps row w0 + lane's factor: pass lane / 2, half-warp lane % 2
           const int sh = __shfl_sync(0xffffffffu, qsh, (lane & 1) * 16);
           if (i == (lane >> 1)) q_unscale = __uint_as_float(static_cast<uint32_t>(127 - sh) << 23);
-          if constexpr (I8) {
-#pragma unroll
-            for (int o = 1; o < 16; o <<= 1) qs += __shfl_xor_sync(0xffffffffu, qs, o);
-            const float mine = __shfl_sync(0xffffffffu, qs, (lane & 1) * 16);
-            if (i == (lane >> 1)) q_offset = 1152.f * mine;
-          }
         }
         *reinterpret_cast<uint4*>(qb + (ch >> 3) * LY::kQHalf + swz(w0 + 2 * i + (lane >> 4), ch & 7)) =
             v[i];
@@ -610,40 +643,58 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
     const int qpos = ctx - n + tok0 + t * TQ + row_token(r);   // this row's position
     const int last = p.causal ? qpos : ctx - 1;                // last key it sees
     const int row_low = wp.window > 0 ? qpos - wp.window + 1 : 0;   // first key of its window
+    // over the warp's rows; rows past the chunk do not count (their outputs are not stored)
+    const int last_min = __reduce_min_sync(0xffffffffu, row_ok ? last : INT32_MAX - 1);
+    const int low_max = __reduce_max_sync(0xffffffffu, row_ok ? row_low : INT32_MIN);
     // Logit factors are kept positive (a zero one is raised to the smallest normal), so that
     // a masked -inf stays -inf under them.
     constexpr float kTiny = 1.17549435e-38f;
     const float sl2 = fmaxf(fabsf(p.qk_scale_log2), kTiny);    // 16-bit caches
     float m = -CUDART_INF_F, l = 0.f;                          // m in log2 units
     bool alive = true;
+    bool s_there = false;   // warp-uniform: S and the stage's mask were seen to be there
     for (int j = 0; j < my_nt && alive; ++j) {
       if (ls.skips(t, j)) continue;
       const int jt = ls.count(t, j), st = j % STAGES;
       const int k0 = ls.key0(j);
       // S ready implies that the stage's K landed; waiting on the stage's barrier as well
       // makes the producer's key mask and scales for it visible here.
-      if (!pw_wait(smem_u32(&s_full[t]), jt & 1, abort_flag) ||
-          !pw_wait(smem_u32(&full[st]), (j / STAGES) & 1, abort_flag))
-        alive = false;
-      if (!__all_sync(0xffffffffu, alive)) break;
+      if (!s_there) {
+        if (!pw_wait(smem_u32(&s_full[t]), jt & 1, abort_flag) ||
+            !pw_wait(smem_u32(&full[st]), (j / STAGES) & 1, abort_flag))
+          alive = false;
+        if (!__all_sync(0xffffffffu, alive)) break;
+      }
       tc_fence_after();
+      // the stage's logit factors and V scales: loads from shared memory take hundreds of
+      // cycles beside the MMAs' and the widening warps', so all are asked for here at once
+      float fk[C8 ? 8 : 1], vk[C8 ? 8 : 1], lk[C8 ? 8 : 1];
+      if constexpr (C8) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const float4 e = *reinterpret_cast<const float4*>(&key_scale[st][u]);
+          fk[u] = fmaxf(e.x * q_unscale, kTiny);
+          vk[u] = e.y;
+          lk[u] = e.z;
+        }
+      }
+      const uint64_t vmask = key_mask[st];
       float sv[kPfKeys];
       pf_ld64(tS, sv);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&s_free[t]));
       // keys the row sees: with cache data, up to `last`, in the window or among the sinks
-      const uint64_t vmask = key_mask[st];
-      uint64_t rmask = vmask & pw_below(last - k0 + 1) &
-                       (~pw_below(row_low - k0) | pw_below(wp.sinks - k0));
-      if (!row_ok) rmask = 0ull;
-      if (!__all_sync(0xffffffffu, rmask == ~0ull)) {
+      if (vmask != ~0ull || k0 + kPfKeys > last_min + 1 ||
+          (k0 < low_max && k0 + kPfKeys > wp.sinks)) {   // not all of them for all of the warp's rows
+        uint64_t rmask = vmask & pw_below(last - k0 + 1) &
+                         (~pw_below(row_low - k0) | pw_below(wp.sinks - k0));
+        if (!row_ok) rmask = 0ull;
         const uint32_t mlo = static_cast<uint32_t>(rmask), mhi = static_cast<uint32_t>(rmask >> 32);
 #pragma unroll
         for (int c = 0; c < kPfKeys; ++c)
           if (!(((c < 32 ? mlo : mhi) >> (c & 31)) & 1u)) sv[c] = -CUDART_INF_F;
       }
-      const PfScale* sc = key_scale[C8 ? st : 0];
       float mt = -CUDART_INF_F;   // the tile's largest logit (8-bit caches: + log2 vs)
       if constexpr (C8) {
 #pragma unroll
@@ -651,7 +702,7 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
           const float a = pf_max3(sv[8 * u], sv[8 * u + 1], sv[8 * u + 2]);
           const float b = pf_max3(sv[8 * u + 3], sv[8 * u + 4], sv[8 * u + 5]);
           const float c = fmaxf(sv[8 * u + 6], sv[8 * u + 7]);
-          mt = fmaxf(mt, fmaf(pf_max3(a, b, c) - q_offset, fmaxf(sc[u].kf * q_unscale, kTiny), sc[u].lv));
+          mt = fmaxf(mt, fmaf(pf_max3(a, b, c), fk[u], lk[u]));
         }
       } else {
         float ma = sv[0], mb = sv[1];
@@ -677,13 +728,12 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
       float2 ls2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const float f = C8 ? fmaxf(sc[u].kf * q_unscale, kTiny) : sl2;
-        const float nm = I8 ? fmaf(-q_offset, f, -mu) : -mu;
-        const float vs = C8 ? sc[u].vs : 1.f;
+        const float f = C8 ? fk[C8 ? u : 0] : sl2;
+        const float vs = C8 ? vk[C8 ? u : 0] : 1.f;
 #pragma unroll
         for (int c = 8 * u; c < 8 * u + 8; c += 2) {
           const float2 x = __ffma2_rn(make_float2(sv[c], sv[c + 1]), make_float2(f, f),
-                                      make_float2(nm, nm));
+                                      make_float2(-mu, -mu));
           float2 y = make_float2(pf_ex2(x.x), pf_ex2(x.y));   // 2^-inf = 0 for masked keys
           ls2[(c >> 1) & 1] = __fadd2_rn(ls2[(c >> 1) & 1], y);
           if constexpr (C8) {
@@ -736,6 +786,10 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
         }
         fence_proxy_async();
       }
+      s_there = __all_sync(0xffffffffu,
+                           !ls.skips(t, j + 1) &&
+                               pw_test2(smem_u32(&s_full[t]), (jt + 1) & 1,
+                                        smem_u32(&full[(j + 1) % STAGES]), ((j + 1) / STAGES) & 1));
       pw_st_wait();
       tc_fence_before();
       __syncwarp();
