@@ -175,7 +175,8 @@ __global__ void __launch_bounds__(NW * 32)
   __shared__ __align__(8) uint64_t bars[NW][STAGES];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // shuffled, so that the compiler knows it uniform (window 1,024, 64 x 8 heads: 54.5 -> 53.5 us)
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int gid = lane >> 2, tig = lane & 3;
   const int s = blockIdx.z, part = blockIdx.y;
   // Groups of 9 to 16 heads run as two CTAs per KV head, the first with the

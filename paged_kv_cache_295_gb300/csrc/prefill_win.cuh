@@ -522,13 +522,10 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
     const int r0 = (warp & 1) * 32;
     const uint8_t* raw = sm + LY::raw() + (is_v ? kPfRawBufs * kRawTile : 0) + (r0 + lane) * 128;
     // Units per pass.  The roles' loops together overrun the instruction cache, which slows
-    // the softmax warps: INT8, whose widening is the longer code, takes 1,300 ns a key tile with
-    // one unit a pass and 1,780 with eight; E4M3 1,245 and 1,200.
-    constexpr int kStep = I8 ? 1 : 8;
-    uint32_t offs[8];
-#pragma unroll
-    for (int u = 0; u < 8; ++u) offs[u] = static_cast<uint32_t>((u ^ (lane & 7)) << 4);
-    auto off = [&](int u) -> uint32_t { return kStep == 8 ? offs[u & 7] : static_cast<uint32_t>((u ^ (lane & 7)) << 4); };
+    // the softmax warps: INT8, whose widening is the longer code, took 1,300 ns a key tile with
+    // one or two units a pass and 1,780 with all eight at once.
+    constexpr int kStep = 2;
+    auto off = [&](int u) { return (u ^ (lane & 7)) << 4; };   // 16-byte unit u in a row = lane (mod 8)
     for (int j = 0; j < ntiles; ++j) {
       const int st = j % STAGES, rb = j % kPfRawBufs;
       bool ok = pw_wait(smem_u32(&raw_full[is_v ? 1 : 0][rb]), (j / kPfRawBufs) & 1, abort_flag);
