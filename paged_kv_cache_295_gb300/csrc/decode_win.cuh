@@ -34,7 +34,7 @@
 // table entry and scales, each load behind the one before: as long as about 110 tokens) on
 // windows of about 1,000.  Measured: 32 sequences x 32 heads, fp8, contexts up to 4,096:
 // 100 us (89 at the copy rate); 8 x 8 heads GQA-4, int8, 32K to 128K: 202 (189); 64 x 8
-// heads GQA-8, bf16, window 1,024 and 4 sinks: 55 (40); 4 x 8 heads, window 256: 7.
+// heads GQA-8, bf16, window 1,024 and 4 sinks: 54 (40); 4 x 8 heads, window 256: 7.
 #pragma once
 
 #include "decode_mma2.cuh"

@@ -31,7 +31,7 @@
 // value (2^-11).  Codes are widened to fp16 exactly.
 //
 // Measured, chunks of 512 tokens at contexts up to 4,096: 16 x 32 heads, bf16, window 1,024,
-// f32 output 196 us (615 TFLOP/s); 16 x 8 heads GQA-4, fp8, no window, bf16 output 284 (920
+// f32 output 197 us (613 TFLOP/s); 16 x 8 heads GQA-4, fp8, no window, bf16 output 283 (923
 // TFLOP/s).  Three ragged chunks of up to 700 tokens, 8 heads GQA-8, window 4,096, bf16
 // output: 123 (1,020 TFLOP/s).  Every CTA has about 10 us of setup, Q, first copies and epilogue
 // besides its key tiles, of which a window leaves few.
