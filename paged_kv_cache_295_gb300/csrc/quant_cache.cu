@@ -25,7 +25,7 @@
 #include "common.cuh"
 #include "quant.cuh"
 
-// Codes and scales that an earlier kernel may have written are read past L1 (__ldcg):
+// Rows, codes and scales that an earlier kernel may have written are read past L1 (__ldcg):
 // with programmatic launches a kernel's CTAs share an SM with the writer's, whose own
 // loads may have left older lines there.
 
@@ -102,7 +102,7 @@ struct Vec8<__nv_bfloat16> {
   static constexpr int kHeld = 8;
   uint32_t w[4];
   __device__ __forceinline__ void load(const __nv_bfloat16* p) {
-    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+    const uint4 v = __ldcg(reinterpret_cast<const uint4*>(p));
     w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
   }
   __device__ __forceinline__ void zero() { w[0] = w[1] = w[2] = w[3] = 0; }
@@ -129,8 +129,8 @@ struct Vec8<float> {
   static constexpr int kHeld = 4;
   uint32_t w[8];
   __device__ __forceinline__ void load(const float* p) {
-    const uint4 a = __ldg(reinterpret_cast<const uint4*>(p));
-    const uint4 b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
+    const uint4 a = __ldcg(reinterpret_cast<const uint4*>(p));
+    const uint4 b = __ldcg(reinterpret_cast<const uint4*>(p) + 1);
     w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
     w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
   }
