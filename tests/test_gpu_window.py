@@ -47,6 +47,16 @@ def test_decode_clusters(lib, kv, d):
     check_decode(lib, case, 6, 19, out="bf16", window=200, sinks=30, partition=64)
 
 
+def test_decode_over_one_wave(lib):
+    """480 sequences and heads of about 1,100 visible tokens: the automatic partition takes
+    more than one wave of CTAs, with a last partition shorter than the others."""
+    rng = np.random.default_rng(3)
+    case = PC.make(23, "bf16", [int(n) for n in rng.integers(900, 1400, 60)], 8, 64, 16)
+    assert lib.workspace_bytes(60, 16, 8, 64, 1400, 0, window=1024, sinks=4) > 0
+    check_decode(lib, case, 16, 24, out="f32", window=1024, sinks=4)
+    check_decode(lib, case, 16, 25, out="bf16")
+
+
 @pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3", "int8"])
 def test_hidden_blocks_are_not_read(lib, kv):
     """Table entries of blocks without a visible token may be anything, and hidden rows NaN."""
@@ -269,3 +279,26 @@ def test_prefill_equals_decode_rows(lib):
             # both round to bf16 (two half steps); weights: one bf16 in prefill, else fp16 or finer
             A = max(float(np.abs(case.values(i)[1]).max()) for i in range(3))
             assert np.abs(a - b).max() <= (2 * 2.0 ** -8 + 2 * 2.0 ** -8 + 2 * 2.0 ** -11) * A
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3", "int8"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_prefill_long(lib, kv, out):
+    """Many key tiles per CTA and more CTAs than SMs, whole and cut tiles in turn."""
+    case = PC.make(31, kv, [2500, 1111, 3000], 4, 128, 32)
+    new = [700, 1111, 65]
+    check_prefill(lib, case, new, 16, 32, out=out, window=1500, sinks=200)
+    check_prefill(lib, case, new, 16, 33, out=out, window=4000 if kv == "bf16" else 0)
+
+
+def test_prefill_repeats_itself(lib):
+    """The same call again and again, beside others: the same bits."""
+    import torch
+    for kv in ("bf16", "int8"):
+        case = PC.make(41, kv, [900, 500, 77], 2, 128, 16)
+        new = [900, 123, 77]
+        q = PC.bf16_bits(np.random.default_rng(5).standard_normal((sum(new), 8, 128)))
+        first = prefill(lib, case, new, q, 0.09, window=200, sinks=5)
+        for _ in range(5):
+            prefill(lib, case, new, q, 0.09, out="bf16", window=600)
+            assert np.array_equal(prefill(lib, case, new, q, 0.09, window=200, sinks=5), first)
