@@ -513,12 +513,12 @@ def _per_head(k_scale, v_scale, where):
         raise ValueError(f"{where} takes one scale per head, not scales per block")
 
 
-def _windowed(out, out_dtype, k_scale, window, sinks) -> bool:
+def _windowed(out, out_dtype, k_scale, v_scale, window, sinks) -> bool:
     """Whether a call needs the form with a window, scales per block or another output type."""
     if window or sinks:
         return True
     f32 = _torch().float32
-    return bool(_block_scales(k_scale)
+    return bool(_block_scales(k_scale) or _block_scales(v_scale)
                 or (out is not None and out.dtype != f32)
                 or (out_dtype is not None and out_dtype != f32))
 
@@ -583,7 +583,7 @@ def paged_attention_decode(q, k_cache, v_cache, block_tables, context_lens, scal
     ``paged_attention_decode_window`` (whose shapes are narrower; its workspace is
     ``workspace_bytes(..., window=window, sinks=sinks)``).
     """
-    if _windowed(out, out_dtype, k_scale, window, sinks):
+    if _windowed(out, out_dtype, k_scale, v_scale, window, sinks):
         return _decode_window(q, k_cache, v_cache, block_tables, context_lens, scale,
                               max_context_len, out, k_scale, v_scale, workspace, partition,
                               device_status, stream, window, sinks, out_dtype)
@@ -668,7 +668,7 @@ def paged_attention_prefill(q, query_start, k_cache, v_cache, block_tables, cont
 
     ``window``, ``sinks``, scales ``[NB, >= Hkv]`` per block and ``out_dtype`` as in
     ``paged_attention_decode``; any of them takes ``paged_attention_prefill_window``."""
-    if _windowed(out, out_dtype, k_scale, window, sinks):
+    if _windowed(out, out_dtype, k_scale, v_scale, window, sinks):
         return _prefill_window(q, query_start, k_cache, v_cache, block_tables, context_lens, scale,
                                max_query_len, max_context_len, causal, out, k_scale, v_scale,
                                device_status, stream, window, sinks, out_dtype)

@@ -250,3 +250,18 @@ def test_calls_with_one_scale_per_head_refuse_block_scales(lib):
                  lambda: lib.paged_attention_decode_noalloc(q, k8, k8, bt, n, 0.1, 32, out, **kw)):
         with pytest.raises(ValueError, match="per head"):
             call()
+
+
+@pytest.mark.parametrize("per_block", ["k_scale", "v_scale"])
+def test_scales_of_two_forms_are_refused(lib, per_block):
+    """One scale per head beside scales per block: refused whichever of the two it is."""
+    k8 = torch.zeros((4, 16, 2, 128), dtype=torch.int8)
+    n, bt = torch.ones(1, dtype=torch.int32), torch.zeros((1, 2), dtype=torch.int32)
+    start = torch.tensor([0, 1], dtype=torch.int32)
+    q = torch.zeros((1, 4, 128), dtype=torch.bfloat16)
+    kw = {"k_scale": torch.ones(2), "v_scale": torch.ones(2), per_block: torch.ones((4, 2))}
+    for call in (lambda **m: lib.paged_attention_decode(q, k8, k8, bt, n, 0.1, 32, **kw, **m),
+                 lambda **m: lib.paged_attention_prefill(q, start, k8, k8, bt, n, 0.1, 1, 32, **kw, **m)):
+        for more in ({}, {"window": 8}):
+            with pytest.raises(ValueError, match="k_scale and v_scale must be"):
+                call(**more)
