@@ -57,6 +57,9 @@ inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, siz
 // Number of SMs of the current device, cached per device.
 int device_sm_count();
 
+// Bytes a test makes later launches wait for in vain (pkv_test_decode_stall); 0 otherwise.
+uint32_t test_stall_bytes();
+
 // Opts kernel `kern` into `bytes` of dynamic shared memory on the current
 // device.  The attribute belongs to the function in each device's context, so
 // the largest value set so far is remembered per (kernel, device).

@@ -38,9 +38,7 @@ bool is_pow2(int64_t x) { return x > 0 && (x & (x - 1)) == 0; }
 // setting with one relaxed atomic load.
 std::atomic<int32_t> g_forced_kernel{PKV_DECODE_KERNEL_AUTO};
 int32_t forced_kernel() { return g_forced_kernel.load(std::memory_order_relaxed); }
-// Bytes a test makes the next transposed-kernel launches wait for in vain
-// (pkv_test_decode_stall); 0 otherwise.
-std::atomic<uint32_t> g_stall_bytes{0};
+std::atomic<uint32_t> g_stall_bytes{0};   // test_stall_bytes()
 
 int log2i(int64_t x) {
   int r = 0;
@@ -141,6 +139,8 @@ LaunchFn pick(int32_t kv_dtype, int D, int G) {
 }
 
 }  // namespace
+
+uint32_t test_stall_bytes() { return g_stall_bytes.load(std::memory_order_relaxed); }
 }  // namespace pkv
 
 extern "C" int32_t paged_attention_partition_tokens(int32_t num_seqs, int32_t num_q_heads,
@@ -257,7 +257,7 @@ pkv_status decode_impl(const void* q, const void* k_cache, const void* v_cache,
   p.max_parts = parts;
   p.q_is_bf16 = q_dtype == PKV_BF16;
   p.qk_scale_log2 = scale * 1.4426950408889634f;
-  p.test_stall_bytes = g_stall_bytes.load(std::memory_order_relaxed);
+  p.test_stall_bytes = test_stall_bytes();
   a.num_seqs = num_seqs;
   a.stream = reinterpret_cast<cudaStream_t>(stream);
   if (fa) {

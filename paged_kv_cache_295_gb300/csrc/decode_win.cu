@@ -206,6 +206,7 @@ extern "C" pkv_status paged_attention_decode_window(
   p.max_parts = static_cast<int32_t>(parts);
   p.q_is_bf16 = q_dtype == PKV_BF16;
   p.qk_scale_log2 = scale * 1.4426950408889634f;
+  p.test_stall_bytes = test_stall_bytes();
   const int chl = codes ? 5 : 4;
   a.w.out = out;
   a.w.scale_stride = codes ? scale_stride : 0;

@@ -281,6 +281,10 @@ __global__ void __launch_bounds__(NW * 32)
 
   const uint32_t k_swz0 = swz(gid, 2 * tig), k_swz1 = swz(gid, 2 * tig + 1);
   const uint32_t v_swz0 = swz(2 * tig, gid), v_swz1 = swz(2 * tig + 1, gid);
+  // Tests of the bounded waits: CTA (0, 0, 0)'s first phase expects bytes that no copy brings.
+  if (p.test_stall_bytes != 0 && threadIdx.x == 0 && blockIdx.x + blockIdx.y + blockIdx.z == 0)
+    mbar_expect_tx(smem_u32(&bars[0][0]), p.test_stall_bytes);
+  __syncwarp();
 #pragma unroll
   for (int st = 0; st < STAGES - 1; ++st) issue(st);
 

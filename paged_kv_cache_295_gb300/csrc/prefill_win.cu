@@ -82,6 +82,7 @@ extern "C" pkv_status paged_attention_prefill_window(
   w.out_bf16 = out_dtype == PKV_BF16;
   w.window = window;
   w.sinks = sinks;
+  w.test_stall_bytes = test_stall_bytes();
 
   CUtensorMap tk, tv;
   const int64_t rows = num_blocks * block_size;

@@ -53,6 +53,7 @@ struct PrefillWinParams {
   int32_t out_bf16;
   int32_t window;           // 0: none
   int32_t sinks;
+  uint32_t test_stall_bytes;   // CTA (0, 0, 0)'s first V tile waits for these in vain; 0 but in tests
 };
 
 // The key tiles a CTA walks: the sinks' tiles, then those from its first query's
@@ -220,6 +221,8 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
       mbar_init(smem_u32(&raw_full[i / kPfRawBufs][i % kPfRawBufs]), 1);
       mbar_init(smem_u32(&raw_free[i / kPfRawBufs][i % kPfRawBufs]), 2);
     }
+    if (wp.test_stall_bytes != 0 && blockIdx.x + blockIdx.y + blockIdx.z == 0)
+      mbar_expect_tx(smem_u32(&full_v[0]), wp.test_stall_bytes);
     abort_sh = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -772,7 +775,8 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
       // V rows that no query sees or without cache data -> 0, once per key tile: by tile A's
       // group while it needs this tile, else by tile B's; after the V copies landed
       if ((t == 0) == (j < nt_a) && vmask != ~0ull) {
-        if (!pw_wait(smem_u32(&full_v[st]), (j / STAGES) & 1, abort_flag)) alive = false;
+        // a vote: lanes that leave the loop alone would miss the warp-wide instructions below
+        if (!pw_wait_all(smem_u32(&full_v[st]), (j / STAGES) & 1, abort_flag)) alive = false;
         if (alive && r < kPfKeys && !((vmask >> r) & 1ull)) {
           uint8_t* vrow = sm + kRing + st * kStage + 2 * kKVHalf + r * 128;
 #pragma unroll

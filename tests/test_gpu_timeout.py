@@ -53,3 +53,42 @@ def test_decode_wait_runs_out_flags_timeout_and_the_next_call_is_clean(lib):
     got = out.cpu().numpy()
     assert got.tobytes() == outs[0].tobytes()
     assert np.abs(got.astype(np.float64) - ref).max() <= 2e-3
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3", "int8"])
+def test_windowed_waits_run_out_and_the_next_calls_are_clean(lib, kv):
+    """Windowed decode and prefill: the prefill's first V tile is a cut one, so the softmax
+    warps that would clear its hidden rows give up beside the product's issuer."""
+    import torch
+    from tests import paged_cases as PC
+    lens, new = [50, 40, 300], [50, 1, 130]
+    case = PC.make(72, kv, lens, 2, 128, 16)
+    d = case.device()
+    q = torch.randn((sum(new), 8, 128), device="cuda").to(torch.bfloat16)
+    start = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device="cuda")
+    kw = {"k_scale": d.get("ks"), "v_scale": d.get("vs"), "window": 30, "sinks": 2}
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def both():
+        for call in (lambda: lib.paged_attention_decode(q[:3].contiguous(), d["k"], d["v"], d["tables"],
+                                                        d["lens"], 0.09, 300, device_status=status, **kw),
+                     lambda: lib.paged_attention_prefill(q, start, d["k"], d["v"], d["tables"], d["lens"],
+                                                         0.09, 130, 300, device_status=status, **kw)):
+            status.zero_()
+            torch.cuda.synchronize()
+            t0 = time.monotonic()
+            out = call()
+            torch.cuda.synchronize()
+            yield out, int(status.item()), time.monotonic() - t0
+
+    clean = [(out, st) for out, st, _ in both()]
+    assert [st for _, st in clean] == [0, 0]
+    lib.stall_decode_for_test(16)
+    try:
+        for _, st, waited in both():
+            assert st & lib.DEV_TIMEOUT, st
+            assert 1.5 <= waited < 30.0, waited
+    finally:
+        lib.stall_decode_for_test(0)
+    for (out, st, _), (want, _) in zip(both(), clean):
+        assert st == 0 and torch.equal(out, want)
