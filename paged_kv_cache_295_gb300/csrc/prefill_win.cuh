@@ -36,8 +36,8 @@
 // output: 123 (1,020 TFLOP/s).  Every CTA has about 10 us of setup, Q, first copies and epilogue
 // besides its key tiles, of which a window leaves few.
 //
-// Every wait is bounded (2 s) and gives up when another role has given up; TMEM is
-// released before the CTA exits.
+// Every wait is bounded (2 s) and gives up when another role has given up; the copies in
+// flight are then waited for, and TMEM is released before the CTA exits.
 #pragma once
 
 #include "prefill_tc.cuh"
@@ -348,6 +348,7 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
   auto issuer_wait = [&](uint32_t bar, uint32_t parity) {
     return C8 ? pw_wait_all(bar, parity, abort_flag) : pw_wait(bar, parity, abort_flag);
   };
+  int copied = 0;   // copying warps: key tiles whose copies were started
   if (warp >= 8) {
   if constexpr (C8) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n");
   if (warp == 8 || warp == 11) {
@@ -392,6 +393,7 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
           const int z = (blk << p.bs_log2) + (kb & ((1 << p.bs_log2) - 1));
           tma_load_3d(dst, is_v ? &tmap_v : &tmap_k, hh * 64, g, z, bar);
         }
+        copied = j + 1;
       }
     } else {
       // Lane i looks up box i and copies its codes, [box_rows][128 B], into one of the raw
@@ -444,6 +446,7 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
           tma_load_3d(raw_a + rb * kRawTile + lane * box_rows * 128, is_v ? &tmap_v : &tmap_k, 0, g, z,
                       rbar);
         }
+        copied = j + 1;
       }
     }
   } else if (warp == 9) {
@@ -847,6 +850,14 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag && (warp == 8 || warp == 11)) {   // copies may be in flight: no role waits for them now
+    constexpr int kBufs = C8 ? kPfRawBufs : STAGES;
+    const int is_v = warp == 11 ? 1 : 0;
+    volatile int no_abort = 0;
+    for (int j = max(0, copied - kBufs); j < copied; ++j)
+      pw_wait(smem_u32(C8 ? &raw_full[is_v][j % kBufs] : is_v ? &full_v[j % kBufs] : &full[j % kBufs]),
+              (j / kBufs) & 1, &no_abort);
+  }
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tm) : "memory");
   if (tid == 0 && *abort_flag) flag_status(p.status, PKV_DEV_TIMEOUT);
