@@ -590,8 +590,9 @@ pkv_status paged_attention_decode_window(
 /* paged_attention_prefill with the same window, sinks, scales and output types:
  * the query at position p (of a chunk's last n_s positions) sees token t <= p when
  * t > p - window or t < sinks.  window > 0 needs causal = 1; sinks need a window.
- * 8-bit caches carry the weights as one fp16 value (2^-11 relative), as
- * paged_attention_prefill does, whatever the output type.  Table entries of blocks
+ * Weights enter P V as 16-bit values: bf16 caches as two bf16 parts (2^-16 of each weight,
+ * whatever the output type), 8-bit caches as one fp16 value (2^-11), as
+ * paged_attention_prefill does.  Table entries of blocks
  * that no query of the chunk sees are not read.  A key that a query does not see, but
  * another one of the same work tile (up to 256 query rows) does, has weight 0 there; a V
  * value of it that is not finite gives NaN.  max_context_len <= 2^30; shapes

@@ -11,7 +11,7 @@
 // come in tiles of 64.  Per key tile and query tile
 //   S_t  = Q_t K^T   M=128 N=64  K=128   A = Q_t (smem), B = K tile (smem)
 //   O_t += P_t V     M=128 N=128 K=64    A = P_t (TMEM), B = V tile (smem)
-// TMEM, per query tile: P in 64 columns (bf16 hi, then lo; or one 16-bit value in
+// TMEM, per query tile: P in 64 columns (bf16 hi, then lo; or one fp16 value in
 // 32), S in 64, O in 128.  With P apart from S, the next key tile's QK runs while
 // this one's softmax is still at its exponentials, and with P out of shared memory
 // the softmax stores it in two instructions.
@@ -21,9 +21,13 @@
 // asked together), S load 110, maximum 260, exponentials 500, P store 200 to 600 - next to the
 // MMAs, which hold both issuers for 1,200 cycles a key tile; and, on 8-bit caches, instruction
 // fetch: the roles' loops together overrun the instruction cache.  So: the issuers' code is
-// uniform (pw_elect); bf16 outputs carry P as one bf16 value (8 PV fewer; its 2^-8 is the size
-// of the output's own rounding); a mask is built only for tiles that cut some row of the warp;
-// 8-bit tiles are widened by four warps of their own.
+// uniform (pw_elect); a mask is built only for tiles that cut some row of the warp; 8-bit tiles
+// are widened by four warps of their own.
+//
+// bf16 caches carry P as two bf16 parts (2^-16 of each weight) whatever the output's type: a bf16
+// output is the float32 one rounded.  One part would be off by 2^-8 of each weight, which is
+// relative to sum p |v| and not to the output: 1.4 times the error against 64 bits on normal
+// values, without bound where they cancel.  It would take 123 us for the ragged chunks below.
 //
 // 8-bit caches: the running reference m follows max(logit + log2 vs), so the weights
 // w = p vs that enter P V stay below 2^8 whatever the blocks' scales; l sums p itself.
@@ -33,7 +37,7 @@
 // Measured, chunks of 512 tokens at contexts up to 4,096: 16 x 32 heads, bf16, window 1,024,
 // f32 output 197 us (613 TFLOP/s); 16 x 8 heads GQA-4, fp8, no window, bf16 output 283 (923
 // TFLOP/s).  Three ragged chunks of up to 700 tokens, 8 heads GQA-8, window 4,096, bf16
-// output: 123 (1,020 TFLOP/s).  Every CTA has about 10 us of setup, Q, first copies and epilogue
+// output: 147 (858 TFLOP/s).  Every CTA has about 10 us of setup, Q, first copies and epilogue
 // besides its key tiles, of which a window leaves few.
 //
 // Every wait is bounded (2 s) and gives up when another role has given up; the copies in
@@ -488,7 +492,6 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
     // released (its QK finished before its P could be written).
     if (C8 || pw_elect()) {
       const uint32_t idesc_pv = tc_idesc(kPfRows, kPfD, false, true, !C8);
-      const bool lo = !C8 && !wp.out_bf16;
       for (int j = 0; j < ntiles; ++j) {
         if (!issuer_wait(smem_u32(&full_v[j % STAGES]), (j / STAGES) & 1)) break;
         const uint64_t vd =
@@ -507,7 +510,7 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
             for (int kk = 0; kk < kPfKeys / 16; ++kk) {
               const uint64_t bdesc = vd + ((kk * 2048) >> 4);
               tc_mma_ts(dO, tm + 256 * t + 8 * kk, bdesc, idesc_pv, (jt > 0 || kk > 0));
-              if (lo) tc_mma_ts(dO, tm + 256 * t + 32 + 8 * kk, bdesc, idesc_pv, 1);
+              if (!C8) tc_mma_ts(dO, tm + 256 * t + 32 + 8 * kk, bdesc, idesc_pv, 1);
             }
             tc_commit(smem_u32(&o_done[t]));
           }
@@ -755,7 +758,7 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
       if (!__all_sync(0xffffffffu, alive)) break;
       tc_fence_after();
       pw_st32(tP, w);   // row = lane, column c = keys 2c and 2c + 1
-      if (!C8 && !wp.out_bf16) {   // what the bf16 value left: 2^-16 together
+      if constexpr (!C8) {   // what the bf16 value left: 2^-16 together
         uint32_t wl[kPfKeys / 2];
 #pragma unroll
         for (int c = 0; c < kPfKeys; c += 2) {

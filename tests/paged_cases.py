@@ -90,7 +90,8 @@ def make(seed, kv, lens, hkv, d, bs, scales="block", stride=None, extra_blocks=3
 # ---- error bounds ------------------------------------------------------------
 # Half steps relative to the value: bf16 2^-8, fp16 2^-11, float32 2^-24.  The tensor cores
 # accumulate in float32; 2^-23 per addition covers truncation.
-def attention_bound(case, q, out, mag, reach, scale, q_f32, out_bf16, hi_lo, longest):
+def attention_bound(case, q, out, mag, reach, scale, q_f32, out_bf16, hi_lo, longest, e_p=None,
+                    floor=None):
     """Elementwise bound on |kernel - out| ``[n, Hq, D]``; ``mag`` = A = sum p |v|, ``reach``
     = max over tokens of sum_d |q_d k_d|, ``longest`` the most tokens a query sees.
 
@@ -107,6 +108,9 @@ def attention_bound(case, q, out, mag, reach, scale, q_f32, out_bf16, hi_lo, lon
     INT8 with one fp16 weight (no hi + lo) carries code + 1152 (at most 1279) in both
     products: 16 float32 steps on sum |q| 1279 ks in z, and a step for each 16 tokens, twice
     (the sum and what is taken off), on 1279 max(vs) in the output.
+
+    ``e_p`` and ``floor``, where given, take the place of the weights' relative term and of the
+    2^-25 of a weight (8-bit caches).
     """
     codes = case.kv in OB.QMAX
     steps = longest / 16 + 24
@@ -115,10 +119,11 @@ def attention_bound(case, q, out, mag, reach, scale, q_f32, out_bf16, hi_lo, lon
     extra = 0.0
     if codes:
         vs, ks = (float(x.max()) for x in (case.vs, case.ks))
-        extra = longest * 2.0 ** -25 * float(OB.QMAX[case.kv]) * vs
+        extra = longest * (2.0 ** -25 if floor is None else floor) * float(OB.QMAX[case.kv]) * vs
         if case.kv == "int8" and not hi_lo:
             dz = dz + 16 * 2.0 ** -23 * scale * 1279 * ks * np.abs(q).sum(-1)
             extra += 2 * steps * 2.0 ** -23 * 1279 * vs
-    e_p = (2.0 ** -22 if codes else 2.0 ** -16) if hi_lo else 2.0 ** (-11 if codes else -8)
+    if e_p is None:
+        e_p = (2.0 ** -22 if codes else 2.0 ** -16) if hi_lo else 2.0 ** (-11 if codes else -8)
     e = 2 * (dz[..., None] + e_p + 2.0 ** -21 + steps * 2.0 ** -23) * mag + extra
     return e + (2.0 ** -8 if out_bf16 else 2.0 ** -23) * (np.abs(out) + e)

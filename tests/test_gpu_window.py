@@ -302,3 +302,65 @@ def test_prefill_repeats_itself(lib):
         for _ in range(5):
             prefill(lib, case, new, q, 0.09, out="bf16", window=600)
             assert np.array_equal(prefill(lib, case, new, q, 0.09, window=200, sinks=5), first)
+
+
+def _fill(case, s, K=None, V=None):
+    """Puts rows ``[n, Hkv, D]`` in storage at positions 0 .. n - 1 of sequence s."""
+    for cache, rows in ((case.k, K), (case.v, V)):
+        for t in range(0 if rows is None else len(rows)):
+            cache[case.tables[s][t // case.bs], t % case.bs] = rows[t]
+
+
+def test_prefill_weights_keep_their_bits_in_bf16_outputs(lib):
+    """bf16 caches and outputs: the weights are two bf16 parts as with a float32 output.
+
+    The values are +u and -u in turn and the weights nearly equal, so a result is a small
+    difference of large terms: the bound on sum p |v| has 2^-16, which one bf16 value (2^-8)
+    exceeds."""
+    n = 200
+    case = PC.make(51, "bf16", [n], 2, 128, 16)
+    rng = np.random.default_rng(52)
+    u = np.abs(rng.standard_normal((2, 128))) + 0.5
+    _fill(case, 0, V=PC.bf16_bits(np.where(np.arange(n) % 2, 1.0, -1.0)[:, None, None] * u))
+    for window in (2, 3, 7, 60):
+        check = _prefill_ratio(lib, case, [n], 8, 53, "bf16", window, 0.02, e_p=2.0 ** -16)
+        assert check <= 1.0, (window, check)
+
+
+def test_prefill_of_one_value_returns_it(lib):
+    """Every V row the same bf16 row: each output is that row, bit for bit.  The weights sum to
+    one within 2^-15, less than half a step (at least 2^-9), whatever the running reference."""
+    import torch
+    n = 500
+    case = PC.make(54, "bf16", [n, 77], 2, 128, 16)
+    v = PC.bf16_bits(np.random.default_rng(55).standard_normal((2, 128)))
+    for s, c in enumerate(case.lens):
+        _fill(case, s, V=np.broadcast_to(v, (c, 2, 128)))
+    new = [300, 77]
+    want = GC.OA.to_f64(v, "bf16").repeat(4, axis=0)
+    for scale in (0.01, 0.09, 0.4):
+        q = PC.bf16_bits(np.random.default_rng(56).standard_normal((sum(new), 8, 128)))
+        for kw in ({}, {"window": 5}, {"window": 130, "sinks": 70}):
+            got = prefill(lib, case, new, q, scale, out="bf16", **kw)
+            assert np.array_equal(got, np.broadcast_to(want, got.shape)), (scale, kw)
+
+
+def _prefill_ratio(lib, case, new, hq, seed, out, window, scale, e_p, floor=None, q=None):
+    """Largest error of a prefill call over ``attention_bound`` with the given weight term."""
+    import torch
+    hkv, d = case.k.shape[2:]
+    if q is None:
+        q = PC.bf16_bits(np.random.default_rng(seed).standard_normal((sum(new), hq, d)))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = prefill(lib, case, new, q, scale, out, status, window=window)
+    assert int(status.item()) == 0
+    q64, worst, row = GC.OA.to_f64(q, "bf16"), 0.0, 0
+    for s, (c, n) in enumerate(zip(case.lens, new)):
+        K, V = case.values(s)
+        x = q64[row:row + n]
+        o, mag, reach = OB.attend(x, np.arange(c - n, c), K, V, scale, window, 0)
+        lim = PC.attention_bound(case, x, o, mag, reach, scale, False, out == "bf16", True,
+                                 min(c, window) if window else c, e_p=e_p, floor=floor)
+        worst = max(worst, float((np.abs(got[row:row + n] - o) / lim).max()))
+        row += n
+    return worst
