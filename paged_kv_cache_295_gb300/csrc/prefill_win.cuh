@@ -30,7 +30,7 @@
 // values, without bound where they cancel.  It would take 123 us for the ragged chunks below.
 //
 // 8-bit caches: the running reference m follows max(logit + log2 vs), so the weights
-// w = p vs that enter P V stay below 2^8 whatever the blocks' scales; l sums p itself.
+// w = p vs that enter P V stay below 2^15 whatever the blocks' scales; l sums p itself.
 // Each row of q is scaled by a power of two into fp16's range; weights are one fp16
 // value (2^-11).  Codes are widened to fp16 exactly.
 //
@@ -84,7 +84,7 @@ struct PfScale {
   float lv;    // log2 vs
   float pad;
 };
-// Smallest V scale (2^-80): keeps log2 vs, and p = w / vs < 2^88, finite.
+// Smallest V scale (2^-80): keeps log2 vs, and p = w / vs <= 2^95, finite.
 constexpr float kPfMinVScale = 8.271806125530277e-25f;
 
 struct PwLayout {
@@ -721,12 +721,16 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
       }
       float alpha = 1.f;
       bool resc = false;
-      if (mt > m + 8.f) {   // the reference moves only when a tile exceeds it by 2^8
+      // The reference moves only when a weight would exceed 2^(kUp + 8).  8-bit caches set it kUp = 7
+      // below the maximum: fp16 weights (at most 2^15) then hold what is 2^-21 of the largest with
+      // all their bits, and what is 2^-31 of it at all.
+      constexpr float kUp = C8 ? 7.f : 0.f;
+      if (mt > m + (kUp + 8.f)) {
         if (m != -CUDART_INF_F) {
-          alpha = pf_ex2(m - mt);
+          alpha = pf_ex2(m - (mt - kUp));
           resc = true;
         }
-        m = mt;
+        m = mt - kUp;
       }
       const float mu = m == -CUDART_INF_F ? 0.f : m;   // rows with nothing seen yet: p = 0
       // p, l and the packed weights; pairs go through the packed fp32 pipe

@@ -364,3 +364,36 @@ def _prefill_ratio(lib, case, new, hq, seed, out, window, scale, e_p, floor=None
         worst = max(worst, float((np.abs(got[row:row + n] - o) / lim).max()))
         row += n
     return worst
+
+
+def _heavy_key(kv, seed, n, gap):
+    """A sequence of n tokens whose first key takes nearly all of every query's weight (the
+    others' are about 2^-gap of it) and whose first V row is zero; and q.  All V rows but the
+    first are ordinary, so the small weights make the whole result."""
+    case = PC.make(seed, kv, [n], 1, 128, 16, scales="head")
+    case.ks[:], case.vs[:] = 0.01, 0.02
+    rng = np.random.default_rng(seed + 1)
+    x = rng.standard_normal((n, 1, 128)).astype(np.float32) * 20
+    x[:, 0, :2] = 0.0
+    x[0, 0, 0] = 100.0
+    y = rng.standard_normal((n, 1, 128)).astype(np.float32) * 30
+    y[0] = 0.0
+    _fill(case, 0, OB.encode(x, kv), OB.encode(y, kv))
+    # q = (a, 0, small ...): the first key's logit is scale * a * 100 * 0.01 = a * scale
+    q = rng.standard_normal((n, 4, 128)) * 0.25
+    q[..., 0] = gap * np.log(2.0)
+    q[..., 1] = 0.0
+    return case, PC.bf16_bits(q)
+
+
+@pytest.mark.parametrize("kv", ["fp8_e4m3", "int8"])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("gap", [14, 18, 22])
+def test_prefill_small_weights_reach_the_product(lib, kv, out, gap):
+    """8-bit caches: the largest weight is at least 2^7 as fp16 holds it, so a small one is off
+    by 2^-32 of the largest (2^-25 / 2^7) and by its own relative 2^-11 (2^-22 for float32
+    outputs' two parts)."""
+    n = 150
+    case, q = _heavy_key(kv, 57 + gap, n, gap)
+    r = _prefill_ratio(lib, case, [n], 4, 0, out, 1000, 1.0, e_p=2.0 ** -11, floor=2.0 ** -32, q=q)
+    assert r <= 1.0, r
