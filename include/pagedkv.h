@@ -591,8 +591,8 @@ pkv_status paged_attention_decode_window(
  * the query at position p (of a chunk's last n_s positions) sees token t <= p when
  * t > p - window or t < sinks.  window > 0 needs causal = 1; sinks need a window.
  * Weights enter P V as 16-bit values: bf16 caches as two bf16 parts (2^-16 of each weight,
- * whatever the output type), 8-bit caches as one fp16 value (2^-11, and
- * 2^-32 of the row's largest weight).  Table entries of blocks
+ * whatever the output type), 8-bit caches as two fp16 parts for a float32 output (2^-22) and
+ * as one for a bf16 output (2^-11), and 2^-32 of the row's largest weight.  Table entries of blocks
  * that no query of the chunk sees are not read.  A key that a query does not see, but
  * another one of the same work tile (up to 256 query rows) does, has weight 0 there; a V
  * value of it that is not finite gives NaN.  max_context_len <= 2^30; shapes

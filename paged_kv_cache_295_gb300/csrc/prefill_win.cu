@@ -99,10 +99,13 @@ extern "C" pkv_status paged_attention_prefill_window(
     return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
   };
   const size_t smem8 = PwLayout::bytes(kPfStagesFp8, true);
+  // 8-bit caches: two fp16 weight parts for a float32 output, one for a bf16 output
   if (kv_dtype == PKV_FP8_E4M3)
-    return launch(paged_prefill_win_kernel<kPfStagesFp8, 1>, kPwThreads8, smem8);
+    return w.out_bf16 ? launch(paged_prefill_win_kernel<kPfStagesFp8, 1, false>, kPwThreads8, smem8)
+                      : launch(paged_prefill_win_kernel<kPfStagesFp8, 1, true>, kPwThreads8, smem8);
   if (kv_dtype == PKV_INT8)
-    return launch(paged_prefill_win_kernel<kPfStagesFp8, 2>, kPwThreads8, smem8);
-  return launch(paged_prefill_win_kernel<kPfStages, 0>, kPfThreads,
+    return w.out_bf16 ? launch(paged_prefill_win_kernel<kPfStagesFp8, 2, false>, kPwThreads8, smem8)
+                      : launch(paged_prefill_win_kernel<kPfStagesFp8, 2, true>, kPwThreads8, smem8);
+  return launch(paged_prefill_win_kernel<kPfStages, 0, true>, kPfThreads,
                 PwLayout::bytes(kPfStages, false));
 }

@@ -11,8 +11,7 @@
 // come in tiles of 64.  Per key tile and query tile
 //   S_t  = Q_t K^T   M=128 N=64  K=128   A = Q_t (smem), B = K tile (smem)
 //   O_t += P_t V     M=128 N=128 K=64    A = P_t (TMEM), B = V tile (smem)
-// TMEM, per query tile: P in 64 columns (bf16 hi, then lo; or one fp16 value in
-// 32), S in 64, O in 128.  With P apart from S, the next key tile's QK runs while
+// TMEM, per query tile: P in 64 columns (hi, then lo; or one value in 32), S in 64, O in 128.  With P apart from S, the next key tile's QK runs while
 // this one's softmax is still at its exponentials, and with P out of shared memory
 // the softmax stores it in two instructions.
 //
@@ -31,12 +30,14 @@
 //
 // 8-bit caches: the running reference m follows max(logit + log2 vs), so the weights
 // w = p vs that enter P V stay below 2^15 whatever the blocks' scales; l sums p itself.
-// Each row of q is scaled by a power of two into fp16's range; weights are one fp16
-// value (2^-11).  Codes are widened to fp16 exactly.
+// Each row of q is scaled by a power of two into fp16's range.  A float32 output takes
+// the weights as two fp16 parts (2^-22), a bf16 one as one (2^-11 of each weight, where the codes
+// themselves are off by up to 2^-4 (E4M3) or half a step (INT8) of their values).  Codes are
+// widened to fp16 exactly.
 //
 // Measured, chunks of 512 tokens at contexts up to 4,096: 16 x 32 heads, bf16, window 1,024,
-// f32 output 197 us (613 TFLOP/s); 16 x 8 heads GQA-4, fp8, no window, bf16 output 283 (923
-// TFLOP/s).  Three ragged chunks of up to 700 tokens, 8 heads GQA-8, window 4,096, bf16
+// f32 output 199 us (607 TFLOP/s); 16 x 8 heads GQA-4, fp8, no window, bf16 output 282 (927
+// TFLOP/s), f32 output 336; the same in int8 292 and 349.  Three ragged chunks of up to 700 tokens, 8 heads GQA-8, window 4,096, bf16
 // output: 147 (858 TFLOP/s).  Every CTA has about 10 us of setup, Q, first copies and epilogue
 // besides its key tiles, of which a window leaves few.
 //
@@ -175,8 +176,8 @@ __device__ __forceinline__ uint64_t pw_below(int n) {
   return n >= 64 ? ~0ull : (n <= 0 ? 0ull : (1ull << n) - 1ull);
 }
 
-// KIND: 0 bf16 cache; 1 FP8-E4M3 codes; 2 INT8 codes.
-template <int STAGES, int KIND>
+// KIND: 0 bf16 cache; 1 FP8-E4M3 codes; 2 INT8 codes.  LO: the weights are two 16-bit parts.
+template <int STAGES, int KIND, bool LO>
 __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
     paged_prefill_win_kernel(const __grid_constant__ CUtensorMap tmap_k,
                              const __grid_constant__ CUtensorMap tmap_v,
@@ -510,7 +511,7 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
             for (int kk = 0; kk < kPfKeys / 16; ++kk) {
               const uint64_t bdesc = vd + ((kk * 2048) >> 4);
               tc_mma_ts(dO, tm + 256 * t + 8 * kk, bdesc, idesc_pv, (jt > 0 || kk > 0));
-              if (!C8) tc_mma_ts(dO, tm + 256 * t + 32 + 8 * kk, bdesc, idesc_pv, 1);
+              if (LO) tc_mma_ts(dO, tm + 256 * t + 32 + 8 * kk, bdesc, idesc_pv, 1);
             }
             tc_commit(smem_u32(&o_done[t]));
           }
@@ -751,6 +752,8 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
             w[c >> 1] = pack_f16(y.x, y.y);
           } else {
             w[c >> 1] = pack_bf16(y.x, y.y);
+          }
+          if constexpr (LO) {
             sv[c] = y.x;
             sv[c + 1] = y.y;
           }
@@ -762,13 +765,17 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
       if (!__all_sync(0xffffffffu, alive)) break;
       tc_fence_after();
       pw_st32(tP, w);   // row = lane, column c = keys 2c and 2c + 1
-      if constexpr (!C8) {   // what the bf16 value left: 2^-16 together
+      if constexpr (LO) {   // what the first part left: 2^-16 together in bf16, 2^-22 in fp16
         uint32_t wl[kPfKeys / 2];
 #pragma unroll
         for (int c = 0; c < kPfKeys; c += 2) {
-          const float2 hi = make_float2(bf16_lo(w[c >> 1]), bf16_hi(w[c >> 1]));
+          float2 hi;
+          if constexpr (C8)
+            hi = __half22float2(*reinterpret_cast<const __half2*>(&w[c >> 1]));
+          else
+            hi = make_float2(bf16_lo(w[c >> 1]), bf16_hi(w[c >> 1]));
           const float2 lo = __ffma2_rn(hi, make_float2(-1.f, -1.f), make_float2(sv[c], sv[c + 1]));
-          wl[c >> 1] = pack_bf16(lo.x, lo.y);
+          wl[c >> 1] = C8 ? pack_f16(lo.x, lo.y) : pack_bf16(lo.x, lo.y);
         }
         pw_st32(tP + 32, wl);
       }

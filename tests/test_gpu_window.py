@@ -397,3 +397,15 @@ def test_prefill_small_weights_reach_the_product(lib, kv, out, gap):
     case, q = _heavy_key(kv, 57 + gap, n, gap)
     r = _prefill_ratio(lib, case, [n], 4, 0, out, 1000, 1.0, e_p=2.0 ** -11, floor=2.0 ** -32, q=q)
     assert r <= 1.0, r
+
+
+@pytest.mark.parametrize("kv", ["fp8_e4m3", "int8"])
+def test_prefill_f32_outputs_of_8_bit_caches(lib, kv):
+    """Float32 outputs carry the weights as two fp16 parts (2^-22), as decode does."""
+    for lens, new, hq, hkv, scale, kw in (([300, 641], [300, 130], 4, 2, 0.05, 0), ([700], [700], 8, 1, 0.2, 90)):
+        case = PC.make(58, kv, lens, hkv, 128, 16, scales="block", spread=0.3)
+        r = _prefill_ratio(lib, case, new, hq, 59, "f32", kw, scale, e_p=2.0 ** -22, floor=2.0 ** -32)
+        assert r <= 1.0, r
+    case, q = _heavy_key(kv, 60, 150, 12)
+    r = _prefill_ratio(lib, case, [150], 4, 0, "f32", 1000, 1.0, e_p=2.0 ** -22, floor=2.0 ** -32, q=q)
+    assert r <= 1.0, r
