@@ -552,12 +552,19 @@ pkv_status gather_cache(const void* k_cache, const void* v_cache, const int32_t*
 /* ------------------------------------------------------------------------ */
 /* Attention with a sliding window and sinks; scales per block.              */
 /* ------------------------------------------------------------------------ */
-/* Split-KV scratch of paged_attention_decode_window (0 when every query's
- * visible tokens fit one partition), for the same arguments. */
+/* Split-KV scratch that is enough for every call of paged_attention_decode_window with up to
+ * num_seqs sequences and contexts of up to max_context_len, the other arguments the same (0 when
+ * every query's visible tokens fit one partition). */
 size_t paged_attention_window_workspace_bytes(int32_t num_seqs, int32_t num_q_heads,
                                               int32_t num_kv_heads, int32_t head_dim,
                                               int32_t max_context_len, int32_t partition_tokens,
                                               int32_t window, int32_t sinks);
+/* What one call with exactly these arguments needs: at most the above, and often 0.  A larger call
+ * may need less than a smaller one. */
+size_t paged_attention_window_call_bytes(int32_t num_seqs, int32_t num_q_heads,
+                                         int32_t num_kv_heads, int32_t head_dim,
+                                         int32_t max_context_len, int32_t partition_tokens,
+                                         int32_t window, int32_t sinks, int32_t kv_dtype);
 
 /* paged_attention_decode over part of the context, with more cache forms.
  * Arguments as there, and:
@@ -572,8 +579,8 @@ size_t paged_attention_window_workspace_bytes(int32_t num_seqs, int32_t num_q_he
  *                  as at least 2^-80.
  *   out, out_dtype : device [num_seqs, num_q_heads, head_dim], f32 or bf16.
  *   partition_tokens : counted in visible tokens.
- *   workspace    : calls whose kernels may overlap on the GPU need one each.
- *                  Small grids merge their partitions within thread-block
+ *   workspace    : of paged_attention_window_call_bytes or more.  Calls whose kernels may
+ *                  overlap on the GPU need one each.  Small grids merge their partitions within thread-block
  *                  clusters and need none.
  * Supported: bf16 caches with head_dim 64, 128 or 256; FP8 and INT8 caches with
  * head_dim 128; num_q_heads / num_kv_heads <= 16; block_size a power of two in

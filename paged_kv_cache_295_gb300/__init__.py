@@ -117,6 +117,7 @@ _SIGS = {
     "gather_cache": (I32, [P, P, P, P, P, I32, I32, I32, I32, I32, I32, I64, I32, I32, P, P, I64,
                            I32, P, P, P, P]),
     "paged_attention_window_workspace_bytes": (SZ, [I32, I32, I32, I32, I32, I32, I32, I32]),
+    "paged_attention_window_call_bytes": (SZ, [I32, I32, I32, I32, I32, I32, I32, I32, I32]),
     "paged_attention_decode_window": (I32, [P, P, P, P, P, I32, I32, I32, I32, I32, I64, I32, I32,
                                             FL, I32, I32, P, P, I64, I32, I32, I32, P, P, SZ, I32,
                                             P, P]),
@@ -420,8 +421,8 @@ def partition_tokens(num_seqs, num_q_heads, num_kv_heads, max_context_len, reque
 
 def workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len,
                     partition=0, window=None, sinks=0) -> int:
-    """Bytes of split-KV scratch of a decode call; with ``window`` (0: none) of a call
-    with a window, sinks or scales per block."""
+    """Bytes of split-KV scratch of a decode call; with ``window`` (0: none) enough for every call
+    with that window, sinks or scales per block of up to ``num_seqs`` and ``max_context_len``."""
     if window is not None:
         return int(library().paged_attention_window_workspace_bytes(
             num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, partition, window,

@@ -321,8 +321,8 @@ PyObject* do_decode(PyObject* const* a, Py_ssize_t na) {
   const at::Device dev = cuda_device(p.q);
   const c10::cuda::CUDAGuard guard(dev);
   Tensor out = attention_out(p, tensor(a[7], "out", true), a[15]), ws = tensor(a[10], "workspace", true);
-  const size_t need = paged_attention_window_workspace_bytes(
-      static_cast<int32_t>(p.S), p.q_heads, p.c.heads, p.c.dim, max_ctx, part, window, sinks);
+  const size_t need = paged_attention_window_call_bytes(static_cast<int32_t>(p.S), p.q_heads, p.c.heads,
+                                                        p.c.dim, max_ctx, part, window, sinks, p.c.code);
   if (need > (ws.defined() ? ws.nbytes() : 0))
     ws = at::empty({static_cast<int64_t>(need)}, p.q.options().dtype(at::kByte));
   const void *q = ptr(p.q, "q", dev), *kc = ptr(p.kc, "k_cache", dev), *vc = ptr(p.vc, "v_cache", dev);

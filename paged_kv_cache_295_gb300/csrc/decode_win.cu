@@ -21,6 +21,15 @@ int64_t visible_tokens(int32_t max_ctx, int32_t window, int32_t sinks) {
   return 32 * max_visible_chunks(max_ctx, window, sinks, 32);
 }
 
+// Most CTAs (heads times partitions) of a launch whose partition is chosen here.  It bounds the
+// scratch of every call up to a given size: it grows with both arguments, where the choice itself
+// goes up and down.  Twice what the box table's 4,096 tokens a CTA need, and at least eight waves,
+// past which shorter partitions gain less than 1.5 % by the estimate below.
+int64_t most_ctas(int64_t heads, int64_t tokens) {
+  const int64_t waves = 8 * 3LL * device_sm_count(), twice = 2 * heads * ((tokens + 4095) / 4096);
+  return twice > waves ? twice : waves;
+}
+
 // Tokens per partition.  `tokens` is what the longest query can see; token_bytes the K and V
 // bytes of one token and head.  With n partitions a launch has heads * n CTAs of about
 // tokens / n tokens, three to an SM, and is estimated (us) as
@@ -28,17 +37,18 @@ int64_t visible_tokens(int32_t max_ctx, int32_t window, int32_t sinks) {
 //   + per full wave of CTA slots: 1 + len * slots * token_bytes / HBM bandwidth
 //   + the last, partial wave: 1 + len * the root of the squares of that rate times how full
 //     the wave is and of the rate of a CTA alone, which its two-stage rings bound (42 KB/us).
-// The n with the least estimate is taken.  Measured (bf16, GQA-8, 64 x 8 heads, window 1024):
+// The n with the least estimate is taken, of those within most_ctas.  Measured (bf16, GQA-8, 64 x 8 heads, window 1024):
 // one partition 57.6 us (1.1 waves), two of 576 and 512 57.4, of 704 and 384 53.0; 16 x 8
 // heads, GQA-4: 20.3 with one, 17.1 with three; 4 x 8 heads: 18.6 with one, 8.7 with six;
 // one sequence, window 4096: 56.9 with two, 10.1 with 33.
 int32_t auto_win_partition(int64_t heads, int64_t tokens, int token_bytes) {
+  const int64_t most = most_ctas(heads, tokens);
   const double slots = 3.0 * device_sm_count();
   const double full = slots * token_bytes / 6.6e6, alone = token_bytes / 4.2e4;
   int32_t best = 4096;
   double least = 1e30;
   auto consider = [&](int64_t len, double t) {
-    if (t < least) {
+    if (t < least && heads * ((tokens + len - 1) / len) <= most) {
       least = t;
       best = static_cast<int32_t>(len);
     }
@@ -120,16 +130,32 @@ extern "C" size_t paged_attention_window_workspace_bytes(int32_t num_seqs, int32
   if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
       max_context_len < 0 || window < 0 || sinks < 0 || num_q_heads % num_kv_heads != 0)
     return 0;
-  // enough for a 16-bit and for an 8-bit cache, whose partitions may differ
   const int64_t tokens = pkv::visible_tokens(max_context_len, window, sinks);
-  size_t most = 0;
-  for (int bytes = 1; bytes <= 2; ++bytes) {
-    const int32_t P = pkv::win_partition(num_seqs, num_q_heads, num_kv_heads, tokens,
-                                         2 * head_dim * bytes, partition_tokens);
-    const size_t need = pkv::window_scratch(num_seqs, num_q_heads, num_kv_heads, head_dim, tokens, P);
-    if (need > most) most = need;
-  }
-  return most;
+  if (partition_tokens != 0)   // grows with the batch and the context
+    return pkv::window_scratch(num_seqs, num_q_heads, num_kv_heads, head_dim, tokens,
+                               pkv::win_partition(num_seqs, num_q_heads, num_kv_heads, tokens, 1,
+                                                  partition_tokens));
+  // an automatic partition has at least 64 tokens and a launch at most most_ctas
+  if (tokens <= 64) return 0;
+  const int64_t group = num_q_heads / num_kv_heads, split = group > 8 ? 2 : 1;
+  const int64_t heads = static_cast<int64_t>(num_seqs) * num_kv_heads * split;
+  const int64_t short_ones = heads * ((tokens + 63) / 64), most = pkv::most_ctas(heads, tokens);
+  const int64_t ctas = short_ones < most ? short_ones : most;
+  return static_cast<size_t>((ctas * group + split - 1) / split) * (head_dim + 2) * sizeof(float);
+}
+
+extern "C" size_t paged_attention_window_call_bytes(int32_t num_seqs, int32_t num_q_heads,
+                                                    int32_t num_kv_heads, int32_t head_dim,
+                                                    int32_t max_context_len,
+                                                    int32_t partition_tokens, int32_t window,
+                                                    int32_t sinks, int32_t kv_dtype) {
+  if (num_seqs <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+      max_context_len < 0 || window < 0 || sinks < 0 || num_q_heads % num_kv_heads != 0)
+    return 0;
+  const int64_t tokens = pkv::visible_tokens(max_context_len, window, sinks);
+  const int32_t P = pkv::win_partition(num_seqs, num_q_heads, num_kv_heads, tokens,
+                                       2 * head_dim * pkv::elem_bytes(kv_dtype), partition_tokens);
+  return pkv::window_scratch(num_seqs, num_q_heads, num_kv_heads, head_dim, tokens, P);
 }
 
 extern "C" pkv_status paged_attention_decode_window(

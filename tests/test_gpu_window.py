@@ -409,3 +409,29 @@ def test_prefill_f32_outputs_of_8_bit_caches(lib, kv):
     case, q = _heavy_key(kv, 60, 150, 12)
     r = _prefill_ratio(lib, case, [150], 4, 0, "f32", 1000, 1.0, e_p=2.0 ** -22, floor=2.0 ** -32, q=q)
     assert r <= 1.0, r
+
+
+def test_workspace_of_the_longest_context_is_used_by_shorter_calls(lib):
+    """A buffer sized for 16 sequences of up to 6,144 tokens serves smaller calls, whose automatic
+    partition may need more scratch than the largest: nothing is allocated beside it."""
+    import torch
+    cap, hkv, hq, d, bs = 6144, 8, 32, 128, 128
+    ws = torch.empty(lib.workspace_bytes(16, hq, hkv, d, cap, window=0), dtype=torch.uint8, device="cuda")
+    torch.manual_seed(9)
+    k, v = (torch.randn((64, bs, hkv, d), device="cuda").to(torch.bfloat16) for _ in range(2))
+    bt = torch.randint(0, 64, (16, cap // bs), dtype=torch.int32, device="cuda")
+    q = torch.randn((16, hq, d), device="cuda").to(torch.bfloat16)
+    used = 0
+    for s, c in ((16, 1024), (16, 1536), (8, 4096), (8, 6144), (4, 6144), (1, 6144), (16, 6144)):
+        lens = torch.full((s,), c, dtype=torch.int32, device="cuda")
+        out = torch.empty((s, hq, d), dtype=torch.bfloat16, device="cuda")
+        args = (q[:s].contiguous(), k, v, bt[:s].contiguous(), lens, 0.09, c)
+        own = lib.paged_attention_decode(*args, out_dtype=torch.bfloat16, partition=128)
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_stats()["allocation.all.allocated"]
+        lib.paged_attention_decode(*args, out=out, workspace=ws)
+        assert torch.cuda.memory_stats()["allocation.all.allocated"] == before
+        used += lib.library().paged_attention_window_call_bytes(s, hq, hkv, d, c, 0, 0, 0, lib.BF16) > 0
+        # two bf16 roundings of results that differ by the merges' float32 steps
+        assert (out.float() - own.float()).abs().max() <= 2.0 ** -7 * own.float().abs().max()
+    assert used

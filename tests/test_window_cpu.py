@@ -265,3 +265,34 @@ def test_scales_of_two_forms_are_refused(lib, per_block):
         for more in ({}, {"window": 8}):
             with pytest.raises(ValueError, match="k_scale and v_scale must be"):
                 call(**more)
+
+
+@pytest.mark.parametrize("hq,hkv,d", [(32, 8, 128), (8, 8, 64), (16, 1, 256), (20, 2, 128), (96, 8, 128)])
+@pytest.mark.parametrize("window,sinks,part", [(0, 0, 0), (1024, 4, 0), (16000, 129, 0), (0, 0, 64),
+                                               (700, 64, 320)])
+def test_workspace_of_the_largest_call_covers_the_smaller_ones(lib, hq, hkv, d, window, sinks, part):
+    """A buffer sized once for the most sequences and the longest context is enough for every
+    smaller call of either cache width, and does not shrink as the sizes grow."""
+    L = lib.library()
+    sizes = [1, 2, 3, 5, 8, 13, 16, 33, 64, 100, 257]
+    ctxs = [1, 64, 65, 200, 1024, 1536, 3071, 4096, 6144, 8192, 20000, 65536, 131072, 300000]
+
+    def bound(s, c):
+        return L.paged_attention_window_workspace_bytes(s, hq, hkv, d, c, part, window, sinks)
+
+    for s in sizes:
+        for c in ctxs:
+            need = max(L.paged_attention_window_call_bytes(s, hq, hkv, d, c, part, window, sinks, kv)
+                       for kv in (lib.BF16, lib.FP8_E4M3))
+            assert need <= bound(s, c)
+            for s2, c2 in ((sizes[-1], c), (s, ctxs[-1]), (s + 1, c), (s, c + 64), (sizes[-1], ctxs[-1])):
+                assert need <= bound(s2, c2), (s, c, s2, c2)
+                assert bound(s, c) <= bound(s2, c2), (s, c, s2, c2)
+
+
+def test_workspace_query_refuses_nothing_to_size(lib):
+    w = lib.library().paged_attention_window_call_bytes
+    assert w(2, 7, 2, 128, 640, 64, 0, 0, lib.BF16) == 0
+    assert w(0, 8, 2, 128, 640, 64, 0, 0, lib.BF16) == 0
+    assert w(2, 8, 2, 128, 640, 64, 0, 0, lib.BF16) == 2 * 8 * 10 * 130 * 4
+    assert w(2, 8, 2, 128, 640, 100, 0, 0, lib.BF16) == 0
