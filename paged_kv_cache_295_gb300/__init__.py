@@ -403,8 +403,8 @@ def _stream(stream):
 def reshape_and_cache(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale=None,
                       v_scale=None, device_status=None, stream=None):
     """Append token rows ``[T, Hkv, D]`` into one layer's ``[NB, bs, Hkv, D]`` cache."""
-    _per_head(k_scale, v_scale, "reshape_and_cache")
     T, hkv, d = k_new.shape
+    _per_head(k_scale, v_scale, hkv, "reshape_and_cache")
     nb, bs = k_cache.shape[0], k_cache.shape[1]
     st = library().reshape_and_cache(
         _dev(k_new, "k_new"), _dev(v_new, "v_new"), _dev(slot_mapping, "slot_mapping"),
@@ -504,22 +504,23 @@ def gather_cache(k_cache, v_cache, block_tables, row_start, num_rows, max_rows, 
                                          v_out, device_status), "gather_cache")
 
 
-def _block_scales(scale) -> bool:
-    """Whether these are scales per block; ``[1, Hkv]`` reads the same as ``[Hkv]``."""
-    return scale is not None and scale.dim() == 2 and scale.shape[0] != 1
+def _block_scales(scale, hkv) -> bool:
+    """Whether these are scales per block; ``[1, Hkv]`` and ``[Hkv, 1]`` read the same as ``[Hkv]``."""
+    return (scale is not None and scale.dim() == 2 and scale.shape[0] != 1
+            and scale.numel() != hkv)
 
 
-def _per_head(k_scale, v_scale, where):
-    if _block_scales(k_scale) or _block_scales(v_scale):
+def _per_head(k_scale, v_scale, hkv, where):
+    if _block_scales(k_scale, hkv) or _block_scales(v_scale, hkv):
         raise ValueError(f"{where} takes one scale per head, not scales per block")
 
 
-def _windowed(out, out_dtype, k_scale, v_scale, window, sinks) -> bool:
+def _windowed(out, out_dtype, k_cache, k_scale, v_scale, window, sinks) -> bool:
     """Whether a call needs the form with a window, scales per block or another output type."""
     if window or sinks:
         return True
-    f32 = _torch().float32
-    return bool(_block_scales(k_scale) or _block_scales(v_scale)
+    f32, hkv = _torch().float32, k_cache.shape[2]
+    return bool(_block_scales(k_scale, hkv) or _block_scales(v_scale, hkv)
                 or (out is not None and out.dtype != f32)
                 or (out_dtype is not None and out_dtype != f32))
 
@@ -584,7 +585,7 @@ def paged_attention_decode(q, k_cache, v_cache, block_tables, context_lens, scal
     ``paged_attention_decode_window`` (whose shapes are narrower; its workspace is
     ``workspace_bytes(..., window=window, sinks=sinks)``).
     """
-    if _windowed(out, out_dtype, k_scale, v_scale, window, sinks):
+    if _windowed(out, out_dtype, k_cache, k_scale, v_scale, window, sinks):
         return _decode_window(q, k_cache, v_cache, block_tables, context_lens, scale,
                               max_context_len, out, k_scale, v_scale, workspace, partition,
                               device_status, stream, window, sinks, out_dtype)
@@ -616,7 +617,7 @@ def paged_attention_decode_append(q, k_new, v_new, slot_mapping, k_cache, v_cach
     """``reshape_and_cache`` of one new token per sequence (``k_new`` / ``v_new``
     ``[S, Hkv, D]``, ``slot_mapping`` int64 ``[S]``, each the slot of position
     ``context_lens[s] - 1``) and ``paged_attention_decode``, as one call."""
-    _per_head(k_scale, v_scale, "paged_attention_decode_append")
+    _per_head(k_scale, v_scale, k_cache.shape[2], "paged_attention_decode_append")
     torch = _torch()
     S, hq, d = q.shape
     nb, bs, hkv, _ = k_cache.shape
@@ -645,7 +646,7 @@ def paged_attention_decode_noalloc(q, k_cache, v_cache, block_tables, context_le
                                    device_status=None, stream=None):
     """``paged_attention_decode`` into a caller-owned ``out`` with the library's
     built-in split-KV scratch (no device allocation by the library or here)."""
-    _per_head(k_scale, v_scale, "paged_attention_decode_noalloc")
+    _per_head(k_scale, v_scale, k_cache.shape[2], "paged_attention_decode_noalloc")
     S, hq, d = q.shape
     nb, bs, hkv, _ = k_cache.shape
     st = library().paged_attention_decode_noalloc(
@@ -669,7 +670,7 @@ def paged_attention_prefill(q, query_start, k_cache, v_cache, block_tables, cont
 
     ``window``, ``sinks``, scales ``[NB, >= Hkv]`` per block and ``out_dtype`` as in
     ``paged_attention_decode``; any of them takes ``paged_attention_prefill_window``."""
-    if _windowed(out, out_dtype, k_scale, v_scale, window, sinks):
+    if _windowed(out, out_dtype, k_cache, k_scale, v_scale, window, sinks):
         return _prefill_window(q, query_start, k_cache, v_cache, block_tables, context_lens, scale,
                                max_query_len, max_context_len, causal, out, k_scale, v_scale,
                                device_status, stream, window, sinks, out_dtype)

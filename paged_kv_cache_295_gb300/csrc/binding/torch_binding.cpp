@@ -143,17 +143,20 @@ int32_t tables_width(const Tensor& bt, int64_t seqs) {
   return count32(bt.size(1), "block_tables");
 }
 
-// Floats between the scales of two blocks; 0 for one scale per head.
+// Floats between the scales of two blocks; 0 for one scale per head ([heads], or any shape of as
+// many elements).
 int64_t scale_stride(const Tensor& ks, const Tensor& vs, const Cache& c) {
   if (!ks.defined() || !vs.defined()) refuse("an 8-bit cache needs k_scale and v_scale");
-  const bool per_head = ks.dim() == 1;
-  if (vs.sizes() != ks.sizes() || ks.scalar_type() != at::kFloat || vs.scalar_type() != at::kFloat ||
-      (per_head ? ks.size(0) != c.heads
-                : ks.dim() != 2 || ks.size(0) != c.blocks || ks.size(1) < c.heads))
+  auto stride = [&](const Tensor& t) -> int64_t {   // -1: neither form
+    if (t.scalar_type() != at::kFloat) return -1;
+    if (t.dim() == 2 && t.size(0) == c.blocks && t.size(1) >= c.heads) return t.size(1);
+    return t.numel() == c.heads ? 0 : -1;
+  };
+  if (stride(ks) < 0 || stride(vs) != stride(ks))
     refuse("k_scale and v_scale must be Float [" + std::to_string(c.heads) + "] or [" +
            std::to_string(c.blocks) + ", >= " + std::to_string(c.heads) + "], both alike, got " +
            show(ks) + " and " + show(vs));
-  return per_head ? 0 : ks.size(1);
+  return stride(ks);
 }
 
 at::ScalarType out_type(PyObject* dtype, const Tensor& out, at::ScalarType otherwise) {

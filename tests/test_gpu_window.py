@@ -435,3 +435,21 @@ def test_workspace_of_the_longest_context_is_used_by_shorter_calls(lib):
         # two bf16 roundings of results that differ by the merges' float32 steps
         assert (out.float() - own.float()).abs().max() <= 2.0 ** -7 * own.float().abs().max()
     assert used
+
+
+def test_scales_per_head_in_a_column(lib):
+    """``[Hkv, 1]`` scales give what ``[Hkv]`` ones do, in the plain and the windowed calls."""
+    import torch
+    case = PC.make(61, "fp8_e4m3", [300, 77], 2, 128, 16, scales="head")
+    d = case.device()
+    q = torch.randn((107, 8, 128), device="cuda").to(torch.bfloat16)
+    start = torch.tensor([0, 30, 107], dtype=torch.int32, device="cuda")
+    for window in (0, 50):
+        got = []
+        for shape in ((2,), (2, 1), (1, 2)):
+            kw = dict(k_scale=d["ks"].view(shape), v_scale=d["vs"].view(shape), window=window)
+            got.append((lib.paged_attention_decode(q[:2].contiguous(), d["k"], d["v"], d["tables"], d["lens"],
+                                                   0.09, 300, **kw),
+                        lib.paged_attention_prefill(q, start, d["k"], d["v"], d["tables"], d["lens"], 0.09,
+                                                    77, 300, **kw)))
+        assert all(torch.equal(a, b) for g in got for a, b in zip(g, got[0]))

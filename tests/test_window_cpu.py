@@ -296,3 +296,31 @@ def test_workspace_query_refuses_nothing_to_size(lib):
     assert w(0, 8, 2, 128, 640, 64, 0, 0, lib.BF16) == 0
     assert w(2, 8, 2, 128, 640, 64, 0, 0, lib.BF16) == 2 * 8 * 10 * 130 * 4
     assert w(2, 8, 2, 128, 640, 100, 0, 0, lib.BF16) == 0
+
+
+def test_scales_per_head_in_a_column_are_taken(lib):
+    """A contiguous ``[Hkv, 1]`` (or ``[1, Hkv]``) holds one scale per head: every call gets past
+    its checks of the scales (and stops at the CPU tensors)."""
+    hkv = 2
+    k8 = torch.zeros((4, 16, hkv, 128), dtype=torch.int8)
+    n, bt = torch.ones(1, dtype=torch.int32), torch.zeros((1, 2), dtype=torch.int32)
+    start = torch.tensor([0, 1], dtype=torch.int32)
+    rows, slots = torch.zeros((1, hkv, 128)), torch.zeros(1, dtype=torch.int64)
+    q, out = torch.zeros((1, 4, 128), dtype=torch.bfloat16), torch.zeros((1, 4, 128))
+    for shape in ((hkv, 1), (1, hkv), (hkv,)):
+        kw = dict(k_scale=torch.ones(shape), v_scale=torch.ones(shape))
+        for call in (lambda: lib.reshape_and_cache(rows, rows, slots, k8, k8, **kw),
+                     lambda: lib.paged_attention_decode_append(q, rows, rows, slots, k8, k8, bt, n, 0.1, 32, **kw),
+                     lambda: lib.paged_attention_decode_noalloc(q, k8, k8, bt, n, 0.1, 32, out, **kw),
+                     lambda: lib.paged_attention_decode(q, k8, k8, bt, n, 0.1, 32, **kw),
+                     lambda: lib.paged_attention_decode(q, k8, k8, bt, n, 0.1, 32, window=8, **kw),
+                     lambda: lib.paged_attention_prefill(q, start, k8, k8, bt, n, 0.1, 1, 32, **kw),
+                     lambda: lib.paged_attention_prefill(q, start, k8, k8, bt, n, 0.1, 1, 32, window=8, **kw),
+                     lambda: lib.gather_cache(k8, k8, bt, start, 1, 1, **kw)):
+            with pytest.raises(ValueError, match="CUDA tensor"):
+                call()
+        with pytest.raises(ValueError, match="num_blocks"):
+            lib.quantize_and_cache(rows, rows, k8, k8, *kw.values(), bt, n)
+    one = torch.zeros((1, 16, hkv, 128), dtype=torch.int8)      # a pool of one block
+    with pytest.raises(ValueError, match="CUDA tensor"):
+        lib.quantize_and_cache(rows, rows, one, one, torch.ones(1, hkv), torch.ones(1, hkv), bt, n)
