@@ -1,5 +1,6 @@
 """In-tree build of libpagedkv.so for sm_103a with nvcc (no cmake, no torch), and of
-_pkv_torch.so, the Python entry points that take torch tensors (g++, torch's headers).
+_pkv_torch.so, the Python entry points that take torch tensors (g++, torch's headers;
+left out where torch is not installed).
 
 Each translation unit compiles in parallel into ``_build/``; the shared
 libraries land next to this file.  A rebuild happens when any source or header
@@ -9,6 +10,7 @@ from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
@@ -36,6 +38,13 @@ def nvcc() -> str:
     return exe
 
 
+def has_torch() -> bool:
+    try:
+        return importlib.util.find_spec("torch") is not None
+    except ValueError:      # a stand-in in sys.modules
+        return False
+
+
 def sources():
     cu = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     cpp = sorted(glob.glob(os.path.join(CSRC, "*.cpp")))
@@ -45,9 +54,10 @@ def sources():
 
 
 def stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    built = [LIB, BINDING] if has_torch() else [LIB]
+    if not all(os.path.exists(f) for f in built):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(f) for f in built)
     return any(os.path.getmtime(f) > t for f in sources()[2] + [__file__])
 
 
@@ -79,8 +89,8 @@ def binding_commands():
 
 
 def build_library(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile every CUDA / C++ unit for sm_103a and link ``libpagedkv.so``, then the torch
-    binding against it."""
+    """Compile every CUDA / C++ unit for sm_103a and link ``libpagedkv.so``, then, where torch is
+    installed, the torch binding against it."""
     if not force and not stale():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
@@ -94,18 +104,21 @@ def build_library(force: bool = False, verbose_ptxas: bool = False) -> str:
     for src in cpp:
         obj = os.path.join(BUILD, os.path.basename(src) + ".o")
         jobs.append([os.environ.get("CXX", "g++"), *CXX_FLAGS, "-c", src, "-o", obj])
-    bind, bind_link = binding_commands()
-    jobs.append(bind)
+    objs = [j[-1] for j in jobs]
+    bind_link = None
+    if has_torch():
+        bind, bind_link = binding_commands()
+        jobs.append(bind)
     logs = []
     with cf.ThreadPoolExecutor(max_workers=max(1, min(len(jobs), os.cpu_count() or 4))) as ex:
         for out in ex.map(_run, jobs):
             logs.append(out)
-    objs = [j[-1] for j in jobs[:-1]]
     tmp = LIB + ".tmp"
     _run([nv, *ARCH, "-shared", "-o", tmp, *objs])
     os.replace(tmp, LIB)
-    _run(bind_link)
-    os.replace(BINDING + ".tmp", BINDING)
+    if bind_link:
+        _run(bind_link)
+        os.replace(BINDING + ".tmp", BINDING)
     if verbose_ptxas:
         with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
             f.write("\n".join(logs))
