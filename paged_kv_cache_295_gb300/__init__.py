@@ -441,6 +441,11 @@ def _binding():
     if _ext is None:
         _torch()
         library()
+        from . import _build
+        built, here = _build.built_abi(), _build.binding_abi()
+        if built not in (None, here):
+            raise RuntimeError(f"_pkv_torch.so was built for {built}, this is {here}: run "
+                               "paged_kv_cache_295_gb300._build.build_library()")
         try:
             from . import _pkv_torch
         except ImportError as e:

@@ -4,16 +4,19 @@ left out where torch is not installed).
 
 Each translation unit compiles in parallel into ``_build/``; the shared
 libraries land next to this file.  A rebuild happens when any source or header
-is newer than a library.
+is newer than a library, or when torch or Python are not the ones that the binding
+was built for.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -45,6 +48,25 @@ def has_torch() -> bool:
         return False
 
 
+def binding_abi() -> str:
+    """What the binding's C++ and Python ABI depend on."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:     # a torch built in place
+        import torch
+        version = torch.__version__
+    return f"torch {version}, {sys.implementation.cache_tag}"
+
+
+def built_abi():
+    """``binding_abi()`` of the binding that is there; None for an unknown one."""
+    try:
+        with open(BINDING + ".abi") as f:
+            return f.read()
+    except OSError:
+        return None
+
+
 def sources():
     cu = sorted(glob.glob(os.path.join(CSRC, "*.cu")))
     cpp = sorted(glob.glob(os.path.join(CSRC, "*.cpp")))
@@ -56,6 +78,8 @@ def sources():
 def stale() -> bool:
     built = [LIB, BINDING] if has_torch() else [LIB]
     if not all(os.path.exists(f) for f in built):
+        return True
+    if has_torch() and built_abi() != binding_abi():
         return True
     t = min(os.path.getmtime(f) for f in built)
     return any(os.path.getmtime(f) > t for f in sources()[2] + [__file__])
@@ -119,6 +143,8 @@ def build_library(force: bool = False, verbose_ptxas: bool = False) -> str:
     if bind_link:
         _run(bind_link)
         os.replace(BINDING + ".tmp", BINDING)
+        with open(BINDING + ".abi", "w") as f:
+            f.write(binding_abi())
     if verbose_ptxas:
         with open(os.path.join(BUILD, "ptxas.log"), "w") as f:
             f.write("\n".join(logs))
@@ -126,5 +152,4 @@ def build_library(force: bool = False, verbose_ptxas: bool = False) -> str:
 
 
 if __name__ == "__main__":
-    import sys
     print(build_library(force=True, verbose_ptxas="-v" in sys.argv))

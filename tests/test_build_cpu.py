@@ -43,3 +43,22 @@ def test_binding_builds_with_torch(recorded):
     del recorded[:]
     _build.build_library()
     assert not recorded
+
+
+def test_another_torch_or_python_rebuilds_the_binding(recorded, monkeypatch):
+    pytest.importorskip("torch")
+    _build.build_library()
+    monkeypatch.setattr(_build.importlib.metadata, "version", lambda name: "99.0")
+    assert _build.stale()
+    del recorded[:]
+    _build.build_library()
+    assert any("-ltorch_python" in cmd for cmd in recorded) and not _build.stale()
+
+
+def test_binding_of_another_torch_is_not_loaded(recorded, monkeypatch, lib):
+    pytest.importorskip("torch")
+    _build.build_library()
+    monkeypatch.setattr(lib, "_ext", None)
+    monkeypatch.setattr(_build.importlib.metadata, "version", lambda name: "99.0")
+    with pytest.raises(RuntimeError, match="built for torch"):
+        lib._binding()
