@@ -362,6 +362,10 @@ PyObject* do_prefill(PyObject* const* a, Py_ssize_t na) {
   const int32_t max_query = integer32(a[7], "max_query_len"), max_ctx = integer32(a[8], "max_context_len"),
                 window = integer32(a[14], "window"), sinks = integer32(a[15], "sinks");
   const int causal = PyObject_IsTrue(a[9]);
+  if (causal < 0) {
+    PyErr_Clear();
+    refuse("causal must be a truth value");
+  }
   const at::Device dev = cuda_device(p.q);
   const c10::cuda::CUDAGuard guard(dev);
   Tensor out = attention_out(p, tensor(a[10], "out", true), a[16]);

@@ -324,3 +324,11 @@ def test_scales_per_head_in_a_column_are_taken(lib):
     one = torch.zeros((1, 16, hkv, 128), dtype=torch.int8)      # a pool of one block
     with pytest.raises(ValueError, match="CUDA tensor"):
         lib.quantize_and_cache(rows, rows, one, one, torch.ones(1, hkv), torch.ones(1, hkv), bt, n)
+
+
+def test_causal_must_be_a_truth_value(lib):
+    k, n = torch.zeros((4, 16, 2, 128), dtype=torch.bfloat16), torch.ones(1, dtype=torch.int32)
+    bt, start = torch.zeros((1, 2), dtype=torch.int32), torch.tensor([0, 1], dtype=torch.int32)
+    q = torch.zeros((1, 4, 128), dtype=torch.bfloat16)
+    with pytest.raises(ValueError, match="causal"):
+        lib.paged_attention_prefill(q, start, k, k, bt, n, 0.1, 1, 32, causal=np.array([1, 0]), window=8)
