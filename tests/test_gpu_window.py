@@ -453,3 +453,55 @@ def test_scales_per_head_in_a_column(lib):
                         lib.paged_attention_prefill(q, start, d["k"], d["v"], d["tables"], d["lens"], 0.09,
                                                     77, 300, **kw)))
         assert all(torch.equal(a, b) for g in got for a, b in zip(g, got[0]))
+
+
+def test_window_over_everything_and_the_plain_decode_agree(lib):
+    """A window that covers every context and the plain call: within the sum of both bounds."""
+    import torch
+    case = PC.make(62, "bf16", [700, 33, 1, 2048], 2, 128, 16)
+    scale = 128 ** -0.5
+    q = PC.bf16_bits(np.random.default_rng(63).standard_normal((4, 8, 128)))
+    d = case.device()
+    plain = lib.paged_attention_decode(GC.to_torch(q, "bf16"), d["k"], d["v"], d["tables"], d["lens"],
+                                       scale, max(case.lens))
+    assert plain.dtype == torch.float32
+    plain = plain.cpu().numpy().astype(np.float64)
+    got = decode(lib, case, q, "bf16", scale, "f32", window=4096)
+    q64 = GC.OA.to_f64(q, "bf16")
+    for s, n in enumerate(case.lens):
+        K, V = case.values(s)
+        o, mag, reach = OB.attend(q64[s:s + 1], [n - 1], K, V, scale, 0, 0)
+        lim = [PC.attention_bound(case, q64[s:s + 1], o, mag, reach, scale, False, False, True, n, e_p=e)[0]
+               for e in (2.0 ** -24, 2.0 ** -16)]
+        assert (np.abs(got[s] - plain[s]) <= lim[0] + lim[1]).all()
+        assert (np.abs(got[s] - o[0]) <= lim[0]).all()
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("q_type", ["bf16", "f32"])
+def test_decode_weights_in_three_parts(lib, d, q_type):
+    """bf16 caches, float32 outputs: weights hold 2^-24, two parts (2^-16) would not pass.
+
+    Each query sees two keys of one chunk, with logits 0 and -1 < z <= 0 from one product each
+    (exact) and values +1 and -1.  In units of 2^-23 of sum p |v| = 1: the exponent's argument is
+    rounded three times, 2^-24 of at most 1 each (1); ex2.approx 2^-22 (2); the parts 2^-24 (1/2):
+    on numerator and denominator, 7.  The products' sums: three MMAs of two terms (6); l, the
+    merge of warps and the quotient (2): 15."""
+    S, hq = 64, 8
+    lens = [18 + (s % 14) for s in range(S)]         # tokens ctx - 2, ctx - 1 in chunk 16 .. 31
+    case = PC.make(64, "bf16", lens, 1, d, 16)
+    one = PC.bf16_bits(np.ones((1, d)))
+    first = np.zeros((1, d))
+    first[0, 0] = -1.0
+    for s, n in enumerate(lens):
+        for t, k, v in ((n - 2, PC.bf16_bits(first), one), (n - 1, PC.bf16_bits(0 * first), one ^ 0x8000)):
+            at = case.tables[s][t // 16], t % 16
+            case.k[at], case.v[at] = k, v
+    q64 = np.random.default_rng(65).standard_normal((S, hq, d))
+    q64[..., 0] = np.random.default_rng(66).uniform(0.0, 1.0, (S, hq))
+    q64 = GC.OA.to_f64(PC.bf16_bits(q64), "bf16")
+    q = q64.astype(np.float32) if q_type == "f32" else PC.bf16_bits(q64)
+    got = decode(lib, case, q, q_type, 0.999, "f32", window=2)
+    p = np.exp(-q64[..., 0] * float(np.float32(0.999)))
+    err = np.abs(got - ((p - 1) / (p + 1))[..., None]).max()
+    assert err <= 15 * 2.0 ** -23, err
