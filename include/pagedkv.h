@@ -578,6 +578,9 @@ size_t paged_attention_window_call_bytes(int32_t num_seqs, int32_t num_q_heads,
  *                  scale_stride 0.  K scales are not negative; V scales count
  *                  as at least 2^-80.
  *   out, out_dtype : device [num_seqs, num_q_heads, head_dim], f32 or bf16.
+ *                  Weights enter P V as 16-bit parts: bf16 caches 2^-24 of each
+ *                  weight (f32) or 2^-16 (bf16), FP8 caches 2^-22, INT8 caches
+ *                  2^-22 (f32) or 2^-11 (bf16).
  *   partition_tokens : counted in visible tokens.
  *   workspace    : of paged_attention_window_call_bytes or more.  Calls whose kernels may
  *                  overlap on the GPU need one each.  Small grids merge their partitions within thread-block

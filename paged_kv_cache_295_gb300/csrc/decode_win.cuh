@@ -25,10 +25,10 @@
 //    scales of the blocks; the sum takes p itself.
 //  * The weights enter P V as 16-bit parts: for a float32 output three of bf16
 //    (2^-24; the third costs 2 % of the time) or, on 8-bit caches (HL), two of
-//    fp16 (2^-22); for a bf16 output two of bf16, or one of fp16 (2^-11, an
-//    eighth of the output's own rounding).  INT8 codes keep their offset of
-//    1152 only in the last case (see decode_mma2.cuh), else they are widened
-//    exactly.
+//    fp16 (2^-22); for a bf16 output two of bf16 (2^-16) or, on FP8 caches, two of
+//    fp16.  INT8 caches with a bf16 output take one of fp16 (2^-11 of each weight,
+//    where a code is off by half a step, 2^-8 or more of its value) and keep the
+//    codes' offset of 1152 (see decode_mma2.cuh), else codes are widened exactly.
 //
 // Bound by HBM on long contexts, by what a CTA costs before its first tile (context length,
 // table entry and scales, each load behind the one before: as long as about 110 tokens) on
@@ -162,7 +162,7 @@ __global__ void __launch_bounds__(NW * 32)
   constexpr bool I8 = std::is_same<KV, INT8>::value;
   constexpr bool BIAS = I8 && !HL;   // INT8 codes enter the products as code + 1152
   static_assert(!F8 || D == 128, "the 8-bit path is built for head_dim 128");
-  static_assert(F8 || HL, "16-bit caches always carry P as hi + lo");
+  static_assert(I8 || HL, "one weight part only beside INT8 codes");
   constexpr int RT = CH / 16;
   constexpr int CHL = CH == 32 ? 5 : 4;
   static_assert(CH == 16 || (F8 && CH == 32), "16-token chunks, or 32 for 8-bit rows");

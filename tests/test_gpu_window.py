@@ -505,3 +505,34 @@ def test_decode_weights_in_three_parts(lib, d, q_type):
     p = np.exp(-q64[..., 0] * float(np.float32(0.999)))
     err = np.abs(got - ((p - 1) / (p + 1))[..., None]).max()
     assert err <= 15 * 2.0 ** -23, err
+
+
+@pytest.mark.parametrize("q_type", ["bf16", "f32"])
+def test_decode_weights_of_fp8_caches_in_two_parts(lib, q_type):
+    """FP8 caches, bf16 outputs: a bf16 output is the float32 one rounded.
+
+    Two keys with logits 0 and -0.005 < z <= 0 and values +1 and -1, as above: the outputs are
+    below 0.0025, so their rounding (2^-8 of them) is below 2^-16, and one fp16 part (2^-11 of a
+    weight) would not pass.  In units of 2^-23: the argument (1), ex2.approx (2) and the parts 2^-22
+    (2) on numerator and denominator, 10; the sums (6), l and the quotient (2): 18."""
+    S, hq, kv = 64, 8, "fp8_e4m3"
+    lens = [34 + (s % 30) for s in range(S)]         # both tokens in chunk 32 .. 63
+    case = PC.make(67, kv, lens, 1, 128, 16, scales="head")
+    case.ks[:], case.vs[:] = 1.0, 2.0 ** -6
+    first = np.zeros((1, 128), dtype=np.float32)
+    first[0, 0] = -1.0
+    for s, n in enumerate(lens):
+        for t, k, v in ((n - 2, first, 64.0), (n - 1, 0 * first, -64.0)):
+            at = case.tables[s][t // 16], t % 16
+            case.k[at] = OB.encode(k, kv)
+            case.v[at] = OB.encode(np.full((1, 128), v, dtype=np.float32), kv)
+    q64 = np.zeros((S, hq, 128))
+    q64[..., 0] = np.random.default_rng(69).uniform(0.0, 0.005, (S, hq))
+    q64 = GC.OA.to_f64(PC.bf16_bits(q64), "bf16")
+    q = q64.astype(np.float32) if q_type == "f32" else PC.bf16_bits(q64)
+    p = np.exp(-q64[..., 0] * float(np.float32(0.999)))
+    want = ((p - 1) / (p + 1))[..., None]
+    for out in ("bf16", "f32"):
+        got = decode(lib, case, q, q_type, 0.999, out, window=2)
+        lim = 18 * 2.0 ** -23 + (2.0 ** -8 * np.abs(want) if out == "bf16" else 0.0)
+        assert (np.abs(got - want) <= lim).all(), (out, float((np.abs(got - want) / lim).max()))
