@@ -515,8 +515,8 @@ pkv_status paged_attention_prefill(const void* q, const int32_t* query_start,
  * Two sequences of one call must not append into the same block (share blocks by
  * copy-on-write).  A bad query_start or context flags PKV_DEV_BAD_CONTEXT and
  * skips the sequence, a bad block flags PKV_DEV_BAD_BLOCK and is skipped.
- * head_dim a multiple of 16; block_size a power of two up to 4096; caches and rows
- * 16-byte aligned. */
+ * head_dim a multiple of 16; block_size a power of two up to 4096 (attention over the cache
+ * needs head_dim 128 and block_size >= 8); caches and rows 16-byte aligned. */
 pkv_status quantize_and_cache(const void* k_new, const void* v_new, const int32_t* query_start,
                               const int32_t* block_tables, const int32_t* context_lens,
                               void* k_cache, void* v_cache, float* k_scales, float* v_scales,

@@ -33,8 +33,9 @@
 // Bound by HBM on long contexts, by what a CTA costs before its first tile (context length,
 // table entry and scales, each load behind the one before: as long as about 110 tokens) on
 // windows of about 1,000.  Measured: 32 sequences x 32 heads, fp8, contexts up to 4,096:
-// 100 us (89 at the copy rate); 8 x 8 heads GQA-4, int8, 32K to 128K: 202 (189); 64 x 8
-// heads GQA-8, bf16, window 1,024 and 4 sinks: 54 (40); 4 x 8 heads, window 256: 7.
+// 103 us (89 at the copy rate); 8 x 8 heads GQA-4, int8, 32K to 128K: 205 (189); 64 x 8
+// heads GQA-8, bf16, window 1,024 and 4 sinks: 54 (40), at head_dim 64 36 (20) and at 256
+// 105 (80); 4 x 8 heads, window 256: 7.
 #pragma once
 
 #include "decode_mma2.cuh"

@@ -15,13 +15,15 @@
 // this one's softmax is still at its exponentials, and with P out of shared memory
 // the softmax stores it in two instructions.
 //
-// What bounds it (clock64 trace, two query tiles of 128 rows, steady state): the chain of a
-// key tile in the softmax warps - look at the barriers (over 100 cycles each, so two are
-// asked together), S load 110, maximum 260, exponentials 500, P store 200 to 600 - next to the
-// MMAs, which hold both issuers for 1,200 cycles a key tile; and, on 8-bit caches, instruction
-// fetch: the roles' loops together overrun the instruction cache.  So: the issuers' code is
-// uniform (pw_elect); a mask is built only for tiles that cut some row of the warp; 8-bit tiles
-// are widened by four warps of their own.
+// What bounds it (clock64 trace with one weight part, two query tiles of 128 rows, steady
+// state): the chain of a key tile in the softmax warps - look at the barriers (over 100 cycles
+// each, so two are asked together), S load 110, maximum 260, exponentials 500, P store 200 to
+// 600 - next to the MMAs, which hold both issuers for 1,200 cycles a key tile; and, on 8-bit
+// caches, instruction fetch: the roles' loops together overrun the instruction cache.  So: the
+// issuers' code is uniform (pw_elect); a mask is built only for tiles that cut some row of the
+// warp; 8-bit tiles are widened by four warps of their own.  A key tile takes 1,050 ns on bf16
+// caches, where its products alone need 1,000, and on 8-bit ones 1,120 to 1,130 with a bf16 output
+// (667) and 1,260 to 1,350 with a float32 one (1,000).
 //
 // bf16 caches carry P as two bf16 parts (2^-16 of each weight) whatever the output's type: a bf16
 // output is the float32 one rounded.  One part would be off by 2^-8 of each weight, which is
@@ -37,8 +39,8 @@
 //
 // Measured, chunks of 512 tokens at contexts up to 4,096: 16 x 32 heads, bf16, window 1,024,
 // f32 output 199 us (607 TFLOP/s); 16 x 8 heads GQA-4, fp8, no window, bf16 output 282 (927
-// TFLOP/s), f32 output 336; the same in int8 292 and 349.  Three ragged chunks of up to 700 tokens, 8 heads GQA-8, window 4,096, bf16
-// output: 147 (858 TFLOP/s).  Every CTA has about 10 us of setup, Q, first copies and epilogue
+// TFLOP/s), f32 output 336; the same in int8 292 and 349.  Three ragged chunks of up to 700
+// tokens, 8 heads GQA-8, window 4,096, bf16 output: 147 (858 TFLOP/s).  Every CTA has about 10 us of setup, Q, first copies and epilogue
 // besides its key tiles, of which a window leaves few.
 //
 // Every wait is bounded (2 s) and gives up when another role has given up; the copies in
@@ -164,7 +166,7 @@ __device__ __forceinline__ void pw_st_wait() {
 
 // One lane of the warp, the same each time; the compiler knows its code uniform, with `warp`,
 // the TMEM base and the lengths shuffled, and keeps descriptors and barriers in uniform
-// registers: the three measured cases took 192, 126 and 287 us, with `lane == 0` 209, 146 and 322.
+// registers: the three measured cases take 196, 146 and 285 us, with `lane == 0` 202, 157 and 302.
 __device__ __forceinline__ bool pw_elect() {
   uint32_t e = 0;
   asm volatile("{\n .reg .b32 x;\n .reg .pred p;\n elect.sync x|p, 0xffffffff;\n @p mov.s32 %0, 1;\n}\n"
@@ -346,8 +348,8 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
 
   // 8-bit caches launch 512 threads of 128 registers; the softmax warps take 168 and the
   // others 88 (256 x 168 + 256 x 88 = 512 x 128).
-  // The issuing roles: one lane's code on bf16 caches (123 us on the three ragged chunks named
-  // above, 130 as a whole warp's), a whole warp's on 8-bit ones (284 us on the fp8 chunks, 292
+  // The issuing roles: one lane's code on bf16 caches (146 us on the three ragged chunks named
+  // above, 149 as a whole warp's), a whole warp's on 8-bit ones (285 us on the fp8 chunks, 291
   // as one lane's).
   auto issuer = [&] { return !C8 || pw_elect(); };
   auto issuer_wait = [&](uint32_t bar, uint32_t parity) {
@@ -532,8 +534,8 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
     const int r0 = (warp & 1) * 32;
     const uint8_t* raw = sm + LY::raw() + (is_v ? kPfRawBufs * kRawTile : 0) + (r0 + lane) * 128;
     // Units per pass.  The roles' loops together overrun the instruction cache, which slows
-    // the softmax warps: INT8, whose widening is the longer code, took 1,300 ns a key tile with
-    // one or two units a pass and 1,780 with all eight at once.
+    // the softmax warps: INT8, whose widening is the longer code, takes 1,349 ns a key tile with
+    // two units a pass and 1,411 with all eight at once (float32 output; bf16 1,130 and 1,118).
     constexpr int kStep = 2;
     auto off = [&](int u) { return (u ^ (lane & 7)) << 4; };   // 16-byte unit u in a row = lane (mod 8)
     for (int j = 0; j < ntiles; ++j) {

@@ -19,7 +19,9 @@
 // Both are bound by HBM: the new rows read once and their codes written (201 MB for 8,192
 // tokens x 32 heads x 128 in bf16: 35.3 us, 29.7 at the copy rate), the codes read and the
 // rows written (35.6 us against 31.9 for the same number of rows).  A call with one token
-// per sequence is launch latency: 3 us.
+// per sequence is launch latency: 3 us.  Large blocks keep a team of up to 512 threads for one
+// head's rows: the same append into blocks of 128 takes 44 us, one of 64 x 128 tokens x 8 heads
+// into blocks of 256 18 (7.4 at the copy rate).
 #include <type_traits>
 
 #include "common.cuh"
@@ -94,7 +96,7 @@ __device__ __forceinline__ Chunk load_chunk(const QuantParams& p, int s) {
 }
 
 // 8 consecutive elements of a row, as loaded.  kHeld of them per thread stay in
-// registers between the maximum and the codes, and as many of the next head's.
+// registers between the maximum and the codes.
 template <typename Src>
 struct Vec8;
 template <>

@@ -35,7 +35,9 @@ class PagedKVCache:
 
     ``block_scales`` (FP8 and INT8): every block holds one scale per layer, K or V, and
     head, chosen as rows are appended (``append_rows``); else ``k_scale`` / ``v_scale``
-    ``[num_layers, num_kv_heads]`` are the caller's.
+    ``[num_layers, num_kv_heads]`` are the caller's.  Such a cache is written and read back at any
+    head_dim that is a multiple of 16 and block size from 1 to 4096; attention over it needs
+    head_dim 128 and blocks of 8 or more.
     """
 
     def __init__(self, num_layers, num_kv_heads, head_dim, block_size, num_blocks, kv_dtype,
