@@ -366,8 +366,8 @@ pkv_status pkv_test_force_decode_kernel(int32_t kernel);
  * copies in flight and leaves its share out of the output; the call itself
  * returns PKV_OK and the context stays usable.  Launches of
  * paged_attention_decode_window do the same; those of
- * paged_attention_prefill_window arm the first V tile of CTA (0, 0, 0), whose
- * rows then stay unwritten.  bytes = 0 restores normal
+ * paged_attention_prefill and paged_attention_prefill_window arm the first V tile
+ * of CTA (0, 0, 0), whose rows then stay unwritten.  bytes = 0 restores normal
  * launches.  bytes must be a multiple of 16 and at most 65536, else
  * INVALID_ARG.  Process-wide, like pkv_test_force_decode_kernel. */
 pkv_status pkv_test_decode_stall(uint32_t bytes);

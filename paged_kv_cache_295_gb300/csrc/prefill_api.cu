@@ -75,6 +75,7 @@ extern "C" pkv_status paged_attention_prefill(
   p.max_context_len = max_context_len;
   p.num_tokens = num_tokens;
   p.qk_scale_log2 = scale * 1.4426950408889634f;
+  p.test_stall_bytes = test_stall_bytes();
   p.k_scale = codes8 ? k_scale : nullptr;
   p.v_scale = codes8 ? v_scale : nullptr;
 

@@ -78,6 +78,7 @@ struct PrefillParams {
   float qk_scale_log2;
   const float* k_scale;          // FP8 caches: [num_kv_heads] dequant scales
   const float* v_scale;
+  uint32_t test_stall_bytes;     // CTA (0, 0, 0)'s first V tile waits for these in vain; 0 but in tests
 };
 
 // 2^x with the MUFU instruction (relative error about 2^-22; 2^-inf = +0,
@@ -241,6 +242,8 @@ __global__ void __launch_bounds__(kPfThreads, 1)
     mbar_init(smem_u32(&drain[1]), 1);
     for (int i = 0; i < 2 * kPfRawBufs; ++i)
       mbar_init(smem_u32(&raw_full[i / kPfRawBufs][i % kPfRawBufs]), 1);
+    if (p.test_stall_bytes != 0 && blockIdx.x + blockIdx.y + blockIdx.z == 0)
+      mbar_expect_tx(smem_u32(&full_v[0]), p.test_stall_bytes);
     abort_sh = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }
@@ -701,8 +704,10 @@ __global__ void __launch_bounds__(kPfThreads, 1)
       // while it still needs this tile, else by tile B's; after the V copies
       // landed (a partly valid box also brings rows past the context)
       const bool zeroer = (t == 0) == (j < nt_a);
+      // (a vote: lanes that left the loop alone would miss the warp-wide instructions below)
       if (zeroer && vmask != ~0ull &&
-          !tc_wait(smem_u32(&full_v[j % STAGES]), (j / STAGES) & 1, abort_flag))
+          !__all_sync(0xffffffffu,
+                      tc_wait(smem_u32(&full_v[j % STAGES]), (j / STAGES) & 1, abort_flag)))
         alive = false;
       if (zeroer && alive && r < kPfKeys && !((vmask >> r) & 1ull)) {
         uint8_t* vrow = sm + kRing + (j % STAGES) * LY::kStage + 2 * LY::kKVHalf + r * 128;

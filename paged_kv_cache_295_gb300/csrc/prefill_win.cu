@@ -75,6 +75,7 @@ extern "C" pkv_status paged_attention_prefill_window(
   p.max_context_len = max_context_len;
   p.num_tokens = num_tokens;
   p.qk_scale_log2 = scale * 1.4426950408889634f;
+  p.test_stall_bytes = test_stall_bytes();
   p.k_scale = codes ? k_scale : nullptr;
   p.v_scale = codes ? v_scale : nullptr;
   w.out = out;
@@ -82,7 +83,6 @@ extern "C" pkv_status paged_attention_prefill_window(
   w.out_bf16 = out_dtype == PKV_BF16;
   w.window = window;
   w.sinks = sinks;
-  w.test_stall_bytes = test_stall_bytes();
 
   CUtensorMap tk, tv;
   const int64_t rows = num_blocks * block_size;

@@ -60,7 +60,6 @@ struct PrefillWinParams {
   int32_t out_bf16;
   int32_t window;           // 0: none
   int32_t sinks;
-  uint32_t test_stall_bytes;   // CTA (0, 0, 0)'s first V tile waits for these in vain; 0 but in tests
 };
 
 // The key tiles a CTA walks: the sinks' tiles, then those from its first query's
@@ -228,8 +227,8 @@ __global__ void __launch_bounds__(KIND == 0 ? kPfThreads : kPwThreads8, 1)
       mbar_init(smem_u32(&raw_full[i / kPfRawBufs][i % kPfRawBufs]), 1);
       mbar_init(smem_u32(&raw_free[i / kPfRawBufs][i % kPfRawBufs]), 2);
     }
-    if (wp.test_stall_bytes != 0 && blockIdx.x + blockIdx.y + blockIdx.z == 0)
-      mbar_expect_tx(smem_u32(&full_v[0]), wp.test_stall_bytes);
+    if (p.test_stall_bytes != 0 && blockIdx.x + blockIdx.y + blockIdx.z == 0)
+      mbar_expect_tx(smem_u32(&full_v[0]), p.test_stall_bytes);
     abort_sh = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
   }

@@ -92,3 +92,37 @@ def test_windowed_waits_run_out_and_the_next_calls_are_clean(lib, kv):
         lib.stall_decode_for_test(0)
     for (out, st, _), (want, _) in zip(both(), clean):
         assert st == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3", "int8"])
+def test_prefill_waits_run_out_and_the_next_call_is_clean(lib, kv):
+    """The plain prefill, whose only V tile is a cut one: as above."""
+    import torch
+    from tests import paged_cases as PC
+    lens = [50, 40, 30]
+    case = PC.make(73, kv, lens, 2, 128, 16, scales="head")
+    d = case.device()
+    q = torch.randn((sum(lens), 8, 128), device="cuda").to(torch.bfloat16)
+    start = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call():
+        status.zero_()
+        torch.cuda.synchronize()
+        t0 = time.monotonic()
+        out = lib.paged_attention_prefill(q, start, d["k"], d["v"], d["tables"], d["lens"], 0.09, 50, 50,
+                                          k_scale=d.get("ks"), v_scale=d.get("vs"), device_status=status)
+        torch.cuda.synchronize()
+        return out, int(status.item()), time.monotonic() - t0
+
+    want, st, _ = call()
+    assert st == 0
+    lib.stall_decode_for_test(16)
+    try:
+        _, st, waited = call()
+        assert st & lib.DEV_TIMEOUT, st
+        assert 1.5 <= waited < 30.0, waited
+    finally:
+        lib.stall_decode_for_test(0)
+    out, st, _ = call()
+    assert st == 0 and torch.equal(out, want)
