@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   // TMEM: tile t's Q at columns 256t + [0, 64), S at 256t + 64, O at 256t + 128
   const uint32_t tm = tmem_base_sh;
 
+  int copied = 0;   // copying warps: key tiles whose copies were started
   if (warp == 8 || warp == 11) {
     // --------------------- TMA producers: warp 8 K, warp 11 V -------------------
     // Per key tile, lane 2i + h looks up box i's block (one round trip, issued
@@ -313,6 +314,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
         const int z = (blk << p.bs_log2) + (kb & ((1 << p.bs_log2) - 1));
         tma_load_3d(dst, is_v ? &tmap_v : &tmap_k, hh * 64, g, z, bar);
       }
+      copied = j + 1;
     }
     } else {
       // FP8 caches.  TMA brings a key tile's codes, [64 keys][128 B] in one
@@ -347,6 +349,7 @@ __global__ void __launch_bounds__(kPfThreads, 1)
           tma_load_3d(raw_a + (jj % kPfRawBufs) * LY::kRawTile + lane * box_rows * 128,
                       is_v ? &tmap_v : &tmap_k, 0, g, z, rbar);
         }
+        copied = jj + 1;
         return valid;
       };
       // valids[i]: the boxes of tile j + i that have data (a window that moves
@@ -747,6 +750,14 @@ __global__ void __launch_bounds__(kPfThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (*abort_flag && (warp == 8 || warp == 11)) {   // copies may be in flight: no role waits for them now
+    constexpr int kBufs = FP8 ? kPfRawBufs : STAGES;
+    const int is_v = warp == 11 ? 1 : 0;
+    volatile int no_abort = 0;
+    for (int j = max(0, copied - kBufs); j < copied; ++j)
+      tc_wait(smem_u32(FP8 ? &raw_full[is_v][j % kBufs] : is_v ? &full_v[j % kBufs] : &full[j % kBufs]),
+              (j / kBufs) & 1, &no_abort);
+  }
   if (warp == 0)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;\n" ::"r"(tm) : "memory");
   if (tid == 0 && *abort_flag) flag_status(p.status, PKV_DEV_TIMEOUT);
