@@ -582,9 +582,10 @@ size_t paged_attention_window_call_bytes(int32_t num_seqs, int32_t num_q_heads,
  *                  weight (f32) or 2^-16 (bf16), FP8 caches 2^-22, INT8 caches
  *                  2^-22 (f32) or 2^-11 (bf16).
  *   partition_tokens : counted in visible tokens.
- *   workspace    : of paged_attention_window_call_bytes or more.  Calls whose kernels may
- *                  overlap on the GPU need one each.  Small grids merge their partitions within thread-block
- *                  clusters and need none.
+ *   workspace    : of paged_attention_window_call_bytes or more.  Calls whose
+ *                  kernels may overlap on the GPU need one each.  Small grids
+ *                  merge their partitions within thread-block clusters and need
+ *                  none.
  * Supported: bf16 caches with head_dim 64, 128 or 256; FP8 and INT8 caches with
  * head_dim 128; num_q_heads / num_kv_heads <= 16; block_size a power of two in
  * [8, 4096]; max_context_len <= 2^30. */
@@ -600,10 +601,10 @@ pkv_status paged_attention_decode_window(
 /* paged_attention_prefill with the same window, sinks, scales and output types:
  * the query at position p (of a chunk's last n_s positions) sees token t <= p when
  * t > p - window or t < sinks.  window > 0 needs causal = 1; sinks need a window.
- * Weights enter P V as 16-bit values: bf16 caches as two bf16 parts (2^-16 of each weight,
- * whatever the output type), 8-bit caches as two fp16 parts for a float32 output (2^-22) and
- * as one for a bf16 output (2^-11), and 2^-32 of the row's largest weight.  Table entries of blocks
- * that no query of the chunk sees are not read.  A key that a query does not see, but
+ * Weights enter P V as 16-bit values: bf16 caches as two bf16 parts (2^-16 of each
+ * weight, whatever the output type), 8-bit caches as two fp16 parts for a float32
+ * output (2^-22) and as one for a bf16 output (2^-11), and 2^-32 of the row's largest
+ * weight.  Table entries of blocks that no query of the chunk sees are not read.  A key that a query does not see, but
  * another one of the same work tile (up to 256 query rows) does, has weight 0 there; a V
  * value of it that is not finite gives NaN.  max_context_len <= 2^30; shapes
  * and errors otherwise as paged_attention_prefill. */

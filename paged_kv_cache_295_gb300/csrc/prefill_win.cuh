@@ -11,9 +11,9 @@
 // come in tiles of 64.  Per key tile and query tile
 //   S_t  = Q_t K^T   M=128 N=64  K=128   A = Q_t (smem), B = K tile (smem)
 //   O_t += P_t V     M=128 N=128 K=64    A = P_t (TMEM), B = V tile (smem)
-// TMEM, per query tile: P in 64 columns (hi, then lo; or one value in 32), S in 64, O in 128.  With P apart from S, the next key tile's QK runs while
-// this one's softmax is still at its exponentials, and with P out of shared memory
-// the softmax stores it in two instructions.
+// TMEM, per query tile: P in 64 columns (hi, then lo; or one value in 32), S in 64, O in
+// 128.  With P apart from S, the next key tile's QK runs while this one's softmax is still at
+// its exponentials, and with P out of shared memory the softmax stores it in two instructions.
 //
 // What bounds it (clock64 trace with one weight part, two query tiles of 128 rows, steady
 // state): the chain of a key tile in the softmax warps - look at the barriers (over 100 cycles
@@ -40,8 +40,8 @@
 // Measured, chunks of 512 tokens at contexts up to 4,096: 16 x 32 heads, bf16, window 1,024,
 // f32 output 199 us (607 TFLOP/s); 16 x 8 heads GQA-4, fp8, no window, bf16 output 282 (927
 // TFLOP/s), f32 output 336; the same in int8 292 and 349.  Three ragged chunks of up to 700
-// tokens, 8 heads GQA-8, window 4,096, bf16 output: 147 (858 TFLOP/s).  Every CTA has about 10 us of setup, Q, first copies and epilogue
-// besides its key tiles, of which a window leaves few.
+// tokens, 8 heads GQA-8, window 4,096, bf16 output: 147 (858 TFLOP/s).  Every CTA has about
+// 10 us of setup, Q, first copies and epilogue besides its key tiles, of which a window leaves few.
 //
 // Every wait is bounded (2 s) and gives up when another role has given up; the copies in
 // flight are then waited for, and TMEM is released before the CTA exits.
