@@ -38,9 +38,9 @@ int64_t most_ctas(int64_t heads, int64_t tokens) {
 //   + the last, partial wave: 1 + len * the root of the squares of that rate times how full
 //     the wave is and of the rate of a CTA alone, which its two-stage rings bound (42 KB/us).
 // The n with the least estimate is taken, of those within most_ctas.  Measured (bf16, GQA-8,
-// 64 x 8 heads, window 1024): one partition 57.6 us (1.1 waves), two of 576 and 512 57.4, of 704 and 384 53.0; 16 x 8
-// heads, GQA-4: 20.3 with one, 17.1 with three; 4 x 8 heads: 18.6 with one, 8.7 with six;
-// one sequence, window 4096: 56.9 with two, 10.1 with 33.
+// 64 x 8 heads, window 1024): one partition 57.6 us (1.1 waves), two of 576 and 512 57.4, of
+// 704 and 384 53.0; 16 x 8 heads, GQA-4: 20.3 with one, 17.1 with three; 4 x 8 heads: 18.6
+// with one, 8.7 with six; one sequence, window 4096: 56.9 with two, 10.1 with 33.
 int32_t auto_win_partition(int64_t heads, int64_t tokens, int token_bytes) {
   const int64_t most = most_ctas(heads, tokens);
   const double slots = 3.0 * device_sm_count();
