@@ -68,6 +68,7 @@ typedef enum {
 #define PKV_DEV_BAD_CONTEXT 0x4   /* context_lens[s] < 0 or > max_blocks_per_seq * block_size */
 #define PKV_DEV_TIMEOUT 0x8       /* an asynchronous copy did not land within 2 s; the CTA
                                      stopped early and its output is not valid */
+#define PKV_DEV_NO_FREE_BLOCK 0x10 /* slots_from_lengths: the free list cannot cover the request */
 
 /* Element types.  INT8 is the tutorial's section 3.1 symmetric 8-bit code
  * (value = code * scale); FP8_E4M3 the OCP E4M3 code (value = e4m3 * scale). */
@@ -616,6 +617,149 @@ pkv_status paged_attention_prefill_window(
     int32_t max_context_len, float scale, int32_t causal, int32_t q_dtype, int32_t kv_dtype,
     const float* k_scale, const float* v_scale, int64_t scale_stride, int32_t window,
     int32_t sinks, int32_t out_dtype, void* out, int32_t* device_status, pkv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* The step around the cache: slots, rotary positions, attention over prompts. */
+/* ------------------------------------------------------------------------ */
+
+/* Block tables and slots of a step's new tokens, built on the device from the request lengths
+ * [TUT 4.2 append_token]: what seq_append_tokens (or seq_append_slots) on each sequence in turn
+ * gives, for callers that have the lengths on the device - a captured loop of decode steps, or a
+ * scheduler there.  With bs = block_size, for sequence s of c = context_lens[s] tokens and
+ * n = new_lens[s] new ones:
+ *   - it holds h = ceil(c / bs) blocks already (at least 1 with first_block_held = 1, as
+ *     seq_create leaves a sequence of length 0) and needs ceil((c + n) / bs) of them; the missing
+ *     ones come from free_blocks, in order, after those of the sequences before it, from index
+ *     *free_start (0 when NULL) on, and their ids are written into its row of block_tables
+ *     (other entries are not touched);
+ *   - its tokens are rows start .. start + n - 1, start = the sum of the new_lens before it:
+ *     positions[row] = c + i, slot_mapping[row] = block * bs + (c + i) % bs.
+ * query_start[s] = start (query_start[num_seqs]: all rows), context_out[s] = c + n and
+ * *free_next = *free_start + blocks taken.  context_out may be context_lens and free_next
+ * free_start: then a replayed graph goes on from step to step.
+ *   new_lens     : device [num_seqs] int32; NULL: one token each.
+ *   row_per_sequence : 1 - sequence s owns row s, as a decode step's q does; each new_lens[s] is 0
+ *                  (row s then has slot -1) or 1, num_tokens >= num_seqs, and query_start is
+ *                  not written.
+ *   slot_mapping : device [num_tokens] int64; rows without a token get -1 (which every append
+ *                  skips), their positions 0.
+ *   positions, query_start, context_out, free_next : device int32, or NULL where not wanted.
+ * A sequence whose lengths are negative or do not fit its table (c + n > max_blocks_per_seq * bs)
+ * flags PKV_DEV_BAD_CONTEXT and gets nothing: slots -1, context_out = c (a negative n: no rows).
+ * A block id outside [0, num_blocks) flags PKV_DEV_BAD_BLOCK, its tokens' slots are -1.
+ * All or nothing: when num_free - *free_start blocks do not suffice (PKV_DEV_NO_FREE_BLOCK) or there
+ * are more than num_tokens rows (PKV_DEV_BAD_CONTEXT), no table changes, every slot is -1,
+ * query_start is all 0, and lengths and free list stay where they were.
+ * The call knows no reference counts: a sequence whose partly filled last block is shared is first
+ * appended to through the pool (copy-on-write).  Any block_size >= 1. */
+pkv_status slots_from_lengths(int32_t* block_tables, const int32_t* context_lens,
+                              const int32_t* new_lens, const int32_t* free_blocks,
+                              const int32_t* free_start, int32_t num_seqs, int32_t num_tokens,
+                              int32_t num_free, int64_t num_blocks, int32_t block_size,
+                              int32_t max_blocks_per_seq, int32_t row_per_sequence,
+                              int32_t first_block_held, int64_t* slot_mapping, int32_t* positions,
+                              int32_t* query_start, int32_t* context_out, int32_t* free_next,
+                              int32_t* device_status, pkv_stream_t stream);
+
+/* Rotary position embedding of q and k rows, with one position per token or several (time, height
+ * and width of images and video), and the append of the turned k and of v to one layer's cache
+ * [TUT 4.2 append_token], in one pass.  For i < rotary_dim / 2 and a token at positions
+ * pos[0 .. num_axes):
+ *   angle_i = pos[axis_i] * inv_freq_i
+ *   y_a = scale * (x_a cos - x_b sin),  y_b = scale * (x_b cos + x_a sin)
+ * for (a, b) = (i, i + rotary_dim / 2), or (2 i, 2 i + 1) with adjacent = 1; dims from rotary_dim on
+ * are copied.  Computed in float32 (angles to 2^-53 of a turn times the position, so far
+ * positions lose nothing) and rounded once, to each output's type: the cache's codes are those of
+ * the float32 values.
+ *   turns        : device [rotary_dim / 2] uint64, rotary_turns() of the inv_freq.
+ *   axis         : device [rotary_dim / 2] int32 in [0, num_axes); NULL: all 0.
+ *   positions    : device [num_axes, num_tokens] int32, any value.
+ *   q, k, v      : device rows, element (t, head, d) at t * token_stride + head * head_stride + d
+ *                  (elements), src_dtype f32 or bf16: parts of one projection's rows will do.
+ *                  q NULL (num_q_heads 0): only k.  v NULL: without a cache.
+ *   q_out, k_out : the same layout with their own strides, src_dtype; may be q and k themselves.
+ *                  k_out NULL: the turned k goes only to the cache.
+ *   k_cache, v_cache, slot_mapping, k_scale, v_scale, block_size, num_blocks, cache_dtype : as in
+ *                  reshape_and_cache (k_scale and v_scale [num_kv_heads]); a token with a
+ *                  negative slot is not appended.  k_cache NULL: no append.  Slots are distinct.
+ * Any head_dim and even rotary_dim <= head_dim; 16-byte loads where pointers, strides and
+ * rotary_dim allow them.  Outputs do not overlap inputs other than as said. */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  void* k_out;
+  int64_t q_token_stride, q_head_stride;
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  int64_t q_out_token_stride, q_out_head_stride;
+  int64_t k_out_token_stride, k_out_head_stride;
+  int32_t num_tokens, num_q_heads, num_kv_heads, head_dim;
+  int32_t src_dtype;
+  const uint64_t* turns;
+  const int32_t* axis;
+  const int32_t* positions;
+  int32_t rotary_dim, num_axes, adjacent;
+  float scale;
+  const int64_t* slot_mapping;
+  void* k_cache;
+  void* v_cache;
+  const float* k_scale;
+  const float* v_scale;
+  int32_t block_size;
+  int64_t num_blocks;
+  int32_t cache_dtype;
+  int32_t* device_status;
+} pkv_rotary_args;
+
+pkv_status rotary_and_cache(const pkv_rotary_args* args, pkv_stream_t stream);
+
+/* Host: turns[i] = inv_freq[i] / (2 pi) * 2^64 modulo 2^64, the turns that one position is
+ * worth as a 64-bit fraction: position * turns[i] modulo 2^64 is then the angle modulo one turn,
+ * whatever the position.  INVALID_ARG for a frequency that is not finite. */
+pkv_status rotary_turns(const double* inv_freq, int32_t n, uint64_t* turns);
+
+/* Attention over packed prompts ("LLM inference tutorial" section 1.2 prefill, 4.4 MHA/GQA): the
+ * keys and values of every sequence lie back to back, as a projection leaves them, and need no
+ * cache.
+ *   q            : device rows [num_tokens, num_q_heads, head_dim] bf16; k, v: [num_keys,
+ *                  num_kv_heads, head_dim] bf16; element (t, head, d) at t * token_stride +
+ *                  head * head_stride + d, strides multiples of 8 elements.
+ *   query_start  : device [num_seqs + 1] int32, as in paged_attention_prefill.
+ *   key_start    : the same for k and v; NULL: query_start (as many keys as queries).
+ *   causal       : 1 - query i of sequence s (of n queries and c keys) has position c - n + i and
+ *                  sees keys 0 .. its position (none where that is negative); 0 - it sees all c.
+ *   window, sinks : as in paged_attention_decode_window; need causal = 1.
+ *   out          : device [num_tokens, num_q_heads, head_dim] contiguous, out_dtype f32 or bf16;
+ *                  a query that sees nothing gets 0; rows outside every sequence are not written.
+ * out[t, h, :] = softmax(scale * q . K_g^T) V_g over the visible keys, g = h / G, accumulated in
+ * float32.  The weights enter P V as two bf16 parts (2^-16 of each weight) for a float32 output and
+ * as one (2^-8, half a step of a bf16 output, of each weight) for a bf16 one.
+ * A key that a query does not see, but another one of its work tile (128 rows) does, has
+ * weight 0 there; a V value of it that is not finite gives NaN.  Keys of other sequences and rows
+ * outside every sequence have no influence, whatever they hold.
+ * Supported: head_dim a multiple of 8 up to 128; G = num_q_heads / num_kv_heads <= 128; 16-byte
+ * aligned q, k, v and out.  A bad start flags PKV_DEV_BAD_CONTEXT and skips its sequence. */
+typedef struct {
+  const void* q;
+  const void* k;
+  const void* v;
+  void* out;
+  int64_t q_token_stride, q_head_stride;
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  const int32_t* query_start;
+  const int32_t* key_start;
+  int32_t num_seqs, num_tokens, num_keys;
+  int32_t num_q_heads, num_kv_heads, head_dim;
+  float scale;
+  int32_t causal, window, sinks;
+  int32_t q_dtype, kv_dtype, out_dtype;
+  int32_t* device_status;
+} pkv_packed_prefill_args;
+
+pkv_status packed_attention_prefill(const pkv_packed_prefill_args* args, pkv_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* CUDA-graph decode step with batch-size buckets and padding.               */

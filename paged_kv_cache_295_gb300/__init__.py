@@ -1,4 +1,4 @@
-"""Python binding of libpagedkv (paged KV cache + PagedAttention decode, sm_103a).
+"""Python binding of libpagedkv (paged KV cache + PagedAttention, sm_103a).
 
 Argument marshalling only: every step of the path runs in the C++ pool and the
 CUDA kernels of ``libpagedkv.so``; torch provides device memory and the
@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+from typing import NamedTuple
 
 import numpy as np
 
@@ -20,6 +21,7 @@ LIB_PATH = os.path.join(_HERE, "libpagedkv.so")
 F32, BF16, FP8_E4M3, INT8 = 0, 1, 2, 3
 DTYPE_NAMES = {F32: "f32", BF16: "bf16", FP8_E4M3: "fp8_e4m3", INT8: "int8"}
 DEV_BAD_BLOCK, DEV_BAD_SLOT, DEV_BAD_CONTEXT, DEV_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+DEV_NO_FREE_BLOCK = 0x10
 
 STATUS = {0: "ok", 1: "invalid_arg", 2: "no_free_block", 3: "bad_block", 4: "refcount",
           5: "unsupported", 6: "cuda", 7: "host_memory", 8: "scratch_limit"}
@@ -60,6 +62,34 @@ class _GraphConfig(C.Structure):
                 ("context_lens", C.c_void_p), ("out", C.c_void_p), ("workspace", C.c_void_p),
                 ("workspace_bytes", C.c_size_t), ("device_status", C.c_void_p),
                 ("buckets", C.POINTER(C.c_int32)), ("num_buckets", C.c_int32)]
+
+
+class _RotaryArgs(C.Structure):
+    _fields_ = ([(n, C.c_void_p) for n in ("q", "k", "v", "q_out", "k_out")]
+                + [(f"{n}_{w}_stride", C.c_int64) for n in ("q", "k", "v", "q_out", "k_out")
+                   for w in ("token", "head")]
+                + [(n, C.c_int32) for n in ("num_tokens", "num_q_heads", "num_kv_heads", "head_dim",
+                                            "src_dtype")]
+                + [(n, C.c_void_p) for n in ("turns", "axis", "positions")]
+                + [(n, C.c_int32) for n in ("rotary_dim", "num_axes", "adjacent")]
+                + [("scale", C.c_float)]
+                + [(n, C.c_void_p) for n in ("slot_mapping", "k_cache", "v_cache", "k_scale",
+                                             "v_scale")]
+                + [("block_size", C.c_int32), ("num_blocks", C.c_int64), ("cache_dtype", C.c_int32),
+                   ("device_status", C.c_void_p)])
+
+
+class _PackedPrefillArgs(C.Structure):
+    _fields_ = ([(n, C.c_void_p) for n in ("q", "k", "v", "out")]
+                + [(f"{n}_{w}_stride", C.c_int64) for n in ("q", "k", "v")
+                   for w in ("token", "head")]
+                + [("query_start", C.c_void_p), ("key_start", C.c_void_p)]
+                + [(n, C.c_int32) for n in ("num_seqs", "num_tokens", "num_keys", "num_q_heads",
+                                            "num_kv_heads", "head_dim")]
+                + [("scale", C.c_float)]
+                + [(n, C.c_int32) for n in ("causal", "window", "sinks", "q_dtype", "kv_dtype",
+                                            "out_dtype")]
+                + [("device_status", C.c_void_p)])
 
 
 _lib = None
@@ -124,6 +154,11 @@ _SIGS = {
     "paged_attention_prefill_window": (I32, [P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, I32,
                                              I64, I32, I32, FL, I32, I32, I32, P, P, I64, I32, I32,
                                              I32, P, P, P]),
+    "slots_from_lengths": (I32, [P, P, P, P, P, I32, I32, I32, I64, I32, I32, I32, I32, P, P, P, P,
+                                 P, P, P]),
+    "rotary_and_cache": (I32, [C.POINTER(_RotaryArgs), P]),
+    "rotary_turns": (I32, [P, I32, P]),
+    "packed_attention_prefill": (I32, [C.POINTER(_PackedPrefillArgs), P]),
     "pkv_test_force_decode_kernel": (I32, [I32]),
     "pkv_test_decode_stall": (I32, [C.c_uint32]),
     "pkv_copy_kernel": (I32, [P, P, SZ, P]),
@@ -694,6 +729,131 @@ def paged_attention_prefill(q, query_start, k_cache, v_cache, block_tables, cont
         _dev(out, "out"), _dev(device_status, "device_status"), _stream(stream))
     _check(st, "paged_attention_prefill")
     return out
+
+
+class Slots(NamedTuple):
+    """What ``slots_from_lengths`` gives, on the device."""
+    slot_mapping: object    # [num_tokens] int64, -1 where there is no token
+    positions: object       # [num_tokens] int32, 0 where there is no token
+    query_start: object     # [S + 1] int32; None with row_per_sequence
+    context_lens: object    # [S] int32, the new tokens included
+    free_start: object      # [1] int32: free blocks taken so far
+
+
+def slots_from_lengths(block_tables, context_lens, new_lens, free_blocks, num_blocks, block_size,
+                       num_tokens=None, free_start=None, row_per_sequence=False,
+                       first_block_held=False, slot_mapping=None, positions=None,
+                       query_start=None, context_out=None, free_next=None, device_status=None,
+                       stream=None):
+    """Block tables and slots of a step's new tokens, built on the device from the lengths: what
+    the pool's ``append_tokens`` on each sequence in turn gives.
+
+    ``context_lens`` and ``new_lens`` int32 ``[S]`` (None: one token each); ``free_blocks`` int32
+    ``[F]``, block ids in the order of their use, of which ``free_start`` (int32 ``[1]``) are taken
+    already.  New entries are written into ``block_tables`` ``[S, max_blocks]`` in place.
+    ``num_tokens``: rows of the outputs, at least the sum of ``new_lens``; the rest get slot -1.
+    ``row_per_sequence``: sequence ``s`` owns row ``s`` and gets no token or one, as in a decode step
+    (``num_tokens`` then defaults to ``S``).  ``first_block_held``: a sequence of length 0
+    has its first block in the table, as ``Pool.seq_create`` leaves it.  ``context_out`` may be
+    ``context_lens`` and ``free_next`` ``free_start``: a captured step then goes on by itself.
+
+    All or nothing: too few free blocks (``DEV_NO_FREE_BLOCK``) or rows (``DEV_BAD_CONTEXT``) leave
+    every table and length as it was, and every slot -1.  Sequences whose partly filled last block
+    is shared are first appended to through the pool (copy-on-write)."""
+    if stream is not None:
+        with _on_stream(stream, context_lens):
+            return slots_from_lengths(block_tables, context_lens, new_lens, free_blocks, num_blocks,
+                                      block_size, num_tokens, free_start, row_per_sequence,
+                                      first_block_held, slot_mapping, positions, query_start,
+                                      context_out, free_next, device_status)
+    return Slots(*_done(_binding().slots_from_lengths(
+        block_tables, context_lens, new_lens, free_blocks, num_blocks, block_size, num_tokens,
+        free_start, row_per_sequence, first_block_held, slot_mapping, positions, query_start,
+        context_out, free_next, device_status), "slots_from_lengths"))
+
+
+class Rotary:
+    """Rotary frequencies of a model, on the device, for ``rotary_and_cache``.
+
+    ``inv_freq``: radians per position of each of the ``rotary_dim / 2`` pairs (default
+    ``base ** (-2 i / rotary_dim)``).  ``sections``: how many pairs in turn belong to each position
+    axis (time, height, width), or ``axes``: the axis of each pair; neither: one axis.
+    ``adjacent``: pairs are dims ``(2 i, 2 i + 1)``, else ``(i, i + rotary_dim / 2)``.  ``scale``
+    multiplies the turned dims (the attention factor of extended contexts)."""
+
+    def __init__(self, rotary_dim, base=10000.0, sections=None, axes=None, inv_freq=None,
+                 adjacent=False, scale=1.0, device="cuda"):
+        torch = _torch()
+        if rotary_dim < 0 or rotary_dim % 2:
+            raise ValueError("rotary_dim must be even")
+        half = rotary_dim // 2
+        if inv_freq is None:
+            inv_freq = float(base) ** (-np.arange(half, dtype=np.float64) / max(half, 1))
+        elif hasattr(inv_freq, "detach"):
+            inv_freq = inv_freq.detach().cpu().double().numpy()
+        inv_freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+        if inv_freq.shape != (half,):
+            raise ValueError(f"inv_freq must have {half} elements")
+        if sections is not None:
+            if axes is not None:
+                raise ValueError("sections or axes, not both")
+            if any(n < 0 for n in sections) or sum(sections) != half:
+                raise ValueError(f"sections must add up to {half}")
+            axes = np.repeat(np.arange(len(sections)), list(sections))
+            self.num_axes = len(sections)
+        elif axes is not None:
+            axes = np.asarray(axes)
+            if axes.shape != (half,) or (half and axes.min() < 0):
+                raise ValueError(f"axes must be {half} axis numbers")
+            self.num_axes = int(axes.max()) + 1 if half else 1
+        else:
+            self.num_axes = 1
+        turns = np.empty(half, dtype=np.uint64)
+        _check(library().rotary_turns(_np_ptr(inv_freq), half, _np_ptr(turns)), "rotary_turns")
+        self.rotary_dim, self.adjacent, self.scale = int(rotary_dim), bool(adjacent), float(scale)
+        self.turns = torch.from_numpy(turns.view(np.int64)).to(device)
+        self.axis = None
+        if self.num_axes > 1:
+            self.axis = torch.from_numpy(axes.astype(np.int32)).to(device)
+
+
+def rotary_and_cache(q, k, v, positions, rotary, slot_mapping=None, k_cache=None, v_cache=None,
+                     k_scale=None, v_scale=None, q_out=None, k_out=None, keep_k=False,
+                     device_status=None, stream=None):
+    """Rotary positions of ``q`` ``[T, Hq, D]`` and ``k`` ``[T, Hkv, D]``, and the append of the turned
+    ``k`` and of ``v`` to one layer's ``[NB, bs, Hkv, D]`` cache, in one pass.  Returns
+    ``(q_out, k_out)``; ``k_out`` is None when the rows go to a cache alone (``keep_k`` False).
+
+    ``positions``: int32 ``[T]``, or ``[axes, T]`` for a ``rotary`` with several axes.  ``q``, ``k``
+    and ``v`` may be parts of one projection's rows, and ``q_out`` and ``k_out`` ``q`` and ``k``
+    themselves.  Without ``k_cache`` nothing is appended (``v`` may be None).  8-bit caches take
+    ``k_scale`` / ``v_scale`` ``[Hkv]``; for scales per block keep ``k`` and append it with
+    ``quantize_and_cache``."""
+    if stream is not None:
+        with _on_stream(stream, k):
+            return rotary_and_cache(q, k, v, positions, rotary, slot_mapping, k_cache, v_cache, k_scale,
+                                    v_scale, q_out, k_out, keep_k, device_status)
+    return _done(_binding().rotary_and_cache(
+        q, k, v, positions, rotary.turns, rotary.axis, rotary.rotary_dim, rotary.num_axes,
+        rotary.adjacent, rotary.scale, slot_mapping, k_cache, v_cache, k_scale, v_scale, q_out, k_out,
+        keep_k, device_status), "rotary_and_cache")
+
+
+def packed_attention_prefill(q, k, v, query_start, scale, key_start=None, causal=True, window=0,
+                             sinks=0, out=None, out_dtype=None, device_status=None, stream=None):
+    """Attention over packed prompts: sequence ``s`` owns rows ``query_start[s] .. query_start[s + 1] - 1``
+    (int32 ``[S + 1]`` on the device) of ``q`` ``[T, Hq, D]`` and, without ``key_start``, the same
+    rows of ``k`` and ``v`` ``[N, Hkv, D]`` (bfloat16, D a multiple of 8 up to 128; parts of one
+    projection's rows will do).  Returns ``[T, Hq, D]`` in float32, or ``out_dtype`` / ``out``'s type.
+
+    ``causal``: the queries are the last positions of their keys and see those up to their own;
+    ``window`` and ``sinks`` as in ``paged_attention_prefill``.  A query that sees nothing gives 0."""
+    if stream is not None:
+        with _on_stream(stream, q):
+            return packed_attention_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks,
+                                            out, out_dtype, device_status)
+    return _done(_binding().packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks,
+                                           out, out_dtype, device_status), "packed_attention_prefill")
 
 
 def copy_blocks(pool_tensor, pairs, device_status=None, stream=None):

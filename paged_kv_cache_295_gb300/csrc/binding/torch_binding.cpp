@@ -1,5 +1,5 @@
-// Python entry points of the block-scaled cache and of windowed attention, taking
-// torch tensors (module _pkv_torch).  A serving loop makes these calls once per
+// Python entry points of the block-scaled cache, of windowed attention and of the step around
+// the cache (slots, rotary positions, packed prompts), taking torch tensors (module _pkv_torch).  A serving loop makes these calls once per
 // layer and step, where the checks and the marshalling of ten tensors in Python cost
 // more than the kernel; here they take about a microsecond.  Each function checks its
 // arguments, makes the tensors' device current, allocates what the caller did not
@@ -20,6 +20,7 @@
 #include <initializer_list>
 #include <stdexcept>
 #include <string>
+#include <utility>
 
 #include "pagedkv.h"
 
@@ -389,6 +390,266 @@ PyObject* do_prefill(PyObject* const* a, Py_ssize_t na) {
   return THPVariable_Wrap(std::move(out));
 }
 
+bool truth(PyObject* o, const char* name) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) {
+    PyErr_Clear();
+    refuse(std::string(name) + " must be a truth value");
+  }
+  return v != 0;
+}
+
+// The device pointer of a tensor of this type and shape, allocated where it was not given.
+template <typename T>
+T* made(Tensor& t, const char* name, std::initializer_list<int64_t> shape, at::ScalarType type,
+        const at::Device& dev) {
+  if (!t.defined()) t = at::empty(at::IntArrayRef(shape), at::TensorOptions().dtype(type).device(dev));
+  want(t, name, shape, {type});
+  return ptr_as<T>(t, name, dev);
+}
+
+PyObject* wrapped(Tensor t) {
+  if (!t.defined()) Py_RETURN_NONE;
+  return THPVariable_Wrap(std::move(t));
+}
+// A tuple of tensors (None for an undefined one).
+template <size_t N>
+PyObject* tuple_of(Tensor (&ts)[N]) {
+  PyObject* out = PyTuple_New(N);
+  if (!out) return nullptr;
+  for (size_t i = 0; i < N; ++i) {
+    PyObject* o = wrapped(std::move(ts[i]));
+    if (!o) {
+      Py_DECREF(out);
+      return nullptr;
+    }
+    PyTuple_SET_ITEM(out, i, o);
+  }
+  return out;
+}
+
+// slots_from_lengths(block_tables, context_lens, new_lens, free_blocks, num_blocks, block_size,
+//                    num_tokens, free_start, row_per_sequence, first_block_held, slot_mapping,
+//                    positions, query_start, context_out, free_next, device_status)
+//   -> (slot_mapping, positions, query_start, context_out, free_next) or status
+PyObject* do_slots(PyObject* const* a, Py_ssize_t na) {
+  arity(na, 16);
+  const Tensor &bt = tensor(a[0], "block_tables"), &cl = tensor(a[1], "context_lens"),
+               &nl = tensor(a[2], "new_lens", true), &fb = tensor(a[3], "free_blocks"),
+               &fs = tensor(a[7], "free_start", true), &st = status_word(a[15]);
+  const int64_t blocks = integer(a[4], "num_blocks");
+  const int32_t block = integer32(a[5], "block_size");
+  const bool per_row = truth(a[8], "row_per_sequence"), held = truth(a[9], "first_block_held");
+  if (cl.dim() != 1) refuse("context_lens must be [S]");
+  const int64_t S = cl.size(0);
+  const int64_t T = a[6] == Py_None && per_row ? S : integer32(a[6], "num_tokens");
+  if (T < 0) refuse("num_tokens is negative");
+  want(cl, "context_lens", {S}, {at::kInt});
+  if (nl.defined()) want(nl, "new_lens", {S}, {at::kInt});
+  if (fb.dim() != 1) refuse("free_blocks must be [F]");
+  want(fb, "free_blocks", {fb.size(0)}, {at::kInt});
+  if (fs.defined()) want(fs, "free_start", {1}, {at::kInt});
+  const int32_t mb = tables_width(bt, S), s32 = count32(S, "context_lens"), f32 = count32(fb.size(0), "free_blocks");
+  const at::Device dev = cuda_device(cl);
+  const c10::cuda::CUDAGuard guard(dev);
+  Tensor out[5] = {tensor(a[10], "slot_mapping", true), tensor(a[11], "positions", true),
+                   tensor(a[12], "query_start", true), tensor(a[13], "context_out", true),
+                   tensor(a[14], "free_next", true)};
+  int64_t* slots = made<int64_t>(out[0], "slot_mapping", {T}, at::kLong, dev);
+  int32_t* pos = made<int32_t>(out[1], "positions", {T}, at::kInt, dev);
+  if (per_row && out[2].defined()) refuse("query_start is not written with row_per_sequence");
+  int32_t* qs = per_row ? nullptr : made<int32_t>(out[2], "query_start", {S + 1}, at::kInt, dev);
+  int32_t* co = made<int32_t>(out[3], "context_out", {S}, at::kInt, dev);
+  int32_t* fn = made<int32_t>(out[4], "free_next", {1}, at::kInt, dev);
+  int32_t *btp = ptr_as<int32_t>(bt, "block_tables", dev), *stp = ptr_as<int32_t>(st, "device_status", dev);
+  const int32_t *clp = ptr_as<int32_t>(cl, "context_lens", dev), *nlp = ptr_as<int32_t>(nl, "new_lens", dev),
+                *fbp = ptr_as<int32_t>(fb, "free_blocks", dev), *fsp = ptr_as<int32_t>(fs, "free_start", dev);
+  const pkv_stream_t stream = stream_of(dev);
+  pkv_status r;
+  Py_BEGIN_ALLOW_THREADS
+  r = slots_from_lengths(btp, clp, nlp, fbp, fsp, s32, static_cast<int32_t>(T), f32, blocks, block, mb, per_row,
+                         held, slots, pos, qs, co, fn, stp, stream);
+  Py_END_ALLOW_THREADS
+  if (r != PKV_OK) return status(r);
+  return tuple_of(out);
+}
+
+// Rows [T, heads, dim] whose elements lie side by side; any strides between rows and heads.
+void want_rows(const Tensor& t, const char* name, int64_t rows, int64_t heads, int64_t dim,
+               at::ScalarType type, const at::Device& dev, bool written = false) {
+  want(t, name, {rows, heads, dim}, {type});
+  if (t.device() != dev) refuse(std::string(name) + " is on " + t.device().str() + ", the call on " + dev.str());
+  if (t.numel() == 0) return;
+  if (dim > 1 && t.stride(2) != 1) refuse(std::string(name) + " must have its last dimension contiguous");
+  if (written)
+    for (int i = 0; i < 2; ++i)
+      if (t.size(i) > 1 && t.stride(i) < dim) refuse(std::string(name) + " must not overlap itself");
+}
+
+// rotary_and_cache(q, k, v, positions, turns, axis, rotary_dim, num_axes, adjacent, scale, slot_mapping,
+//                  k_cache, v_cache, k_scale, v_scale, q_out, k_out, keep_k, device_status)
+//   -> (q_out, k_out) or status
+PyObject* do_rotary(PyObject* const* a, Py_ssize_t na) {
+  arity(na, 19);
+  const Tensor &q = tensor(a[0], "q", true), &k = tensor(a[1], "k"), &v = tensor(a[2], "v", true),
+               &pos = tensor(a[3], "positions"), &turns = tensor(a[4], "turns"),
+               &axis = tensor(a[5], "axis", true), &slots = tensor(a[10], "slot_mapping", true),
+               &kc = tensor(a[11], "k_cache", true), &vc = tensor(a[12], "v_cache", true),
+               &ks = tensor(a[13], "k_scale", true), &vs = tensor(a[14], "v_scale", true),
+               &st = status_word(a[18]);
+  Tensor out[2] = {tensor(a[15], "q_out", true), tensor(a[16], "k_out", true)};
+  const bool keep_k = truth(a[17], "keep_k"), cached = kc.defined();
+  pkv_rotary_args p{};
+  p.rotary_dim = integer32(a[6], "rotary_dim");
+  p.num_axes = integer32(a[7], "num_axes");
+  p.adjacent = truth(a[8], "adjacent");
+  p.scale = real(a[9], "scale");
+  if (k.dim() != 3 || (q.defined() && q.dim() != 3)) refuse("q and k must be [T, heads, dim]");
+  const int64_t T = k.size(0), hkv = k.size(1), dim = k.size(2), hq = q.defined() ? q.size(1) : 0;
+  const at::ScalarType type = k.scalar_type();
+  if (type != at::kFloat && type != at::kBFloat16) refuse("k must be Float or BFloat16, got " + show(k));
+  if (hq > (1 << 20) || hkv > (1 << 20) || dim > (1 << 20)) refuse("too many heads or dims");
+  const at::Device dev = cuda_device(k);
+  const c10::cuda::CUDAGuard guard(dev);
+  want_rows(k, "k", T, hkv, dim, type, dev);
+  if (q.defined()) {
+    want_rows(q, "q", T, hq, dim, type, dev);
+    if (!out[0].defined()) out[0] = at::empty({T, hq, dim}, q.options());
+    want_rows(out[0], "q_out", T, hq, dim, type, dev, true);
+  } else if (out[0].defined()) {
+    refuse("q_out without q");
+  }
+  if (!out[1].defined() && (keep_k || !cached)) out[1] = at::empty({T, hkv, dim}, k.options());
+  if (out[1].defined()) want_rows(out[1], "k_out", T, hkv, dim, type, dev, true);
+  if (p.rotary_dim < 0 || p.rotary_dim % 2 != 0 || p.rotary_dim > dim)
+    refuse("rotary_dim must be even and at most " + std::to_string(dim));
+  want(turns, "turns", {p.rotary_dim / 2}, {at::kLong});
+  if (axis.defined()) want(axis, "axis", {p.rotary_dim / 2}, {at::kInt});
+  if (p.num_axes == 1 && pos.dim() == 1)
+    want(pos, "positions", {T}, {at::kInt});
+  else
+    want(pos, "positions", {p.num_axes, T}, {at::kInt});
+  if (cached) {
+    const Cache c = cache_of(kc, vc);
+    if (c.heads != hkv || c.dim != dim)
+      refuse("the caches must be [num_blocks, block_size, " + std::to_string(hkv) + ", " + std::to_string(dim) +
+             "], got " + show(kc));
+    if (!v.defined()) refuse("v must be a tensor");
+    if (!slots.defined()) refuse("slot_mapping must be a tensor");
+    want_rows(v, "v", T, hkv, dim, type, dev);
+    want(slots, "slot_mapping", {T}, {at::kLong});
+    if (is_codes(c.code)) {
+      if (scale_stride(ks, vs, c) != 0)
+        refuse("rotary_and_cache takes one scale per head, not scales per block");
+      p.k_scale = ptr_as<float>(ks, "k_scale", dev);
+      p.v_scale = ptr_as<float>(vs, "v_scale", dev);
+    }
+    p.slot_mapping = ptr_as<int64_t>(slots, "slot_mapping", dev);
+    p.k_cache = ptr(kc, "k_cache", dev);
+    p.v_cache = ptr(vc, "v_cache", dev);
+    p.block_size = c.block_size;
+    p.num_blocks = c.blocks;
+    p.cache_dtype = c.code;
+    p.v = v.data_ptr();
+    p.v_token_stride = v.stride(0);
+    p.v_head_stride = v.stride(1);
+  } else if (vc.defined()) {
+    refuse("v_cache without k_cache");
+  }
+  p.k = k.data_ptr();
+  p.k_token_stride = k.stride(0);
+  p.k_head_stride = k.stride(1);
+  if (q.defined()) {
+    p.q = q.data_ptr();
+    p.q_token_stride = q.stride(0);
+    p.q_head_stride = q.stride(1);
+    p.q_out = out[0].data_ptr();
+    p.q_out_token_stride = out[0].stride(0);
+    p.q_out_head_stride = out[0].stride(1);
+  }
+  if (out[1].defined()) {
+    p.k_out = out[1].data_ptr();
+    p.k_out_token_stride = out[1].stride(0);
+    p.k_out_head_stride = out[1].stride(1);
+  }
+  p.num_tokens = count32(T, "k");
+  p.num_q_heads = static_cast<int32_t>(hq);
+  p.num_kv_heads = static_cast<int32_t>(hkv);
+  p.head_dim = static_cast<int32_t>(dim);
+  p.src_dtype = code_of(type);
+  p.turns = reinterpret_cast<const uint64_t*>(ptr_as<int64_t>(turns, "turns", dev));
+  p.axis = ptr_as<int32_t>(axis, "axis", dev);
+  p.positions = ptr_as<int32_t>(pos, "positions", dev);
+  p.device_status = ptr_as<int32_t>(st, "device_status", dev);
+  const pkv_stream_t stream = stream_of(dev);
+  pkv_status r;
+  Py_BEGIN_ALLOW_THREADS
+  r = rotary_and_cache(&p, stream);
+  Py_END_ALLOW_THREADS
+  if (r != PKV_OK) return status(r);
+  return tuple_of(out);
+}
+
+// packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks, out, out_dtype,
+//                device_status) -> out or status
+PyObject* do_packed(PyObject* const* a, Py_ssize_t na) {
+  arity(na, 12);
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"),
+               &qs = tensor(a[3], "query_start"), &ks = tensor(a[5], "key_start", true),
+               &st = status_word(a[11]);
+  if (q.dim() != 3 || k.dim() != 3) refuse("q, k and v must be [T, heads, dim]");
+  if (qs.dim() != 1 || qs.size(0) < 1) refuse("query_start must be [S + 1]");
+  const int64_t T = q.size(0), hq = q.size(1), dim = q.size(2), N = k.size(0), hkv = k.size(1), S = qs.size(0) - 1;
+  if (hq > (1 << 20) || hkv > (1 << 20) || dim > (1 << 20)) refuse("too many heads or dims");
+  pkv_packed_prefill_args p{};
+  p.scale = real(a[4], "scale");
+  p.causal = truth(a[6], "causal");
+  p.window = integer32(a[7], "window");
+  p.sinks = integer32(a[8], "sinks");
+  const at::Device dev = cuda_device(q);
+  const c10::cuda::CUDAGuard guard(dev);
+  want_rows(q, "q", T, hq, dim, at::kBFloat16, dev);
+  want_rows(k, "k", N, hkv, dim, at::kBFloat16, dev);
+  want_rows(v, "v", N, hkv, dim, at::kBFloat16, dev);
+  want(qs, "query_start", {S + 1}, {at::kInt});
+  if (ks.defined())
+    want(ks, "key_start", {S + 1}, {at::kInt});
+  else if (N != T)
+    refuse("k must have as many rows as q, or key_start be given");
+  for (const auto& x : {std::make_pair(&q, "q"), std::make_pair(&k, "k"), std::make_pair(&v, "v")})
+    for (int i = 0; i < 2; ++i)
+      if (x.first->size(i) > 1 && (x.first->stride(i) <= 0 || x.first->stride(i) % 8 != 0))
+        refuse(std::string(x.second) + " must have strides that are multiples of 8 elements");
+  Tensor out = tensor(a[9], "out", true);
+  const at::ScalarType type = out_type(a[10], out, at::kFloat);
+  if (type != at::kFloat && type != at::kBFloat16) refuse("the output must be Float or BFloat16");
+  if (!out.defined()) out = at::empty({T, hq, dim}, q.options().dtype(type));
+  want(out, "out", {T, hq, dim}, {type});
+  p.out = ptr(out, "out", dev);
+  p.q = q.data_ptr(), p.k = k.data_ptr(), p.v = v.data_ptr();
+  p.q_token_stride = q.stride(0), p.q_head_stride = q.stride(1);
+  p.k_token_stride = k.stride(0), p.k_head_stride = k.stride(1);
+  p.v_token_stride = v.stride(0), p.v_head_stride = v.stride(1);
+  p.query_start = ptr_as<int32_t>(qs, "query_start", dev);
+  p.key_start = ptr_as<int32_t>(ks, "key_start", dev);
+  p.num_seqs = count32(S, "query_start");
+  p.num_tokens = count32(T, "q");
+  p.num_keys = count32(N, "k");
+  p.num_q_heads = static_cast<int32_t>(hq);
+  p.num_kv_heads = static_cast<int32_t>(hkv);
+  p.head_dim = static_cast<int32_t>(dim);
+  p.q_dtype = p.kv_dtype = PKV_BF16;
+  p.out_dtype = code_of(type);
+  p.device_status = ptr_as<int32_t>(st, "device_status", dev);
+  const pkv_stream_t stream = stream_of(dev);
+  pkv_status r;
+  Py_BEGIN_ALLOW_THREADS
+  r = packed_attention_prefill(&p, stream);
+  Py_END_ALLOW_THREADS
+  if (r != PKV_OK) return status(r);
+  return THPVariable_Wrap(std::move(out));
+}
+
 // No C++ exception leaves an entry point.
 template <PyObject* (*F)(PyObject* const*, Py_ssize_t)>
 PyObject* entry(PyObject*, PyObject* const* a, Py_ssize_t na) {
@@ -407,6 +668,9 @@ PyMethodDef kMethods[] = {
     {"gather_cache", reinterpret_cast<PyCFunction>(entry<do_gather>), METH_FASTCALL, nullptr},
     {"decode_window", reinterpret_cast<PyCFunction>(entry<do_decode>), METH_FASTCALL, nullptr},
     {"prefill_window", reinterpret_cast<PyCFunction>(entry<do_prefill>), METH_FASTCALL, nullptr},
+    {"slots_from_lengths", reinterpret_cast<PyCFunction>(entry<do_slots>), METH_FASTCALL, nullptr},
+    {"rotary_and_cache", reinterpret_cast<PyCFunction>(entry<do_rotary>), METH_FASTCALL, nullptr},
+    {"packed_prefill", reinterpret_cast<PyCFunction>(entry<do_packed>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_pkv_torch", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

@@ -1,0 +1,108 @@
+// packed_attention_prefill: argument checks, tensor maps and the launch of the tcgen05 kernel over
+// packed prompts.
+#include <cmath>
+
+#include "packed_prefill.cuh"
+#include "tmap.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int64_t kMaxStride = int64_t{1} << 38;   // elements; a tensor map takes 2^40 bytes
+
+// 3-D map over rows [rows][heads][dim] of bf16 with these strides (elements): boxes of 64 dims (what lies
+// past `dim` reads as 0), box_heads heads and box_rows rows.
+bool rows_map(CUtensorMap* m, const void* base, int dim, int heads, int64_t rows, int64_t head_stride,
+              int64_t row_stride, int box_heads, int box_rows) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  if (heads == 1) head_stride = (dim + 7) / 8 * 8;   // of a single one the stride says nothing
+  if (rows == 1) row_stride = (dim + 7) / 8 * 8;
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(dim), static_cast<cuuint64_t>(heads),
+                        static_cast<cuuint64_t>(rows)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(head_stride) * 2, static_cast<cuuint64_t>(row_stride) * 2};
+  cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+  cuuint32_t estr[3] = {1u, 1u, 1u};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// A stride between rows or heads, where there is more than one of them.
+bool stride_ok(int64_t stride, int64_t count) {
+  return count <= 1 || (stride > 0 && stride % 8 == 0 && stride < kMaxStride);
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" pkv_status packed_attention_prefill(const pkv_packed_prefill_args* args, pkv_stream_t stream) {
+  using namespace pkv;
+  if (!args) return PKV_ERR_INVALID_ARG;
+  const pkv_packed_prefill_args& a = *args;
+  if (a.num_seqs < 0 || a.num_tokens < 0 || a.num_keys < 0 || a.num_q_heads <= 0 || a.num_kv_heads <= 0 ||
+      a.head_dim <= 0 || a.window < 0 || a.sinks < 0 || (a.causal != 0 && a.causal != 1) ||
+      a.num_q_heads % a.num_kv_heads != 0 || !std::isfinite(a.scale))
+    return PKV_ERR_INVALID_ARG;
+  if ((a.window > 0 && !a.causal) || (a.sinks > 0 && a.window == 0)) return PKV_ERR_INVALID_ARG;
+  const int G = a.num_q_heads / a.num_kv_heads;
+  if (a.q_dtype != PKV_BF16 || a.kv_dtype != PKV_BF16 || (a.out_dtype != PKV_F32 && a.out_dtype != PKV_BF16))
+    return PKV_ERR_UNSUPPORTED;
+  if (a.head_dim > 128 || a.head_dim % 8 != 0 || G > kPkRows || a.num_seqs > (1 << 24) ||
+      a.num_tokens > (1 << 30) || a.num_keys > (1 << 30) || a.num_q_heads > (1 << 16))
+    return PKV_ERR_UNSUPPORTED;
+  if (!stride_ok(a.q_token_stride, a.num_tokens) || !stride_ok(a.q_head_stride, a.num_q_heads) ||
+      !stride_ok(a.k_token_stride, a.num_keys) || !stride_ok(a.k_head_stride, a.num_kv_heads) ||
+      !stride_ok(a.v_token_stride, a.num_keys) || !stride_ok(a.v_head_stride, a.num_kv_heads))
+    return PKV_ERR_INVALID_ARG;
+  if (a.num_seqs == 0 || a.num_tokens == 0) return PKV_OK;
+  if (!a.q || !a.out || !a.query_start || (a.num_keys > 0 && (!a.k || !a.v))) return PKV_ERR_INVALID_ARG;
+  if (!a.key_start && a.num_keys != a.num_tokens) return PKV_ERR_INVALID_ARG;
+  if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.out) || !aligned4(a.query_start) ||
+      !aligned4(a.key_start))
+    return PKV_ERR_INVALID_ARG;
+
+  PackedParams p{};
+  p.out = a.out;
+  p.query_start = a.query_start;
+  p.key_start = a.key_start ? a.key_start : a.query_start;
+  p.status = a.device_status;
+  p.num_seqs = a.num_seqs, p.num_tokens = a.num_tokens, p.num_keys = a.num_keys;
+  p.num_q_heads = a.num_q_heads, p.num_kv_heads = a.num_kv_heads, p.dim = a.head_dim;
+  p.tile_tokens = kPkRows / G;
+  p.causal = a.causal, p.window = a.window, p.sinks = a.sinks;
+  p.out_bf16 = a.out_dtype == PKV_BF16;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.test_stall_bytes = test_stall_bytes();
+
+  CUtensorMap tq, tk, tv;
+  // without keys no key tile is read: any map will do
+  const void* k = a.num_keys > 0 ? a.k : a.q;
+  const void* v = a.num_keys > 0 ? a.v : a.q;
+  const int64_t keys = a.num_keys > 0 ? a.num_keys : 1;
+  if (!rows_map(&tq, a.q, a.head_dim, a.num_q_heads, a.num_tokens, a.q_head_stride, a.q_token_stride, G,
+                p.tile_tokens) ||
+      !rows_map(&tk, k, a.head_dim, a.num_kv_heads, keys, a.k_head_stride, a.k_token_stride, 1, kPkKeys) ||
+      !rows_map(&tv, v, a.head_dim, a.num_kv_heads, keys, a.v_head_stride, a.v_token_stride, 1, kPkKeys))
+    return PKV_ERR_CUDA;
+
+  // no more CTAs than items: a sequence's last pair may be short
+  const int64_t units =
+      ((static_cast<int64_t>(a.num_tokens) + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens) + a.num_seqs) *
+      a.num_kv_heads;
+  if (units > INT32_MAX / 2) return PKV_ERR_UNSUPPORTED;   // the items are counted in 32 bits
+  const int64_t sms = device_sm_count();
+  const dim3 grid(static_cast<unsigned>(units < sms ? units : sms));
+  auto launch = [&](auto kern, size_t smem) {
+    if (!opt_in_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem))) return PKV_ERR_CUDA;
+    kern<<<grid, kPkThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(tq, tk, tv, p);
+    return cuda_status(cudaGetLastError());
+  };
+  if (a.head_dim > 64)
+    return p.out_bf16 ? launch(packed_prefill_kernel<2, 4, false>, PkLayout<2, 4>::bytes())
+                      : launch(packed_prefill_kernel<2, 4, true>, PkLayout<2, 4>::bytes());
+  return p.out_bf16 ? launch(packed_prefill_kernel<1, 8, false>, PkLayout<1, 8>::bytes())
+                    : launch(packed_prefill_kernel<1, 8, true>, PkLayout<1, 8>::bytes());
+}

@@ -151,19 +151,6 @@ struct Vec8<float> {
   static __device__ __forceinline__ uint32_t top_bits(uint32_t m) { return m; }
 };
 
-// x / s rounded to nearest, for two finite x given as -x, without a divide per
-// element, by Markstein's theorem ("Computation of elementary functions on the IBM
-// RISC System/6000 processor", 1990): with r = 1 / s rounded to nearest and q within
-// one ulp of x / s, q - (q s - x) r, whose residual one fma gives exactly, is x / s
-// rounded to nearest.  x r is within two ulps, so one step makes it faithful and a
-// second one exact.  s >= 2^-64 keeps the residuals of every quotient that rounds to
-// a non-zero code in the normal range; the sign of a zero x is kept.
-__device__ __forceinline__ float2 quotient2(float2 neg_x, float2 s, float2 neg_r) {
-  float2 q = __fmul2_rn(neg_x, neg_r);
-  q = __ffma2_rn(__ffma2_rn(q, s, neg_x), neg_r, q);
-  return __ffma2_rn(__ffma2_rn(q, s, neg_x), neg_r, q);
-}
-
 // Codes of 8 elements; FINITE: none is an infinity or NaN.
 template <typename Src, typename Q, bool FINITE>
 __device__ __forceinline__ uint2 codes8(const Vec8<Src>& v, float s, float r) {

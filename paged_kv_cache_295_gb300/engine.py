@@ -14,9 +14,10 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (BF16, F32, FP8_E4M3, INT8, Pool, copy_blocks, gather_cache, paged_attention_decode,
-               paged_attention_decode_append, paged_attention_prefill, quantize_and_cache,
-               reshape_and_cache, swap_blocks, workspace_bytes)
+from . import (BF16, F32, FP8_E4M3, INT8, Pool, copy_blocks, gather_cache, packed_attention_prefill,
+               paged_attention_decode, paged_attention_decode_append, paged_attention_prefill,
+               quantize_and_cache, reshape_and_cache, rotary_and_cache, slots_from_lengths,
+               swap_blocks, workspace_bytes)
 
 
 def _torch():
@@ -100,6 +101,38 @@ class PagedKVCache:
                            self.k_scale[layer], self.v_scale[layer], block_tables, context_lens,
                            query_start=query_start, max_query_len=max_query_len,
                            device_status=device_status, stream=stream)
+
+    def slots(self, block_tables, context_lens, new_lens, free_blocks, num_tokens=None, **kw):
+        """A step's slots and positions from the lengths, on the device (``slots_from_lengths``).
+        ``free_blocks``: the pool's free list on the device (``pool.free_list()``, or ids taken
+        with ``pool.block_alloc``).  The pool itself learns of the tokens when the same appends
+        are made on it: as long as it hands out no other blocks, it takes the same ones."""
+        return slots_from_lengths(block_tables, context_lens, new_lens, free_blocks,
+                                  self.num_blocks, self.block_size, num_tokens, **kw)
+
+    def append_rotary(self, layer, q, k, v, positions, rotary, slot_mapping, q_out=None, k_out=None,
+                      keep_k=False, device_status=None, stream=None):
+        """Rotary positions of q and k and the append of k and v in one pass
+        (``rotary_and_cache``); returns ``(q, k)`` turned, k None unless ``keep_k``."""
+        if self.scales is not None:
+            raise ValueError("a cache with block scales: rotary_and_cache without a cache, then "
+                             "append_rows")
+        ks = None if self.k_scale is None else self.k_scale[layer]
+        vs = None if self.v_scale is None else self.v_scale[layer]
+        return rotary_and_cache(q, k, v, positions, rotary, slot_mapping, self.k_cache(layer),
+                                self.v_cache(layer), ks, vs, q_out=q_out, k_out=k_out, keep_k=keep_k,
+                                device_status=device_status, stream=stream)
+
+    def prompt(self, layer, q, k, v, positions, rotary, slots, window=0, sinks=0, out=None,
+               out_dtype=None, device_status=None, stream=None):
+        """One layer of a step over whole prompts (sequences with nothing cached before): rotary
+        positions, the append, and causal attention over the packed rows.  ``slots`` as
+        ``self.slots`` gives them for this step."""
+        q, k = self.append_rotary(layer, q, k, v, positions, rotary, slots.slot_mapping, keep_k=True,
+                                  device_status=device_status, stream=stream)
+        return packed_attention_prefill(q, k, v, slots.query_start, self.scale, window=window,
+                                        sinks=sinks, out=out, out_dtype=out_dtype,
+                                        device_status=device_status, stream=stream)
 
     def gather(self, layer, block_tables, row_start, num_rows, max_rows, first_pos=None,
                out_dtype=None, k_out=None, v_out=None, device_status=None, stream=None):

@@ -1,0 +1,323 @@
+"""Attention over packed prompts on the GPU, against float64."""
+import time
+import types
+
+import numpy as np
+import pytest
+
+from oracle import step as OS
+from tests import paged_cases as PC
+
+pytestmark = pytest.mark.gpu
+
+BF16 = types.SimpleNamespace(kv="bf16")
+
+
+def starts(lens, gap=0):
+    """Packed row starts; ``gap`` rows of nobody before the first and behind the last."""
+    return np.concatenate([[0], np.cumsum(lens)]).astype(np.int32) + gap
+
+
+def inputs(seed, T, N, hq, hkv, dim, layout="own", k_size=1.0):
+    """bf16 rows on the GPU; "fused": parts of one projection's rows (T = N)."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    if layout == "fused":
+        x = torch.randn((T, hq + 2 * hkv, dim), generator=gen, device="cuda")
+        x[:, hq:hq + hkv] *= k_size
+        x = x.bfloat16()
+        return x[:, :hq], x[:, hq:hq + hkv], x[:, hq + hkv:]
+    if layout == "heads":     # heads outside, tokens inside
+        return tuple((s * torch.randn((h, n, dim), generator=gen, device="cuda")).bfloat16().transpose(0, 1)
+                     for n, h, s in ((T, hq, 1.0), (N, hkv, k_size), (N, hkv, 1.0)))
+    return tuple((s * torch.randn((n, h, dim), generator=gen, device="cuda")).bfloat16()
+                 for n, h, s in ((T, hq, 1.0), (N, hkv, k_size), (N, hkv, 1.0)))
+
+
+def check(lib, q, k, v, qs, ks, scale, out_type="bf16", causal=True, window=0, sinks=0, **kw):
+    """One call, checked whole; rows outside every sequence keep what they held."""
+    import torch
+    dt = torch.bfloat16 if out_type == "bf16" else torch.float32
+    out = torch.full(q.shape, 77.0, dtype=dt, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = lib.packed_attention_prefill(
+        q, k, v, torch.from_numpy(qs).cuda(), scale, key_start=None if ks is None else torch.from_numpy(ks).cuda(),
+        causal=causal, window=window, sinks=sinks, out=out, device_status=status, **kw)
+    assert got is out or got.data_ptr() == out.data_ptr()
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    x = [t.double().cpu().numpy() for t in (q, k, v)]
+    want, mag, reach, seen = OS.packed(*x, qs, qs if ks is None else ks, scale, causal, window, sinks)
+    y = out.double().cpu().numpy()
+    inside = ~np.isnan(want[:, 0, 0]) if want.size else np.zeros(0, dtype=bool)
+    assert (y[~inside] == 77.0).all()
+    e = PC.attention_bound(BF16, x[0], want, mag, reach, scale, False, out_type == "bf16",
+                           out_type == "f32", int(seen.max(initial=1)))
+    assert (np.abs(y - want)[inside] <= e[inside]).all(), np.nanmax((np.abs(y - want) / e)[inside])
+    return out
+
+
+@pytest.mark.parametrize("dim", [8, 16, 40, 64, 72, 80, 96, 112, 128])
+@pytest.mark.parametrize("out_type", ["bf16", "f32"])
+def test_dims(lib, dim, out_type):
+    lens = [130, 1, 0, 257, 33]
+    q, k, v = inputs(dim, sum(lens), sum(lens), 4, 2, dim, "fused")
+    for causal in (True, False):
+        check(lib, q, k, v, starts(lens), None, dim ** -0.5, out_type, causal)
+
+
+@pytest.mark.parametrize("group,hkv", [(1, 3), (2, 2), (3, 1), (5, 2), (7, 1), (8, 2), (16, 1), (31, 1), (40, 1),
+                                       (64, 2), (100, 1), (128, 1)])
+def test_groups(lib, group, hkv):
+    lens = [max(1, 150 // group), 1, 300 // group + 2]
+    q, k, v = inputs(group, sum(lens), sum(lens), group * hkv, hkv, 64)
+    check(lib, q, k, v, starts(lens), None, 0.125, "f32")
+
+
+@pytest.mark.parametrize("n", [1, 2, 63, 64, 65, 127, 128, 129, 255, 256, 257, 383, 384, 385, 511, 513])
+@pytest.mark.parametrize("causal", [False, True])
+def test_lengths(lib, n, causal):
+    """Sequences that end at, before and behind a tile's and a pair's end, next to others."""
+    q, k, v = inputs(n, n + 9, n + 9, 2, 1, 128, "heads")
+    check(lib, q, k, v, starts([4, n, 5]), None, 0.09, "bf16", causal)
+    check(lib, q, k, v, starts([n, 9]), None, 0.09, "f32", causal)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (17, 4), (100, 0), (128, 129), (200, 300), (5000, 2)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_windows(lib, window, sinks, dim):
+    lens = [700, 3, 129, 400]
+    q, k, v = inputs(window, sum(lens), sum(lens), 3, 1, dim)
+    check(lib, q, k, v, starts(lens), None, 0.1, "f32", window=window, sinks=sinks)
+    more = [x + y for x, y in zip(lens, (260, 128, 0, 1))]
+    q, k, v = inputs(window, sum(lens), sum(more), 4, 2, dim)
+    check(lib, q, k, v, starts(lens), starts(more), 0.1, "bf16", window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("causal", [False, True])
+def test_other_key_lengths(lib, causal):
+    """More keys than queries, fewer (rows that see nothing), none at all."""
+    lens, keys = [50, 200, 1, 300, 7, 20, 0], [300, 60, 500, 0, 1, 20, 40]
+    q, k, v = inputs(5, sum(lens), sum(keys), 4, 2, 80)
+    for out_type in ("bf16", "f32"):
+        out = check(lib, q, k, v, starts(lens), starts(keys), 0.1, out_type, causal)
+        assert (out[251:551] == 0).all()
+        if causal:
+            assert (out[50:190] == 0).all() and (out[551:557] == 0).all()
+    q, k, v = inputs(6, 30, 0, 4, 2, 64)
+    assert (check(lib, q, k, v, starts([30]), starts([0]), 0.1, "bf16", causal) == 0).all()
+
+
+@pytest.mark.parametrize("out_type", ["bf16", "f32"])
+def test_neighbours_have_no_influence(lib, out_type):
+    """NaN and infinities in other sequences, before the first and behind the last."""
+    import torch
+    lens = [70, 130, 1, 300]
+    qs = starts(lens, 40)
+    q, k, v = inputs(7, 600, 600, 4, 2, 128, "fused")
+    clean = check(lib, q, k, v, qs, None, 0.09, out_type)
+    for bad in (float("nan"), float("inf"), -float("inf")):
+        for x in (q, k, v):
+            y = [t.clone() for t in (q, k, v)]
+            z = y[0 if x is q else 1 if x is k else 2]
+            z[:40] = bad
+            z[qs[-1]:] = bad
+            z[qs[1]:qs[2]] = bad          # sequence 1
+            out = torch.full(q.shape, 77.0, dtype=clean.dtype, device="cuda")
+            lib.packed_attention_prefill(*y, torch.from_numpy(qs).cuda(), 0.09, out=out)
+            keep = torch.ones(600, dtype=torch.bool, device="cuda")
+            keep[qs[1]:qs[2]] = False
+            assert torch.equal(out[keep], clean[keep])
+
+
+def test_hidden_rows(lib):
+    """Keys that causality or the window hides from a whole query tile: whatever they hold."""
+    import torch
+    q, k, v = inputs(8, 640, 640, 1, 1, 64)
+    a = lib.packed_attention_prefill(q, k, v, torch.tensor([0, 640], dtype=torch.int32, device="cuda"), 0.1)
+    k[512:], v[512:] = float("nan"), float("nan")
+    b = lib.packed_attention_prefill(q, k, v, torch.tensor([0, 640], dtype=torch.int32, device="cuda"), 0.1)
+    assert torch.equal(a[:512], b[:512]) and b[600:].isnan().all()
+    # hidden keys (not values) of the same tile: no influence either
+    q, k, v = inputs(9, 100, 100, 1, 1, 64)
+    a = lib.packed_attention_prefill(q, k, v, torch.tensor([0, 100], dtype=torch.int32, device="cuda"), 0.1)
+    k[60:] = float("inf")
+    b = lib.packed_attention_prefill(q, k, v, torch.tensor([0, 100], dtype=torch.int32, device="cuda"), 0.1)
+    assert torch.equal(a[:60], b[:60])
+
+
+@pytest.mark.parametrize("scale", [0.0, -0.1, 3.0, -2.0, 1e-30])
+def test_scales(lib, scale):
+    """Negative, zero, tiny and large factors."""
+    for size in (1.0, 6.0):
+        q, k, v = inputs(10, 500, 500, 2, 1, 128, k_size=size)
+        check(lib, q, k, v, starts([500]), None, scale, "f32")
+        check(lib, q, k, v, starts([500]), None, scale, "bf16", causal=False)
+
+
+def test_rising_logits(lib):
+    """Every key tile's logits are far above the one before: the reference moves each time."""
+    import torch
+    q, k, v = inputs(11, 700, 700, 2, 1, 64)
+    q[:] = q.abs()
+    k[:] = (k.float().abs() * (torch.arange(700, device="cuda") // 100 + 1).view(-1, 1, 1)).bfloat16()
+    check(lib, q, k, v, starts([700]), None, 1.0, "f32", causal=False)
+    check(lib, q, k, v, starts([700]), None, 1.0, "bf16", causal=False)
+    k[:] = k.flip(0)
+    check(lib, q, k, v, starts([700]), None, 1.0, "f32")
+
+
+@pytest.mark.parametrize("seqs", [300, 1024, 1025, 2300])
+def test_many_sequences(lib, seqs):
+    """More sequences than are ordered together; most of them short, some without a row."""
+    rng = np.random.default_rng(seqs)
+    lens = rng.integers(0, 4, seqs)
+    lens[rng.integers(0, seqs, 5)] = 140
+    T = int(lens.sum())
+    q, k, v = inputs(seqs, T, T, 2, 1, 64)
+    check(lib, q, k, v, starts(lens), None, 0.125, "bf16")
+
+
+@pytest.mark.parametrize("out_type", ["bf16", "f32"])
+def test_more_items_than_ctas(lib, out_type):
+    """Several items per CTA, of one key tile to many, both query tiles and one; twice the same bits."""
+    import torch
+    lens = [1, 400, 129, 257, 20, 128, 700, 1, 64, 300]
+    q, k, v = inputs(12, sum(lens), sum(lens), 64, 32, 64, "fused")
+    qs = torch.from_numpy(starts(lens)).cuda()
+    dt = torch.bfloat16 if out_type == "bf16" else torch.float32
+    a = lib.packed_attention_prefill(q, k, v, qs, 0.125, out_dtype=dt)
+    for _ in range(3):
+        assert torch.equal(a, lib.packed_attention_prefill(q, k, v, qs, 0.125, out_dtype=dt))
+    for h in (0, 17, 63):     # a head among the others and alone
+        one = check(lib, q[:, h:h + 1], k[:, h // 2:h // 2 + 1], v[:, h // 2:h // 2 + 1], starts(lens), None, 0.125,
+                    out_type)
+        # (grouped heads share a query tile: another order of nothing, the same numbers)
+        assert torch.equal(one[:, 0], a[:, h])
+
+
+def long_reference(q, k, v, scale, causal):
+    """float64 on the GPU, one sequence, one head."""
+    import torch
+    q, k, v = (x.double() for x in (q, k, v))
+    z = q @ k.t() * float(np.float32(scale))
+    if causal:
+        n, c = z.shape
+        z += torch.triu(torch.full((n, c), -torch.inf, dtype=torch.float64, device="cuda"), c - n + 1)
+    return torch.softmax(z, -1) @ v
+
+
+@pytest.mark.parametrize("keys", [3000, 20000])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_long_float32(lib, keys, dim):
+    """The tensor cores cut each sum in O towards zero, up to 2^-23 of it: over 64 k-steps of 16 keys
+    twice (two parts of the weights) that is 2^-16 at most and, as cuts are half of that on average,
+    2^-17; the weights' second part is off by 2^-17.  Their sum over independent elements stays under
+    1.2e-5 of the norm, however many keys there are."""
+    import torch
+    q, k, v = inputs(13, 260, keys, 1, 1, dim)
+    for causal in (True, False):
+        want = long_reference(q[:, 0], k[:, 0], v[:, 0], 0.1, causal)
+        got = lib.packed_attention_prefill(q, k, v, torch.tensor([0, 260], dtype=torch.int32, device="cuda"), 0.1,
+                                           key_start=torch.tensor([0, keys], dtype=torch.int32, device="cuda"),
+                                           causal=causal)
+        assert ((got[:, 0].double() - want).norm() / want.norm()).item() <= 1.2e-5
+
+
+def test_flags(lib):
+    import torch
+    q, k, v = inputs(14, 100, 100, 2, 1, 64)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call(qs, ks=None):
+        out = torch.full(q.shape, 5.0, device="cuda")
+        status.zero_()
+        lib.packed_attention_prefill(q, k, v, torch.tensor(qs, dtype=torch.int32, device="cuda"), 0.125,
+                                     key_start=None if ks is None else torch.tensor(ks, dtype=torch.int32, device="cuda"),
+                                     out=out, device_status=status)
+        torch.cuda.synchronize()
+        return out, int(status.item())
+
+    good, st = call([0, 30, 100])
+    assert st == 0
+    for qs, ks, whole in (([0, 30, 101], None, 30), ([0, 30, 10], None, 30), ([0, 30, 100], [0, 30, 200], 30),
+                          ([0, 30, 100], [0, 30, 20], 30), ([0, 30, 2 ** 31 - 1], None, 30)):
+        out, st = call(qs, ks)
+        assert st == lib.DEV_BAD_CONTEXT
+        assert torch.equal(out[:whole], good[:whole]) and (out[whole:] == 5.0).all()
+    out, st = call([-1, 30, 100])
+    assert st == lib.DEV_BAD_CONTEXT and torch.equal(out[30:], good[30:]) and (out[:30] == 5.0).all()
+
+
+def test_streams_graphs_and_refusals(lib):
+    """Two calls at once on two streams, a captured one, replayed on new inputs; arguments refused."""
+    import torch
+    lens = [300, 1, 200]
+    a, b = inputs(15, 501, 501, 8, 2, 128), inputs(16, 501, 501, 8, 2, 128, "fused")
+    qs = torch.from_numpy(starts(lens)).cuda()
+    want = [lib.packed_attention_prefill(*x, qs, 0.09, out_dtype=torch.bfloat16) for x in (a, b)]
+    s = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        got = [lib.packed_attention_prefill(*x, qs, 0.09, out_dtype=torch.bfloat16, stream=t)
+               for x, t in zip((a, b), s)]
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+    g, out = torch.cuda.CUDAGraph(), torch.empty_like(want[0])
+    hold = [x.clone() for x in a]
+    with torch.cuda.graph(g, stream=s[0]):
+        lib.packed_attention_prefill(*hold, qs, 0.09, out=out)
+    for x, y in ((a, want[0]), (b, want[1])):
+        for h, t in zip(hold, x):
+            h.copy_(t)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, y)
+    q, k, v = a
+
+    def call(**kw):
+        x = dict(q=q, k=k, v=v, query_start=qs, scale=0.09)
+        x.update(kw)
+        return lib.packed_attention_prefill(x.pop("q"), x.pop("k"), x.pop("v"), x.pop("query_start"), x.pop("scale"), **x)
+
+    for kw in (dict(k=k[:-1]), dict(k=k.float()), dict(v=v[:, :1]), dict(q=q[:, :7]), dict(query_start=qs.long()),
+               dict(key_start=qs[:-1]), dict(q=q[..., ::2], k=k[..., ::2], v=v[..., ::2]),
+               dict(k=k[:, :1].expand(501, 2, 128)), dict(q=q.cpu()), dict(out=out.double()),
+               dict(out=out.transpose(0, 1)), dict(out_dtype=torch.float16), dict(window=-1), dict(sinks=4),
+               dict(window=8, causal=False), dict(scale=float("inf"))):
+        with pytest.raises((ValueError, lib.PagedKVError)):
+            call(**kw)
+    # rows that begin on no 16-byte boundary
+    with pytest.raises((ValueError, lib.PagedKVError)):
+        call(q=torch.zeros(501 * 8 * 128 + 1, device="cuda", dtype=torch.bfloat16)[1:].view(501, 8, 128))
+
+
+@pytest.mark.parametrize("out_type", ["bf16", "f32"])
+def test_waits_run_out_and_the_next_call_is_clean(lib, out_type):
+    """The first V tile's copies never complete: the call flags it and returns, nothing hangs."""
+    import torch
+    lens = [50, 300]
+    q, k, v = inputs(17, 350, 350, 4, 2, 64)
+    qs = torch.from_numpy(starts(lens)).cuda()
+    dt = torch.bfloat16 if out_type == "bf16" else torch.float32
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def call():
+        status.zero_()
+        torch.cuda.synchronize()
+        t0 = time.monotonic()
+        out = lib.packed_attention_prefill(q, k, v, qs, 0.125, out_dtype=dt, device_status=status)
+        torch.cuda.synchronize()
+        return out, int(status.item()), time.monotonic() - t0
+
+    want, st, _ = call()
+    assert st == 0
+    lib.stall_decode_for_test(16)
+    try:
+        _, st, waited = call()
+        assert st & lib.DEV_TIMEOUT, st
+        assert 1.5 <= waited < 30.0, waited
+    finally:
+        lib.stall_decode_for_test(0)
+    out, st, _ = call()
+    assert st == 0 and torch.equal(out, want)
