@@ -13,16 +13,16 @@
 // TMEM: S_A, S_B (128 columns each; P_t takes the place of S_t, two bf16 to a column), O_A, O_B.
 //
 // A persistent CTA per SM takes items, longest first, so that the roles of one item run into the
-// next: while the last products of an item and its epilogue are under way, the next one's Q and first
-// keys are loaded and its first scores computed.  Warps:
-//   0-3, 4-7  softmax of tile A, of tile B (thread = row)
-//   8-11      epilogue: O out of TMEM, divided by the row's sum, to global memory
-//   12        issues the MMAs: PV_A(j), QK_A(j+1), PV_B(j), QK_B(j+1), so that one tile's softmax
-//             runs under the other's products
-//   13        TMA loads (Q_A, Q_B; a ring of K and V tiles)
-//   14        finds the items: the u-th unit of the batch, longest first
-//   15        clears the rows of a V tile past its sequence's end: they belong to another sequence,
-//             and a weight of 0 times what is not finite would be NaN
+// next: while the last products of an item are under way, the next one's first keys are loaded.  Warps:
+//   0-7, 8-15  softmax and epilogue of tile A, of tile B: 16 rows a warp, four lanes on a row.  With a row per
+//              thread and four warps a tile, a key tile's softmax took 1,750 cycles of a chain of 3,500:
+//              one warp on a sub-partition waits for its own loads, exponentials and stores in turn
+//   16         issues the MMAs: PV_A(j), QK_A(j+1), PV_B(j), QK_B(j+1), so that one tile's softmax
+//              runs under the other's products (P takes S's place: the next scores wait for the product)
+//   17         TMA loads (Q_A, Q_B; a ring of K and V tiles)
+//   18         finds the items: the u-th unit of the batch, longest first
+// Rows of a V tile past its sequence's end belong to another sequence, and a weight of 0 times what is
+// not finite would be NaN: the softmax warps clear them before they hand over the tile's weights.
 // The running reference m moves only when a weight would exceed 2^kPkLag, so that O is hardly ever
 // scaled; S_t(j) being there implies that PV_t(j-1) is done (one thread issues both), so the softmax
 // warps scale it themselves.
@@ -37,7 +37,7 @@ namespace pkv {
 
 constexpr int kPkRows = 128;      // accumulator rows of a query tile (M)
 constexpr int kPkKeys = 128;      // keys of a tile (N of QK, K of PV)
-constexpr int kPkThreads = 512;
+constexpr int kPkThreads = 640;
 constexpr int kPkRank = 1024;     // sequences whose items are ordered by length together
 constexpr int kPkSlab = 128 * 128;   // 128 rows of 64 bf16 (128-byte swizzle)
 // The reference m moves only when a weight would exceed 2^kPkLag: the weights, their sum and O are
@@ -49,7 +49,6 @@ constexpr float kPkLag = 24.f;
 // up to 2^-23 of O for each 16 keys and weight part, which adds up (20,000 keys in one go: 4.4e-5 of the
 // norm); 8 tiles are 128 such sums.  In between the epilogue adds in float32, in the output's own rows.
 constexpr int kPkPart = 8;
-constexpr int kPkOut = 4 * 4096;     // epilogue: 32 rows of 128 bytes per warp
 
 struct PackedParams {
   void* out;                    // [T, Hq, D]
@@ -88,60 +87,114 @@ template <int SLABS, int STAGES>
 struct PkLayout {
   static constexpr int kTile = SLABS * kPkSlab;   // a query or key tile
   static constexpr int kRing = 2 * kTile;         // after Q_A, Q_B
-  static constexpr int kStage = kRing + STAGES * kTile;
-  static constexpr int kRankAt = kStage + kPkOut;
+  static constexpr int kRankAt = kRing + STAGES * kTile;
   static constexpr size_t bytes() { return 1024 + kRankAt + kPkRank * 8; }
 };
 
-// 128 consecutive TMEM columns of this warp's 32 lanes -> 128 registers.
-__device__ __forceinline__ void pk_ld128(uint32_t taddr, float* v) {
-  uint32_t r[128];
-#define PKV_R8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), "=r"(r[i + 4]), \
-                  "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
-#define PKV_LD32(i) \
-  asm volatile( \
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14," \
-      "%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n" \
-      : PKV_R8(i), PKV_R8(i + 8), PKV_R8(i + 16), PKV_R8(i + 24) \
-      : "r"(taddr + i))
-  PKV_LD32(0);
-  PKV_LD32(32);
-  PKV_LD32(64);
-  PKV_LD32(96);
-#undef PKV_LD32
-#undef PKV_R8
+// 16 rows x 64 TMEM columns -> 32 registers a lane, in two steps: they hold the columns after
+// pk_ld_wait.  Registers 4g, 4g + 1 are columns 8g + 2c, 8g + 2c + 1 of row lane / 4, c = lane % 4, and
+// 4g + 2, 4g + 3 those of row lane / 4 + 8.
+__device__ __forceinline__ void pk_ld64(uint32_t taddr, float* v) {
+#define PKV_F8(i) "=f"(v[i]), "=f"(v[i + 1]), "=f"(v[i + 2]), "=f"(v[i + 3]), "=f"(v[i + 4]), \
+                  "=f"(v[i + 5]), "=f"(v[i + 6]), "=f"(v[i + 7])
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+      : PKV_F8(0), PKV_F8(8), PKV_F8(16), PKV_F8(24)
+      : "r"(taddr));
+#undef PKV_F8
+}
+__device__ __forceinline__ void pk_ld_wait(float* v) {
   asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 128; ++i) v[i] = __uint_as_float(r[i]);
+  // nothing that reads them moves before the wait
+#define PKV_F8(i) "+f"(v[i]), "+f"(v[i + 1]), "+f"(v[i + 2]), "+f"(v[i + 3]), "+f"(v[i + 4]), \
+                  "+f"(v[i + 5]), "+f"(v[i + 6]), "+f"(v[i + 7])
+  asm volatile("" : PKV_F8(0), PKV_F8(8), PKV_F8(16), PKV_F8(24));
+#undef PKV_F8
 }
 
-// 16 registers to 16 TMEM columns of this warp's lanes, without the wait.
-__device__ __forceinline__ void pk_st16(uint32_t taddr, const uint32_t* v) {
+// 16 registers to 16 rows x 32 TMEM columns, without the wait: registers 2g, 2g + 1 are column 4g + c of
+// rows lane / 4 and lane / 4 + 8.
+__device__ __forceinline__ void pk_st32(uint32_t taddr, const uint32_t* v) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
       "%16};\n" ::"r"(taddr),
       "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
       "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
       : "memory");
 }
 
-// 16 TMEM columns of this warp's lanes, times f, without the wait for the stores (few registers: the
-// scores are in the others).
-__device__ __forceinline__ void pk_scale16(uint32_t taddr, float f) {
-  uint32_t r[16];
+// 16 TMEM columns of 16 rows, times f0 (row lane / 4) and f1 (row lane / 4 + 8), without the wait for the
+// stores.
+__device__ __forceinline__ void pk_scale16(uint32_t taddr, float f0, float f1) {
+  uint32_t r[8];
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n"
       " tcgen05.wait::ld.sync.aligned;\n"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
       : "r"(taddr)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
-  pk_st16(taddr, r);
+  for (int i = 0; i < 8; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * ((i & 2) ? f1 : f0));
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
 }
 
-// Warp 14: the items of one CTA.  Units (sequence, pair of query tiles, KV head) are ordered by
+// 32 bytes to global memory, on a 32-byte boundary: a whole sector.
+__device__ __forceinline__ void pk_store32(void* dst, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(dst), "r"(v[0]), "r"(v[1]),
+               "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// Waits for the barriers of those lanes that have one, looked at in one instruction.
+__device__ __forceinline__ bool pk_wait_lanes(bool any, uint32_t bar, uint32_t parity, volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 0;; ++n) {
+    uint32_t there = 1;
+    if (any)
+      asm volatile(
+          "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+          " selp.u32 %0, 1, 0, p;\n}\n"
+          : "=r"(there)
+          : "r"(bar), "r"(parity)
+          : "memory");
+    if (__all_sync(0xffffffffu, there != 0)) return true;
+    if ((n & 63u) == 0) {
+      bool stop = *abort_flag != 0;
+      const uint64_t now = global_ns();
+      if (n == 0) t0 = now;
+      if (now - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        stop = true;
+      }
+      if (__any_sync(0xffffffffu, stop)) return false;
+    }
+  }
+}
+
+// Two phases, looked at together by a whole warp.
+__device__ __forceinline__ bool pk_wait2(uint32_t bar_a, uint32_t par_a, uint32_t bar_b, uint32_t par_b,
+                                         volatile int* abort_flag) {
+  uint64_t t0 = 0;
+  for (uint32_t n = 0;; ++n) {
+    if (__all_sync(0xffffffffu, pw_test2(bar_a, par_a, bar_b, par_b))) return true;
+    if ((n & 63u) == 63u) {
+      bool stop = *abort_flag != 0;
+      const uint64_t now = global_ns();
+      if (n == 63u) t0 = now;
+      if (now - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        stop = true;
+      }
+      if (__any_sync(0xffffffffu, stop)) return false;
+    }
+  }
+}
+
+// Warp 18: the items of one CTA.  Units (sequence, pair of query tiles, KV head) are ordered by
 // the length of their key lists, longest first and KV heads fastest, within each kPkRank sequences;
 // round k of a grid of n CTAs takes units kn .. kn + n - 1, every other round in the opposite
 // order.  Order by counting: the units of sequence s that are at least x long are known in closed
@@ -244,9 +297,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t kv_full[STAGES], kv_empty[STAGES];
   __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], o_empty[2],
-      item_full[2], item_empty[2], drain;
-  // by item slot: these roles may be one item ahead of the one that waits
-  __shared__ __align__(8) uint64_t l_full[2][2], v_loading[2], v_clean[2];
+      l_full[2], item_full[2], item_empty[2], drain;
   __shared__ PkItem items[2];
   __shared__ float row_sum[2][2][kPkRows], row_ref[LO ? 2 : 1][2][kPkRows];   // [item slot][tile]
   __shared__ uint32_t tmem_base_sh;
@@ -265,16 +316,13 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       mbar_init(smem_u32(&q_full[t]), 1);
       mbar_init(smem_u32(&q_empty[t]), 1);
       mbar_init(smem_u32(&s_full[t]), 1);
-      mbar_init(smem_u32(&p_full[t][0]), 4);
-      mbar_init(smem_u32(&p_full[t][1]), 4);
+      mbar_init(smem_u32(&p_full[t][0]), 8);
+      mbar_init(smem_u32(&p_full[t][1]), 8);
       mbar_init(smem_u32(&o_full[t]), 1);
-      mbar_init(smem_u32(&o_empty[t]), 4);
-      mbar_init(smem_u32(&l_full[t][0]), 4);
-      mbar_init(smem_u32(&l_full[t][1]), 4);
-      mbar_init(smem_u32(&v_loading[t]), 1);
-      mbar_init(smem_u32(&v_clean[t]), 1);
+      mbar_init(smem_u32(&o_empty[t]), 8);
+      mbar_init(smem_u32(&l_full[t]), 8);
       mbar_init(smem_u32(&item_full[t]), 1);
-      mbar_init(smem_u32(&item_empty[t]), 15);   // 8 softmax, 4 epilogue warps, 12, 13, 15
+      mbar_init(smem_u32(&item_empty[t]), 18);   // 16 softmax warps, 16, 17
     }
     mbar_init(smem_u32(&drain), 1);
     if (p.test_stall_bytes != 0 && blockIdx.x == 0)
@@ -304,50 +352,62 @@ __global__ void __launch_bounds__(kPkThreads, 1)
     it = items[i & 1];
     return it.valid != 0;
   };
-  int loads = 0, copied_q[2] = {0, 0};   // warp 13: copies started, K/V tiles and Q tiles
+  int loads = 0, copied_q[2] = {0, 0};   // warp 17: copies started, K/V tiles and Q tiles
 
-  // 512 threads of 128 registers; 2 x 128 x 184 + 128 x 80 + 128 x 64 = 512 x 128
-  if (warp >= 12) {
+  // 640 threads of 96 registers; 512 x 104 + 128 x 64 = 640 x 96
+  if (warp >= 16) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n");
-    if (warp == 12) {
+    if (warp == 16) {
       // ------------------------------ MMA issuer ------------------------------
       // The whole warp walks the lists, so that the compiler knows stages and descriptors uniform, and one
-      // lane issues.
-      const uint32_t idesc_qk = tc_idesc(kPkRows, kPkKeys, false, false, true);
+      // lane issues.  Barriers are looked at together, a lane each: the tensor cores queue little, and
+      // every look (100 to 200 cycles) is time they lie idle.
+      // a negative logit scale turns q's sign (bit 13), so that a larger product is a larger logit
+      const uint32_t idesc_qk =
+          tc_idesc(kPkRows, kPkKeys, false, false, true) | (p.scale_log2 < 0.f ? 1u << 13 : 0u);
       const uint32_t idesc_pv = tc_idesc(kPkRows, (p.dim + 15) & ~15, false, true, true);
       const int ksteps = (p.dim + 15) / 16;
       const uint64_t qd0 = tc_desc(sma, 0, 1024), kd0 = tc_desc(sma + LY::kRing, 0, 1024),
                      vd0 = tc_desc(sma + LY::kRing, kPkSlab, 1024);
-      // phases gone by, one bit each: q_full[t], p_full[t], o_empty[t], v_clean[slot]
-      uint32_t ph_q = 0, ph_p = 0, ph_o = 3, ph_c = 0;
-      auto flip = [](uint32_t& bits, int b) {
-        const uint32_t parity = (bits >> b) & 1;
-        bits ^= 1u << b;
-        return parity;
-      };
-      auto qk = [&](int t, int st, bool done) {   // `done`: the item's last scores of this tile
-        tc_fence_after();
-        if (pw_elect()) {
-          const uint64_t qd = qd0 + ((t * LY::kTile) >> 4), kd = kd0 + ((st * LY::kTile) >> 4);
+      // phases gone by, one bit per tile: q_full, p_full, o_empty (nothing to wait for at first)
+      uint32_t ph_q = 0, ph_p = 0, ph_o = 3;
+      auto qk = [&](int t, int st, bool ends) {   // by one lane; `ends`: Q_t is not needed after this
+        const uint64_t qd = qd0 + ((t * LY::kTile) >> 4), kd = kd0 + ((st * LY::kTile) >> 4);
 #pragma unroll
-          for (int ks = 0; ks < 4 * SLABS; ++ks) {   // 16 dims: slab ks / 4, 32 bytes each
-            const int at = ((ks >> 2) * kPkSlab + (ks & 3) * 32) >> 4;
-            if (ks < ksteps) tc_mma(tm + 128 * t, qd + at, kd + at, idesc_qk, ks > 0);
-          }
-          tc_commit(smem_u32(&s_full[t]));
-          if (done) tc_commit(smem_u32(&q_empty[t]));
+        for (int ks = 0; ks < 4 * SLABS; ++ks) {   // 16 dims: slab ks / 4, 32 bytes each
+          const int at = ((ks >> 2) * kPkSlab + (ks & 3) * 32) >> 4;
+          if (ks < ksteps) tc_mma(tm + 128 * t, qd + at, kd + at, idesc_qk, ks > 0);
         }
-        __syncwarp();
+        tc_commit(smem_u32(&s_full[t]));
+        if (ends) tc_commit(smem_u32(&q_empty[t]));
+      };
+      auto pv = [&](int t, int st, int half, bool first) {   // by one lane
+        const uint64_t vd = vd0 + ((st * LY::kTile) >> 4);
+        const uint32_t dO = tm + 256 + 128 * t;
+#pragma unroll
+        for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {   // 16 keys: 16 rows of 128 bytes
+          const uint64_t bd = vd + ((kk * 2048) >> 4);
+          tc_mma_ts(dO, tm + 128 * t + 8 * kk, bd, idesc_pv, (!first || kk > 0));
+          if (LO) tc_mma_ts(dO, tm + 128 * t + 64 + 8 * kk, bd, idesc_pv, 1);
+        }
+      };
+      // Waits for up to three barriers: lane 0, 1 and 2's.
+      auto wait3 = [&](bool a, uint32_t bar_a, uint32_t par_a, bool b, uint32_t bar_b, uint32_t par_b, bool c,
+                       uint32_t bar_c, uint32_t par_c) {
+        const uint32_t bar = lane == 0 ? bar_a : lane == 1 ? bar_b : bar_c;
+        const uint32_t par = lane == 0 ? par_a : lane == 1 ? par_b : par_c;
+        const bool any = lane == 0 ? a : lane == 1 ? b : lane == 2 ? c : false;
+        return pk_wait_lanes(any, bar, par, abort_flag);
       };
       int nt[2] = {0, 0}, nn[2] = {0, 0}, fl = 0, nfl = 0;   // lists of this item and the next
-      constexpr int kRagged = 1, kFirst = 2, kEnds = 4;   // kEnds << t
-      auto lists = [&](int i, int& a, int& b, int& r) {
+      constexpr int kFirst = 1, kEnds = 2;   // kEnds << t
+      auto lists = [&](int i, int& a, int& b, int& f) {
         if (!pw_wait_all(smem_u32(&item_full[i & 1]), (i >> 1) & 1, abort_flag)) return false;
         const PkItem& it = items[i & 1];
         a = __shfl_sync(0xffffffffu, it.nt_a, 0);
         b = __shfl_sync(0xffffffffu, it.nt_b, 0);
-        r = __shfl_sync(0xffffffffu, (it.ragged ? kRagged : 0) | (it.j0 == 0 ? kFirst : 0) |
-                                         (it.ends(0) ? kEnds : 0) | (it.ends(1) ? 2 * kEnds : 0), 0);
+        f = __shfl_sync(0xffffffffu, (it.j0 == 0 ? kFirst : 0) | (it.ends(0) ? kEnds : 0) |
+                                         (it.ends(1) ? 2 * kEnds : 0), 0);
         return __shfl_sync(0xffffffffu, it.valid, 0) != 0;
       };
       bool ok = true, more = lists(0, nt[0], nt[1], fl);
@@ -362,12 +422,15 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       };
       // the first item's first scores
       if (more && max(nt[0], nt[1]) > 0) {
-        ok = pw_wait_all(smem_u32(&kv_full[0]), 0, abort_flag);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           if (!ok || nt[t] == 0) continue;
-          ok = pw_wait_all(smem_u32(&q_full[t]), flip(ph_q, t), abort_flag);
-          if (ok) qk(t, 0, nt[t] == 1 && (fl & (kEnds << t)));
+          ok = wait3(true, smem_u32(&kv_full[0]), 0, true, smem_u32(&q_full[t]), 0, false, 0, 0);
+          ph_q ^= 1u << t;
+          if (!ok) break;
+          tc_fence_after();
+          if (pw_elect()) qk(t, 0, nt[t] == 1 && (fl & (kEnds << t)));
+          __syncwarp();
         }
         if (ok && pw_elect()) tc_commit(smem_u32(&kv_empty[0]));
         __syncwarp();
@@ -376,7 +439,43 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       for (int i = 0; more && ok; ++i) {
         const int most = max(nt[0], nt[1]), steps = max(most, 1);
         bool go_on = false;
-        for (int j = 0; j < steps && ok; ++j) {
+        int j = 0;
+        // Steps in which both tiles have weights and next scores of this item: nearly all of a long list.
+        const int plain = min(nt[0], nt[1]) - 1;
+        if (plain > 0) {
+          ok = wait3(true, smem_u32(&o_empty[0]), ph_o & 1, true, smem_u32(&o_empty[1]), ph_o >> 1, false, 0, 0);
+          ph_o ^= 3u;
+        }
+        for (; j < plain && ok; ++j) {
+          const int vs = st;
+          const uint32_t v_ph = st_ph;
+          advance();
+          const int ks = st;
+          const uint32_t k_ph = st_ph;
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            ok = pk_wait2(smem_u32(&p_full[t][0]), (ph_p >> t) & 1, smem_u32(&kv_full[vs]), v_ph, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            if (pw_elect()) pv(t, vs, 0, j == 0);
+            __syncwarp();
+            ok = pk_wait2(smem_u32(&p_full[t][1]), (ph_p >> t) & 1, smem_u32(&kv_full[ks]), k_ph, abort_flag);
+            if (!ok) break;
+            tc_fence_after();
+            if (pw_elect()) {
+              pv(t, vs, 1, false);
+              qk(t, ks, j + 2 == nt[t] && (fl & (kEnds << t)));
+              if (t == 1) {   // both tiles are done with these
+                tc_commit(smem_u32(&kv_empty[vs]));
+                tc_commit(smem_u32(&kv_empty[ks]));
+              }
+            }
+            __syncwarp();
+          }
+          ph_p ^= 3u;
+          advance();
+        }
+        for (; j < steps && ok; ++j) {
           const bool last = j == steps - 1;
           if (last) go_on = lists(i + 1, nn[0], nn[1], nfl);
           // V_j, then K_(j+1) or the next item's K_0
@@ -385,58 +484,47 @@ __global__ void __launch_bounds__(kPkThreads, 1)
           if (most > 0) advance();
           const int ks = st;
           const uint32_t k_ph = st_ph;
-          const bool any_k = last ? go_on && max(nn[0], nn[1]) > 0 : true;
-          bool v_there = false, k_there = false;
+          const bool any_k = !last || (go_on && max(nn[0], nn[1]) > 0);
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
-            if (!ok) break;
-            if (j < nt[t]) {
-              const uint32_t pp = flip(ph_p, t);
-              ok = pw_wait_all(smem_u32(&p_full[t][0]), pp, abort_flag);
-              if (ok && !v_there) {
-                ok = pw_wait_all(smem_u32(&kv_full[vs]), v_ph, abort_flag);
-                if (ok && last && (fl & kRagged))
-                  ok = pw_wait_all(smem_u32(&v_clean[i & 1]), flip(ph_c, i & 1), abort_flag);
-                v_there = true;
-              }
-              if (ok && j == 0) ok = pw_wait_all(smem_u32(&o_empty[t]), flip(ph_o, t), abort_flag);
-              const uint64_t vd = vd0 + ((vs * LY::kTile) >> 4);
-              const uint32_t dO = tm + 256 + 128 * t;
-#pragma unroll
-              for (int half = 0; half < 2; ++half) {
-                if (half == 1 && ok) ok = pw_wait_all(smem_u32(&p_full[t][1]), pp, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                if (pw_elect()) {
-#pragma unroll
-                  for (int kk = 4 * half; kk < 4 * half + 4; ++kk) {   // 16 keys: 16 rows of 128 bytes
-                    const uint64_t bd = vd + ((kk * 2048) >> 4);
-                    tc_mma_ts(dO, tm + 128 * t + 8 * kk, bd, idesc_pv, (j > 0 || kk > 0));
-                    if (LO) tc_mma_ts(dO, tm + 128 * t + 64 + 8 * kk, bd, idesc_pv, 1);
-                  }
-                  if (half == 1 && j == nt[t] - 1) tc_commit(smem_u32(&o_full[t]));
+            const bool work = j < nt[t], need = last ? go_on && nn[t] > 0 : j + 1 < nt[t];
+            const bool new_q = need && last && (nfl & kFirst);
+            if (work) {
+              ok = wait3(true, smem_u32(&p_full[t][0]), (ph_p >> t) & 1, true, smem_u32(&kv_full[vs]), v_ph,
+                         j == 0, smem_u32(&o_empty[t]), (ph_o >> t) & 1);
+              if (j == 0) ph_o ^= 1u << t;
+              if (!ok) break;
+              tc_fence_after();
+              if (pw_elect()) pv(t, vs, 0, j == 0);
+              __syncwarp();
+            }
+            if (work || need) {
+              ok = wait3(work, smem_u32(&p_full[t][1]), (ph_p >> t) & 1, need, smem_u32(&kv_full[ks]), k_ph, new_q,
+                         smem_u32(&q_full[t]), (ph_q >> t) & 1);
+              if (work) ph_p ^= 1u << t;
+              if (new_q) ph_q ^= 1u << t;
+              if (!ok) break;
+              tc_fence_after();
+              if (pw_elect()) {
+                if (work) {
+                  pv(t, vs, 1, false);
+                  if (j == nt[t] - 1) tc_commit(smem_u32(&o_full[t]));
                 }
-                __syncwarp();
+                if (need) qk(t, ks, last ? nn[t] == 1 && (nfl & (kEnds << t)) : j + 2 == nt[t] && (fl & (kEnds << t)));
+                if (t == 1) {   // both tiles are done with these
+                  if (most > 0) tc_commit(smem_u32(&kv_empty[vs]));
+                  if (any_k) tc_commit(smem_u32(&kv_empty[ks]));
+                }
               }
-              if (!ok) break;
-            }
-            const bool need = last ? go_on && nn[t] > 0 : j + 1 < nt[t];
-            if (need) {
-              if (!k_there) {
-                ok = pw_wait_all(smem_u32(&kv_full[ks]), k_ph, abort_flag);
-                k_there = true;
+              __syncwarp();
+            } else if (t == 1) {
+              if (pw_elect()) {
+                if (most > 0) tc_commit(smem_u32(&kv_empty[vs]));
+                if (any_k) tc_commit(smem_u32(&kv_empty[ks]));
               }
-              if (ok && last && (nfl & kFirst)) ok = pw_wait_all(smem_u32(&q_full[t]), flip(ph_q, t), abort_flag);
-              if (!ok) break;
-              qk(t, ks, last ? nn[t] == 1 && (nfl & (kEnds << t)) : j + 2 == nt[t] && (fl & (kEnds << t)));
+              __syncwarp();
             }
           }
-          if (!ok) break;
-          if (pw_elect()) {
-            if (v_there) tc_commit(smem_u32(&kv_empty[vs]));
-            if (k_there) tc_commit(smem_u32(&kv_empty[ks]));
-          }
-          __syncwarp();
           if (any_k) advance();
         }
         if (ok && lane == 0) mbar_arrive(smem_u32(&item_empty[i & 1]));
@@ -449,27 +537,14 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       __syncwarp();
       volatile int no_abort = 0;
       pw_wait(smem_u32(&drain), 0, &no_abort);
-    } else if (warp == 13) {
+    } else if (warp == 17) {
       // ------------------------------ TMA loads -------------------------------
       if (pw_elect()) {
         PkItem it;
         bool ok = true;
         for (int i = 0; ok && next_item(i, it); ++i) {
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (!ok || it.j0 > 0 || it.nt(t) == 0) continue;
-            if (copied_q[t] > 0) ok = pw_wait(smem_u32(&q_empty[t]), (copied_q[t] - 1) & 1, abort_flag);
-            if (!ok) break;
-            const uint32_t bar = smem_u32(&q_full[t]);
-            mbar_arrive_expect_tx(bar, SLABS * G * TQ * 128);
-#pragma unroll
-            for (int h = 0; h < SLABS; ++h)
-              tma_load_3d(sma + t * LY::kTile + h * kPkSlab, &tmap_q, 64 * h, it.head * G,
-                          it.row0 + t * TQ, bar);
-            ++copied_q[t];
-          }
           const int nt = it.most();
-          for (int x = 0; x < 2 * nt && ok; ++x) {   // K_0, V_0, K_1, V_1, ...
+          for (int x = 0; x < 2 * nt && ok; ++x) {   // K_0, Q_A, Q_B, V_0, K_1, V_1, ...
             const int st = loads % STAGES;
             if (loads >= STAGES)
               ok = pw_wait(smem_u32(&kv_empty[st]), ((loads / STAGES) - 1) & 1, abort_flag);
@@ -482,15 +557,28 @@ __global__ void __launch_bounds__(kPkThreads, 1)
               tma_load_3d(stage_at(loads) + h * kPkSlab, (x & 1) ? &tmap_v : &tmap_k, 64 * h, it.head, row,
                           bar);
             ++loads;
+            if (x > 0 || it.j0 > 0) continue;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (!ok || it.nt(t) == 0) continue;
+              if (copied_q[t] > 0) ok = pw_wait(smem_u32(&q_empty[t]), (copied_q[t] - 1) & 1, abort_flag);
+              if (!ok) break;
+              const uint32_t qbar = smem_u32(&q_full[t]);
+              mbar_arrive_expect_tx(qbar, SLABS * G * TQ * 128);
+#pragma unroll
+              for (int h = 0; h < SLABS; ++h)
+                tma_load_3d(sma + t * LY::kTile + h * kPkSlab, &tmap_q, 64 * h, it.head * G, it.row0 + t * TQ,
+                            qbar);
+              ++copied_q[t];
+            }
           }
-          if (ok && it.ragged) mbar_arrive(smem_u32(&v_loading[i & 1]));
           if (ok) mbar_arrive(smem_u32(&item_empty[i & 1]));
         }
       }
       loads = __reduce_max_sync(0xffffffffu, loads);
       copied_q[0] = __reduce_max_sync(0xffffffffu, copied_q[0]);
       copied_q[1] = __reduce_max_sync(0xffffffffu, copied_q[1]);
-    } else if (warp == 14) {
+    } else if (warp == 18) {
       // ------------------------------- items ----------------------------------
       int32_t* pairs = reinterpret_cast<int32_t*>(sm + LY::kRankAt);
       PkOrder order{p, pairs, pairs + kPkRank, !p.causal || p.window > 0};
@@ -552,164 +640,51 @@ __global__ void __launch_bounds__(kPkThreads, 1)
         __syncwarp();
         if (!found) break;
       }
-    } else {
-      // ---------------- V rows past the sequence's end -> 0 --------------------
-      // The loader says when the tile's copy is under way: the phase that its barrier then waits for is
-      // this copy's, and not an earlier one of the same parity.
-      PkItem it;
-      int base = 0;
-      uint32_t phase = 0;   // bit: of v_loading[slot]
-      for (int i = 0; __all_sync(0xffffffffu, next_item(i, it)); ++i) {
-        const int nt = it.most();
-        if (it.ragged) {
-          const int vi = base + 2 * (nt - 1) + 1;
-          if (!pw_wait_all(smem_u32(&v_loading[i & 1]), (phase >> (i & 1)) & 1, abort_flag) ||
-              !pw_wait_all(kv_bar(vi), (vi / STAGES) & 1, abort_flag))
-            break;
-          phase ^= 1u << (i & 1);
-          const int from = it.keys - key_tile(it, it.j0 + nt - 1) * kPkKeys;
-          uint8_t* v = sm + LY::kRing + (vi % STAGES) * LY::kTile;
-          for (int u = lane; u < (kPkKeys - from) * 8; u += 32) {
-#pragma unroll
-            for (int h = 0; h < SLABS; ++h)
-              *reinterpret_cast<uint4*>(v + h * kPkSlab + from * 128 + u * 16) = make_uint4(0, 0, 0, 0);
-          }
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&v_clean[i & 1]));
-        }
-        base += 2 * nt;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&item_empty[i & 1]));
-      }
-    }
-  } else if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n");
-    // ------------------------------ epilogue ----------------------------------
-    // 128 bytes of each row at a time through shared memory, so that a store is of whole lines.
-    const int w0 = (warp & 3) * 32;
-    uint8_t* stage = sm + LY::kStage + (warp & 3) * 4096;
-    const int esz = p.out_bf16 ? 2 : 4, cols = 128 / esz;
-    const uint32_t g_inv = (65536u + G - 1) / G;   // row / G for row < 128: exact for G <= 128
-    uint32_t phase_o = 0, phase_l = 0;   // bits: phases of o_full[t], of l_full[slot][t]
-    float ref_a = 0.f, ref_b = 0.f;      // the row's reference in the part before
-    PkItem it;
-    for (int i = 0; __all_sync(0xffffffffu, next_item(i, it)); ++i) {
-      bool ok = true;
-#pragma unroll 1
-      for (int t = 0; t < 2 && ok; ++t) {
-        // rows of the sequence; those of an earlier part that this one adds nothing to are done
-        if (t * TQ >= it.tokens || (it.j0 > 0 && it.nt(t) == 0)) continue;
-        uint8_t* dst[8];   // rows 4 r + lane / 8, eight lanes each
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const int row = w0 + 4 * r + (lane >> 3);
-          const int tk = static_cast<int>((row * g_inv) >> 16), tok = t * TQ + tk;
-          dst[r] = nullptr;
-          if (row < TQ * G && tok < it.tokens)
-            dst[r] = static_cast<uint8_t*>(p.out) + (lane & 7) * 16 +
-                     (static_cast<int64_t>(it.row0 + tok) * p.num_q_heads + it.head * G + row - tk * G) *
-                         (p.dim * esz);
-        }
-        const bool some = it.nt(t) > 0;
-        float inv = 0.f, keep = 0.f;   // of O, of what earlier parts left
-        if (some) {
-          const int bl = (i & 1) * 2 + t;
-          ok = pw_wait_all(smem_u32(&l_full[i & 1][t]), (phase_l >> bl) & 1, abort_flag) &&
-               pw_wait_all(smem_u32(&o_full[t]), (phase_o >> t) & 1, abort_flag);
-          if (!ok) break;
-          phase_l ^= 1u << bl;
-          phase_o ^= 1u << t;
-          tc_fence_after();
-          const float l = row_sum[i & 1][t][w0 + lane];
-          inv = !LO || it.ends(t) ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-          if constexpr (LO) {   // the parts' references differ where the row's has moved
-            const float ref = row_ref[i & 1][t][w0 + lane], was = t == 0 ? ref_a : ref_b;
-            keep = was == ref ? inv : pf_ex2(was - ref) * inv;
-            if (t == 0) ref_a = ref; else ref_b = ref;
-          }
-        }
-        const uint32_t tO = tm + 256 + 128 * t + (static_cast<uint32_t>(w0) << 16);
-        for (int c = 0; c < p.dim; c += cols) {
-          for (int hf = 0; hf < cols; hf += 32) {
-            float o[32];
-            if (some) {
-              tc_ld32(tO + c + hf, o);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] = 0.f;
-            }
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= inv;
-            if (p.out_bf16) {
-#pragma unroll
-              for (int u = 0; u < 4; ++u)
-                *reinterpret_cast<uint4*>(stage + swz(lane, hf / 8 + u)) =
-                    make_uint4(pack_bf16(o[8 * u], o[8 * u + 1]), pack_bf16(o[8 * u + 2], o[8 * u + 3]),
-                               pack_bf16(o[8 * u + 4], o[8 * u + 5]), pack_bf16(o[8 * u + 6], o[8 * u + 7]));
-            } else {
-#pragma unroll
-              for (int u = 0; u < 8; ++u)
-                *reinterpret_cast<float4*>(stage + swz(lane, u)) =
-                    make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
-            }
-          }
-          if (some && c + cols >= p.dim) {   // O has been read
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&o_empty[t]));
-          }
-          __syncwarp();
-          const bool inside = c * esz + (lane & 7) * 16 < p.dim * esz;
-          if (LO && it.j0 > 0) {
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-              const float f = __shfl_sync(0xffffffffu, keep, 4 * r + (lane >> 3));
-              if (!dst[r] || !inside) continue;
-              float4* d = reinterpret_cast<float4*>(dst[r] + c * esz);
-              const float4 a = *d, b = *reinterpret_cast<const float4*>(stage + swz(4 * r + (lane >> 3), lane & 7));
-              *d = make_float4(fmaf(a.x, f, b.x), fmaf(a.y, f, b.y), fmaf(a.z, f, b.z), fmaf(a.w, f, b.w));
-            }
-          } else if (inside) {
-#pragma unroll
-            for (int r = 0; r < 8; ++r)
-              if (dst[r])
-                *reinterpret_cast<uint4*>(dst[r] + c * esz) =
-                    *reinterpret_cast<const uint4*>(stage + swz(4 * r + (lane >> 3), lane & 7));
-          }
-          __syncwarp();
-        }
-      }
-      if (!ok) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&item_empty[i & 1]));
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 184;\n");
-    // -------------------- softmax warpgroups (A: 0-3, B: 4-7) -------------------
-    const int t = warp >> 2, w0 = (warp & 3) * 32, r = w0 + lane;
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n");
+    // ---------------- softmax and epilogue (A: warps 0-7, B: 8-15) ---------------
+    // Softmax: rows w0 + lane / 4 and 8 further, columns 2 (lane % 4) and the next one of every eight.
+    const int t = warp >> 3, quad = (warp & 3) * 32, half = (warp >> 2) & 1, w0 = quad + 16 * half;
+    const int c2 = 2 * (lane & 3);
     const uint32_t tS = tm + 128 * t + (static_cast<uint32_t>(w0) << 16);
     const uint32_t tO = tS + 256;
-    const int my_token = t * TQ + r / G;
-    const bool neg = p.scale_log2 < 0.f;
+    const uint32_t g_inv = (65536u + G - 1) / G;   // row / G for row < 128: exact for G <= 128
     // raised to the smallest normal, so that a masked -inf stays -inf under it
     const float sl2 = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
-    float m = -CUDART_INF_F, l = 0.f;   // the row's reference (in log2 units) and sum
-    int n_s = 0;   // score tiles done
+    const int esz = p.out_bf16 ? 2 : 4;
+    float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};   // references (in log2 units), sums
+    float ref = 0.f;         // row quad + lane's reference in the part before
+    uint32_t n_s = 0, n_o = 0;   // score tiles and items done
+    int entries = 0;         // ring entries of the items before
     PkItem it;
     bool alive = true;
+    auto hand_over = [&](int part) {   // the part's weights are in TMEM
+      pw_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&p_full[t][part]));
+    };
     for (int i = 0; alive && __all_sync(0xffffffffu, next_item(i, it)); ++i) {
       const int my_nt = it.nt(t);
-      const bool row_ok = r < TQ * G && my_token < it.tokens;
-      const int qpos = it.pos0 + my_token;
-      const int last = p.causal ? qpos : it.keys - 1;               // last key that the row sees
-      const int low = p.window > 0 ? qpos - p.window + 1 : 0;       // first key of its window
-      const int last_min = __reduce_min_sync(0xffffffffu, row_ok ? last : INT32_MAX - 1);
-      const int low_max = __reduce_max_sync(0xffffffffu, row_ok ? low : INT32_MIN);
-      if (it.j0 == 0) {
-        m = -CUDART_INF_F;
-        l = 0.f;
+      int last[2], low[2], last_min = INT32_MAX - 1, low_max = INT32_MIN;   // keys that the rows see
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int row = w0 + (lane >> 2) + 8 * e, token = t * TQ + static_cast<int>((row * g_inv) >> 16);
+        const int pos = it.pos0 + token;
+        last[e] = p.causal ? pos : it.keys - 1;
+        low[e] = p.window > 0 ? pos - p.window + 1 : 0;
+        if (row < TQ * G && token < it.tokens) {
+          last_min = min(last_min, last[e]);
+          low_max = max(low_max, low[e]);
+        }
+        if (it.j0 == 0) {
+          m[e] = -CUDART_INF_F;
+          l[e] = 0.f;
+        }
       }
+      last_min = __reduce_min_sync(0xffffffffu, last_min);
+      low_max = __reduce_max_sync(0xffffffffu, low_max);
       for (int j = 0; j < my_nt; ++j) {
         if (!pw_wait_all(smem_u32(&s_full[t]), n_s & 1, abort_flag)) {
           alive = false;
@@ -718,99 +693,216 @@ __global__ void __launch_bounds__(kPkThreads, 1)
         ++n_s;
         tc_fence_after();
         const int k0 = key_tile(it, it.j0 + j) * kPkKeys;
-        float sv[kPkKeys];
-        pk_ld128(tS, sv);
-        if (neg) {
-#pragma unroll
-          for (int c = 0; c < kPkKeys; ++c) sv[c] = -sv[c];
-        }
-        if (k0 + kPkKeys > last_min + 1 || (k0 < low_max && k0 + kPkKeys > p.sinks)) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {   // bits of the keys that the row sees
+        float sv[64];
+        const bool cut = k0 + kPkKeys > last_min + 1 || (k0 < low_max && k0 + kPkKeys > p.sinks);
+        auto look = [&](int h, float (&mt)[2]) {   // 64 keys: those that the row sees, the largest scores
+          float* x = sv + 32 * h;
+          if (cut) {
             const int k = k0 + 64 * h;
-            const uint64_t seen = pw_below(last + 1 - k) & (~pw_below(low - k) | pw_below(p.sinks - k));
-            const uint32_t w[2] = {static_cast<uint32_t>(seen), static_cast<uint32_t>(seen >> 32)};
 #pragma unroll
-            for (int c = 0; c < 64; ++c)
-              sv[64 * h + c] = ((w[c >> 5] >> (c & 31)) & 1u) ? sv[64 * h + c] : -CUDART_INF_F;
-          }
-        }
-        float ma = sv[0], mb = sv[1];
+            for (int e = 0; e < 2; ++e) {
+              const uint64_t seen = (pw_below(last[e] + 1 - k) & (~pw_below(low[e] - k) | pw_below(p.sinks - k))) >> c2;
+              const uint32_t w[2] = {static_cast<uint32_t>(seen), static_cast<uint32_t>(seen >> 32)};
 #pragma unroll
-        for (int c = 2; c + 3 < kPkKeys; c += 4) {
-          ma = pf_max3(ma, sv[c], sv[c + 1]);
-          mb = pf_max3(mb, sv[c + 2], sv[c + 3]);
-        }
-        const float mt = fmaxf(pf_max3(ma, sv[kPkKeys - 2], sv[kPkKeys - 1]), mb) * sl2;
-        float alpha = 1.f;
-        bool resc = false;
-        if (mt > m + kPkLag) {
-          if (m != -CUDART_INF_F) {
-            alpha = pf_ex2(m - mt);
-            resc = j > 0;   // a part's first products begin a new O
+              for (int g = 0; g < 8; ++g) {
+                float* y = x + 4 * g + 2 * e;
+                y[0] = ((w[g >> 2] >> (8 * (g & 3))) & 1u) ? y[0] : -CUDART_INF_F;
+                y[1] = ((w[g >> 2] >> (8 * (g & 3) + 1)) & 1u) ? y[1] : -CUDART_INF_F;
+              }
+            }
           }
-          m = mt;
-        }
-        const float mu = m == -CUDART_INF_F ? 0.f : m;   // rows with nothing seen yet: p = 0
-        if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float a = x[2 * e], b = x[2 * e + 1];
+#pragma unroll
+            for (int g = 1; g < 7; g += 2) {
+              a = pf_max3(a, x[4 * g + 2 * e], x[4 * g + 2 * e + 1]);
+              b = pf_max3(b, x[4 * g + 4 + 2 * e], x[4 * g + 5 + 2 * e]);
+            }
+            mt[e] = pf_max3(a, b, fmaxf(x[28 + 2 * e], x[29 + 2 * e])) * sl2;
+          }
+        };
+        // The references of rows with a score too far above theirs move: what is summed up so far is
+        // scaled, `done` registers of this tile's weights among it.
+        auto move = [&](float (&mt)[2], int done) {
+          float alpha[2];
+          bool resc = false;
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {   // over the row's four lanes
+            mt[e] = fmaxf(mt[e], __shfl_xor_sync(0xffffffffu, mt[e], 1));
+            mt[e] = fmaxf(mt[e], __shfl_xor_sync(0xffffffffu, mt[e], 2));
+            const bool up = mt[e] > m[e] + kPkLag;
+            alpha[e] = up ? pf_ex2(m[e] - mt[e]) : 1.f;
+            resc = resc || (up && m[e] != -CUDART_INF_F);
+            m[e] = up ? mt[e] : m[e];
+            l[e] *= alpha[e];
+          }
+          if (done) {
+#pragma unroll
+            for (int n = 0; n < 32; ++n) sv[n] *= alpha[(n >> 1) & 1];
+          }
+          if (j > 0 && __any_sync(0xffffffffu, resc)) {   // (a part's first products begin a new O)
 #pragma unroll 1
-          for (int c = 0; c < p.dim; c += 16) pk_scale16(tO + c, alpha);
-          pw_st_wait();
-        }
-        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int part = 0; part < 4; ++part) {   // 32 keys at a time: 16 registers of weights
-          uint32_t w[16];
-          float* x = sv + 32 * part;
-#pragma unroll
-          for (int c = 0; c < 32; c += 2) {
-            const float2 z = __ffma2_rn(make_float2(x[c], x[c + 1]), make_float2(sl2, sl2),
-                                        make_float2(-mu, -mu));
-            const float2 y = make_float2(pf_ex2(z.x), pf_ex2(z.y));   // 2^-inf = 0 for masked keys
-            ls[(c >> 1) & 1] = __fadd2_rn(ls[(c >> 1) & 1], y);
-            w[c >> 1] = pack_bf16(y.x, y.y);
-            if constexpr (LO) {
-              x[c] = y.x;
-              x[c + 1] = y.y;
-            }
-          }
-          pk_st16(tS + 16 * part, w);   // row = lane, column c = keys 2c and 2c + 1
-          if constexpr (LO) {   // what the first part left
-            uint32_t wl[16];
-#pragma unroll
-            for (int c = 0; c < 32; c += 2) {
-              const float2 lo = __ffma2_rn(make_float2(bf16_lo(w[c >> 1]), bf16_hi(w[c >> 1])),
-                                           make_float2(-1.f, -1.f), make_float2(x[c], x[c + 1]));
-              wl[c >> 1] = pack_bf16(lo.x, lo.y);
-            }
-            pk_st16(tS + 64 + 16 * part, wl);
-          }
-          if (part == 3) {
-            l = l * alpha + ((ls[0].x + ls[0].y) + (ls[1].x + ls[1].y));
-            if (j == my_nt - 1) {
-              row_sum[i & 1][t][r] = l;
-              if constexpr (LO) row_ref[i & 1][t][r] = m;
-            }
-          }
-          if (part & 1) {
+            for (int c = 0; c < p.dim; c += 16) pk_scale16(tO + c, alpha[0], alpha[1]);
             pw_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-              mbar_arrive(smem_u32(&p_full[t][part >> 1]));
-              if (part == 3 && j == my_nt - 1) mbar_arrive(smem_u32(&l_full[i & 1][t]));
+          }
+        };
+        auto exps = [&](int h) {
+          float* x = sv + 32 * h;
+          const float mu[2] = {m[0] == -CUDART_INF_F ? 0.f : m[0], m[1] == -CUDART_INF_F ? 0.f : m[1]};
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {   // register pair n: group n / 2, row n % 2
+            const int e = n & 1;
+            const float2 z = __ffma2_rn(make_float2(x[2 * n], x[2 * n + 1]), make_float2(sl2, sl2),
+                                        make_float2(-mu[e], -mu[e]));
+            x[2 * n] = pf_ex2(z.x);   // 2^-inf = 0 for masked keys
+            x[2 * n + 1] = pf_ex2(z.y);
+          }
+        };
+        pk_ld64(tS, sv);
+        pk_ld_wait(sv);
+        pk_ld64(tS + 64, sv + 32);
+        float mt0[2], mt1[2];
+        look(0, mt0);
+        if (__any_sync(0xffffffffu, mt0[0] > m[0] + kPkLag || mt0[1] > m[1] + kPkLag)) move(mt0, 0);
+        exps(0);
+        pk_ld_wait(sv + 32);
+        look(1, mt1);
+        if (__any_sync(0xffffffffu, mt1[0] > m[0] + kPkLag || mt1[1] > m[1] + kPkLag)) move(mt1, 32);
+        if (it.ragged && j == it.most() - 1) {
+          // S is there, so every ring entry before this K tile has been seen to land: the phase waited for
+          // is this V tile's
+          const int vi = entries + 2 * j + 1, r = quad + lane;
+          if (!pw_wait_all(kv_bar(vi), (vi / STAGES) & 1, abort_flag)) {
+            alive = false;
+            break;
+          }
+          if (r >= it.keys - k0) {
+            uint8_t* v = sm + LY::kRing + (vi % STAGES) * LY::kTile + r * 128 + half * (SLABS == 2 ? kPkSlab : 64);
+#pragma unroll
+            for (int u = 0; u < 4 * SLABS; ++u) *reinterpret_cast<uint4*>(v + u * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async();
+        }
+        float2 ls[2][2] = {};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[16], wl[LO ? 16 : 1];
+          const float* x = sv + 32 * h;
+          if (h == 1) exps(1);
+#pragma unroll
+          for (int n = 0; n < 16; ++n) {
+            const float2 y = make_float2(x[2 * n], x[2 * n + 1]);
+            ls[n & 1][(n >> 1) & 1] = __fadd2_rn(ls[n & 1][(n >> 1) & 1], y);
+            w[n] = pack_bf16(y.x, y.y);
+            if constexpr (LO) {   // what the first part left
+              const float2 lo = __ffma2_rn(make_float2(bf16_lo(w[n]), bf16_hi(w[n])), make_float2(-1.f, -1.f), y);
+              wl[n] = pack_bf16(lo.x, lo.y);
+            }
+          }
+          if (h == 1) hand_over(0);   // its stores are done by now
+          pk_st32(tS + 32 * h, w);   // column c = keys 2c and 2c + 1
+          if constexpr (LO) pk_st32(tS + 64 + 32 * h, wl);
+          if (h == 1) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float2 all = __fadd2_rn(ls[e][0], ls[e][1]);
+              l[e] += all.x + all.y;
+            }
+          }
+        }
+        hand_over(1);
+      }
+      if (!alive) break;
+      entries += 2 * it.most();
+      // Epilogue: row quad + lane, half of the columns.
+      const int row = quad + lane, tk = static_cast<int>((row * g_inv) >> 16), token = t * TQ + tk;
+      const bool valid = row < TQ * G && token < it.tokens;
+      if (my_nt > 0 || it.j0 == 0) {
+        float inv = 0.f, keep = 0.f;   // factors of O and of what earlier parts left
+        if (my_nt > 0) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float sum = l[e] + __shfl_xor_sync(0xffffffffu, l[e], 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            if ((lane & 3) == 0) {
+              row_sum[i & 1][t][w0 + (lane >> 2) + 8 * e] = sum;
+              if constexpr (LO) row_ref[i & 1][t][w0 + (lane >> 2) + 8 * e] = m[e];
+            }
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&l_full[t]));
+          if (!pw_wait_all(smem_u32(&l_full[t]), n_o & 1, abort_flag) ||
+              !pw_wait_all(smem_u32(&o_full[t]), n_o & 1, abort_flag))
+            break;
+          ++n_o;
+          tc_fence_after();
+          const float sum = row_sum[i & 1][t][row];
+          inv = !LO || it.ends(t) ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+          if constexpr (LO) {   // the parts' references differ where the row's has moved
+            const float now = row_ref[i & 1][t][row];
+            keep = ref == now ? inv : pf_ex2(ref - now) * inv;
+            ref = now;
+          }
+        }
+        constexpr int kCols = 32 * SLABS;
+        const int col0 = half * kCols;
+        uint8_t* dst = static_cast<uint8_t*>(p.out) +
+                       ((static_cast<int64_t>(it.row0 + token) * p.num_q_heads + it.head * G + row - tk * G) * p.dim +
+                        col0) * esz;
+        const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
+#pragma unroll
+        for (int c = 0; c < kCols; c += 32) {
+          float o[32];
+          if (my_nt > 0) {
+            tc_ld32(tm + 256 + 128 * t + (static_cast<uint32_t>(quad) << 16) + col0 + c, o);
+            if (c + 32 >= kCols) {   // O has been read
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&o_empty[t]));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+          if (!valid) continue;
+          if (p.out_bf16) {
+#pragma unroll
+            for (int u = 0; u < 32; u += 16) {
+              uint32_t w[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) w[e] = pack_bf16(o[u + 2 * e] * inv, o[u + 2 * e + 1] * inv);
+              uint8_t* d = dst + (c + u) * 2;
+              if (col0 + c + u + 16 <= p.dim && sectors) {
+                pk_store32(d, w);
+              } else {   // dims are a multiple of 8
+                if (col0 + c + u < p.dim) *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (col0 + c + u + 8 < p.dim) *reinterpret_cast<uint4*>(d + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int u = 0; u < 32; u += 4) {
+              if (col0 + c + u >= p.dim) continue;
+              float4* d = reinterpret_cast<float4*>(dst + (c + u) * 4);
+              float4 b = make_float4(o[u] * inv, o[u + 1] * inv, o[u + 2] * inv, o[u + 3] * inv);
+              if (LO && it.j0 > 0) {
+                const float4 a = *d;
+                b = make_float4(fmaf(a.x, keep, b.x), fmaf(a.y, keep, b.y), fmaf(a.z, keep, b.z),
+                                fmaf(a.w, keep, b.w));
+              }
+              *d = b;
             }
           }
         }
       }
-      if (!alive) break;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&item_empty[i & 1]));
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (*abort_flag && warp == 13) {   // copies may be in flight: no role waits for them now
+  if (*abort_flag && warp == 17) {   // copies may be in flight: no role waits for them now
     volatile int no_abort = 0;
     for (int x = max(0, loads - STAGES); x < loads; ++x)
       pw_wait(kv_bar(x), (x / STAGES) & 1, &no_abort);
