@@ -73,7 +73,6 @@ extern "C" pkv_status packed_attention_prefill(const pkv_packed_prefill_args* ar
   p.num_q_heads = a.num_q_heads, p.num_kv_heads = a.num_kv_heads, p.dim = a.head_dim;
   p.tile_tokens = kPkRows / G;
   p.causal = a.causal, p.window = a.window, p.sinks = a.sinks;
-  p.out_bf16 = a.out_dtype == PKV_BF16;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.test_stall_bytes = test_stall_bytes();
 
@@ -97,12 +96,13 @@ extern "C" pkv_status packed_attention_prefill(const pkv_packed_prefill_args* ar
   const dim3 grid(static_cast<unsigned>(units < sms ? units : sms));
   auto launch = [&](auto kern, size_t smem) {
     if (!opt_in_smem(reinterpret_cast<const void*>(kern), static_cast<int>(smem))) return PKV_ERR_CUDA;
-    kern<<<grid, kPkThreads, smem, reinterpret_cast<cudaStream_t>(stream)>>>(tq, tk, tv, p);
-    return cuda_status(cudaGetLastError());
+    return cuda_status(launch_pdl(kern, grid, dim3(kPkThreads), smem, reinterpret_cast<cudaStream_t>(stream), tq, tk,
+                                  tv, p));
   };
+  const bool bf16 = a.out_dtype == PKV_BF16;
   if (a.head_dim > 64)
-    return p.out_bf16 ? launch(packed_prefill_kernel<2, 4, false>, PkLayout<2, 4>::bytes())
+    return bf16 ? launch(packed_prefill_kernel<2, 4, false>, PkLayout<2, 4>::bytes())
                       : launch(packed_prefill_kernel<2, 4, true>, PkLayout<2, 4>::bytes());
-  return p.out_bf16 ? launch(packed_prefill_kernel<1, 8, false>, PkLayout<1, 8>::bytes())
+  return bf16 ? launch(packed_prefill_kernel<1, 8, false>, PkLayout<1, 8>::bytes())
                     : launch(packed_prefill_kernel<1, 8, true>, PkLayout<1, 8>::bytes());
 }

@@ -48,7 +48,7 @@ constexpr float kPkLag = 24.f;
 // Key tiles after which a float32 output takes O up.  The tensor cores cut every sum towards zero:
 // up to 2^-23 of O for each 16 keys and weight part, which adds up (20,000 keys in one go: 4.4e-5 of the
 // norm); 8 tiles are 128 such sums.  In between the epilogue adds in float32, in the output's own rows.
-constexpr int kPkPart = 8;
+constexpr int kPkPart = 16;
 
 struct PackedParams {
   void* out;                    // [T, Hq, D]
@@ -59,7 +59,6 @@ struct PackedParams {
   int32_t num_q_heads, num_kv_heads, dim;
   int32_t tile_tokens;          // TQ = 128 / G
   int32_t causal, window, sinks;
-  int32_t out_bf16;
   float scale_log2;
   uint32_t test_stall_bytes;    // CTA 0's first V tile waits for these in vain; 0 but in tests
 };
@@ -140,6 +139,20 @@ __device__ __forceinline__ void pk_scale16(uint32_t taddr, float f0, float f1) {
       "tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
       : "memory");
+}
+
+// 16 consecutive TMEM columns of this warp's 32 lanes.
+__device__ __forceinline__ void pk_ld16(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+      " tcgen05.wait::ld.sync.aligned;\n"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // 32 bytes to global memory, on a 32-byte boundary: a whole sector.
@@ -283,7 +296,7 @@ struct PkOrder {
   }
 };
 
-// LO: the weights are two bf16 parts (float32 output).
+// LO: float32 output, the weights are two bf16 parts; else bf16 output, one part.
 template <int SLABS, int STAGES, bool LO>
 __global__ void __launch_bounds__(kPkThreads, 1)
     packed_prefill_kernel(const __grid_constant__ CUtensorMap tmap_q,
@@ -307,6 +320,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
   volatile int* abort_flag = &abort_sh;
 
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
+  allow_dependents();
   if (tid == kPkThreads - 1) {
     for (int st = 0; st < STAGES; ++st) {
       mbar_init(smem_u32(&kv_full[st]), 1);
@@ -539,6 +553,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       pw_wait(smem_u32(&drain), 0, &no_abort);
     } else if (warp == 17) {
       // ------------------------------ TMA loads -------------------------------
+      grid_dependency_wait();
       if (pw_elect()) {
         PkItem it;
         bool ok = true;
@@ -580,6 +595,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       copied_q[1] = __reduce_max_sync(0xffffffffu, copied_q[1]);
     } else if (warp == 18) {
       // ------------------------------- items ----------------------------------
+      grid_dependency_wait();
       int32_t* pairs = reinterpret_cast<int32_t*>(sm + LY::kRankAt);
       PkOrder order{p, pairs, pairs + kPkRank, !p.causal || p.window > 0};
       order.lane = lane;
@@ -652,7 +668,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
     const uint32_t g_inv = (65536u + G - 1) / G;   // row / G for row < 128: exact for G <= 128
     // raised to the smallest normal, so that a masked -inf stays -inf under it
     const float sl2 = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
-    const int esz = p.out_bf16 ? 2 : 4;
+    constexpr int esz = LO ? 4 : 2;
     float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};   // references (in log2 units), sums
     float ref = 0.f;         // row quad + lane's reference in the part before
     uint32_t n_s = 0, n_o = 0;   // score tiles and items done
@@ -819,6 +835,19 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       const int row = quad + lane, tk = static_cast<int>((row * g_inv) >> 16), token = t * TQ + tk;
       const bool valid = row < TQ * G && token < it.tokens;
       if (my_nt > 0 || it.j0 == 0) {
+        constexpr int kCols = 32 * SLABS, kStep = LO ? 16 : 32;
+        const int col0 = half * kCols, cols = valid ? min(kCols, p.dim - col0) : 0;   // (dims are a multiple of 8)
+        uint8_t* dst = static_cast<uint8_t*>(p.out) +
+                       ((static_cast<int64_t>(it.row0 + token) * p.num_q_heads + it.head * G + row - tk * G) * p.dim +
+                        col0) * esz;
+        float4 was[LO ? kCols / 4 : 1];   // what earlier parts left, asked for while the products run
+        if constexpr (LO) {
+          if (it.j0 > 0) {
+#pragma unroll
+            for (int u = 0; u < kCols / 4; ++u)
+              if (4 * u < cols) was[u] = reinterpret_cast<const float4*>(dst)[u];
+          }
+        }
         float inv = 0.f, keep = 0.f;   // factors of O and of what earlier parts left
         if (my_nt > 0) {
 #pragma unroll
@@ -845,53 +874,49 @@ __global__ void __launch_bounds__(kPkThreads, 1)
             ref = now;
           }
         }
-        constexpr int kCols = 32 * SLABS;
-        const int col0 = half * kCols;
-        uint8_t* dst = static_cast<uint8_t*>(p.out) +
-                       ((static_cast<int64_t>(it.row0 + token) * p.num_q_heads + it.head * G + row - tk * G) * p.dim +
-                        col0) * esz;
         const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
 #pragma unroll
-        for (int c = 0; c < kCols; c += 32) {
-          float o[32];
+        for (int c = 0; c < kCols; c += kStep) {
+          float o[kStep];
           if (my_nt > 0) {
-            tc_ld32(tm + 256 + 128 * t + (static_cast<uint32_t>(quad) << 16) + col0 + c, o);
-            if (c + 32 >= kCols) {   // O has been read
+            const uint32_t at = tm + 256 + 128 * t + (static_cast<uint32_t>(quad) << 16) + col0 + c;
+            if constexpr (LO)
+              pk_ld16(at, o);
+            else
+              tc_ld32(at, o);
+            if (c + kStep >= kCols) {   // O has been read
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(smem_u32(&o_empty[t]));
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            for (int e = 0; e < kStep; ++e) o[e] = 0.f;
           }
-          if (!valid) continue;
-          if (p.out_bf16) {
+          if constexpr (!LO) {
 #pragma unroll
-            for (int u = 0; u < 32; u += 16) {
+            for (int u = 0; u < kStep; u += 16) {
               uint32_t w[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) w[e] = pack_bf16(o[u + 2 * e] * inv, o[u + 2 * e + 1] * inv);
               uint8_t* d = dst + (c + u) * 2;
-              if (col0 + c + u + 16 <= p.dim && sectors) {
+              if (c + u + 16 <= cols && sectors) {
                 pk_store32(d, w);
-              } else {   // dims are a multiple of 8
-                if (col0 + c + u < p.dim) *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
-                if (col0 + c + u + 8 < p.dim) *reinterpret_cast<uint4*>(d + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+              } else {
+                if (c + u < cols) *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (c + u + 8 < cols) *reinterpret_cast<uint4*>(d + 16) = make_uint4(w[4], w[5], w[6], w[7]);
               }
             }
           } else {
 #pragma unroll
-            for (int u = 0; u < 32; u += 4) {
-              if (col0 + c + u >= p.dim) continue;
-              float4* d = reinterpret_cast<float4*>(dst + (c + u) * 4);
+            for (int u = 0; u < kStep; u += 4) {
               float4 b = make_float4(o[u] * inv, o[u + 1] * inv, o[u + 2] * inv, o[u + 3] * inv);
-              if (LO && it.j0 > 0) {
-                const float4 a = *d;
+              if (it.j0 > 0) {
+                const float4 a = was[(c + u) / 4];
                 b = make_float4(fmaf(a.x, keep, b.x), fmaf(a.y, keep, b.y), fmaf(a.z, keep, b.z),
                                 fmaf(a.w, keep, b.w));
               }
-              *d = b;
+              if (c + u < cols) reinterpret_cast<float4*>(dst)[(c + u) / 4] = b;
             }
           }
         }

@@ -104,53 +104,70 @@ struct Seg<__nv_bfloat16> {
   }
 };
 
-// E float32 values to the cache, in its type, at element `at`.
+// Codes of N float32 values x / s.
+template <int N>
+__device__ __forceinline__ void codes(const RotaryParams& p, const float* x, float s, float neg_r, bool plain,
+                                      uint32_t* w) {
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    float q[4];
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      float2 v;
+      if (plain)
+        v = quotient2(make_float2(-x[4 * i + e], -x[4 * i + e + 1]), make_float2(s, s), make_float2(neg_r, neg_r));
+      else
+        v = make_float2(__fdiv_rn(x[4 * i + e], s), __fdiv_rn(x[4 * i + e + 1], s));
+      q[e] = v.x;
+      q[e + 1] = v.y;
+    }
+    w[i] = p.kind == 2 ? quant4<FP8>(q) : quant4<INT8>(q);
+  }
+}
+
+// A pair of segments to the cache, in its type: x at element `at` + a, y (where there is one) at `at` + b.
 template <typename Src>
-__device__ __forceinline__ void to_cache(const RotaryParams& p, bool is_v, int head, int64_t at,
-                                         const float* y) {
+__device__ __forceinline__ void to_cache(const RotaryParams& p, bool is_v, int head, int64_t at, int a, int b,
+                                         bool has_b, const float* x, const float* y) {
   constexpr int E = Seg<Src>::E;
   void* cache = is_v ? p.v_cache : p.k_cache;
   if (p.kind == 1) {
-    *reinterpret_cast<uint4*>(static_cast<Src*>(cache) + at) = Seg<Src>::pack(y);
+    Src* dst = static_cast<Src*>(cache) + at;
+    *reinterpret_cast<uint4*>(dst + a) = Seg<Src>::pack(x);
+    if (has_b) *reinterpret_cast<uint4*>(dst + b) = Seg<Src>::pack(y);
     return;
   }
   const float s = __ldg((is_v ? p.v_scale : p.k_scale) + head);
-  float most = 0.f;
+  uint32_t most = 0;   // the largest |value|, as bits: infinities and NaN are larger than any
 #pragma unroll
-  for (int e = 0; e < E; ++e) most = fmaxf(most, fabsf(y[e]));
-  float odd = 0.f;   // NaN where an element is
-#pragma unroll
-  for (int e = 0; e < E; ++e) odd += y[e] * 0.f;
-  uint32_t w[E / 4];
+  for (int e = 0; e < E; ++e) {
+    most = max(most, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+    if (has_b) most = max(most, __float_as_uint(y[e]) & 0x7FFFFFFFu);
+  }
   // quotient2's range: scales from 2^-64 to 2^64 and elements below 2^60
-  if (odd == 0.f && most < 1152921504606846976.f && s >= 5.421010862427522e-20f && s <= 18446744073709551616.f) {
-    const float r = __frcp_rn(s);
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      float x[4];
-#pragma unroll
-      for (int e = 0; e < 4; e += 2) {
-        const float2 v = quotient2(make_float2(-y[4 * i + e], -y[4 * i + e + 1]), make_float2(s, s),
-                                   make_float2(-r, -r));
-        x[e] = v.x;
-        x[e + 1] = v.y;
-      }
-      w[i] = p.kind == 2 ? quant4<FP8>(x) : quant4<INT8>(x);
+  const bool plain = most < 0x5D800000u && s >= 5.421010862427522e-20f && s <= 18446744073709551616.f;
+  const float neg_r = plain ? -__frcp_rn(s) : 0.f;
+  uint8_t* dst = static_cast<uint8_t*>(cache) + at;
+  uint32_t w[2];
+  if (__builtin_expect(plain, 1)) {
+    codes<E>(p, x, s, neg_r, true, w);
+    if constexpr (E == 8) *reinterpret_cast<uint2*>(dst + a) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(dst + a) = w[0];
+    if (has_b) {
+      codes<E>(p, y, s, neg_r, true, w);
+      if constexpr (E == 8) *reinterpret_cast<uint2*>(dst + b) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(dst + b) = w[0];
     }
   } else {
-#pragma unroll
-    for (int i = 0; i < E / 4; ++i) {
-      float x[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = __fdiv_rn(y[4 * i + e], s);
-      w[i] = p.kind == 2 ? quant4<FP8>(x) : quant4<INT8>(x);
+    codes<E>(p, x, s, 0.f, false, w);
+    if constexpr (E == 8) *reinterpret_cast<uint2*>(dst + a) = make_uint2(w[0], w[1]);
+    else *reinterpret_cast<uint32_t*>(dst + a) = w[0];
+    if (has_b) {
+      codes<E>(p, y, s, 0.f, false, w);
+      if constexpr (E == 8) *reinterpret_cast<uint2*>(dst + b) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(dst + b) = w[0];
     }
   }
-  uint8_t* dst = static_cast<uint8_t*>(cache) + at;
-  if constexpr (E == 8)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-  else
-    *reinterpret_cast<uint32_t*>(dst) = w[0];
 }
 
 // Rows whose halves (or whose whole, with neighbouring pairs) are multiples of 16 bytes.
@@ -257,8 +274,7 @@ __global__ void __launch_bounds__(kRoThreads, kRoCtas) rotary_kernel(const __gri
       }
       if (!is_q && append) {
         const int64_t at = (slot * p.hkv + head) * p.dim;
-        to_cache<Src>(p, is_v, head, at + a, x);
-        if (has_b) to_cache<Src>(p, is_v, head, at + b, y);
+        to_cache<Src>(p, is_v, head, at, a, b, has_b, x, y);
       }
     }
     r += lanes * kRoBatch;

@@ -7,17 +7,17 @@
 // where its blocks begin in the free list and its rows in the outputs; every row is then
 // independent of the others: a search in the starts finds its sequence.
 //
-// One cluster of CTAs does it in one launch.  Every CTA scans all lengths itself (a thousand
-// sequences at a time, one a thread), so that nothing waits for another CTA's sums, and fills its
-// share of the rows.  The cluster's barrier stands between the last read of the lengths and the
-// first write of the new ones, which may be the same memory.
+// One launch does it.  Every CTA scans all lengths itself (a thousand sequences at a time, one a
+// thread), so that nothing waits for another CTA's sums, and fills its share of the rows.  Where the new
+// lengths (or the free list's new start) take the old ones' place, the CTAs are one cluster, whose
+// barrier stands between the last read and the first write.
 #include "common.cuh"
 
 namespace pkv {
 namespace {
 
 constexpr int kSlThreads = 1024;
-constexpr int kSlMaxCtas = 8;          // a portable cluster
+constexpr int kSlCluster = 8;          // CTAs of a portable cluster
 constexpr int kSlRowsPerCta = 2048;    // below this many rows a CTA more does not pay
 
 struct SlotsParams {
@@ -59,8 +59,13 @@ __device__ __forceinline__ Request read_request(const SlotsParams& p, int s) {
   return r;
 }
 
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+// The CTA's barrier, or the cluster's.
+template <bool CLUSTER>
+__device__ __forceinline__ void all_read() {
+  if constexpr (CLUSTER)
+    asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+  else
+    __syncthreads();
 }
 
 // Inclusive sums over the CTA of (rows, need); their totals too.
@@ -100,6 +105,7 @@ __device__ __forceinline__ void scan2(int64_t& rows, int64_t& need, int64_t& all
   __syncthreads();   // sh may be written again
 }
 
+template <bool CLUSTER>
 __global__ void __launch_bounds__(kSlThreads, 1) slots_kernel(const __grid_constant__ SlotsParams p) {
   __shared__ int64_t sh[32][2];
   __shared__ int32_t start_sh[kSlThreads + 1], base_sh[kSlThreads], ctx_sh[kSlThreads],
@@ -151,7 +157,7 @@ __global__ void __launch_bounds__(kSlThreads, 1) slots_kernel(const __grid_const
       held_sh[tid] = mine.ok ? mine.held : -1;
     }
     if (go && tid == 0) start_sh[ns] = static_cast<int32_t>(rows0 + tile_rows);
-    cluster_barrier();   // every CTA has read this tile's lengths (and the free list's start)
+    all_read<CLUSTER>();   // this tile's lengths (and the free list's start)
     if (cta == 0 && tid < ns) {
       const int s = s0 + tid;
       int32_t n = 0;
@@ -198,7 +204,7 @@ __global__ void __launch_bounds__(kSlThreads, 1) slots_kernel(const __grid_const
     need0 += tile_need;
     __syncthreads();   // the tile's arrays are written again
   }
-  if (p.num_seqs == 0) cluster_barrier();
+  if (p.num_seqs == 0) all_read<CLUSTER>();
   if (cta == 0 && tid == 0) {
     if (p.free_next) *p.free_next = static_cast<int32_t>(first_free + (go ? all_need : 0));
     if (p.query_start && !p.row_per_seq) p.query_start[p.num_seqs] = go ? static_cast<int32_t>(all_rows) : 0;
@@ -209,6 +215,12 @@ __global__ void __launch_bounds__(kSlThreads, 1) slots_kernel(const __grid_const
     p.slots[row] = -1;
     if (p.positions) p.positions[row] = 0;
   }
+}
+
+// Whether two ranges of bytes have one in common.
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
 }
 
 bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -245,10 +257,19 @@ extern "C" pkv_status slots_from_lengths(
                 positions, query_start, context_out, free_next, device_status, num_blocks,
                 num_seqs, num_tokens, num_free, block_size, max_blocks_per_seq, row_per_sequence,
                 first_block_held};
-  int ctas = 1;
-  while (ctas < kSlMaxCtas && static_cast<int64_t>(ctas) * kSlRowsPerCta < num_tokens) ctas *= 2;
+  const size_t len = 4 * static_cast<size_t>(num_seqs);
+  const bool in_place = overlap(context_out, len, context_lens, len) || overlap(free_next, 4, free_start, 4) ||
+                        overlap(context_out, len, new_lens, len) || overlap(context_out, len, free_start, 4) ||
+                        overlap(free_next, 4, context_lens, len) || overlap(free_next, 4, new_lens, len);
+  int64_t ctas = (static_cast<int64_t>(num_tokens) + kSlRowsPerCta - 1) / kSlRowsPerCta;
+  if (ctas > 1 && in_place) {   // 66,000 rows: 10.8 us by eight CTAs, 5.6 by one for each 2,048
+    ctas = ctas <= 2 ? 2 : ctas <= 4 ? 4 : kSlCluster;
+  } else {
+    const int64_t sms = device_sm_count();
+    ctas = ctas < 1 ? 1 : ctas > sms ? sms : ctas;
+  }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(ctas);
+  cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kSlThreads);
   cfg.stream = reinterpret_cast<cudaStream_t>(stream);
   cudaLaunchAttribute attr[2];
@@ -257,6 +278,7 @@ extern "C" pkv_status slots_from_lengths(
   attr[1].id = cudaLaunchAttributeClusterDimension;
   attr[1].val.clusterDim = {static_cast<unsigned>(ctas), 1, 1};
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cuda_status(cudaLaunchKernelEx(&cfg, slots_kernel, p));
+  cfg.numAttrs = in_place && ctas > 1 ? 2 : 1;
+  return cuda_status(in_place && ctas > 1 ? cudaLaunchKernelEx(&cfg, slots_kernel<true>, p)
+                                          : cudaLaunchKernelEx(&cfg, slots_kernel<false>, p));
 }
