@@ -210,10 +210,10 @@ def long_reference(q, k, v, scale, causal):
 @pytest.mark.parametrize("keys", [3000, 20000])
 @pytest.mark.parametrize("dim", [64, 128])
 def test_long_float32(lib, keys, dim):
-    """The tensor cores cut each sum in O towards zero, up to 2^-23 of it: over 64 k-steps of 16 keys
-    twice (two parts of the weights) that is 2^-16 at most and, as cuts are half of that on average,
-    2^-17; the weights' second part is off by 2^-17.  Their sum over independent elements stays under
-    1.2e-5 of the norm, however many keys there are."""
+    """The tensor cores cut each sum in O towards zero, up to 2^-23 of it.  Over 16 key tiles, 8 k-steps each
+    for two parts of the weights, that is 256 cuts: half of the most on average, of an O that is
+    on average half its last size, 256 2^-25 = 2^-17.  The weights' second part is off by 2^-17 at most.
+    Together they stay under 1.2e-5 of the norm, however many keys there are."""
     import torch
     q, k, v = inputs(13, 260, keys, 1, 1, dim)
     for causal in (True, False):

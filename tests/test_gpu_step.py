@@ -1,0 +1,213 @@
+"""The step around the cache as a whole: slots from lengths, rotary positions with the append and
+attention, prompts and then tokens, against float64."""
+import numpy as np
+import pytest
+
+from oracle import step as OS
+from tests import paged_cases as PC
+from tests.test_gpu_packed import BF16
+
+pytestmark = pytest.mark.gpu
+
+HQ, HKV, D, BS = 8, 2, 128, 16
+FREQ = 10000.0 ** (-np.arange(64) / 64)
+
+
+def dev(x):
+    import torch
+    return torch.from_numpy(np.ascontiguousarray(x, dtype=np.int32)).cuda()
+
+
+class Model:
+    """One layer's rows of a few sequences, their positions on three axes, and what float64 makes of
+    them."""
+
+    def __init__(self, lib, kv, seed):
+        from paged_kv_cache_295_gb300.engine import PagedKVCache
+        self.lib, self.rng = lib, np.random.default_rng(seed)
+        self.cache = PagedKVCache(1, HKV, D, BS, 120, kv, initial_free_order=self.rng.permutation(120).tolist())
+        if kv == lib.FP8_E4M3:
+            self.cache.k_scale.fill_(4.0 / 448)
+            self.cache.v_scale.fill_(4.0 / 448)
+        self.kv = kv
+        self.rotary = lib.Rotary(D, sections=[16, 24, 24])
+        self.axes = [0] * 16 + [1] * 24 + [2] * 24
+        self.rows = {}      # sequence: float64 K (turned), V so far
+
+    def step(self, rows):
+        """Rows [T, HQ + 2 HKV, D] in bf16, as a projection leaves them."""
+        import torch
+        return torch.from_numpy(self.rng.standard_normal((rows, HQ + 2 * HKV, D)).astype(np.float32)).cuda().bfloat16()
+
+    def grid(self, positions):
+        """Time, height and width from a token's place: rows of 7."""
+        import torch
+        return torch.stack([positions // 49, positions // 7 % 7, positions % 7]).to(torch.int32).contiguous()
+
+    def turned(self, x, pos):
+        return OS.rotary(x.double().cpu().numpy(), pos.cpu().numpy(), FREQ, self.axes)
+
+    def remember(self, seqs, starts, k, v):
+        for s, a, b in zip(seqs, starts[:-1], starts[1:]):
+            old = self.rows.get(s, (np.zeros((0, HKV, D)), np.zeros((0, HKV, D))))
+            self.rows[s] = tuple(np.concatenate([o, x[a:b]]) for o, x in zip(old, (k, v)))
+
+    def check(self, got, seqs, starts, q, out_bf16, prompt):
+        """Attention over the rows so far.  The operands are the float64 ones rounded: q and k to bf16 (2^-8
+        of |q| |k| each in a score, whose effect on the weights is twice that), and in an 8-bit cache
+        k and v to E4M3 (2^-4), on top of the kernels' own bound."""
+        codes = self.kv == self.lib.FP8_E4M3 and not prompt
+        for s, a, b in zip(seqs, starts[:-1], starts[1:]):
+            k, v = self.rows[s]
+            n = b - a
+            o, mag, reach, seen = OS.packed(q[a:b], k, v, [0, n], [0, k.shape[0]], self.cache.scale)
+            e_k, e_v = (2.0 ** -4, 2.0 ** -4) if codes else (2.0 ** -8, 0.0)
+            if codes:      # the smallest codes: half of their step
+                e_v_abs = 2.0 ** -10 * 4.0 / 448
+                e_k_abs = 2.0 ** -10 * 4.0 / 448 * np.abs(q[a:b]).sum(-1)
+            else:
+                e_v_abs, e_k_abs = 0.0, 0.0
+            dz = self.cache.scale * (reach * (2.0 ** -8 + e_k) + e_k_abs)
+            bound = PC.attention_bound(BF16, q[a:b], o, mag, reach, self.cache.scale, False, out_bf16, not out_bf16,
+                                       int(seen.max()))
+            bound = bound + 2 * np.expm1(2 * dz)[..., None] * mag + e_v * mag + e_v_abs
+            assert (np.abs(got[a:b].double().cpu().numpy() - o) <= bound).all()
+
+
+@pytest.mark.parametrize("kv", ["BF16", "FP8_E4M3"])
+def test_prompts_then_tokens(lib, kv):
+    """Three prompts of very different lengths, a token each, one more prompt beside two of
+    them, and a captured loop of tokens; the host pool, told of the same appends, has the same tables."""
+    import torch
+    m = Model(lib, getattr(lib, kv), 3)
+    cache, pool = m.cache, m.cache.pool
+    free, start = dev(pool.free_list()), dev([0])
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    tables, lens = torch.full((4, 40), -1, dtype=torch.int32, device="cuda"), dev([0, 0, 0, 0])
+
+    def prompts(new):
+        T = sum(new)
+        x = m.step(T)
+        q, k, v = x[:, :HQ], x[:, HQ:HQ + HKV], x[:, HQ + HKV:]
+        sl = cache.slots(tables, lens, dev(new), free, T, free_start=start, context_out=lens, free_next=start,
+                         device_status=status)
+        pos = m.grid(sl.positions)
+        out = cache.prompt(0, q, k, v, pos, m.rotary, sl, out_dtype=torch.bfloat16, device_status=status)
+        starts = [0, *np.cumsum(new)]
+        m.remember(range(4), starts, m.turned(k, pos), v.double().cpu().numpy())
+        seqs = [s for s in range(4) if new[s]]
+        at = [starts[s] for s in seqs] + [T]
+        m.check(out, seqs, at, m.turned(q, pos), True, True)
+
+    def tell_the_pool(new):
+        for s, n in enumerate(new):
+            if n:
+                if not any(s == x for x in told):
+                    pool.seq_create(s)
+                    told.append(s)
+                pool.append_tokens(s, n)
+        assert np.array_equal(tables[told].cpu().numpy(), pool.batch_tables(told, 40)[0])
+        assert np.array_equal(lens[told].cpu().numpy(), pool.batch_tables(told, 40)[1])
+        assert free[int(start.item()):].tolist() == pool.free_list()
+
+    told = []
+    prompts([37, 200, 1, 0])
+    tell_the_pool([37, 200, 1, 0])
+
+    x = torch.empty((4, HQ + 2 * HKV, D), dtype=torch.bfloat16, device="cuda")
+    alive = dev([1, 1, 1, 0])
+    slots = torch.empty(4, dtype=torch.int64, device="cuda")
+    pos, q_out = torch.empty(4, dtype=torch.int32, device="cuda"), torch.empty((4, HQ, D), dtype=torch.bfloat16, device="cuda")
+    out = torch.empty((4, HQ, D), device="cuda")
+    ws = cache.workspace_for(4, HQ, 640)
+
+    def token():
+        sl = cache.slots(tables, lens, alive, free, row_per_sequence=True, free_start=start, context_out=lens,
+                         free_next=start, slot_mapping=slots, positions=pos, device_status=status)
+        cache.append_rotary(0, x[:, :HQ], x[:, HQ:HQ + HKV], x[:, HQ + HKV:], m.grid(sl.positions), m.rotary,
+                            sl.slot_mapping, q_out=q_out, device_status=status)
+        cache.attend(0, q_out, tables, lens, 640, out=out, workspace=ws, device_status=status)
+
+    def check_token(new):
+        torch.cuda.synchronize()
+        g = m.grid(pos)
+        k, v = m.turned(x[:, HQ:HQ + HKV], g), x[:, HQ + HKV:].double().cpu().numpy()
+        q = m.turned(x[:, :HQ], g)
+        for s in range(4):
+            if new[s]:
+                m.remember([s], [0, 1], k[s:s + 1], v[s:s + 1])
+                m.check(out[s:s + 1], [s], [0, 1], q[s:s + 1], False, False)
+            else:
+                assert int(slots[s].item()) == -1
+        tell_the_pool(new)
+
+    for _ in range(3):
+        x.copy_(m.step(4))
+        token()
+        check_token([1, 1, 1, 0])
+    prompts([0, 0, 0, 50])
+    tell_the_pool([0, 0, 0, 50])
+    # a captured step: the lengths, the free list and the tables go on by themselves
+    alive.copy_(dev([1, 0, 1, 1]))
+    side = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=side):
+        token()
+    for _ in range(20):
+        x.copy_(m.step(4))
+        g.replay()
+        check_token([1, 0, 1, 1])
+    assert int(status.item()) == 0
+
+
+def test_chunk_behind_a_cached_prefix(lib):
+    """A prompt's second chunk: its rows are rotated and appended, the attention reads the cache."""
+    import torch
+    m = Model(lib, lib.BF16, 5)
+    cache = m.cache
+    free, start, lens = dev(cache.pool.free_list()), dev([0]), dev([0, 0])
+    tables = torch.full((2, 20), -1, dtype=torch.int32, device="cuda")
+    for new in ([100, 3], [30, 77]):
+        T = sum(new)
+        x = m.step(T)
+        q, k, v = x[:, :HQ], x[:, HQ:HQ + HKV], x[:, HQ + HKV:]
+        sl = cache.slots(tables, lens, dev(new), free, T, free_start=start, context_out=lens, free_next=start)
+        pos = m.grid(sl.positions)
+        qr, _ = cache.append_rotary(0, q, k, v, pos, m.rotary, sl.slot_mapping)
+        out = cache.prefill(0, qr, sl.query_start, tables, lens, max(new), 320)
+        starts = [0, *np.cumsum(new)]
+        m.remember(range(2), starts, m.turned(k, pos), v.double().cpu().numpy())
+        m.check(out, range(2), starts, m.turned(q, pos), False, False)
+
+
+def test_prompt_equals_prefill_through_the_cache(lib):
+    """The packed call and the paged one over the same rows, within both bounds."""
+    import torch
+    rng = np.random.default_rng(6)
+    lens = [130, 1, 300]
+    T, qs = sum(lens), dev([0, 130, 131, 431])
+    q, k, v = (torch.from_numpy(rng.standard_normal((T, h, D)).astype(np.float32)).cuda().bfloat16()
+               for h in (HQ, HKV, HKV))
+    from paged_kv_cache_295_gb300.engine import PagedKVCache
+    cache = PagedKVCache(1, HKV, D, BS, 40, lib.BF16)
+    tables = torch.full((3, 20), -1, dtype=torch.int32, device="cuda")
+    sl = cache.slots(tables, dev([0, 0, 0]), dev(lens), dev(cache.pool.free_list()), T)
+    cache.append(0, k, v, sl.slot_mapping)
+    for kw in ({}, {"window": 100, "sinks": 3}):
+        a = cache.prefill(0, q, qs, tables, sl.context_lens, 300, 320, **kw)
+        b = lib.packed_attention_prefill(q, k, v, qs, cache.scale, **kw)
+        x = [t.double().cpu().numpy() for t in (q, k, v)]
+        o, mag, reach, seen = OS.packed(*x, [0, 130, 131, 431], [0, 130, 131, 431], cache.scale, True,
+                                        kw.get("window", 0), kw.get("sinks", 0))
+        e = PC.attention_bound(BF16, x[0], o, mag, reach, cache.scale, False, False, True, 300)
+        assert (np.abs((a - b).double().cpu().numpy()) <= 2 * e).all()
+
+
+def test_engine_refusals(lib):
+    import torch
+    from paged_kv_cache_295_gb300.engine import PagedKVCache
+    cache = PagedKVCache(1, 2, 128, 16, 4, lib.INT8, block_scales=True)
+    q = torch.zeros((1, 2, 128), device="cuda", dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        cache.append_rotary(0, q, q, q, dev([0]), lib.Rotary(128), torch.zeros(1, dtype=torch.int64, device="cuda"))
