@@ -766,7 +766,7 @@ def slots_from_lengths(block_tables, context_lens, new_lens, free_blocks, num_bl
                                       block_size, num_tokens, free_start, row_per_sequence,
                                       first_block_held, slot_mapping, positions, query_start,
                                       context_out, free_next, device_status)
-    return Slots(*_done(_binding().slots_from_lengths(
+    return Slots(*_done((_ext or _binding()).slots_from_lengths(
         block_tables, context_lens, new_lens, free_blocks, num_blocks, block_size, num_tokens,
         free_start, row_per_sequence, first_block_held, slot_mapping, positions, query_start,
         context_out, free_next, device_status), "slots_from_lengths"))
@@ -815,6 +815,8 @@ class Rotary:
         self.axis = None
         if self.num_axes > 1:
             self.axis = torch.from_numpy(axes.astype(np.int32)).to(device)
+        # as the binding takes it
+        self.plan = (self.turns, self.axis, self.rotary_dim, self.num_axes, self.adjacent, self.scale)
 
 
 def rotary_and_cache(q, k, v, positions, rotary, slot_mapping=None, k_cache=None, v_cache=None,
@@ -833,9 +835,8 @@ def rotary_and_cache(q, k, v, positions, rotary, slot_mapping=None, k_cache=None
         with _on_stream(stream, k):
             return rotary_and_cache(q, k, v, positions, rotary, slot_mapping, k_cache, v_cache, k_scale,
                                     v_scale, q_out, k_out, keep_k, device_status)
-    return _done(_binding().rotary_and_cache(
-        q, k, v, positions, rotary.turns, rotary.axis, rotary.rotary_dim, rotary.num_axes,
-        rotary.adjacent, rotary.scale, slot_mapping, k_cache, v_cache, k_scale, v_scale, q_out, k_out,
+    return _done((_ext or _binding()).rotary_and_cache(
+        q, k, v, positions, rotary.plan, slot_mapping, k_cache, v_cache, k_scale, v_scale, q_out, k_out,
         keep_k, device_status), "rotary_and_cache")
 
 
@@ -852,7 +853,7 @@ def packed_attention_prefill(q, k, v, query_start, scale, key_start=None, causal
         with _on_stream(stream, q):
             return packed_attention_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks,
                                             out, out_dtype, device_status)
-    return _done(_binding().packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks,
+    return _done((_ext or _binding()).packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks,
                                            out, out_dtype, device_status), "packed_attention_prefill")
 
 

@@ -486,24 +486,26 @@ void want_rows(const Tensor& t, const char* name, int64_t rows, int64_t heads, i
       if (t.size(i) > 1 && t.stride(i) < dim) refuse(std::string(name) + " must not overlap itself");
 }
 
-// rotary_and_cache(q, k, v, positions, turns, axis, rotary_dim, num_axes, adjacent, scale, slot_mapping,
+// rotary_and_cache(q, k, v, positions, (turns, axis, rotary_dim, num_axes, adjacent, scale), slot_mapping,
 //                  k_cache, v_cache, k_scale, v_scale, q_out, k_out, keep_k, device_status)
 //   -> (q_out, k_out) or status
 PyObject* do_rotary(PyObject* const* a, Py_ssize_t na) {
-  arity(na, 19);
+  arity(na, 14);
+  if (!PyTuple_Check(a[4]) || PyTuple_GET_SIZE(a[4]) != 6) refuse("rotary must be a Rotary's plan");
+  PyObject* const* plan = &PyTuple_GET_ITEM(a[4], 0);
   const Tensor &q = tensor(a[0], "q", true), &k = tensor(a[1], "k"), &v = tensor(a[2], "v", true),
-               &pos = tensor(a[3], "positions"), &turns = tensor(a[4], "turns"),
-               &axis = tensor(a[5], "axis", true), &slots = tensor(a[10], "slot_mapping", true),
-               &kc = tensor(a[11], "k_cache", true), &vc = tensor(a[12], "v_cache", true),
-               &ks = tensor(a[13], "k_scale", true), &vs = tensor(a[14], "v_scale", true),
-               &st = status_word(a[18]);
-  Tensor out[2] = {tensor(a[15], "q_out", true), tensor(a[16], "k_out", true)};
-  const bool keep_k = truth(a[17], "keep_k"), cached = kc.defined();
+               &pos = tensor(a[3], "positions"), &turns = tensor(plan[0], "turns"),
+               &axis = tensor(plan[1], "axis", true), &slots = tensor(a[5], "slot_mapping", true),
+               &kc = tensor(a[6], "k_cache", true), &vc = tensor(a[7], "v_cache", true),
+               &ks = tensor(a[8], "k_scale", true), &vs = tensor(a[9], "v_scale", true),
+               &st = status_word(a[13]);
+  Tensor out[2] = {tensor(a[10], "q_out", true), tensor(a[11], "k_out", true)};
+  const bool keep_k = truth(a[12], "keep_k"), cached = kc.defined();
   pkv_rotary_args p{};
-  p.rotary_dim = integer32(a[6], "rotary_dim");
-  p.num_axes = integer32(a[7], "num_axes");
-  p.adjacent = truth(a[8], "adjacent");
-  p.scale = real(a[9], "scale");
+  p.rotary_dim = integer32(plan[2], "rotary_dim");
+  p.num_axes = integer32(plan[3], "num_axes");
+  p.adjacent = truth(plan[4], "adjacent");
+  p.scale = real(plan[5], "scale");
   if (k.dim() != 3 || (q.defined() && q.dim() != 3)) refuse("q and k must be [T, heads, dim]");
   const int64_t T = k.size(0), hkv = k.size(1), dim = k.size(2), hq = q.defined() ? q.size(1) : 0;
   const at::ScalarType type = k.scalar_type();

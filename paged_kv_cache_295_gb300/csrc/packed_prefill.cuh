@@ -776,8 +776,8 @@ __global__ void __launch_bounds__(kPkThreads, 1)
           }
         };
         pk_ld64(tS, sv);
-        pk_ld_wait(sv);
         pk_ld64(tS + 64, sv + 32);
+        pk_ld_wait(sv);
         float mt0[2], mt1[2];
         look(0, mt0);
         if (__any_sync(0xffffffffu, mt0[0] > m[0] + kPkLag || mt0[1] > m[1] + kPkLag)) move(mt0, 0);
@@ -805,9 +805,15 @@ __global__ void __launch_bounds__(kPkThreads, 1)
         for (int h = 0; h < 2; ++h) {
           uint32_t w[16], wl[LO ? 16 : 1];
           const float* x = sv + 32 * h;
-          if (h == 1) exps(1);
+          const float mu[2] = {m[0] == -CUDART_INF_F ? 0.f : m[0], m[1] == -CUDART_INF_F ? 0.f : m[1]};
 #pragma unroll
           for (int n = 0; n < 16; ++n) {
+            if (h == 0) {   // the second half's exponentials, between the first half's sums and conversions
+              const float2 z = __ffma2_rn(make_float2(sv[32 + 2 * n], sv[33 + 2 * n]), make_float2(sl2, sl2),
+                                          make_float2(-mu[n & 1], -mu[n & 1]));
+              sv[32 + 2 * n] = pf_ex2(z.x);
+              sv[33 + 2 * n] = pf_ex2(z.y);
+            }
             const float2 y = make_float2(x[2 * n], x[2 * n + 1]);
             ls[n & 1][(n >> 1) & 1] = __fadd2_rn(ls[n & 1][(n >> 1) & 1], y);
             w[n] = pack_bf16(y.x, y.y);

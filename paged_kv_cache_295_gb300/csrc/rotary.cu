@@ -12,9 +12,18 @@
 // What bounds it: HBM.  Every row is read and written once; the angles of a token are computed
 // once per CTA, into shared memory, and kept in registers over the rows of the token: a group of 64
 // threads works on one token, thread = (16-byte pair of segments in the row, row), so that the
-// same frequencies serve all rows a thread meets.  V rows go through the same loop with no turn.
+// same frequencies serve all rows a thread meets.  V rows go through the same loop with no turn.  Three
+// rows a thread are in flight, the first of them asked for before the angles are computed, and three CTAs
+// an SM fit (two rows and four CTAs: 36.9 us for the first case below; four rows 44; one kind of row
+// after another, without a choice per row, 40).
+//
+// Measured: 8,192 tokens of 32 + 8 heads x 128, bf16, three axes, turned k kept and appended 36.5 us
+// (6.0 TB/s, 89 % of the copy rate); 8,191 tokens of 32 + 32 heads into an fp8 cache 66.5 us (5.0 TB/s,
+// 75 %: the codes' arithmetic and its latency, 59 % of the issue slots; 75 with a bounds check per
+// element, 107 with a divide per element); 8 tokens of 32 + 8 heads 2.0 us in a graph.
 #include <cmath>
 #include <initializer_list>
+#include <type_traits>
 
 #include "quant.cuh"
 
@@ -42,6 +51,7 @@ struct RotaryParams {
   int64_t num_slots;
   int32_t kind;       // cache: 0 none, 1 the rows' own type, 2 FP8, 3 INT8
   int32_t adjacent;
+  int32_t small_scale; // |scale| <= 2^29
   int32_t units;      // pairs of 16-byte segments in a row
   int32_t rows_per_y; // rows of a token that one CTA takes
   int32_t* status;
@@ -125,48 +135,58 @@ __device__ __forceinline__ void codes(const RotaryParams& p, const float* x, flo
   }
 }
 
-// A pair of segments to the cache, in its type: x at element `at` + a, y (where there is one) at `at` + b.
+// The largest |element| of two segments, as a float32's bits, at least; infinities and NaN are larger
+// than any.
 template <typename Src>
-__device__ __forceinline__ void to_cache(const RotaryParams& p, bool is_v, int head, int64_t at, int a, int b,
-                                         bool has_b, const float* x, const float* y) {
+__device__ __forceinline__ uint32_t top_of(const uint4& a, const uint4& b, bool has_b) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, has_b ? b.x : 0u, has_b ? b.y : 0u, has_b ? b.z : 0u, has_b ? b.w : 0u};
+  if constexpr (sizeof(Src) == 2) {
+    __nv_bfloat162 t = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
+#pragma unroll
+    for (int i = 1; i < 8; ++i) t = __hmax2_nan(t, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+    const uint32_t m = *reinterpret_cast<const uint32_t*>(&t) & 0x7FFF7FFFu;
+    return max(m << 16, m & 0x7FFF0000u);
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+    return m;
+  }
+}
+
+// A pair of segments to the cache, in its type: x at element `at` + a, y (where there is one) at `at` + b.
+// `top`: top_of() the source's segments, which the turned ones exceed by |scale| sqrt(2) at most.
+template <typename Src>
+__device__ __forceinline__ void to_cache(const RotaryParams& p, void* cache, const float* scales, int head,
+                                         int64_t at, int a, int b, bool has_b, uint32_t top, const float* x,
+                                         const float* y) {
   constexpr int E = Seg<Src>::E;
-  void* cache = is_v ? p.v_cache : p.k_cache;
   if (p.kind == 1) {
     Src* dst = static_cast<Src*>(cache) + at;
     *reinterpret_cast<uint4*>(dst + a) = Seg<Src>::pack(x);
     if (has_b) *reinterpret_cast<uint4*>(dst + b) = Seg<Src>::pack(y);
     return;
   }
-  const float s = __ldg((is_v ? p.v_scale : p.k_scale) + head);
-  uint32_t most = 0;   // the largest |value|, as bits: infinities and NaN are larger than any
-#pragma unroll
-  for (int e = 0; e < E; ++e) {
-    most = max(most, __float_as_uint(x[e]) & 0x7FFFFFFFu);
-    if (has_b) most = max(most, __float_as_uint(y[e]) & 0x7FFFFFFFu);
-  }
-  // quotient2's range: scales from 2^-64 to 2^64 and elements below 2^60
-  const bool plain = most < 0x5D800000u && s >= 5.421010862427522e-20f && s <= 18446744073709551616.f;
-  const float neg_r = plain ? -__frcp_rn(s) : 0.f;
+  const float s = __ldg(scales + head);
+  // quotient2's range: scales from 2^-64 to 2^64 and elements below 2^60 (|scale| up to 2^29, elements of
+  // the source below 2^30)
+  const bool plain = top < 0x4E800000u && p.small_scale && s >= 5.421010862427522e-20f && s <= 18446744073709551616.f;
   uint8_t* dst = static_cast<uint8_t*>(cache) + at;
-  uint32_t w[2];
+  auto put = [&](int to, const float* v, float neg_r, auto fast) {
+    uint32_t w[2];
+    codes<E>(p, v, s, neg_r, decltype(fast)::value, w);
+    if constexpr (E == 8)
+      *reinterpret_cast<uint2*>(dst + to) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(dst + to) = w[0];
+  };
   if (__builtin_expect(plain, 1)) {
-    codes<E>(p, x, s, neg_r, true, w);
-    if constexpr (E == 8) *reinterpret_cast<uint2*>(dst + a) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t*>(dst + a) = w[0];
-    if (has_b) {
-      codes<E>(p, y, s, neg_r, true, w);
-      if constexpr (E == 8) *reinterpret_cast<uint2*>(dst + b) = make_uint2(w[0], w[1]);
-      else *reinterpret_cast<uint32_t*>(dst + b) = w[0];
-    }
+    const float neg_r = -__frcp_rn(s);
+    put(a, x, neg_r, std::true_type{});
+    if (has_b) put(b, y, neg_r, std::true_type{});
   } else {
-    codes<E>(p, x, s, 0.f, false, w);
-    if constexpr (E == 8) *reinterpret_cast<uint2*>(dst + a) = make_uint2(w[0], w[1]);
-    else *reinterpret_cast<uint32_t*>(dst + a) = w[0];
-    if (has_b) {
-      codes<E>(p, y, s, 0.f, false, w);
-      if constexpr (E == 8) *reinterpret_cast<uint2*>(dst + b) = make_uint2(w[0], w[1]);
-      else *reinterpret_cast<uint32_t*>(dst + b) = w[0];
-    }
+    put(a, x, 0.f, std::false_type{});
+    if (has_b) put(b, y, 0.f, std::false_type{});
   }
 }
 
@@ -274,7 +294,8 @@ __global__ void __launch_bounds__(kRoThreads, kRoCtas) rotary_kernel(const __gri
       }
       if (!is_q && append) {
         const int64_t at = (slot * p.hkv + head) * p.dim;
-        to_cache<Src>(p, is_v, head, at, a, b, has_b, x, y);
+        to_cache<Src>(p, is_v ? p.v_cache : p.k_cache, is_v ? p.v_scale : p.k_scale, head, at, a, b, has_b,
+                      p.kind > 1 ? top_of<Src>(va[n], vb[n], has_b) : 0u, x, y);
       }
     }
     r += lanes * kRoBatch;
@@ -422,6 +443,7 @@ extern "C" pkv_status rotary_and_cache(const pkv_rotary_args* args, pkv_stream_t
   p.k_scale = a.k_scale, p.v_scale = a.v_scale;
   p.num_slots = cached ? a.num_blocks * a.block_size : 0;
   p.kind = kind, p.adjacent = a.adjacent, p.status = a.device_status;
+  p.small_scale = std::fabs(a.scale) <= 536870912.f;
 
   const int rows = p.hq + (cached ? 2 : 1) * p.hkv;
   const int E = 16 / static_cast<int>(es);
