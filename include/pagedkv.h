@@ -738,7 +738,7 @@ pkv_status rotary_turns(const double* inv_freq, int32_t n, uint64_t* turns);
  * as one (2^-8, half a step of a bf16 output, of each weight) for a bf16 one.
  * A key that a query does not see, but another one of its work tile (128 rows) does, has
  * weight 0 there; a V value of it that is not finite gives NaN.  Keys of other sequences and rows
- * outside every sequence have no influence, whatever they hold.
+ * outside every sequence have no influence, whatever they hold.  out overlaps no input.
  * Supported: head_dim a multiple of 8 up to 128; G = num_q_heads / num_kv_heads <= 128; 16-byte
  * aligned q, k, v and out.  A bad start flags PKV_DEV_BAD_CONTEXT and skips its sequence. */
 typedef struct {

@@ -27,6 +27,27 @@
 // scaled; S_t(j) being there implies that PV_t(j-1) is done (one thread issues both), so the softmax
 // warps scale it themselves.
 //
+// Precision.  Scores, sums and O are float32.  A float32 output takes the weights as two bf16 parts (2^-17
+// of each at most), a bf16 one as one (2^-9): beside the output's own rounding that is 1.2 to 1.4 times the
+// error against 64 bits on normal values (2.0e-3 to 2.4e-3 of the norm for 1.6e-3), where a second part
+// would double the product's time.
+//
+// What bounds it.  At head_dim 128 the chain of a key tile: softmax 1,400 cycles, product and next scores
+// 770 of its 1,024 behind it, and about 450 until each sees that the other is done, with the other tile's
+// products in between: 2,600 cycles for a pair of tiles whose products need 2,048.  What it took to get
+// there: no mask code in tiles without one; a plain loop for the issuer (its general steps took 3,100
+// cycles a pair); references that move only on a vote; both halves' scores asked for together.  Without the
+// exponentials it would be 6 % faster, without the maxima 4 %.  Short lists wait for their first rows
+// (Q and K of the next item reach shared memory 2 to 3 us after they are asked for, as all CTAs ask at
+// once) and a cold CTA for its code.  Tried and left out: one issuer for each tile (both tiles' phases
+// fall together), with and without turns; prefetches of the next item to L2 (16 prompts of 512 tokens 77
+// -> 90 us); lists of equal length for both tiles; the halves as a loop (20 % slower); Q before K.
+//
+// Measured: three prompts of 700 to 8,192 tokens, 32 heads on 8, causal 460 to 477 us (1,510 to 1,570
+// TFLOP/s); 16 prompts of 512 tokens, 32 heads 66 us; 11 images of 64 to 1,156 patches, 16 heads of 80, not
+// causal 45 us; nine chunks of up to 1,500 tokens behind 333 keys, 16 heads on 2 of 64, window 1,024,
+// float32 output 51 us; four prompts of up to 60 tokens 9.4 us.
+//
 // Every wait is bounded (2 s) and gives up when another role has given up; copies in flight are then
 // waited for, and TMEM is released before the CTA exits.
 #pragma once
@@ -47,7 +68,9 @@ constexpr int kPkSlab = 128 * 128;   // 128 rows of 64 bf16 (128-byte swizzle)
 constexpr float kPkLag = 24.f;
 // Key tiles after which a float32 output takes O up.  The tensor cores cut every sum towards zero:
 // up to 2^-23 of O for each 16 keys and weight part, which adds up (20,000 keys in one go: 4.4e-5 of the
-// norm); 8 tiles are 128 such sums.  In between the epilogue adds in float32, in the output's own rows.
+// norm, and no end to it); 16 tiles are 256 such sums, 5.3e-6 of the norm however many there are (8 tiles:
+// 3.4e-6, and 62 us for the windowed chunks above, whose lists of up to 12 tiles then come in two parts).
+// In between the epilogue adds in float32, in the output's own rows.
 constexpr int kPkPart = 16;
 
 struct PackedParams {
@@ -354,6 +377,8 @@ __global__ void __launch_bounds__(kPkThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
+  // Every role waits for earlier work here: the bounded waits below begin after it.
+  grid_dependency_wait();
   const uint32_t tm = __shfl_sync(0xffffffffu, tmem_base_sh, 0);
   // S_t and P_t at columns 128 t, O_t at 256 + 128 t
 
@@ -553,7 +578,6 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       pw_wait(smem_u32(&drain), 0, &no_abort);
     } else if (warp == 17) {
       // ------------------------------ TMA loads -------------------------------
-      grid_dependency_wait();
       if (pw_elect()) {
         PkItem it;
         bool ok = true;
@@ -595,7 +619,6 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       copied_q[1] = __reduce_max_sync(0xffffffffu, copied_q[1]);
     } else if (warp == 18) {
       // ------------------------------- items ----------------------------------
-      grid_dependency_wait();
       int32_t* pairs = reinterpret_cast<int32_t*>(sm + LY::kRankAt);
       PkOrder order{p, pairs, pairs + kPkRank, !p.causal || p.window > 0};
       order.lane = lane;

@@ -83,6 +83,14 @@ def test_lengths(lib, n, causal):
     check(lib, q, k, v, starts([n, 9]), None, 0.09, "f32", causal)
 
 
+@pytest.mark.parametrize("keys", [1, 2, 130])
+def test_one_query(lib, keys):
+    """A single row of q, as a decode step over packed keys has it."""
+    q, k, v = inputs(keys, 1, keys, 6, 2, 128)
+    for out_type in ("bf16", "f32"):
+        check(lib, q, k, v, starts([1]), starts([keys]), 0.09, out_type)
+
+
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (17, 4), (100, 0), (128, 129), (200, 300), (5000, 2)])
 @pytest.mark.parametrize("dim", [64, 128])
 def test_windows(lib, window, sinks, dim):
