@@ -367,8 +367,9 @@ pkv_status pkv_test_force_decode_kernel(int32_t kernel);
  * copies in flight and leaves its share out of the output; the call itself
  * returns PKV_OK and the context stays usable.  Launches of
  * paged_attention_decode_window do the same; those of
- * paged_attention_prefill and paged_attention_prefill_window arm the first V tile
- * of CTA (0, 0, 0), whose rows then stay unwritten.  bytes = 0 restores normal
+ * paged_attention_prefill, paged_attention_prefill_window and
+ * packed_attention_prefill arm the first V tile of their first CTA, whose rows
+ * then stay unwritten (packed_attention_prefill: all that it had not written).  bytes = 0 restores normal
  * launches.  bytes must be a multiple of 16 and at most 65536, else
  * INVALID_ARG.  Process-wide, like pkv_test_force_decode_kernel. */
 pkv_status pkv_test_decode_stall(uint32_t bytes);
@@ -636,7 +637,8 @@ pkv_status paged_attention_prefill_window(
  *     positions[row] = c + i, slot_mapping[row] = block * bs + (c + i) % bs.
  * query_start[s] = start (query_start[num_seqs]: all rows), context_out[s] = c + n and
  * *free_next = *free_start + blocks taken.  context_out may be context_lens and free_next
- * free_start: then a replayed graph goes on from step to step.
+ * free_start: then a replayed graph goes on from step to step.  No other array that is written may
+ * overlap another one.  Calls on one table or free list follow one another, on one stream or by events.
  *   new_lens     : device [num_seqs] int32; NULL: one token each.
  *   row_per_sequence : 1 - sequence s owns row s, as a decode step's q does; each new_lens[s] is 0
  *                  (row s then has slot -1) or 1, num_tokens >= num_seqs, and query_start is
@@ -734,8 +736,8 @@ pkv_status rotary_turns(const double* inv_freq, int32_t n, uint64_t* turns);
  *   out          : device [num_tokens, num_q_heads, head_dim] contiguous, out_dtype f32 or bf16;
  *                  a query that sees nothing gets 0; rows outside every sequence are not written.
  * out[t, h, :] = softmax(scale * q . K_g^T) V_g over the visible keys, g = h / G, accumulated in
- * float32.  The weights enter P V as two bf16 parts (2^-16 of each weight) for a float32 output and
- * as one (2^-8, half a step of a bf16 output, of each weight) for a bf16 one.
+ * float32.  The weights enter P V as two bf16 parts (2^-17 of each weight) for a float32 output and
+ * as one (2^-9 of each weight, as the output's own rounding) for a bf16 one.
  * A key that a query does not see, but another one of its work tile (128 rows) does, has
  * weight 0 there; a V value of it that is not finite gives NaN.  Keys of other sequences and rows
  * outside every sequence have no influence, whatever they hold.  out overlaps no input.

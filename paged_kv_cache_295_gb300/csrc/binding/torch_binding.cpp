@@ -481,9 +481,11 @@ void want_rows(const Tensor& t, const char* name, int64_t rows, int64_t heads, i
   if (t.device() != dev) refuse(std::string(name) + " is on " + t.device().str() + ", the call on " + dev.str());
   if (t.numel() == 0) return;
   if (dim > 1 && t.stride(2) != 1) refuse(std::string(name) + " must have its last dimension contiguous");
-  if (written)
-    for (int i = 0; i < 2; ++i)
-      if (t.size(i) > 1 && t.stride(i) < dim) refuse(std::string(name) + " must not overlap itself");
+  if (!written) return;
+  const int inner = t.size(0) > 1 && (t.size(1) <= 1 || t.stride(0) < t.stride(1)) ? 0 : 1, outer = 1 - inner;
+  const int64_t span = t.size(inner) > 1 ? (t.size(inner) - 1) * t.stride(inner) + dim : dim;
+  if ((t.size(inner) > 1 && t.stride(inner) < dim) || (t.size(outer) > 1 && t.stride(outer) < span))
+    refuse(std::string(name) + " must not overlap itself");
 }
 
 // rotary_and_cache(q, k, v, positions, (turns, axis, rotary_dim, num_axes, adjacent, scale), slot_mapping,

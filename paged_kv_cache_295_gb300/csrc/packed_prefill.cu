@@ -64,6 +64,20 @@ extern "C" pkv_status packed_attention_prefill(const pkv_packed_prefill_args* ar
       !aligned4(a.key_start))
     return PKV_ERR_INVALID_ARG;
 
+  // from the first element to the last one
+  auto range = [&](int64_t rows, int64_t heads, int64_t row_stride, int64_t head_stride) {
+    return static_cast<size_t>(2 * ((rows > 1 ? (rows - 1) * row_stride : 0) + (heads > 1 ? (heads - 1) * head_stride : 0) +
+                                    a.head_dim));
+  };
+  const size_t out_bytes = static_cast<size_t>(a.num_tokens) * a.num_q_heads * a.head_dim * elem_bytes(a.out_dtype);
+  const size_t starts = 4 * (static_cast<size_t>(a.num_seqs) + 1);
+  if (overlap(a.out, out_bytes, a.q, range(a.num_tokens, a.num_q_heads, a.q_token_stride, a.q_head_stride)) ||
+      (a.num_keys > 0 &&
+       (overlap(a.out, out_bytes, a.k, range(a.num_keys, a.num_kv_heads, a.k_token_stride, a.k_head_stride)) ||
+        overlap(a.out, out_bytes, a.v, range(a.num_keys, a.num_kv_heads, a.v_token_stride, a.v_head_stride)))) ||
+      overlap(a.out, out_bytes, a.query_start, starts) || overlap(a.out, out_bytes, a.key_start, starts))
+    return PKV_ERR_INVALID_ARG;
+
   PackedParams p{};
   p.out = a.out;
   p.query_start = a.query_start;

@@ -7,10 +7,15 @@
 // where its blocks begin in the free list and its rows in the outputs; every row is then
 // independent of the others: a search in the starts finds its sequence.
 //
-// One launch does it.  Every CTA scans all lengths itself (a thousand sequences at a time, one a
+// What bounds it: latency.  A step's lists are 16 to 800 KB, 0.12 us of HBM's time at the most; the launch,
+// two dependent loads (length, then table or free list), the scan and the search are the rest.  So one
+// launch does it: every CTA scans all lengths itself (a thousand sequences at a time, one a
 // thread), so that nothing waits for another CTA's sums, and fills its share of the rows.  Where the new
 // lengths (or the free list's new start) take the old ones' place, the CTAs are one cluster, whose
 // barrier stands between the last read and the first write.
+//
+// Measured: 8 sequences of one token 3.6 us, 512 of them 4.2 us, 64 prompts and chunks of up to 2,047 tokens
+// (66,000 rows) 4.9 us.
 #include "common.cuh"
 
 namespace pkv {
@@ -217,12 +222,6 @@ __global__ void __launch_bounds__(kSlThreads, 1) slots_kernel(const __grid_const
   }
 }
 
-// Whether two ranges of bytes have one in common.
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + nb && y < x + na;
-}
-
 bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 }  // namespace
@@ -257,12 +256,27 @@ extern "C" pkv_status slots_from_lengths(
                 positions, query_start, context_out, free_next, device_status, num_blocks,
                 num_seqs, num_tokens, num_free, block_size, max_blocks_per_seq, row_per_sequence,
                 first_block_held};
+  // what is written overlaps nothing else, but for the two pairs that may be the same array
   const size_t len = 4 * static_cast<size_t>(num_seqs);
-  const bool in_place = overlap(context_out, len, context_lens, len) || overlap(free_next, 4, free_start, 4) ||
-                        overlap(context_out, len, new_lens, len) || overlap(context_out, len, free_start, 4) ||
-                        overlap(free_next, 4, context_lens, len) || overlap(free_next, 4, new_lens, len);
+  struct Range {
+    const void* ptr;
+    size_t bytes;
+  };
+  const Range arrays[] = {{context_out, len}, {free_next, 4}, {block_tables, len * max_blocks_per_seq},
+                          {slot_mapping, 8 * static_cast<size_t>(num_tokens)},
+                          {positions, 4 * static_cast<size_t>(num_tokens)},
+                          {row_per_sequence ? nullptr : query_start, len + 4},
+                          {device_status, 4},   // the last one that is written
+                          {context_lens, len}, {new_lens, len}, {free_start, 4},
+                          {free_blocks, 4 * static_cast<size_t>(num_free)}};
+  for (int i = 0; i < 7; ++i)
+    for (int j = i + 1; j < 11; ++j)
+      if (overlap(arrays[i].ptr, arrays[i].bytes, arrays[j].ptr, arrays[j].bytes) &&
+          !(arrays[i].ptr == arrays[j].ptr && ((i == 0 && j == 7) || (i == 1 && j == 9))))
+        return PKV_ERR_INVALID_ARG;
+  const bool in_place = (len > 0 && context_out == context_lens) || (free_next && free_next == free_start);
   int64_t ctas = (static_cast<int64_t>(num_tokens) + kSlRowsPerCta - 1) / kSlRowsPerCta;
-  if (ctas > 1 && in_place) {   // 66,000 rows: 10.8 us by eight CTAs, 5.6 by one for each 2,048
+  if (ctas > 1 && in_place) {   // 66,000 rows: 10.8 us by eight CTAs, 4.9 by one for each 2,048
     ctas = ctas <= 2 ? 2 : ctas <= 4 ? 4 : kSlCluster;
   } else {
     const int64_t sms = device_sm_count();

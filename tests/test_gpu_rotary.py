@@ -9,9 +9,9 @@ pytestmark = pytest.mark.gpu
 
 
 def bound(x, plan, y, adjacent, scale):
-    """Elementwise bound on the float32 result.  cos and sin are off by at most 2^-22 (two units of
-    their last place and the argument's rounding, pi 2^-25), the two products, their sum and the
-    factor by 2^-24 of each product, rounded up to 2^-22 together."""
+    """Elementwise bound on the float32 result.  cos and sin are off by less than 2^-23 (one unit of
+    their last place), times the factor by 2^-24 more; the two products and their sum by 2^-24 of each
+    product: 2^-22 together and rounded up to 2^-21."""
     half = plan.rotary_dim // 2
     e = np.zeros(y.shape)
     a, b = (np.s_[..., 0:2 * half:2], np.s_[..., 1:2 * half:2]) if adjacent else \
@@ -276,3 +276,22 @@ def test_captured_and_on_another_stream(lib):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, want)
+
+
+def test_outputs_that_overlap_themselves(lib):
+    """Rows and heads of an output lie apart, whichever of the two is the outer one."""
+    import torch
+    plan = lib.Rotary(64)
+    q = torch.randn((4, 3, 64), device="cuda").bfloat16()
+    pos = torch.arange(4, dtype=torch.int32, device="cuda")
+    want, _ = lib.rotary_and_cache(q, q, None, pos, plan)
+    room = torch.empty(4096, device="cuda", dtype=torch.bfloat16)
+    for strides in ((64, 64, 1), (128, 64, 1), (184, 64, 1), (64, 248, 1), (32, 512, 1), (0, 64, 1), (192, 0, 1)):
+        bad = room.as_strided((4, 3, 64), strides)
+        for kw in (dict(q_out=bad), dict(k_out=bad)):
+            with pytest.raises(ValueError):
+                lib.rotary_and_cache(q, q, None, pos, plan, **kw)
+    for strides in ((192, 64, 1), (64, 256, 1), (200, 64, 1), (72, 284, 1)):
+        out = room.as_strided((4, 3, 64), strides)
+        assert lib.rotary_and_cache(q, q, None, pos, plan, q_out=out)[0] is not None
+        assert torch.equal(out, want)

@@ -211,3 +211,17 @@ def test_engine_refusals(lib):
     q = torch.zeros((1, 2, 128), device="cuda", dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         cache.append_rotary(0, q, q, q, dev([0]), lib.Rotary(128), torch.zeros(1, dtype=torch.int64, device="cuda"))
+
+
+def test_a_prompt_that_is_refused_appends_nothing(lib):
+    import torch
+    from paged_kv_cache_295_gb300.engine import PagedKVCache
+    cache = PagedKVCache(num_layers=1, num_kv_heads=2, head_dim=64, block_size=16, num_blocks=4, kv_dtype=lib.F32)
+    cache.k_cache(0).zero_()
+    lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sl = cache.slots(torch.zeros((1, 4), dtype=torch.int32, device="cuda"), lens, lens + 5,
+                     torch.arange(4, dtype=torch.int32, device="cuda"), 5)
+    q, k = torch.ones((5, 4, 64), device="cuda"), torch.ones((5, 2, 64), device="cuda")
+    with pytest.raises(ValueError):
+        cache.prompt(0, q, k, k, sl.positions, lib.Rotary(64), sl)
+    assert not cache.k_cache(0).any()

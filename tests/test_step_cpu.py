@@ -15,11 +15,16 @@ OK, INVALID, UNSUPPORTED = 0, 1, 5
 PTR = C.c_void_p(1 << 20)      # aligned, never dereferenced: the calls below are refused first
 
 
+def at(n):
+    return C.c_void_p((1 << 20) + n)
+
+
 def slots(lib, **kw):
-    a = dict(bt=PTR, ctx=PTR, new=PTR, free=PTR, fs=PTR, S=2, T=8, F=5, nb=10, bs=16, mb=4, per_row=0,
-             held=0, slots=PTR, pos=PTR, qs=PTR, co=PTR, fn=PTR)
+    a = dict(bt=at(0), ctx=at(0x100), new=at(0x200), free=at(0x300), fs=at(0x400), S=2, T=8, F=5, nb=10, bs=16,
+             mb=4, per_row=0, held=0, slots=at(0x500), pos=at(0x600), qs=at(0x700), co=at(0x800), fn=at(0x900),
+             status=None)
     a.update(kw)
-    return lib.library().slots_from_lengths(*a.values(), None, None)
+    return lib.library().slots_from_lengths(*a.values(), None)
 
 
 @pytest.mark.parametrize("kw,want", [
@@ -31,6 +36,16 @@ def slots(lib, **kw):
     (dict(fn=C.c_void_p(1)), INVALID), (dict(qs=C.c_void_p(6)), INVALID)])
 def test_slots_refusals(lib, kw, want):
     assert slots(lib, **kw) == want
+
+
+@pytest.mark.parametrize("kw", [
+    dict(co=at(0x200)), dict(co=at(0x104)), dict(co=at(0xFC)), dict(co=at(0x400)), dict(fn=at(0x104)),
+    dict(fn=at(0x200)), dict(fn=at(0x310)), dict(bt=at(0xE4)), dict(bt=at(0x30C)), dict(slots=at(0x1C8)),
+    dict(pos=at(0x51C)), dict(qs=at(0xF8)), dict(qs=at(0x804)), dict(co=at(0x700)), dict(fn=at(0x61C)),
+    dict(status=at(0x104)), dict(status=at(0x01C)), dict(status=at(0x800)), dict(pos=at(0x200), new=at(0x21C))])
+def test_slots_outputs_overlap_nothing(lib, kw):
+    """8 bytes of lengths, 32 of tables, positions and 64 of slots: by one element, from either side."""
+    assert slots(lib, **kw) == INVALID
 
 
 def rotary(lib, **kw):
@@ -65,8 +80,8 @@ def test_rotary_refusals(lib, kw, want):
 
 
 def packed(lib, **kw):
-    a = dict(q=PTR, k=PTR, v=PTR, out=PTR, query_start=PTR, key_start=PTR, num_seqs=2, num_tokens=8,
-             num_keys=8, num_q_heads=4, num_kv_heads=2, head_dim=64, scale=0.1, causal=1, window=0, sinks=0,
+    a = dict(q=at(0), k=at(0x10000), v=at(0x20000), out=at(0x30000), query_start=at(0x40000), key_start=at(0x50000),
+             num_seqs=2, num_tokens=8, num_keys=8, num_q_heads=4, num_kv_heads=2, head_dim=64, scale=0.1, causal=1, window=0, sinks=0,
              q_dtype=1, kv_dtype=1, out_dtype=1)
     for n in ("q", "k", "v"):
         a[f"{n}_token_stride"], a[f"{n}_head_stride"] = 256, 64
@@ -90,6 +105,15 @@ def packed(lib, **kw):
 def test_packed_refusals(lib, kw, want):
     assert packed(lib, **kw) == want
     assert lib.library().packed_attention_prefill(None, None) == INVALID
+
+
+@pytest.mark.parametrize("kw", [
+    dict(out=at(0)), dict(out=at(0x10000)), dict(out=at(0x20000 - 0xFF0)), dict(out=at(0x20000 + 7 * 512 + 240)),
+    dict(out=at(0x40000 - 0xFF0)), dict(key_start=at(0x30FFC)),
+    dict(out=at(0x10000), num_tokens=1, num_keys=1)])
+def test_packed_output_overlaps_no_input(lib, kw):
+    """Rows of 4 heads (512 bytes) for q and of 2 (256 of 512) for k and v, 4,096 bytes of output."""
+    assert packed(lib, **kw) == INVALID
 
 
 def test_python_refusals(lib):
