@@ -18,9 +18,9 @@
 // after another, without a choice per row, 40).
 //
 // Measured: 8,192 tokens of 32 + 8 heads x 128, bf16, three axes, turned k kept and appended 36.5 us
-// (6.0 TB/s, 89 % of the copy rate); 8,191 tokens of 32 + 32 heads into an fp8 cache 66.5 us (5.0 TB/s,
-// 75 %: the codes' arithmetic and its latency, 59 % of the issue slots; 75 with a bounds check per
-// element, 107 with a divide per element); 8 tokens of 32 + 8 heads 2.0 us in a graph.
+// (6.0 TB/s, 89 % of the copy rate); 8,191 tokens of 32 + 32 heads into an fp8 cache 63 us (5.3 TB/s,
+// 79 %: the codes' arithmetic and its latency; 67 with the cache's type looked at per row and one segment's
+// codes after the other's, 75 with a bounds check per element, 107 with a divide per element); 8 tokens of 32 + 8 heads 2.0 us in a graph.
 #include <cmath>
 #include <initializer_list>
 #include <type_traits>
@@ -115,8 +115,8 @@ struct Seg<__nv_bfloat16> {
 };
 
 // Codes of N float32 values x / s.
-template <int N>
-__device__ __forceinline__ void codes(const RotaryParams& p, const float* x, float s, float neg_r, bool plain,
+template <typename Q, int N>
+__device__ __forceinline__ void codes(const float* x, float s, float neg_r, bool plain,
                                       uint32_t* w) {
 #pragma unroll
   for (int i = 0; i < N / 4; ++i) {
@@ -131,15 +131,15 @@ __device__ __forceinline__ void codes(const RotaryParams& p, const float* x, flo
       q[e] = v.x;
       q[e + 1] = v.y;
     }
-    w[i] = p.kind == 2 ? quant4<FP8>(q) : quant4<INT8>(q);
+    w[i] = quant4<Q>(q);
   }
 }
 
 // The largest |element| of two segments, as a float32's bits, at least; infinities and NaN are larger
 // than any.
 template <typename Src>
-__device__ __forceinline__ uint32_t top_of(const uint4& a, const uint4& b, bool has_b) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, has_b ? b.x : 0u, has_b ? b.y : 0u, has_b ? b.z : 0u, has_b ? b.w : 0u};
+__device__ __forceinline__ uint32_t top_of(const uint4& a, const uint4& b) {
+  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   if constexpr (sizeof(Src) == 2) {
     __nv_bfloat162 t = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
 #pragma unroll
@@ -156,42 +156,44 @@ __device__ __forceinline__ uint32_t top_of(const uint4& a, const uint4& b, bool 
 
 // A pair of segments to the cache, in its type: x at element `at` + a, y (where there is one) at `at` + b.
 // `top`: top_of() the source's segments, which the turned ones exceed by |scale| sqrt(2) at most.
-template <typename Src>
+// Q: the codes' type; Src: the rows' own.
+template <typename Src, typename Q>
 __device__ __forceinline__ void to_cache(const RotaryParams& p, void* cache, const float* scales, int head,
                                          int64_t at, int a, int b, bool has_b, uint32_t top, const float* x,
                                          const float* y) {
   constexpr int E = Seg<Src>::E;
-  if (p.kind == 1) {
+  if constexpr (std::is_same_v<Src, Q>) {
     Src* dst = static_cast<Src*>(cache) + at;
     *reinterpret_cast<uint4*>(dst + a) = Seg<Src>::pack(x);
     if (has_b) *reinterpret_cast<uint4*>(dst + b) = Seg<Src>::pack(y);
-    return;
-  }
-  const float s = __ldg(scales + head);
-  // quotient2's range: scales from 2^-64 to 2^64 and elements below 2^60 (|scale| up to 2^29, elements of
-  // the source below 2^30)
-  const bool plain = top < 0x4E800000u && p.small_scale && s >= 5.421010862427522e-20f && s <= 18446744073709551616.f;
-  uint8_t* dst = static_cast<uint8_t*>(cache) + at;
-  auto put = [&](int to, const float* v, float neg_r, auto fast) {
-    uint32_t w[2];
-    codes<E>(p, v, s, neg_r, decltype(fast)::value, w);
-    if constexpr (E == 8)
-      *reinterpret_cast<uint2*>(dst + to) = make_uint2(w[0], w[1]);
-    else
-      *reinterpret_cast<uint32_t*>(dst + to) = w[0];
-  };
-  if (__builtin_expect(plain, 1)) {
-    const float neg_r = -__frcp_rn(s);
-    put(a, x, neg_r, std::true_type{});
-    if (has_b) put(b, y, neg_r, std::true_type{});
   } else {
-    put(a, x, 0.f, std::false_type{});
-    if (has_b) put(b, y, 0.f, std::false_type{});
+    const float s = __ldg(scales + head);
+    // quotient2's range: scales from 2^-64 to 2^64 and elements below 2^60 (|scale| up to 2^29, elements of
+    // the source below 2^30)
+    const bool plain = top < 0x4E800000u && p.small_scale && s >= 5.421010862427522e-20f && s <= 18446744073709551616.f;
+    uint8_t* dst = static_cast<uint8_t*>(cache) + at;
+    uint32_t wx[E / 4], wy[E / 4];   // both segments' quotients run side by side
+    if (__builtin_expect(plain, 1)) {
+      const float neg_r = -__frcp_rn(s);
+      codes<Q, E>(x, s, neg_r, true, wx);
+      codes<Q, E>(y, s, neg_r, true, wy);
+    } else {
+      codes<Q, E>(x, s, 0.f, false, wx);
+      codes<Q, E>(y, s, 0.f, false, wy);
+    }
+    if constexpr (E == 8) {
+      *reinterpret_cast<uint2*>(dst + a) = make_uint2(wx[0], wx[1]);
+      if (has_b) *reinterpret_cast<uint2*>(dst + b) = make_uint2(wy[0], wy[1]);
+    } else {
+      *reinterpret_cast<uint32_t*>(dst + a) = wx[0];
+      if (has_b) *reinterpret_cast<uint32_t*>(dst + b) = wy[0];
+    }
   }
 }
 
-// Rows whose halves (or whose whole, with neighbouring pairs) are multiples of 16 bytes.
-template <typename Src, bool ADJ>
+// Rows whose halves (or whose whole, with neighbouring pairs) are multiples of 16 bytes.  Q: the cache's
+// type where it is one of codes, else Src (a cache of the rows' own type, or none).
+template <typename Src, bool ADJ, typename Q>
 __global__ void __launch_bounds__(kRoThreads, kRoCtas) rotary_kernel(const __grid_constant__ RotaryParams p) {
   using S = Seg<Src>;
   constexpr int E = S::E;
@@ -227,7 +229,7 @@ __global__ void __launch_bounds__(kRoThreads, kRoCtas) rotary_kernel(const __gri
                            ? static_cast<const Src*>(p.k) + t * p.k_ts + (row - p.hq) * p.k_hs
                            : static_cast<const Src*>(p.v) + t * p.v_ts + (row - p.hq - p.hkv) * p.v_hs;
       va[n] = *reinterpret_cast<const uint4*>(src + a);
-      if (has_b) vb[n] = *reinterpret_cast<const uint4*>(src + b);
+      vb[n] = has_b ? *reinterpret_cast<const uint4*>(src + b) : make_uint4(0u, 0u, 0u, 0u);
     }
   };
   grid_dependency_wait();
@@ -259,7 +261,7 @@ __global__ void __launch_bounds__(kRoThreads, kRoCtas) rotary_kernel(const __gri
       const int head = is_q ? row : is_v ? row - p.hq - p.hkv : row - p.hq;
       float x[E], y[E];
       S::unpack(va[n], x);
-      if (has_b) S::unpack(vb[n], y);
+      S::unpack(vb[n], y);
       if (!is_v && !ADJ && u < tu) {   // dims past rotary_dim keep infinities: no product with 0
 #pragma unroll
         for (int e = 0; e < E; ++e) {
@@ -294,8 +296,8 @@ __global__ void __launch_bounds__(kRoThreads, kRoCtas) rotary_kernel(const __gri
       }
       if (!is_q && append) {
         const int64_t at = (slot * p.hkv + head) * p.dim;
-        to_cache<Src>(p, is_v ? p.v_cache : p.k_cache, is_v ? p.v_scale : p.k_scale, head, at, a, b, has_b,
-                      p.kind > 1 ? top_of<Src>(va[n], vb[n], has_b) : 0u, x, y);
+        to_cache<Src, Q>(p, is_v ? p.v_cache : p.k_cache, is_v ? p.v_scale : p.k_scale, head, at, a, b, has_b,
+                         std::is_same_v<Src, Q> ? 0u : top_of<Src>(va[n], vb[n]), x, y);
       }
     }
     r += lanes * kRoBatch;
@@ -469,14 +471,16 @@ extern "C" pkv_status rotary_and_cache(const pkv_rotary_args* args, pkv_stream_t
     const int tu = p.adjacent ? (p.rot + 2 * E - 1) / (2 * E) : half / E;
     const size_t smem = sizeof(float2) * kRoTokens * tu * E;
     const dim3 grid(groups, ys);
-    cudaError_t e;
-    if (a.src_dtype == PKV_F32)
-      e = p.adjacent ? launch_pdl(rotary_kernel<float, true>, grid, dim3(kRoThreads), smem, st, p)
-                     : launch_pdl(rotary_kernel<float, false>, grid, dim3(kRoThreads), smem, st, p);
-    else
-      e = p.adjacent ? launch_pdl(rotary_kernel<__nv_bfloat16, true>, grid, dim3(kRoThreads), smem, st, p)
-                     : launch_pdl(rotary_kernel<__nv_bfloat16, false>, grid, dim3(kRoThreads), smem, st, p);
-    return cuda_status(e);
+    auto launch = [&](auto kernel) { return cuda_status(launch_pdl(kernel, grid, dim3(kRoThreads), smem, st, p)); };
+    auto of = [&](auto src, auto adj) {
+      using Src = decltype(src);
+      constexpr bool A = decltype(adj)::value;
+      return kind == 2   ? launch(rotary_kernel<Src, A, FP8>)
+             : kind == 3 ? launch(rotary_kernel<Src, A, INT8>)
+                         : launch(rotary_kernel<Src, A, Src>);
+    };
+    if (a.src_dtype == PKV_F32) return p.adjacent ? of(float{}, std::true_type{}) : of(float{}, std::false_type{});
+    return p.adjacent ? of(__nv_bfloat16{}, std::true_type{}) : of(__nv_bfloat16{}, std::false_type{});
   }
   const int64_t work = static_cast<int64_t>(p.tokens) * rows * (p.dim - half);
   const int64_t want = (work + kRoThreads - 1) / kRoThreads, cap = static_cast<int64_t>(device_sm_count()) * 16;
