@@ -41,12 +41,12 @@
 // (Q and K of the next item reach shared memory 2 to 3 us after they are asked for, as all CTAs ask at
 // once) and a cold CTA for its code.  Tried and left out: one issuer for each tile (both tiles' phases
 // fall together), with and without turns; prefetches of the next item to L2 (16 prompts of 512 tokens 77
-// -> 90 us); lists of equal length for both tiles; the halves as a loop (20 % slower); Q before K.
+// -> 90 us); the order of items kept within sequences whose keys fit L2; lists of equal length for both tiles; the halves as a loop (20 % slower); Q before K.
 //
 // Measured: three prompts of 700 to 8,192 tokens, 32 heads on 8, causal 460 to 477 us (1,510 to 1,570
-// TFLOP/s); 16 prompts of 512 tokens, 32 heads 66 us; 11 images of 64 to 1,156 patches, 16 heads of 80, not
+// TFLOP/s); 16 prompts of 512 tokens, 32 heads 64.5 us; 11 images of 64 to 1,156 patches, 16 heads of 80, not
 // causal 45 us; nine chunks of up to 1,500 tokens behind 333 keys, 16 heads on 2 of 64, window 1,024,
-// float32 output 49 us; four prompts of up to 60 tokens 9.4 us.
+// float32 output 48 us; four prompts of up to 60 tokens 9.4 us.
 //
 // Every wait is bounded (2 s) and gives up when another role has given up; copies in flight are then
 // waited for, and TMEM is released before the CTA exits.
@@ -69,7 +69,7 @@ constexpr float kPkLag = 24.f;
 // Key tiles after which a float32 output takes O up.  The tensor cores cut every sum towards zero:
 // up to 2^-23 of O for each 16 keys and weight part, which adds up (20,000 keys in one go: 4.4e-5 of the
 // norm, and no end to it); 16 tiles are 256 such sums, 5.3e-6 of the norm however many there are (8 tiles:
-// 3.4e-6, and 62 us for the windowed chunks above, whose lists of up to 12 tiles then come in two parts).
+// 3.4e-6, and a fifth more time for the windowed chunks above, whose lists of up to 12 tiles then come in two parts).
 // In between the epilogue adds in float32, in the output's own rows.
 constexpr int kPkPart = 16;
 
@@ -231,7 +231,7 @@ __device__ __forceinline__ bool pk_wait2(uint32_t bar_a, uint32_t par_a, uint32_
 }
 
 // Warp 18: the items of one CTA.  Units (sequence, pair of query tiles, KV head) are ordered by
-// the length of their key lists, longest first and KV heads fastest, within each kPkRank sequences;
+// the length of their key lists (in pairs of query tiles, cut at the window), longest first and KV heads fastest, within each kPkRank sequences;
 // round k of a grid of n CTAs takes units kn .. kn + n - 1, every other round in the opposite
 // order.  Order by counting: the units of sequence s that are at least x long are known in closed
 // form, so the length of the u-th unit is found by halving.
@@ -240,11 +240,13 @@ struct PkOrder {
   int32_t* pairs;    // shared, [kPkRank]: pairs of query tiles of a sequence
   int32_t* level;    // shared: length of its first pair, in pairs
   bool flat;         // all pairs of a sequence are alike
+  int cap;           // a window lets no list grow past this level
   int first = 0, count = 0, top = 0, lane;   // the sequences at hand; the longest unit
   uint32_t before = 0, total = 0;            // units before them; theirs
 
   __device__ __forceinline__ int longer(int i, int x) const {   // units of sequence i of level >= x
-    return flat ? (level[i] >= x ? pairs[i] : 0) : min(max(level[i] + pairs[i] - x, 0), pairs[i]);
+    if (flat) return level[i] >= x ? pairs[i] : 0;
+    return x > cap ? 0 : min(max(level[i] + pairs[i] - x, 0), pairs[i]);
   }
   __device__ __forceinline__ void fill(int s0, bool report) {
     first = s0;
@@ -262,12 +264,12 @@ struct PkOrder {
       } else {
         n = static_cast<int>((static_cast<int64_t>(q1) - q0 + per - 1) / per);
         const int c = k1 - k0;
-        lv = flat ? (p.window > 0 ? 0 : c / per) : max(c - (q1 - q0), 0) / per;
+        lv = flat ? c / per : max(c - (q1 - q0), 0) / per;
       }
       pairs[i] = n;
       level[i] = lv;
       sum += n;
-      if (n > 0) hi = max(hi, flat ? lv : lv + n - 1);
+      if (n > 0) hi = max(hi, flat ? lv : min(lv + n - 1, cap));
     }
     __syncwarp();
     if (report && __any_sync(0xffffffffu, bad) && lane == 0) flag_status(p.status, PKV_DEV_BAD_CONTEXT);
@@ -310,7 +312,7 @@ struct PkOrder {
         const int at = __ffs(hit) - 1;
         const int offset = left - (__shfl_sync(0xffffffffu, incl, at) - __shfl_sync(0xffffffffu, mine, at));
         s = first + i0 + at;
-        pair = flat ? offset : lo - level[i0 + at];
+        pair = offset + (flat ? 0 : max(lo - level[i0 + at], 0));
         return true;
       }
       left -= __shfl_sync(0xffffffffu, incl, 31);
@@ -620,7 +622,8 @@ __global__ void __launch_bounds__(kPkThreads, 1)
     } else if (warp == 18) {
       // ------------------------------- items ----------------------------------
       int32_t* pairs = reinterpret_cast<int32_t*>(sm + LY::kRankAt);
-      PkOrder order{p, pairs, pairs + kPkRank, !p.causal || p.window > 0};
+      PkOrder order{p, pairs, pairs + kPkRank, !p.causal,
+                    p.window > 0 ? (p.window - 1) / (2 * TQ) + 2 : INT32_MAX / 4};
       order.lane = lane;
       order.fill(0, blockIdx.x == 0);
       const uint32_t n = gridDim.x;
@@ -674,6 +677,19 @@ __global__ void __launch_bounds__(kPkThreads, 1)
         if (!ok) break;
         if (lane == 0) {
           items[i & 1] = it;
+          // its rows of q on their way to L2: there is room for them only when the item before has taken
+          // its last scores (16 prompts of 512 tokens 66.1 -> 64.5 us; the other cases keep their times)
+          if (i > 0 && it.valid && it.j0 == 0) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (it.nt(t) == 0) continue;
+#pragma unroll
+              for (int h = 0; h < SLABS; ++h)
+                asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];\n" ::"l"(&tmap_q),
+                             "r"(64 * h), "r"(it.head * G), "r"(it.row0 + t * TQ)
+                             : "memory");
+            }
+          }
           mbar_arrive(smem_u32(&item_full[i & 1]));
         }
         __syncwarp();

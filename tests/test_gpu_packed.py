@@ -102,6 +102,23 @@ def test_windows(lib, window, sinks, dim):
     check(lib, q, k, v, starts(lens), starts(more), 0.1, "bf16", window=window, sinks=sinks)
 
 
+@pytest.mark.parametrize("window,group", [(1, 8), (40, 8), (64, 16), (65, 16), (300, 3), (10 ** 9, 8)])
+def test_every_item_under_a_window(lib, window, group):
+    """Lists that grow up to the window and stay there, in sequences of all lengths: every row is written once."""
+    lens, ahead = [900, 5, 333, 0, 64, 600, 1], [0, 200, 17, 9, 70, 900, 0]
+    for more in (None, [x + y for x, y in zip(lens, ahead)]):
+        q, k, v = inputs(group, sum(lens), sum(more or lens), 2 * group, 2, 64)
+        check(lib, q, k, v, starts(lens), None if more is None else starts(more), 0.1, "bf16", window=window, sinks=3)
+
+
+def test_many_sequences_under_a_window(lib):
+    rng = np.random.default_rng(4)
+    lens = rng.integers(0, 4, 1500)
+    lens[rng.integers(0, 1500, 5)] = 140
+    q, k, v = inputs(4, int(lens.sum()), int(lens.sum()), 32, 1, 64)
+    check(lib, q, k, v, starts(lens), None, 0.125, "bf16", window=20, sinks=1)
+
+
 @pytest.mark.parametrize("causal", [False, True])
 def test_other_key_lengths(lib, causal):
     """More keys than queries, fewer (rows that see nothing), none at all."""
