@@ -127,7 +127,8 @@ class PagedKVCache:
                out_dtype=None, device_status=None, stream=None):
         """One layer of a step over whole prompts (sequences with nothing cached before): rotary
         positions, the append, and causal attention over the packed rows.  ``slots`` as
-        ``self.slots`` gives them for this step.  bfloat16 rows, head_dim a multiple of 8 up to 128."""
+        ``self.slots`` gives them for this step; rows of the output behind the last sequence are not
+        written.  bfloat16 rows, head_dim a multiple of 8 up to 128."""
         if q.dtype != _torch().bfloat16 or self.head_dim > 128 or self.head_dim % 8:
             raise ValueError("prompt takes bfloat16 rows and a head_dim that is a multiple of 8 up to 128")
         q, k = self.append_rotary(layer, q, k, v, positions, rotary, slots.slot_mapping, keep_k=True,

@@ -346,3 +346,30 @@ def test_waits_run_out_and_the_next_call_is_clean(lib, out_type):
         lib.stall_decode_for_test(0)
     out, st, _ = call()
     assert st == 0 and torch.equal(out, want)
+
+
+def test_rows_past_32_bits(lib):
+    """Rows and heads whose elements lie past 2^32 bytes, and past 2^31 elements."""
+    import torch
+    lens = [5, 2]
+    q, k, v = inputs(21, 7, 7, 4, 2, 64)
+    want = check(lib, q, k, v, starts(lens), None, 0.125, "f32")
+    far = []
+    for x in (q, k, v):
+        y = torch.empty((7, 2 ** 29), device="cuda", dtype=torch.bfloat16)[:, -x[0].numel():].view(x.shape)
+        y.copy_(x)
+        far.append(y)
+    qs = torch.from_numpy(starts(lens)).cuda()
+    assert torch.equal(lib.packed_attention_prefill(*far, qs, 0.125), want)
+    del far, y
+    # an output of more than 2^32 bytes: its last rows
+    T = 2 ** 32 // (2 * 32 * 128) + 40
+    q = torch.empty((T, 32, 128), device="cuda", dtype=torch.bfloat16)
+    a, k, v = inputs(22, 50, 50, 32, 1, 128)
+    q[-50:] = a
+    out = torch.empty_like(q)
+    lib.packed_attention_prefill(q, k, v, torch.tensor([T - 50, T], dtype=torch.int32, device="cuda"), 0.09, out=out,
+                                 key_start=torch.tensor([0, 50], dtype=torch.int32, device="cuda"))
+    alone = lib.packed_attention_prefill(a, k, v, torch.tensor([0, 50], dtype=torch.int32, device="cuda"), 0.09,
+                                         out_dtype=torch.bfloat16)
+    assert torch.equal(out[-50:], alone)

@@ -295,3 +295,29 @@ def test_outputs_that_overlap_themselves(lib):
         out = room.as_strided((4, 3, 64), strides)
         assert lib.rotary_and_cache(q, q, None, pos, plan, q_out=out)[0] is not None
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "int8"])
+def test_slots_past_32_bits(lib, kv):
+    """The last blocks of a cache of more than 2^32 elements, and rows of a source far apart."""
+    import torch
+    bs, hkv, dim = 16, 8, 128
+    nb = 2 ** 32 // (bs * hkv * dim) + 3 if kv == "int8" else 2 ** 31 // (bs * hkv * dim) + 3
+    dt = torch.int8 if kv == "int8" else torch.bfloat16
+    k_cache, v_cache = (torch.empty((nb, bs, hkv, dim), device="cuda", dtype=dt) for _ in range(2))
+    small = [torch.empty((3, bs, hkv, dim), device="cuda", dtype=dt) for _ in range(2)]
+    room = torch.empty((3, 2 ** 30), device="cuda", dtype=torch.bfloat16)
+    x = room[:, -(2 + 2 * hkv) * dim:].view(3, -1, dim)
+    x.copy_(torch.randn(x.shape, device="cuda"))
+    q, k, v = x[:, :2], x[:, 2:2 + hkv], x[:, 2 + hkv:]
+    plan, pos = lib.Rotary(dim), torch.tensor([5, 77, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    kw = dict(keep_k=True)
+    if kv == "int8":
+        kw.update(k_scale=torch.full((hkv,), 0.03, device="cuda"), v_scale=torch.full((hkv,), 0.03, device="cuda"))
+    slots = torch.tensor([(nb - 1) * bs + 15, (nb - 2) * bs, (nb - 3) * bs + 7], device="cuda")
+    a = lib.rotary_and_cache(q, k, v, pos, plan, slots, k_cache, v_cache, **kw)
+    b = lib.rotary_and_cache(q.contiguous(), k.contiguous(), v.contiguous(), pos, plan, slots - (nb - 3) * bs, *small, **kw)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    for big, few in ((k_cache, small[0]), (v_cache, small[1])):
+        at = slots - (nb - 3) * bs
+        assert torch.equal(big[-3:].view(-1, hkv, dim)[at], few.view(-1, hkv, dim)[at])
