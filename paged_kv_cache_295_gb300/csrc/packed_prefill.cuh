@@ -44,9 +44,9 @@
 // -> 90 us); the order of items kept within sequences whose keys fit L2; lists of equal length for both tiles; the halves as a loop (20 % slower); Q before K.
 //
 // Measured: three prompts of 700 to 8,192 tokens, 32 heads on 8, causal 460 to 477 us (1,510 to 1,570
-// TFLOP/s); 16 prompts of 512 tokens, 32 heads 64.5 us; 11 images of 64 to 1,156 patches, 16 heads of 80, not
+// TFLOP/s; float32 output 706); 16 prompts of 512 tokens, 32 heads 64.5 us (float32 output 80); 11 images of 64 to 1,156 patches, 16 heads of 80, not
 // causal 45 us; nine chunks of up to 1,500 tokens behind 333 keys, 16 heads on 2 of 64, window 1,024,
-// float32 output 48 us; four prompts of up to 60 tokens 9.4 us.
+// float32 output 45 us; four prompts of up to 60 tokens 9.2 us.
 //
 // Every wait is bounded (2 s) and gives up when another role has given up; copies in flight are then
 // waited for, and TMEM is released before the CTA exits.
@@ -335,9 +335,8 @@ __global__ void __launch_bounds__(kPkThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t kv_full[STAGES], kv_empty[STAGES];
   __shared__ __align__(8) uint64_t q_full[2], q_empty[2], s_full[2], p_full[2][2], o_full[2], o_empty[2],
-      l_full[2], item_full[2], item_empty[2], drain;
+      item_full[2], item_empty[2], drain;
   __shared__ PkItem items[2];
-  __shared__ float row_sum[2][2][kPkRows], row_ref[LO ? 2 : 1][2][kPkRows];   // [item slot][tile]
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -359,7 +358,6 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       mbar_init(smem_u32(&p_full[t][1]), 8);
       mbar_init(smem_u32(&o_full[t]), 1);
       mbar_init(smem_u32(&o_empty[t]), 8);
-      mbar_init(smem_u32(&l_full[t]), 8);
       mbar_init(smem_u32(&item_full[t]), 1);
       mbar_init(smem_u32(&item_empty[t]), 18);   // 16 softmax warps, 16, 17
     }
@@ -709,7 +707,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
     const float sl2 = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
     constexpr int esz = LO ? 4 : 2;
     float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};   // references (in log2 units), sums
-    float ref = 0.f;         // row quad + lane's reference in the part before
+    float ref[2] = {0.f, 0.f};   // references in the part before
     uint32_t n_s = 0, n_o = 0;   // score tiles and items done
     int entries = 0;         // ring entries of the items before
     PkItem it;
@@ -876,96 +874,111 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       }
       if (!alive) break;
       entries += 2 * it.most();
-      // Epilogue: row quad + lane, half of the columns.
-      const int row = quad + lane, tk = static_cast<int>((row * g_inv) >> 16), token = t * TQ + tk;
-      const bool valid = row < TQ * G && token < it.tokens;
+      // Epilogue: the rows of the softmax, 64 columns at a time.  The four lanes of a row have two columns in
+      // every eight each; they exchange them so that a store takes 128 bytes of a row (bf16) or 64 (f32) at a
+      // time.  With a row per lane every store met 32 rows' lines: float32 outputs took up to a quarter longer
+      // (16 prompts of 512 tokens, 32 heads 101 us for 80); bf16 ones are as fast, 2 % either way.
       if (my_nt > 0 || it.j0 == 0) {
-        constexpr int kCols = 32 * SLABS, kStep = LO ? 16 : 32;
-        const int col0 = half * kCols, cols = valid ? min(kCols, p.dim - col0) : 0;   // (dims are a multiple of 8)
-        uint8_t* dst = static_cast<uint8_t*>(p.out) +
-                       ((static_cast<int64_t>(it.row0 + token) * p.num_q_heads + it.head * G + row - tk * G) * p.dim +
-                        col0) * esz;
-        float inv = 0.f, keep = 0.f;   // factors of O and of what earlier parts left
+        float inv[2] = {0.f, 0.f}, keep[2] = {0.f, 0.f};   // factors of O and of what earlier parts left
         if (my_nt > 0) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float sum = l[e] + __shfl_xor_sync(0xffffffffu, l[e], 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            if ((lane & 3) == 0) {
-              row_sum[i & 1][t][w0 + (lane >> 2) + 8 * e] = sum;
-              if constexpr (LO) row_ref[i & 1][t][w0 + (lane >> 2) + 8 * e] = m[e];
+            inv[e] = !LO || it.ends(t) ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+            if constexpr (LO) {   // the parts' references differ where the row's has moved
+              keep[e] = ref[e] == m[e] ? inv[e] : pf_ex2(ref[e] - m[e]) * inv[e];
+              ref[e] = m[e];
             }
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&l_full[t]));
-          if (!pw_wait_all(smem_u32(&l_full[t]), n_o & 1, abort_flag) ||
-              !pw_wait_all(smem_u32(&o_full[t]), n_o & 1, abort_flag))
-            break;
+          if (!pw_wait_all(smem_u32(&o_full[t]), n_o & 1, abort_flag)) break;
           ++n_o;
           tc_fence_after();
-          const float sum = row_sum[i & 1][t][row];
-          inv = !LO || it.ends(t) ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
-          if constexpr (LO) {   // the parts' references differ where the row's has moved
-            const float now = row_ref[i & 1][t][row];
-            keep = ref == now ? inv : pf_ex2(ref - now) * inv;
-            ref = now;
-          }
         }
-        const bool sectors = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;
+        uint8_t* dst[2];
+        bool valid[2];
 #pragma unroll
-        for (int c = 0; c < kCols; c += kStep) {
-          float o[kStep];
+        for (int e = 0; e < 2; ++e) {
+          const int row = w0 + (lane >> 2) + 8 * e, tk = static_cast<int>((row * g_inv) >> 16), token = t * TQ + tk;
+          valid[e] = row < TQ * G && token < it.tokens;
+          dst[e] = static_cast<uint8_t*>(p.out) +
+                   ((static_cast<int64_t>(it.row0 + token) * p.num_q_heads + it.head * G + row - tk * G) * p.dim) * esz;
+        }
+        const bool odd = lane & 1, high = lane & 2;
+#pragma unroll
+        for (int h = 0; h < SLABS; ++h) {
+          float v[32];
           if (my_nt > 0) {
-            const uint32_t at = tm + 256 + 128 * t + (static_cast<uint32_t>(quad) << 16) + col0 + c;
-            if constexpr (LO)
-              pk_ld16(at, o);
-            else
-              tc_ld32(at, o);
-            if (c + kStep >= kCols) {   // O has been read
+            pk_ld64(tO + 64 * h, v);
+            pk_ld_wait(v);
+            if (h == SLABS - 1) {   // O has been read
               tc_fence_before();
               __syncwarp();
               if (lane == 0) mbar_arrive(smem_u32(&o_empty[t]));
             }
           } else {
 #pragma unroll
-            for (int e = 0; e < kStep; ++e) o[e] = 0.f;
+            for (int n = 0; n < 32; ++n) v[n] = 0.f;
           }
-          if constexpr (!LO) {
 #pragma unroll
-            for (int u = 0; u < kStep; u += 16) {
-              uint32_t w[8];
+          for (int e = 0; e < 2; ++e) {
+            if constexpr (!LO) {
+              uint32_t w[8], x[8], y[8];   // column group g; then 2 (kept group) + source; then the lane's 32 bytes
 #pragma unroll
-              for (int e = 0; e < 8; ++e) w[e] = pack_bf16(o[u + 2 * e] * inv, o[u + 2 * e + 1] * inv);
-              uint8_t* d = dst + (c + u) * 2;
-              if (c + u + 16 <= cols && sectors) {
-                pk_store32(d, w);
-              } else {
-                if (c + u < cols) *reinterpret_cast<uint4*>(d) = make_uint4(w[0], w[1], w[2], w[3]);
-                if (c + u + 8 < cols) *reinterpret_cast<uint4*>(d + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+              for (int g = 0; g < 8; ++g) w[g] = pack_bf16(v[4 * g + 2 * e] * inv[e], v[4 * g + 2 * e + 1] * inv[e]);
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {   // groups 0 to 3 to the lower two lanes
+                const uint32_t mine = high ? w[g + 4] : w[g];
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, high ? w[g] : w[g + 4], 2);
+                x[2 * g] = high ? other : mine;
+                x[2 * g + 1] = high ? mine : other;
               }
-            }
-          } else {
-            float4* at = reinterpret_cast<float4*>(dst) + c / 4;
 #pragma unroll
-            for (int e = 0; e < kStep; ++e) o[e] *= inv;
-            // What earlier parts left, step by step: all of it asked for before the waits spills (16 prompts of
-            // 512 tokens, 32 heads 117 us for 102, though a single part has none of it).
-            if (it.j0 > 0) {
-              float4 was[kStep / 4];
-#pragma unroll
-              for (int u = 0; u < kStep / 4; ++u)
-                was[u] = c + 4 * u < cols ? at[u] : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-              for (int u = 0; u < kStep / 4; ++u) {
-                o[4 * u] = fmaf(was[u].x, keep, o[4 * u]);
-                o[4 * u + 1] = fmaf(was[u].y, keep, o[4 * u + 1]);
-                o[4 * u + 2] = fmaf(was[u].z, keep, o[4 * u + 2]);
-                o[4 * u + 3] = fmaf(was[u].w, keep, o[4 * u + 3]);
+              for (int n = 0; n < 4; ++n) {   // and of these two the first ones to the even lane
+                const uint32_t mine = odd ? x[n + 4] : x[n];
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, odd ? x[n] : x[n + 4], 1);
+                y[2 * n] = odd ? other : mine;
+                y[2 * n + 1] = odd ? mine : other;
               }
-            }
+              const int col = 64 * h + 16 * (lane & 3);
+              uint8_t* d = dst[e] + 2 * col;
+              if (valid[e]) {
+                if (col + 16 <= p.dim && (reinterpret_cast<uintptr_t>(d) & 31) == 0) {
+                  pk_store32(d, y);
+                } else {
+                  if (col < p.dim) *reinterpret_cast<uint4*>(d) = make_uint4(y[0], y[1], y[2], y[3]);
+                  if (col + 8 < p.dim) *reinterpret_cast<uint4*>(d + 16) = make_uint4(y[4], y[5], y[6], y[7]);
+                }
+              }
+            } else {
+              float4 rows[4], *to[4];
+              bool there[4];
 #pragma unroll
-            for (int u = 0; u < kStep / 4; ++u)
-              if (c + 4 * u < cols) at[u] = make_float4(o[4 * u], o[4 * u + 1], o[4 * u + 2], o[4 * u + 3]);
+              for (int n = 0; n < 4; ++n) {   // even groups to the even lanes
+                const int g = 2 * n, z = 4 * g + 2 * e;
+                const float m0 = odd ? v[z + 4] : v[z], m1 = odd ? v[z + 5] : v[z + 1];
+                const float o0 = __shfl_xor_sync(0xffffffffu, odd ? v[z] : v[z + 4], 1),
+                            o1 = __shfl_xor_sync(0xffffffffu, odd ? v[z + 1] : v[z + 5], 1);
+                float4 r = odd ? make_float4(o0, o1, m0, m1) : make_float4(m0, m1, o0, o1);
+                r = make_float4(r.x * inv[e], r.y * inv[e], r.z * inv[e], r.w * inv[e]);
+                const int col = 64 * h + 8 * (g + (lane & 1)) + 2 * (lane & 2);
+                rows[n] = r;
+                there[n] = valid[e] && col < p.dim;
+                to[n] = reinterpret_cast<float4*>(dst[e] + 4 * col);
+              }
+              if (it.j0 > 0) {   // four reads at a time: more spill, fewer wait in turn
+                float4 was[4];
+#pragma unroll
+                for (int n = 0; n < 4; ++n) was[n] = there[n] ? *to[n] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int n = 0; n < 4; ++n)
+                  rows[n] = make_float4(fmaf(was[n].x, keep[e], rows[n].x), fmaf(was[n].y, keep[e], rows[n].y),
+                                        fmaf(was[n].z, keep[e], rows[n].z), fmaf(was[n].w, keep[e], rows[n].w));
+              }
+#pragma unroll
+              for (int n = 0; n < 4; ++n)
+                if (there[n]) *to[n] = rows[n];
+            }
           }
         }
       }
