@@ -11,7 +11,7 @@
 //
 // What bounds it: HBM.  Every row is read and written once; the angles of a token are computed
 // once per CTA, into shared memory, and kept in registers over the rows of the token: a group of 64
-// threads works on one token, thread = (16-byte pair of segments in the row, row), so that the
+// threads works on one token, thread = (pair of 16-byte segments in the row, row), so that the
 // same frequencies serve all rows a thread meets.  V rows go through the same loop with no turn.  Three
 // rows a thread are in flight, the first of them asked for before the angles are computed, and three CTAs
 // an SM fit (two rows and four CTAs: 36.9 us for the first case below; four rows 44; one kind of row
@@ -90,39 +90,49 @@ __device__ __forceinline__ float2 turn_of(const RotaryParams& p, int t, int i) {
   return make_float2(v.x * p.scale, v.y * p.scale);
 }
 
-template <typename Src>
-struct Seg;   // 16 bytes of a row
-template <>
-struct Seg<float> {
-  static constexpr int E = 4;
-  static __device__ __forceinline__ void unpack(const uint4& v, float* x) { decode16<F32>(v, x); }
-  static __device__ __forceinline__ uint4 pack(const float* x) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
-                      __float_as_uint(x[3]));
-  }
+// 4 N bytes of a row.
+template <int N>
+struct alignas(4 * N) Words {
+  uint32_t w[N];
 };
-template <>
-struct Seg<__nv_bfloat16> {
-  static constexpr int E = 8;
-  static __device__ __forceinline__ void unpack(const uint4& v, float* x) { decode16<BF16>(v, x); }
-  static __device__ __forceinline__ uint32_t two(float a, float b) {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t*>(&h);
+
+template <typename Src, int N>
+struct Seg {
+  static constexpr int E = 4 * N / static_cast<int>(sizeof(Src));
+  static __device__ __forceinline__ void unpack(const Words<N>& v, float* x) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (sizeof(Src) == 2) {
+        x[2 * i] = __uint_as_float(v.w[i] << 16);
+        x[2 * i + 1] = __uint_as_float(v.w[i] & 0xFFFF0000u);
+      } else {
+        x[i] = __uint_as_float(v.w[i]);
+      }
+    }
   }
-  static __device__ __forceinline__ uint4 pack(const float* x) {
-    return make_uint4(two(x[0], x[1]), two(x[2], x[3]), two(x[4], x[5]), two(x[6], x[7]));
+  static __device__ __forceinline__ Words<N> pack(const float* x) {
+    Words<N> v;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if constexpr (sizeof(Src) == 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        v.w[i] = *reinterpret_cast<const uint32_t*>(&h);
+      } else {
+        v.w[i] = __float_as_uint(x[i]);
+      }
+    }
+    return v;
   }
 };
 
-// Codes of N float32 values x / s.
-template <typename Q, int N>
-__device__ __forceinline__ void codes(const float* x, float s, float neg_r, bool plain,
-                                      uint32_t* w) {
+// Codes of E float32 values x / s.
+template <typename Q, int E>
+__device__ __forceinline__ void codes(const float* x, float s, float neg_r, bool plain, uint32_t* w) {
 #pragma unroll
-  for (int i = 0; i < N / 4; ++i) {
-    float q[4];
+  for (int i = 0; i < (E + 3) / 4; ++i) {
+    float q[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int e = 0; e < 4; e += 2) {
+    for (int e = 0; e < 4 && 4 * i + e < E; e += 2) {
       float2 v;
       if (plain)
         v = quotient2(make_float2(-x[4 * i + e], -x[4 * i + e + 1]), make_float2(s, s), make_float2(neg_r, neg_r));
@@ -134,22 +144,31 @@ __device__ __forceinline__ void codes(const float* x, float s, float neg_r, bool
     w[i] = quant4<Q>(q);
   }
 }
+template <int E>
+__device__ __forceinline__ void put_codes(uint8_t* dst, const uint32_t* w) {
+  if constexpr (E == 8)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  else if constexpr (E == 4)
+    *reinterpret_cast<uint32_t*>(dst) = w[0];
+  else
+    *reinterpret_cast<uint16_t*>(dst) = static_cast<uint16_t>(w[0]);
+}
 
 // The largest |element| of two segments, as a float32's bits, at least; infinities and NaN are larger
 // than any.
-template <typename Src>
-__device__ __forceinline__ uint32_t top_of(const uint4& a, const uint4& b) {
-  const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+template <typename Src, int N>
+__device__ __forceinline__ uint32_t top_of(const Words<N>& a, const Words<N>& b) {
   if constexpr (sizeof(Src) == 2) {
-    __nv_bfloat162 t = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
+    __nv_bfloat162 t = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&a.w[0]));
 #pragma unroll
-    for (int i = 1; i < 8; ++i) t = __hmax2_nan(t, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+    for (int i = 1; i < 2 * N; ++i)
+      t = __hmax2_nan(t, __habs2(*reinterpret_cast<const __nv_bfloat162*>(i < N ? &a.w[i] : &b.w[i - N])));
     const uint32_t m = *reinterpret_cast<const uint32_t*>(&t) & 0x7FFF7FFFu;
     return max(m << 16, m & 0x7FFF0000u);
   } else {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+    for (int i = 0; i < N; ++i) m = max(m, max(a.w[i] & 0x7FFFFFFFu, b.w[i] & 0x7FFFFFFFu));
     return m;
   }
 }
@@ -157,22 +176,23 @@ __device__ __forceinline__ uint32_t top_of(const uint4& a, const uint4& b) {
 // A pair of segments to the cache, in its type: x at element `at` + a, y (where there is one) at `at` + b.
 // `top`: top_of() the source's segments, which the turned ones exceed by |scale| sqrt(2) at most.
 // Q: the codes' type; Src: the rows' own.
-template <typename Src, typename Q>
+template <typename Src, typename Q, int N>
 __device__ __forceinline__ void to_cache(const RotaryParams& p, void* cache, const float* scales, int head,
                                          int64_t at, int a, int b, bool has_b, uint32_t top, const float* x,
                                          const float* y) {
-  constexpr int E = Seg<Src>::E;
+  using S = Seg<Src, N>;
+  constexpr int E = S::E;
   if constexpr (std::is_same_v<Src, Q>) {
     Src* dst = static_cast<Src*>(cache) + at;
-    *reinterpret_cast<uint4*>(dst + a) = Seg<Src>::pack(x);
-    if (has_b) *reinterpret_cast<uint4*>(dst + b) = Seg<Src>::pack(y);
+    *reinterpret_cast<Words<N>*>(dst + a) = S::pack(x);
+    if (has_b) *reinterpret_cast<Words<N>*>(dst + b) = S::pack(y);
   } else {
     const float s = __ldg(scales + head);
     // quotient2's range: scales from 2^-64 to 2^64 and elements below 2^60 (|scale| up to 2^29, elements of
     // the source below 2^30)
     const bool plain = top < 0x4E800000u && p.small_scale && s >= 5.421010862427522e-20f && s <= 18446744073709551616.f;
     uint8_t* dst = static_cast<uint8_t*>(cache) + at;
-    uint32_t wx[E / 4], wy[E / 4];   // both segments' quotients run side by side
+    uint32_t wx[(E + 3) / 4], wy[(E + 3) / 4];   // both segments' quotients run side by side
     if (__builtin_expect(plain, 1)) {
       const float neg_r = -__frcp_rn(s);
       codes<Q, E>(x, s, neg_r, true, wx);
@@ -181,21 +201,16 @@ __device__ __forceinline__ void to_cache(const RotaryParams& p, void* cache, con
       codes<Q, E>(x, s, 0.f, false, wx);
       codes<Q, E>(y, s, 0.f, false, wy);
     }
-    if constexpr (E == 8) {
-      *reinterpret_cast<uint2*>(dst + a) = make_uint2(wx[0], wx[1]);
-      if (has_b) *reinterpret_cast<uint2*>(dst + b) = make_uint2(wy[0], wy[1]);
-    } else {
-      *reinterpret_cast<uint32_t*>(dst + a) = wx[0];
-      if (has_b) *reinterpret_cast<uint32_t*>(dst + b) = wy[0];
-    }
+    put_codes<E>(dst + a, wx);
+    if (has_b) put_codes<E>(dst + b, wy);
   }
 }
 
-// Rows whose halves (or whose whole, with neighbouring pairs) are multiples of 16 bytes.  Q: the cache's
+// Rows whose halves (or whose whole, with neighbouring pairs) are multiples of 4 N bytes.  Q: the cache's
 // type where it is one of codes, else Src (a cache of the rows' own type, or none).
-template <typename Src, bool ADJ, typename Q>
+template <typename Src, bool ADJ, typename Q, int N>
 __global__ void __launch_bounds__(kRoThreads, kRoCtas) rotary_kernel(const __grid_constant__ RotaryParams p) {
-  using S = Seg<Src>;
+  using S = Seg<Src, N>;
   constexpr int E = S::E;
   extern __shared__ float2 cs[];   // [kRoTokens][E][turned units]: (cos, sin)
   const int half = p.rot / 2, tid = threadIdx.x;
@@ -218,7 +233,7 @@ __global__ void __launch_bounds__(kRoThreads, kRoCtas) rotary_kernel(const __gri
   const int rows = p.hq + (p.kind ? 2 : 1) * p.hkv;
   const int r1 = min(rows, (static_cast<int>(blockIdx.y) + 1) * p.rows_per_y);
   int r = t < p.tokens && lane < lanes ? blockIdx.y * p.rows_per_y + lane : r1;
-  uint4 va[kRoBatch], vb[kRoBatch];
+  Words<N> va[kRoBatch], vb[kRoBatch];
   auto load = [&] {
 #pragma unroll
     for (int n = 0; n < kRoBatch; ++n) {
@@ -228,8 +243,8 @@ __global__ void __launch_bounds__(kRoThreads, kRoCtas) rotary_kernel(const __gri
                        : row < p.hq + p.hkv
                            ? static_cast<const Src*>(p.k) + t * p.k_ts + (row - p.hq) * p.k_hs
                            : static_cast<const Src*>(p.v) + t * p.v_ts + (row - p.hq - p.hkv) * p.v_hs;
-      va[n] = *reinterpret_cast<const uint4*>(src + a);
-      vb[n] = has_b ? *reinterpret_cast<const uint4*>(src + b) : make_uint4(0u, 0u, 0u, 0u);
+      va[n] = *reinterpret_cast<const Words<N>*>(src + a);
+      vb[n] = has_b ? *reinterpret_cast<const Words<N>*>(src + b) : Words<N>{};
     }
   };
   grid_dependency_wait();
@@ -291,13 +306,13 @@ __global__ void __launch_bounds__(kRoThreads, kRoCtas) rotary_kernel(const __gri
       else if (!is_v && p.k_out)
         dst = static_cast<Src*>(p.k_out) + t * p.ko_ts + head * p.ko_hs;
       if (dst) {
-        *reinterpret_cast<uint4*>(dst + a) = S::pack(x);
-        if (has_b) *reinterpret_cast<uint4*>(dst + b) = S::pack(y);
+        *reinterpret_cast<Words<N>*>(dst + a) = S::pack(x);
+        if (has_b) *reinterpret_cast<Words<N>*>(dst + b) = S::pack(y);
       }
       if (!is_q && append) {
         const int64_t at = (slot * p.hkv + head) * p.dim;
-        to_cache<Src, Q>(p, is_v ? p.v_cache : p.k_cache, is_v ? p.v_scale : p.k_scale, head, at, a, b, has_b,
-                         std::is_same_v<Src, Q> ? 0u : top_of<Src>(va[n], vb[n]), x, y);
+        to_cache<Src, Q, N>(p, is_v ? p.v_cache : p.k_cache, is_v ? p.v_scale : p.k_scale, head, at, a, b, has_b,
+                         std::is_same_v<Src, Q> ? 0u : top_of<Src, N>(va[n], vb[n]), x, y);
       }
     }
     r += lanes * kRoBatch;
@@ -448,19 +463,22 @@ extern "C" pkv_status rotary_and_cache(const pkv_rotary_args* args, pkv_stream_t
   p.small_scale = std::fabs(a.scale) <= 536870912.f;
 
   const int rows = p.hq + (cached ? 2 : 1) * p.hkv;
-  const int E = 16 / static_cast<int>(es);
   const int half = p.rot / 2;
-  // 16-byte loads: every segment of every row begins on a 16-byte boundary, and pairs of segments
-  // turn together
-  const bool wide =
-      aligned_to(p.q, 16) && aligned_to(p.k, 16) && (!cached || aligned_to(p.v, 16)) &&
-      aligned_to(p.q_out, 16) && aligned_to(p.k_out, 16) && p.dim % E == 0 &&
-      (p.adjacent || half % E == 0) &&
-      (p.hq == 0 || multiple({p.q_ts, p.q_hs, p.qo_ts, p.qo_hs}, E)) && multiple({p.k_ts, p.k_hs}, E) &&
-      (!p.k_out || multiple({p.ko_ts, p.ko_hs}, E)) && (!cached || multiple({p.v_ts, p.v_hs}, E));
-  p.units = p.adjacent ? (p.dim + 2 * E - 1) / (2 * E) : half / E + (p.dim - p.rot + 2 * E - 1) / (2 * E);
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
-  if (wide && p.units <= kRoGroup) {
+  // Loads of 4 n bytes: every segment of every row begins on such a boundary, and pairs of segments
+  // turn together.  16 bytes where they will do; halves of 20 dims, as 40 of 80 have, take 8 (8,192 tokens
+  // of 32 + 8 heads of 80, bf16: 26 us, 146 element by element, as what is left goes).
+  for (int n = 4; n >= 2; n -= 2) {
+    const int E = 4 * n / static_cast<int>(es);
+    const unsigned bytes = 4u * n;
+    const bool wide =
+        aligned_to(p.q, bytes) && aligned_to(p.k, bytes) && (!cached || aligned_to(p.v, bytes)) &&
+        aligned_to(p.q_out, bytes) && aligned_to(p.k_out, bytes) && p.dim % E == 0 &&
+        (p.adjacent || half % E == 0) &&
+        (p.hq == 0 || multiple({p.q_ts, p.q_hs, p.qo_ts, p.qo_hs}, E)) && multiple({p.k_ts, p.k_hs}, E) &&
+        (!p.k_out || multiple({p.ko_ts, p.ko_hs}, E)) && (!cached || multiple({p.v_ts, p.v_hs}, E));
+    p.units = p.adjacent ? (p.dim + 2 * E - 1) / (2 * E) : half / E + (p.dim - p.rot + 2 * E - 1) / (2 * E);
+    if (!wide || p.units > kRoGroup) continue;
     const int lanes = kRoGroup / p.units, groups = (p.tokens + kRoTokens - 1) / kRoTokens;
     // few tokens: their rows are shared out among CTAs, no thread taking more than one at a time
     int ys = 1;
@@ -472,15 +490,20 @@ extern "C" pkv_status rotary_and_cache(const pkv_rotary_args* args, pkv_stream_t
     const size_t smem = sizeof(float2) * kRoTokens * tu * E;
     const dim3 grid(groups, ys);
     auto launch = [&](auto kernel) { return cuda_status(launch_pdl(kernel, grid, dim3(kRoThreads), smem, st, p)); };
-    auto of = [&](auto src, auto adj) {
+    auto of = [&](auto src, auto adj, auto words) {
       using Src = decltype(src);
       constexpr bool A = decltype(adj)::value;
-      return kind == 2   ? launch(rotary_kernel<Src, A, FP8>)
-             : kind == 3 ? launch(rotary_kernel<Src, A, INT8>)
-                         : launch(rotary_kernel<Src, A, Src>);
+      constexpr int N = decltype(words)::value;
+      return kind == 2   ? launch(rotary_kernel<Src, A, FP8, N>)
+             : kind == 3 ? launch(rotary_kernel<Src, A, INT8, N>)
+                         : launch(rotary_kernel<Src, A, Src, N>);
     };
-    if (a.src_dtype == PKV_F32) return p.adjacent ? of(float{}, std::true_type{}) : of(float{}, std::false_type{});
-    return p.adjacent ? of(__nv_bfloat16{}, std::true_type{}) : of(__nv_bfloat16{}, std::false_type{});
+    auto with = [&](auto words) {
+      if (a.src_dtype == PKV_F32)
+        return p.adjacent ? of(float{}, std::true_type{}, words) : of(float{}, std::false_type{}, words);
+      return p.adjacent ? of(__nv_bfloat16{}, std::true_type{}, words) : of(__nv_bfloat16{}, std::false_type{}, words);
+    };
+    return n == 4 ? with(std::integral_constant<int, 4>{}) : with(std::integral_constant<int, 2>{});
   }
   const int64_t work = static_cast<int64_t>(p.tokens) * rows * (p.dim - half);
   const int64_t want = (work + kRoThreads - 1) / kRoThreads, cap = static_cast<int64_t>(device_sm_count()) * 16;

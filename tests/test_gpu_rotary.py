@@ -321,3 +321,14 @@ def test_slots_past_32_bits(lib, kv):
     for big, few in ((k_cache, small[0]), (v_cache, small[1])):
         at = slots - (nb - 3) * bs
         assert torch.equal(big[-3:].view(-1, hkv, dim)[at], few.view(-1, hkv, dim)[at])
+
+
+@pytest.mark.parametrize("kv", ["", "same", "fp8", "int8"])
+@pytest.mark.parametrize("dim,rot", [(80, 40), (20, 8), (36, 28), (84, 84), (100, 48), (60, 0), (6, 4), (512, 8)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("adjacent", [False, True])
+def test_halves_of_few_dims(lib, kv, dim, rot, dtype, adjacent):
+    """Halves, heads and strides that are multiples of 8 bytes, or of less, and not of 16."""
+    import torch
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    run(lib, dim + rot, 19, 5, 3, dim, rot, dt, kv, adjacent=adjacent, keep_k=True)
