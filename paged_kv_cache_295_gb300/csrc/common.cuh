@@ -17,11 +17,6 @@ namespace pkv {
 
 constexpr int kElemBytes[4] = {4, 2, 1, 1};
 
-// Whether two ranges of bytes have one in common.
-inline bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && na && nb && x < y + nb && y < x + na;
-}
 inline int elem_bytes(int32_t dt) { return (dt >= 0 && dt <= 3) ? kElemBytes[dt] : 0; }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

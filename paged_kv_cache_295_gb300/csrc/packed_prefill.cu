@@ -3,6 +3,7 @@
 #include <cmath>
 
 #include "packed_prefill.cuh"
+#include "ranges.cuh"
 #include "tmap.cuh"
 
 namespace pkv {

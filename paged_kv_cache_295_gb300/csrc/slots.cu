@@ -17,6 +17,7 @@
 // Measured: 8 sequences of one token 3.6 us, 512 of them 4.2 us, 64 prompts and chunks of up to 2,047 tokens
 // (66,000 rows) 4.9 us.
 #include "common.cuh"
+#include "ranges.cuh"
 
 namespace pkv {
 namespace {
