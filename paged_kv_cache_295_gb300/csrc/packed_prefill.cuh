@@ -43,9 +43,9 @@
 // fall together), with and without turns; prefetches of the next item to L2 (16 prompts of 512 tokens 77
 // -> 90 us); the order of items kept within sequences whose keys fit L2; lists of equal length for both tiles; the halves as a loop (20 % slower); Q before K.
 //
-// Measured: three prompts of 700 to 8,192 tokens, 32 heads on 8, causal 460 to 477 us (1,510 to 1,570
-// TFLOP/s; float32 output 706); 16 prompts of 512 tokens, 32 heads 64.5 us (float32 output 80); 11 images of 64 to 1,156 patches, 16 heads of 80, not
-// causal 45 us; nine chunks of up to 1,500 tokens behind 333 keys, 16 heads on 2 of 64, window 1,024,
+// Measured: three prompts of 700 to 8,192 tokens, 32 heads on 8, causal 460 to 480 us (1,500 to 1,570
+// TFLOP/s; float32 output 706); 16 prompts of 512 tokens, 32 heads 65 us (float32 output 80); 11 images of 64 to 1,156 patches, 16 heads of 80, not
+// causal 46 to 47 us; nine chunks of up to 1,500 tokens behind 333 keys, 16 heads on 2 of 64, window 1,024,
 // float32 output 45 us; four prompts of up to 60 tokens 9.2 us.
 //
 // Every wait is bounded (2 s) and gives up when another role has given up; copies in flight are then
