@@ -76,7 +76,7 @@ def packed(q, k, v, q_start, k_start, scale, causal=True, window=0, sinks=0):
     out, mag = np.full(q.shape, np.nan), np.zeros(q.shape)
     reach, seen = np.zeros(q.shape[:2]), np.zeros(q.shape[0], dtype=np.int64)
     for s in range(len(q_start) - 1):
-        a, b, c0, c1 = q_start[s], q_start[s + 1], k_start[s], k_start[s + 1]
+        a, b, c0, c1 = (int(x) for x in (q_start[s], q_start[s + 1], k_start[s], k_start[s + 1]))
         n, c = b - a, c1 - c0
         j = np.arange(c)
         for i in range(n):

@@ -1,5 +1,6 @@
 // packed_attention_prefill: argument checks, tensor maps and the launch of the tcgen05 kernel over
 // packed prompts.
+#include <algorithm>
 #include <cmath>
 
 #include "packed_prefill.cuh"
@@ -87,7 +88,9 @@ extern "C" pkv_status packed_attention_prefill(const pkv_packed_prefill_args* ar
   p.num_seqs = a.num_seqs, p.num_tokens = a.num_tokens, p.num_keys = a.num_keys;
   p.num_q_heads = a.num_q_heads, p.num_kv_heads = a.num_kv_heads, p.dim = a.head_dim;
   p.tile_tokens = kPkRows / G;
-  p.causal = a.causal, p.window = a.window, p.sinks = a.sinks;
+  // A window past all keys hides none, and one of that size does: position - window, of a query before
+  // every key too (-2^30 at the least), stays within 32 bits.
+  p.causal = a.causal, p.window = std::min(a.window, std::max(a.num_keys, 1)), p.sinks = a.sinks;
   p.scale_log2 = a.scale * 1.4426950408889634f;
   p.test_stall_bytes = test_stall_bytes();
 

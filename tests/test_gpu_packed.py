@@ -111,6 +111,17 @@ def test_every_item_under_a_window(lib, window, group):
         check(lib, q, k, v, starts(lens), None if more is None else starts(more), 0.1, "bf16", window=window, sinks=3)
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 200, 2 ** 30 + 3])
+@pytest.mark.parametrize("sinks", [0, 4, 2 ** 31 - 1])
+@pytest.mark.parametrize("group", [1, 8])
+def test_largest_windows_over_fewer_keys_than_queries(lib, window, sinks, group):
+    """A window that hides nothing, where position - window of the first queries is below -2^31."""
+    lens, keys = [10, 300, 5, 400, 64], [5, 150, 5, 1, 500]
+    q, k, v = inputs(group, sum(lens), sum(keys), 2 * group, 2, 64)
+    for out_type in ("bf16", "f32"):
+        check(lib, q, k, v, starts(lens), starts(keys), 0.1, out_type, window=window, sinks=sinks)
+
+
 def test_many_sequences_under_a_window(lib):
     rng = np.random.default_rng(4)
     lens = rng.integers(0, 4, 1500)
