@@ -763,6 +763,11 @@ typedef struct {
 
 pkv_status packed_attention_prefill(const pkv_packed_prefill_args* args, pkv_stream_t stream);
 
+/* Host: what packed_attention_prefill refuses of these arguments, without a launch - for callers
+ * that write something else first (the cache) and would rather not have half of a step done.  No
+ * pointer is followed. */
+pkv_status packed_attention_prefill_check(const pkv_packed_prefill_args* args);
+
 /* ------------------------------------------------------------------------ */
 /* CUDA-graph decode step with batch-size buckets and padding.               */
 /* ------------------------------------------------------------------------ */

@@ -159,6 +159,7 @@ _SIGS = {
     "rotary_and_cache": (I32, [C.POINTER(_RotaryArgs), P]),
     "rotary_turns": (I32, [P, I32, P]),
     "packed_attention_prefill": (I32, [C.POINTER(_PackedPrefillArgs), P]),
+    "packed_attention_prefill_check": (I32, [C.POINTER(_PackedPrefillArgs)]),
     "pkv_test_force_decode_kernel": (I32, [I32]),
     "pkv_test_decode_stall": (I32, [C.c_uint32]),
     "pkv_copy_kernel": (I32, [P, P, SZ, P]),
@@ -853,8 +854,17 @@ def packed_attention_prefill(q, k, v, query_start, scale, key_start=None, causal
         with _on_stream(stream, q):
             return packed_attention_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks,
                                             out, out_dtype, device_status)
+    return _packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks, out, out_dtype,
+                           device_status, True)
+
+
+def _packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks, out, out_dtype, device_status,
+                    launch):
+    """``packed_attention_prefill`` on the current stream; without ``launch`` only its checks: returns the
+    output that the call with these arguments would write."""
     return _done((_ext or _binding()).packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks,
-                                           out, out_dtype, device_status), "packed_attention_prefill")
+                                                     out, out_dtype, device_status, launch),
+                 "packed_attention_prefill")
 
 
 def copy_blocks(pool_tensor, pairs, device_status=None, stream=None):

@@ -595,9 +595,9 @@ PyObject* do_rotary(PyObject* const* a, Py_ssize_t na) {
 }
 
 // packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks, out, out_dtype,
-//                device_status) -> out or status
+//                device_status, launch) -> out or status; without launch only the checks
 PyObject* do_packed(PyObject* const* a, Py_ssize_t na) {
-  arity(na, 12);
+  arity(na, 13);
   const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"),
                &qs = tensor(a[3], "query_start"), &ks = tensor(a[5], "key_start", true),
                &st = status_word(a[11]);
@@ -610,6 +610,7 @@ PyObject* do_packed(PyObject* const* a, Py_ssize_t na) {
   p.causal = truth(a[6], "causal");
   p.window = integer32(a[7], "window");
   p.sinks = integer32(a[8], "sinks");
+  const bool launch = truth(a[12], "launch");
   const at::Device dev = cuda_device(q);
   const c10::cuda::CUDAGuard guard(dev);
   want_rows(q, "q", T, hq, dim, at::kBFloat16, dev);
@@ -648,7 +649,7 @@ PyObject* do_packed(PyObject* const* a, Py_ssize_t na) {
   const pkv_stream_t stream = stream_of(dev);
   pkv_status r;
   Py_BEGIN_ALLOW_THREADS
-  r = packed_attention_prefill(&p, stream);
+  r = launch ? packed_attention_prefill(&p, stream) : packed_attention_prefill_check(&p);
   Py_END_ALLOW_THREADS
   if (r != PKV_OK) return status(r);
   return THPVariable_Wrap(std::move(out));

@@ -37,13 +37,14 @@ bool stride_ok(int64_t stride, int64_t count) {
   return count <= 1 || (stride > 0 && stride % 8 == 0 && stride < kMaxStride);
 }
 
-}  // namespace
-}  // namespace pkv
+// Items of a call at most: a sequence's last pair of query tiles may be short.
+int64_t units_of(const pkv_packed_prefill_args& a) {
+  const int pair = 2 * (kPkRows / (a.num_q_heads / a.num_kv_heads));
+  return ((static_cast<int64_t>(a.num_tokens) + pair - 1) / pair + a.num_seqs) * a.num_kv_heads;
+}
 
-extern "C" pkv_status packed_attention_prefill(const pkv_packed_prefill_args* args, pkv_stream_t stream) {
-  using namespace pkv;
-  if (!args) return PKV_ERR_INVALID_ARG;
-  const pkv_packed_prefill_args& a = *args;
+// What packed_attention_prefill refuses.
+pkv_status refusal(const pkv_packed_prefill_args& a) {
   if (a.num_seqs < 0 || a.num_tokens < 0 || a.num_keys < 0 || a.num_q_heads <= 0 || a.num_kv_heads <= 0 ||
       a.head_dim <= 0 || a.window < 0 || a.sinks < 0 || (a.causal != 0 && a.causal != 1) ||
       a.num_q_heads % a.num_kv_heads != 0 || !std::isfinite(a.scale))
@@ -80,6 +81,25 @@ extern "C" pkv_status packed_attention_prefill(const pkv_packed_prefill_args* ar
       overlap(a.out, out_bytes, a.query_start, starts) || overlap(a.out, out_bytes, a.key_start, starts))
     return PKV_ERR_INVALID_ARG;
 
+  // the items are counted in 32 bits
+  if (units_of(a) > INT32_MAX / 2) return PKV_ERR_UNSUPPORTED;
+  return PKV_OK;
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" pkv_status packed_attention_prefill_check(const pkv_packed_prefill_args* args) {
+  return args ? pkv::refusal(*args) : PKV_ERR_INVALID_ARG;
+}
+
+extern "C" pkv_status packed_attention_prefill(const pkv_packed_prefill_args* args, pkv_stream_t stream) {
+  using namespace pkv;
+  const pkv_status refused = packed_attention_prefill_check(args);
+  if (refused != PKV_OK) return refused;
+  const pkv_packed_prefill_args& a = *args;
+  if (a.num_seqs == 0 || a.num_tokens == 0) return PKV_OK;
+  const int G = a.num_q_heads / a.num_kv_heads;
   PackedParams p{};
   p.out = a.out;
   p.query_start = a.query_start;
@@ -105,11 +125,7 @@ extern "C" pkv_status packed_attention_prefill(const pkv_packed_prefill_args* ar
       !rows_map(&tv, v, a.head_dim, a.num_kv_heads, keys, a.v_head_stride, a.v_token_stride, 1, kPkKeys))
     return PKV_ERR_CUDA;
 
-  // no more CTAs than items: a sequence's last pair may be short
-  const int64_t units =
-      ((static_cast<int64_t>(a.num_tokens) + 2 * p.tile_tokens - 1) / (2 * p.tile_tokens) + a.num_seqs) *
-      a.num_kv_heads;
-  if (units > INT32_MAX / 2) return PKV_ERR_UNSUPPORTED;   // the items are counted in 32 bits
+  const int64_t units = units_of(a);   // no more CTAs than items
   const int64_t sms = device_sm_count();
   const dim3 grid(static_cast<unsigned>(units < sms ? units : sms));
   auto launch = [&](auto kern, size_t smem) {

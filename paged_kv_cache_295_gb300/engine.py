@@ -14,7 +14,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (BF16, F32, FP8_E4M3, INT8, Pool, copy_blocks, gather_cache, packed_attention_prefill,
+from . import (BF16, F32, FP8_E4M3, INT8, Pool, _on_stream, _packed_prefill, copy_blocks, gather_cache,
                paged_attention_decode, paged_attention_decode_append, paged_attention_prefill,
                quantize_and_cache, reshape_and_cache, rotary_and_cache, slots_from_lengths,
                swap_blocks, workspace_bytes)
@@ -129,13 +129,20 @@ class PagedKVCache:
         positions, the append, and causal attention over the packed rows.  ``slots`` as
         ``self.slots`` gives them for this step; rows of the output behind the last sequence are not
         written.  bfloat16 rows, head_dim a multiple of 8 up to 128."""
-        if q.dtype != _torch().bfloat16 or self.head_dim > 128 or self.head_dim % 8:
+        if stream is not None:
+            with _on_stream(stream, q):
+                return self.prompt(layer, q, k, v, positions, rotary, slots, window, sinks, out, out_dtype,
+                                   device_status)
+        torch = _torch()
+        if q.dtype != torch.bfloat16 or self.head_dim > 128 or self.head_dim % 8:
             raise ValueError("prompt takes bfloat16 rows and a head_dim that is a multiple of 8 up to 128")
-        q, k = self.append_rotary(layer, q, k, v, positions, rotary, slots.slot_mapping, keep_k=True,
-                                  device_status=device_status, stream=stream)
-        return packed_attention_prefill(q, k, v, slots.query_start, self.scale, window=window,
-                                        sinks=sinks, out=out, out_dtype=out_dtype,
-                                        device_status=device_status, stream=stream)
+        # what the attention refuses is known before the append: a refused prompt writes nothing
+        turned = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k)]
+        args = (*turned, v, slots.query_start, self.scale, None, True, window, sinks)
+        out = _packed_prefill(*args, out, out_dtype, device_status, False)
+        self.append_rotary(layer, q, k, v, positions, rotary, slots.slot_mapping, *turned,
+                           device_status=device_status)
+        return _packed_prefill(*args, out, out_dtype, device_status, True)
 
     def gather(self, layer, block_tables, row_start, num_rows, max_rows, first_pos=None,
                out_dtype=None, k_out=None, v_out=None, device_status=None, stream=None):

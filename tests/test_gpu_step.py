@@ -225,3 +225,43 @@ def test_a_prompt_that_is_refused_appends_nothing(lib):
     with pytest.raises(ValueError):
         cache.prompt(0, q, k, k, sl.positions, lib.Rotary(64), sl)
     assert not cache.k_cache(0).any()
+
+
+def test_every_refusal_of_a_prompt_comes_before_its_append(lib):
+    """What the rotary call would take and the attention refuses: neither cache is written."""
+    import torch
+    from paged_kv_cache_295_gb300.engine import PagedKVCache
+    T, i32 = 5, dict(dtype=torch.int32, device="cuda")
+    cache = PagedKVCache(num_layers=1, num_kv_heads=2, head_dim=64, block_size=16, num_blocks=4, kv_dtype=lib.BF16)
+    cache.storage.zero_()
+    sl = cache.slots(torch.zeros((1, 4), **i32), torch.zeros(1, **i32), torch.full((1,), T, **i32),
+                     torch.arange(4, **i32), T)
+    rows = dict(dtype=torch.bfloat16, device="cuda")
+    q, k, v = (torch.ones((T, h, 64), **rows) for h in (4, 2, 2))
+    off = torch.ones(T * 2 * 64 + 1, **rows)[1:].view(T, 2, 64)          # on no 16-byte boundary
+    odd = torch.ones((T, 2, 68), **rows)[..., :64]                       # strides of 68
+    over = torch.ones((T, 4, 64), **rows)
+    plan, done = lib.Rotary(64), dict(out_dtype=torch.bfloat16)
+
+    def call(q=q, v=v, sl=sl, **kw):
+        return cache.prompt(0, q, k, v, sl.positions, plan, sl, **kw)
+
+    for kw in (dict(window=-1), dict(sinks=4), dict(window=8, sinks=-1), dict(window="x"), dict(window=2 ** 31),
+               dict(out=over[:4]), dict(out=over.double()), dict(out=over.half()), dict(out=over.cpu()),
+               dict(out=over.transpose(0, 1)), dict(out=over, out_dtype=torch.float32), dict(out_dtype=torch.float16),
+               dict(v=over[:, 2:], out=over), dict(v=off), dict(v=odd), dict(sl=sl._replace(query_start=None)),
+               dict(sl=sl._replace(query_start=sl.query_start.long())), dict(q=torch.ones((T, 3, 64), **rows)),
+               dict(q=torch.ones((T, 2 * 129, 64), **rows)), dict(q=q[:4]), dict(v=v[:, :1]),
+               dict(device_status=torch.zeros(1, device="cuda"))):
+        for stream in (None, torch.cuda.Stream()):
+            with pytest.raises((ValueError, lib.PagedKVError)):
+                call(stream=stream, **kw)
+            torch.cuda.synchronize()
+            assert not cache.storage.any(), kw
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    out = call(stream=side, **done)
+    side.synchronize()
+    assert torch.equal(out, torch.ones_like(out))     # every v is 1
+    assert torch.equal(cache.v_cache(0).flatten(0, 1)[:T], v) and cache.k_cache(0).flatten(0, 1)[:T].any()
+    assert call(out=over, **done) is over or torch.equal(over, out)

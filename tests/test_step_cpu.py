@@ -107,6 +107,30 @@ def test_packed_refusals(lib, kw, want):
     assert lib.library().packed_attention_prefill(None, None) == INVALID
 
 
+def test_packed_check(lib):
+    """The check alone answers as the call does, without a launch: these arguments are taken."""
+    a = dict(q=at(0), k=at(0x10000), v=at(0x20000), out=at(0x30000), query_start=at(0x100000), num_seqs=2,
+             num_tokens=8, num_keys=8, num_q_heads=4, num_kv_heads=2, head_dim=64, scale=0.1, causal=1, q_dtype=1,
+             kv_dtype=1, out_dtype=1)
+    for n in ("q", "k", "v"):
+        a[f"{n}_token_stride"], a[f"{n}_head_stride"] = 256, 64
+
+    def check(**kw):
+        b = {n: v.value if isinstance(v, C.c_void_p) else v for n, v in {**a, **kw}.items()}
+        return lib.library().packed_attention_prefill_check(C.byref(lib._PackedPrefillArgs(**b)))
+
+    for kw in ({}, dict(out_dtype=0), dict(window=2 ** 31 - 1, sinks=2 ** 31 - 1), dict(causal=0),
+               dict(key_start=at(0x110000), num_keys=3), dict(num_seqs=0, q=None), dict(num_q_heads=256)):
+        assert check(**kw) == OK, kw
+    for kw in (dict(window=-1), dict(sinks=1), dict(out=at(0)), dict(v=at(8)), dict(num_keys=9),
+               dict(v_token_stride=260), dict(window=4, causal=0)):
+        assert check(**kw) == INVALID, kw
+    for kw in (dict(num_q_heads=258), dict(head_dim=136), dict(out_dtype=2), dict(num_tokens=2 ** 30 + 1),
+               dict(num_seqs=2 ** 24, num_q_heads=128, num_kv_heads=64)):
+        assert check(**kw) == UNSUPPORTED, kw
+    assert lib.library().packed_attention_prefill_check(None) == INVALID
+
+
 @pytest.mark.parametrize("kw", [
     dict(out=at(0)), dict(out=at(0x10000)), dict(out=at(0x20000 - 0xFF0)), dict(out=at(0x20000 + 7 * 512 + 240)),
     dict(out=at(0x40000 - 0xFF0)), dict(key_start=at(0x30FFC)),
