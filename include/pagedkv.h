@@ -685,7 +685,8 @@ pkv_status slots_from_lengths(int32_t* block_tables, const int32_t* context_lens
  *                  reshape_and_cache (k_scale and v_scale [num_kv_heads]); a token with a
  *                  negative slot is not appended.  k_cache NULL: no append.  Slots are distinct.
  * Any head_dim and even rotary_dim <= head_dim; 16- or 8-byte loads where pointers, strides
- * and rotary_dim allow them, else element by element.  Outputs do not overlap inputs other than as said. */
+ * and rotary_dim allow them, else element by element.  INVALID_ARG where an output (q_out, k_out, the
+ * caches) has a byte in common with another one or with an input, but for rows turned in place. */
 typedef struct {
   const void* q;
   const void* k;

@@ -829,7 +829,7 @@ def rotary_and_cache(q, k, v, positions, rotary, slot_mapping=None, k_cache=None
 
     ``positions``: int32 ``[T]``, or ``[axes, T]`` for a ``rotary`` with several axes.  ``q``, ``k``
     and ``v`` may be parts of one projection's rows, and ``q_out`` and ``k_out`` ``q`` and ``k``
-    themselves.  Without ``k_cache`` nothing is appended (``v`` may be None).  8-bit caches take
+    themselves; outputs that overlap anything else are refused.  Without ``k_cache`` nothing is appended (``v`` may be None).  8-bit caches take
     ``k_scale`` / ``v_scale`` ``[Hkv]``; for scales per block keep ``k`` and append it with
     ``quantize_and_cache``."""
     if stream is not None:

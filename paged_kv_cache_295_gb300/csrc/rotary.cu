@@ -26,6 +26,7 @@
 #include <type_traits>
 
 #include "quant.cuh"
+#include "ranges.cuh"
 
 namespace pkv {
 namespace {
@@ -396,6 +397,33 @@ bool multiple(std::initializer_list<int64_t> xs, int64_t n) {
 }
 bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
+// Whether what a call writes overlaps something else that it reads or writes, but for rows turned in place.
+bool outputs_overlap(const pkv_rotary_args& a, bool cached, bool codes) {
+  const int64_t es = elem_bytes(a.src_dtype), T = a.num_tokens;
+  auto rows = [&](const void* base, int32_t heads, int64_t ts, int64_t hs) {
+    return Rows(base, T, heads, Wide{ts} * es, Wide{hs} * es, a.head_dim * es);
+  };
+  const Rows q = rows(a.q, a.num_q_heads, a.q_token_stride, a.q_head_stride);
+  const Rows k = rows(a.k, a.num_kv_heads, a.k_token_stride, a.k_head_stride);
+  const Rows v = rows(cached ? a.v : nullptr, a.num_kv_heads, a.v_token_stride, a.v_head_stride);
+  const Rows qo = rows(a.q_out, a.num_q_heads, a.q_out_token_stride, a.q_out_head_stride);
+  const Rows ko = rows(a.k_out, a.num_kv_heads, a.k_out_token_stride, a.k_out_head_stride);
+  const int64_t cache = cached ? a.num_blocks * a.block_size * a.num_kv_heads * a.head_dim * elem_bytes(a.cache_dtype) : 0;
+  const Rows kc(a.k_cache, cache), vc(a.v_cache, cache);
+  if ((meet(qo, q) && !(qo == q)) || (meet(ko, k) && !(ko == k))) return true;
+  if (meet(qo, k) || meet(qo, v) || meet(qo, ko) || meet(ko, q) || meet(ko, v) || meet(kc, vc)) return true;
+  for (const Rows* c : {&kc, &vc})
+    for (const Rows* x : {&q, &k, &v, &qo, &ko})
+      if (meet(*c, *x)) return true;
+  const int64_t half = a.rotary_dim / 2, scales = codes ? 4 * int64_t{a.num_kv_heads} : 0;
+  for (const Rows& x : {Rows(a.turns, 8 * half), Rows(a.axis, 4 * half), Rows(a.positions, 4 * T * a.num_axes),
+                        Rows(cached ? a.slot_mapping : nullptr, 8 * T), Rows(a.k_scale, scales),
+                        Rows(a.v_scale, scales), Rows(a.device_status, 4)})
+    for (const Rows* w : {&qo, &ko, &kc, &vc})
+      if (meet(x, *w)) return true;
+  return false;
+}
+
 }  // namespace
 }  // namespace pkv
 
@@ -431,6 +459,8 @@ extern "C" pkv_status rotary_and_cache(const pkv_rotary_args* args, pkv_stream_t
   }
   if (a.num_q_heads > (1 << 20) || a.num_kv_heads > (1 << 20) || a.head_dim > (1 << 20))
     return PKV_ERR_UNSUPPORTED;
+  if (cached && a.num_blocks * a.block_size > INT64_MAX / (int64_t{a.num_kv_heads} * a.head_dim * 4))
+    return PKV_ERR_UNSUPPORTED;   // a cache's bytes
   if (a.num_tokens == 0) return PKV_OK;
   const unsigned es = static_cast<unsigned>(elem_bytes(a.src_dtype));
   if ((a.num_q_heads > 0 && (!a.q || !a.q_out)) || !a.k || (!cached && !a.k_out) ||
@@ -445,6 +475,7 @@ extern "C" pkv_status rotary_and_cache(const pkv_rotary_args* args, pkv_stream_t
     if (!aligned_to(ptr, 4)) return PKV_ERR_INVALID_ARG;
   if (!aligned_to(a.turns, 8) || !aligned_to(a.slot_mapping, 8)) return PKV_ERR_INVALID_ARG;
   if (cached && (!aligned_to(a.k_cache, 16) || !aligned_to(a.v_cache, 16))) return PKV_ERR_INVALID_ARG;
+  if (outputs_overlap(a, cached, kind >= 2)) return PKV_ERR_INVALID_ARG;
 
   RotaryParams p{};
   p.q = a.q, p.k = a.k, p.v = a.v, p.q_out = a.q_out, p.k_out = a.k_out;

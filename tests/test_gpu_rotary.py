@@ -332,3 +332,53 @@ def test_halves_of_few_dims(lib, kv, dim, rot, dtype, adjacent):
     import torch
     dt = torch.bfloat16 if dtype == "bf16" else torch.float32
     run(lib, dim + rot, 19, 5, 3, dim, rot, dt, kv, adjacent=adjacent, keep_k=True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_outputs_that_overlap_inputs(lib, dtype):
+    """Rows turned in place, parts of one projection's rows between others and parts of each head are taken; an
+    output over another input, a cache or the other output is refused and nothing is written."""
+    import torch
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    T, D, plan = 9, 64, lib.Rotary(64)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    slots = torch.arange(T, device="cuda")
+    pool = torch.zeros((2, 3, 4, 2, D), device="cuda", dtype=dt)
+
+    def call(q, k, v, **kw):
+        return lib.rotary_and_cache(q, k, v, pos, plan, slots, pool[0], pool[1], **kw)
+
+    def views(layout):
+        x = torch.randn((T, 2, 3, D) if layout == "heads" else (T, 6, D), device="cuda").to(dt)
+        if layout == "heads":        # q, k and v of a head side by side
+            return x, x[:, :, 0], x[:, :, 1], x[:, :, 2]
+        return x, x[:, :2], x[:, 2:4], x[:, 4:]
+
+    for layout in ("heads", "rows"):
+        x, q, k, v = views(layout)
+        want = call(q, k, v, keep_k=True)
+        caches = pool.clone()
+        for places in (dict(q_out=q, k_out=k), dict(q_out=q), dict(k_out=k)):
+            y = x.clone()
+            q2, k2, v2 = (y[:, :, i] for i in range(3)) if layout == "heads" else (y[:, :2], y[:, 2:4], y[:, 4:])
+            pool.zero_()
+            got = call(q2, k2, v2, keep_k=True, **{n: q2 if n == "q_out" else k2 for n in places})
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+            assert torch.equal(v2, v) and torch.equal(pool, caches)
+        # the rows of this step within those of a longer one
+        room = torch.zeros((T, 12, D), device="cuda", dtype=dt)
+        got = call(room[:, 2:4].copy_(q), room[:, 6:8].copy_(k), room[:, 10:12].copy_(v), q_out=room[:, :2],
+                   k_out=room[:, 8:10])
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+        x, q, k, v = views(layout)
+        before, pool_before = x.clone(), pool.clone()
+        own = torch.empty((T, 2, D), device="cuda", dtype=dt)
+        for kw in (dict(q_out=k), dict(q_out=v), dict(k_out=q), dict(k_out=v), dict(q_out=own, k_out=own),
+                   dict(k_out=pool[0].view(-1, 2, D)[:T]), dict(q_out=pool[1].view(-1, 2, D)[1:T + 1])):
+            with pytest.raises((ValueError, lib.PagedKVError)):
+                call(q, k, v, **kw)
+        with pytest.raises((ValueError, lib.PagedKVError)):
+            lib.rotary_and_cache(q, k, v, pos, plan, slots, pool[0], pool[0])
+        torch.cuda.synchronize()
+        assert torch.equal(x, before) and torch.equal(pool, pool_before)

@@ -2,6 +2,8 @@
 before a launch), the frequencies of rotary positions, and pins of the oracle."""
 import ctypes as C
 import math
+import os
+import subprocess
 
 import numpy as np
 import pytest
@@ -77,6 +79,85 @@ def rotary(lib, **kw):
 def test_rotary_refusals(lib, kw, want):
     assert rotary(lib, **kw) == want
     assert lib.library().rotary_and_cache(None, None) == INVALID
+
+
+def apart(**kw):
+    """Arguments whose arrays lie apart: 4 tokens of 4 + 2 + 2 heads of 64 in one projection's bf16 rows."""
+    a = dict(q=at(0), k=at(512), v=at(768), q_out=at(0x10000), k_out=at(0x20000), turns=at(0x30000),
+             positions=at(0x31000), slot_mapping=at(0x32000), k_cache=at(0x40000), v_cache=at(0x50000),
+             axis=at(0x33000), q_token_stride=512, k_token_stride=512, v_token_stride=512,
+             q_out_token_stride=256, k_out_token_stride=128)
+    return {**a, **kw}
+
+
+@pytest.mark.parametrize("kw", [
+    dict(q_out=at(2)), dict(q_out=at(512)), dict(q_out=at(512 - 126)), dict(q_out=at(768)), dict(k_out=at(768)),
+    dict(q_out=at(0), q_out_token_stride=520), dict(q_out=at(0)), dict(k_out=at(0)), dict(k_out=at(512)),
+    dict(k_out=at(512 + 128), k_out_token_stride=512), dict(k_out=at(512 - 2), k_out_token_stride=512),
+    dict(q_out=at(1024 - 128), q_out_token_stride=512), dict(q_out=at(0x10000), k_out=at(0x10000 + 2048 - 2)),
+    dict(v_cache=at(0x40000)), dict(v_cache=at(0x40000 + 16 * 4 * 256 - 16)), dict(k_cache=at(0x10000 - 0x3FF0)),
+    dict(q_out=at(0x40000 - 2046)), dict(k_out=at(0x50000 + 16 * 4 * 256 - 2)), dict(k=at(0x40000)),
+    dict(q_out=at(0x30000 - 2046)), dict(q_out=at(0x30000 + 32 * 8 - 4)), dict(q_out=at(0x31000 + 12)),
+    dict(k_out=at(0x32000 + 28)), dict(q_out=at(0x33000 + 32 * 4 - 4)), dict(device_status=at(0x40004)),
+    dict(cache_dtype=2, k_scale=at(0x34000), v_scale=at(0x35000), k_out=at(0x34004)),
+    dict(cache_dtype=2, k_scale=at(0x34000), v_scale=at(0x50000)), dict(src_dtype=0, cache_dtype=0, q_out=at(0x20000 - 4092))])
+def test_rotary_outputs_overlap_nothing(lib, kw):
+    """By one element or aligned unit, from either side; in place only where it is the same rows."""
+    assert rotary(lib, **apart(**kw)) == INVALID
+
+
+def test_rotary_cache_bytes(lib):
+    assert rotary(lib, **apart(num_blocks=1 << 52, num_kv_heads=1 << 20)) == UNSUPPORTED
+
+
+def test_rows_that_meet(tmp_path):
+    """The check of strided rows against every byte of them, and its answer where strides are huge."""
+    src = tmp_path / "meet.cpp"
+    src.write_text('''
+#include "ranges.cuh"
+extern "C" int meets(const long long* x, const long long* y, int budget) {
+  auto of = [](const long long* a) {
+    return pkv::Rows(reinterpret_cast<const void*>(a[0]), a[1], a[2], a[3], a[4], a[5]);
+  };
+  return pkv::meet(of(x), of(y), budget);
+}
+''')
+    so = tmp_path / "meet.so"
+    csrc = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "paged_kv_cache_295_gb300", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-Werror", "-shared", "-fPIC", f"-I{csrc}", str(src), "-o", str(so)],
+                   check=True)
+    fn = C.CDLL(str(so)).meets
+
+    def meets(x, y, budget=4096):
+        return fn((C.c_longlong * 6)(*x), (C.c_longlong * 6)(*y), budget)
+
+    rng = np.random.default_rng(0)
+    seen = [0, 0]
+    for trial in range(6000):
+        sets = []
+        for _ in range(2):
+            rows, heads, n = (int(z) for z in rng.integers(1, (6, 5, 9)))
+            ts, hs = (int(z) for z in rng.integers(-40, 120, 2))
+            if trial % 2 and sets:
+                ts, hs = sets[0][3:5]
+            sets.append((int(rng.integers(2000, 2300)), rows, heads, ts, hs, n))
+        byte = [{b + i * ts + j * hs + e for i in range(r) for j in range(h) for e in range(n)}
+                for b, r, h, ts, hs, n in sets]
+        want = int(bool(byte[0] & byte[1]))
+        assert meets(*sets) == want, sets
+        assert meets(*sets, 1) >= want
+        seen[want] += 1
+    assert min(seen) > 1000
+    far = (4096, 2 ** 31 - 1, 2 ** 20, 2 ** 62, 2 ** 62 - 1, 4096)
+    assert meets(far, (4096 + 4095, 1, 1, 0, 0, 1)) and not meets(far, (4096 + 4096, 1, 1, 0, 0, 1))
+    qkv = 10240 * 2       # 8,192 tokens of 32 + 4 + 4 heads of 256 bytes, and the three parts of each head
+    parts = [(1 << 30, 8192, 32, qkv // 2, 256, 256), ((1 << 30) + 8192, 8192, 4, qkv // 2, 256, 256)]
+    assert not meets(*parts, 8) and meets(parts[0], ((1 << 30) + 8191, *parts[1][1:]), 8)
+    parts = [((1 << 30) + 256 * i, 8192, 32, 32 * 768, 768, 256) for i in range(3)]
+    assert not meets(parts[0], parts[1], 8) and not meets(parts[2], parts[0], 8)
+    assert meets(parts[0], (parts[1][0] - 1, *parts[1][1:]), 8)
+    for none in ((0, 4, 4, 64, 64, 64), (4096, 0, 4, 64, 64, 64), (4096, 4, 4, 64, 64, 0)):
+        assert not meets(none, (4096, 4, 4, 64, 64, 64))
 
 
 def packed(lib, **kw):
