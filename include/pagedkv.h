@@ -737,8 +737,10 @@ pkv_status rotary_turns(const double* inv_freq, int32_t n, uint64_t* turns);
  *   out          : device [num_tokens, num_q_heads, head_dim] contiguous, out_dtype f32 or bf16;
  *                  a query that sees nothing gets 0; rows outside every sequence are not written.
  * out[t, h, :] = softmax(scale * q . K_g^T) V_g over the visible keys, g = h / G, accumulated in
- * float32.  The weights enter P V as two bf16 parts (2^-17 of each weight) for a float32 output and
- * as one (2^-9 of each weight, as the output's own rounding) for a bf16 one.
+ * float32.  The weights enter P V as two bf16 parts (2^-17 of each weight), so that a bf16 output is
+ * the float32 one rounded.
+ *   weight_parts : 0 or 2 - as said; 1 - one part (2^-9 of each weight, as a bf16 output's own
+ *                  rounding) in half the product's time, for a bf16 output alone.
  * A key that a query does not see, but another one of its work tile (128 rows) does, has
  * weight 0 there; a V value of it that is not finite gives NaN.  Keys of other sequences and rows
  * outside every sequence have no influence, whatever they hold.  out overlaps no input.
@@ -759,6 +761,7 @@ typedef struct {
   float scale;
   int32_t causal, window, sinks;
   int32_t q_dtype, kv_dtype, out_dtype;
+  int32_t weight_parts;
   int32_t* device_status;
 } pkv_packed_prefill_args;
 

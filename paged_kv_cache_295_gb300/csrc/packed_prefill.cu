@@ -2,6 +2,7 @@
 // packed prompts.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "packed_prefill.cuh"
 #include "ranges.cuh"
@@ -50,9 +51,11 @@ pkv_status refusal(const pkv_packed_prefill_args& a) {
       a.num_q_heads % a.num_kv_heads != 0 || !std::isfinite(a.scale))
     return PKV_ERR_INVALID_ARG;
   if ((a.window > 0 && !a.causal) || (a.sinks > 0 && a.window == 0)) return PKV_ERR_INVALID_ARG;
+  if (a.weight_parts < 0 || a.weight_parts > 2) return PKV_ERR_INVALID_ARG;
   const int G = a.num_q_heads / a.num_kv_heads;
   if (a.q_dtype != PKV_BF16 || a.kv_dtype != PKV_BF16 || (a.out_dtype != PKV_F32 && a.out_dtype != PKV_BF16))
     return PKV_ERR_UNSUPPORTED;
+  if (a.weight_parts == 1 && a.out_dtype != PKV_BF16) return PKV_ERR_UNSUPPORTED;
   if (a.head_dim > 128 || a.head_dim % 8 != 0 || G > kPkRows || a.num_seqs > (1 << 24) ||
       a.num_tokens > (1 << 30) || a.num_keys > (1 << 30) || a.num_q_heads > (1 << 16))
     return PKV_ERR_UNSUPPORTED;
@@ -133,10 +136,13 @@ extern "C" pkv_status packed_attention_prefill(const pkv_packed_prefill_args* ar
     return cuda_status(launch_pdl(kern, grid, dim3(kPkThreads), smem, reinterpret_cast<cudaStream_t>(stream), tq, tk,
                                   tv, p));
   };
-  const bool bf16 = a.out_dtype == PKV_BF16;
-  if (a.head_dim > 64)
-    return bf16 ? launch(packed_prefill_kernel<2, 4, false>, PkLayout<2, 4>::bytes())
-                      : launch(packed_prefill_kernel<2, 4, true>, PkLayout<2, 4>::bytes());
-  return bf16 ? launch(packed_prefill_kernel<1, 8, false>, PkLayout<1, 8>::bytes())
-                    : launch(packed_prefill_kernel<1, 8, true>, PkLayout<1, 8>::bytes());
+  auto of = [&](auto slabs, auto stages) {
+    constexpr int N = decltype(slabs)::value, ST = decltype(stages)::value;
+    const size_t smem = PkLayout<N, ST>::bytes();
+    return a.out_dtype == PKV_F32 ? launch(packed_prefill_kernel<N, ST, true, true>, smem)
+           : a.weight_parts == 1  ? launch(packed_prefill_kernel<N, ST, false, false>, smem)
+                                  : launch(packed_prefill_kernel<N, ST, false, true>, smem);
+  };
+  return a.head_dim > 64 ? of(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{})
+                         : of(std::integral_constant<int, 1>{}, std::integral_constant<int, 8>{});
 }

@@ -27,10 +27,10 @@
 // scaled; S_t(j) being there implies that PV_t(j-1) is done (one thread issues both), so the softmax
 // warps scale it themselves.
 //
-// Precision.  Scores, sums and O are float32.  A float32 output takes the weights as two bf16 parts (2^-17
-// of each at most), a bf16 one as one (2^-9): beside the output's own rounding that is 1.2 to 1.4 times the
-// error against 64 bits on normal values (2.0e-3 to 2.4e-3 of the norm for 1.6e-3), where a second part
-// would double the product's time.
+// Precision.  Scores, sums and O are float32, and the weights enter the product as two bf16 parts (2^-17 of
+// each at most): a bf16 output is the float32 one rounded.  A caller may ask for one part (2^-9 of each)
+// for a bf16 output: 1.2 to 1.4 times the error against 64 bits on normal values (2.0e-3 to 2.4e-3 of
+// the norm for 1.6e-3) and half the product's time.
 //
 // What bounds it.  At head_dim 128 the chain of a key tile: softmax 1,400 cycles, product and next scores
 // 770 of its 1,024 behind it, and about 450 until each sees that the other is done, with the other tile's
@@ -321,8 +321,8 @@ struct PkOrder {
   }
 };
 
-// LO: float32 output, the weights are two bf16 parts; else bf16 output, one part.
-template <int SLABS, int STAGES, bool LO>
+// F32: float32 output, else bf16.  LO: the weights are two bf16 parts, else one.
+template <int SLABS, int STAGES, bool F32, bool LO>
 __global__ void __launch_bounds__(kPkThreads, 1)
     packed_prefill_kernel(const __grid_constant__ CUtensorMap tmap_q,
                           const __grid_constant__ CUtensorMap tmap_k,
@@ -625,7 +625,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
       order.lane = lane;
       order.fill(0, blockIdx.x == 0);
       const uint32_t n = gridDim.x;
-      constexpr int kPart = LO ? kPkPart : INT32_MAX / 2;
+      constexpr int kPart = F32 ? kPkPart : INT32_MAX / 2;
       PkItem it = {};
       bool found = false;
       int at = 0;      // of the unit at hand: entries handed out, and all of them
@@ -705,7 +705,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
     const uint32_t g_inv = (65536u + G - 1) / G;   // row / G for row < 128: exact for G <= 128
     // raised to the smallest normal, so that a masked -inf stays -inf under it
     const float sl2 = fmaxf(fabsf(p.scale_log2), 1.17549435e-38f);
-    constexpr int esz = LO ? 4 : 2;
+    constexpr int esz = F32 ? 4 : 2;
     float m[2] = {-CUDART_INF_F, -CUDART_INF_F}, l[2] = {0.f, 0.f};   // references (in log2 units), sums
     float ref[2] = {0.f, 0.f};   // references in the part before
     uint32_t n_s = 0, n_o = 0;   // score tiles and items done
@@ -885,8 +885,8 @@ __global__ void __launch_bounds__(kPkThreads, 1)
           for (int e = 0; e < 2; ++e) {
             float sum = l[e] + __shfl_xor_sync(0xffffffffu, l[e], 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            inv[e] = !LO || it.ends(t) ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
-            if constexpr (LO) {   // the parts' references differ where the row's has moved
+            inv[e] = !F32 || it.ends(t) ? (sum > 0.f ? 1.f / sum : 0.f) : 1.f;
+            if constexpr (F32) {   // the parts' references differ where the row's has moved
               keep[e] = ref[e] == m[e] ? inv[e] : pf_ex2(ref[e] - m[e]) * inv[e];
               ref[e] = m[e];
             }
@@ -922,7 +922,7 @@ __global__ void __launch_bounds__(kPkThreads, 1)
           }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            if constexpr (!LO) {
+            if constexpr (!F32) {
               uint32_t w[8], x[8], y[8];   // column group g; then 2 (kept group) + source; then the lane's 32 bytes
 #pragma unroll
               for (int g = 0; g < 8; ++g) w[g] = pack_bf16(v[4 * g + 2 * e] * inv[e], v[4 * g + 2 * e + 1] * inv[e]);

@@ -124,7 +124,7 @@ class PagedKVCache:
                                 device_status=device_status, stream=stream)
 
     def prompt(self, layer, q, k, v, positions, rotary, slots, window=0, sinks=0, out=None,
-               out_dtype=None, device_status=None, stream=None):
+               out_dtype=None, device_status=None, stream=None, weight_parts=2):
         """One layer of a step over whole prompts (sequences with nothing cached before): rotary
         positions, the append, and causal attention over the packed rows.  ``slots`` as
         ``self.slots`` gives them for this step; rows of the output behind the last sequence are not
@@ -132,13 +132,13 @@ class PagedKVCache:
         if stream is not None:
             with _on_stream(stream, q):
                 return self.prompt(layer, q, k, v, positions, rotary, slots, window, sinks, out, out_dtype,
-                                   device_status)
+                                   device_status, weight_parts=weight_parts)
         torch = _torch()
         if q.dtype != torch.bfloat16 or self.head_dim > 128 or self.head_dim % 8:
             raise ValueError("prompt takes bfloat16 rows and a head_dim that is a multiple of 8 up to 128")
         # what the attention refuses is known before the append: a refused prompt writes nothing
         turned = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k)]
-        args = (*turned, v, slots.query_start, self.scale, None, True, window, sinks)
+        args = (*turned, v, slots.query_start, self.scale, None, True, window, sinks, weight_parts)
         out = _packed_prefill(*args, out, out_dtype, device_status, False)
         self.append_rotary(layer, q, k, v, positions, rotary, slots.slot_mapping, *turned,
                            device_status=device_status)

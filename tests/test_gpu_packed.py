@@ -384,3 +384,40 @@ def test_rows_past_32_bits(lib):
     alone = lib.packed_attention_prefill(a, k, v, torch.tensor([0, 50], dtype=torch.int32, device="cuda"), 0.09,
                                          out_dtype=torch.bfloat16)
     assert torch.equal(out[-50:], alone)
+
+
+@pytest.mark.parametrize("dim,group,hkv", [(128, 4, 2), (64, 8, 1), (80, 1, 3), (40, 3, 2), (128, 1, 2)])
+@pytest.mark.parametrize("kw", [{}, {"causal": False}, {"window": 150, "sinks": 3}])
+def test_bf16_outputs_are_the_float32_ones_rounded(lib, dim, group, hkv, kw):
+    """The same weights in two parts and the same sums (lists of up to seven key tiles: a float32 output takes
+    them in one go too), so the same float32 numbers, rounded once; with logits from small to large."""
+    import torch
+    lens, ahead = [130, 1, 600, 257, 33], [0, 200, 250, 0, 7]
+    keys = [x + y for x, y in zip(lens, ahead)]
+    for size in (0.2, 1.0, 5.0):
+        q, k, v = inputs(dim, sum(lens), sum(keys), group * hkv, hkv, dim, k_size=size)
+        qs, ks = (torch.from_numpy(starts(x)).cuda() for x in (lens, keys))
+
+        def call(dt, **more):
+            return lib.packed_attention_prefill(q, k, v, qs, dim ** -0.5, key_start=ks, out_dtype=dt, **kw, **more)
+
+        want = call(torch.float32)
+        assert torch.equal(call(torch.bfloat16), want.bfloat16())
+        assert torch.equal(call(torch.bfloat16, weight_parts=2), want.bfloat16())
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_one_weight_part(lib, dim):
+    """Asked for: weights off by up to 2^-8 of each, as the bound without a second part has it; a float32 output does
+    not take it."""
+    import torch
+    lens = [300, 1, 129]
+    q, k, v = inputs(3, sum(lens), sum(lens), 6, 2, dim, "fused")
+    one = check(lib, q, k, v, starts(lens), None, dim ** -0.5, "bf16", weight_parts=1)
+    two = check(lib, q, k, v, starts(lens), None, dim ** -0.5, "bf16")
+    assert not torch.equal(one, two)
+    qs = torch.from_numpy(starts(lens)).cuda()
+    for kw in (dict(weight_parts=1), dict(weight_parts=0), dict(weight_parts=3, out_dtype=torch.bfloat16),
+               dict(weight_parts="x"), dict(weight_parts=-1)):
+        with pytest.raises((ValueError, lib.PagedKVError)):
+            lib.packed_attention_prefill(q, k, v, qs, 0.1, **kw)

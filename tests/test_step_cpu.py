@@ -203,6 +203,12 @@ def test_packed_check(lib):
     for kw in ({}, dict(out_dtype=0), dict(window=2 ** 31 - 1, sinks=2 ** 31 - 1), dict(causal=0),
                dict(key_start=at(0x110000), num_keys=3), dict(num_seqs=0, q=None), dict(num_q_heads=256)):
         assert check(**kw) == OK, kw
+    for parts in (0, 1, 2):
+        assert check(weight_parts=parts) == OK
+    assert check(weight_parts=2, out_dtype=0) == OK and check(weight_parts=1, out_dtype=0) == UNSUPPORTED
+    assert check(weight_parts=3) == INVALID and check(weight_parts=-1) == INVALID
+    # as the C compiler lays the arguments out
+    assert lib._PackedPrefillArgs.device_status.offset == 152 and C.sizeof(lib._PackedPrefillArgs) == 160
     for kw in (dict(window=-1), dict(sinks=1), dict(out=at(0)), dict(v=at(8)), dict(num_keys=9),
                dict(v_token_stride=260), dict(window=4, causal=0)):
         assert check(**kw) == INVALID, kw
