@@ -66,12 +66,14 @@ constexpr int kPkSlab = 128 * 128;   // 128 rows of 64 bf16 (128-byte swizzle)
 // O is scaled for logits that grow by 16 from one key tile to another, where one of 8 has most
 // short prompts' second tiles scale it (a first row of few keys is enough), at 1,500 cycles.
 constexpr float kPkLag = 24.f;
-// Key tiles after which a float32 output takes O up.  The tensor cores cut every sum towards zero:
-// up to 2^-23 of O for each 16 keys and weight part, which adds up (20,000 keys in one go: 4.4e-5 of the
-// norm, and no end to it); 16 tiles are 256 such sums, 5.3e-6 of the norm however many there are (8 tiles:
-// 3.4e-6, and a fifth more time for the windowed chunks above, whose lists of up to 12 tiles then come in two parts).
-// In between the epilogue adds in float32, in the output's own rows.
-constexpr int kPkPart = 16;
+// Key tiles after which a float32 output takes O up.  The tensor cores cut their sums towards zero, half a
+// step of O's last place each time on average, which adds up with the keys: 8 tiles are 128 sums (8 of 16 keys a
+// tile, two weight parts) and 2.9e-6 of an output of one sign; measured 2.2e-6 to 2.8e-6, and 3.2e-6 to 3.6e-6 of
+// the norm for normal values, over 3,000 keys as over a million.  16 tiles are off by twice that (5.3e-6 to
+// 6.5e-6) and up to 8 % faster (three prompts to 8,192 tokens 706 us for 767).  In between the epilogue adds in float32,
+// in the output's own rows.  A bf16 output has no room for that in them and stays in the tensor cores to its end: 3e-4 of
+// the norm over 130,000 keys, 2.3e-3 over a million (5.1e-3 for values of one sign; its own rounding: 1.7e-3).
+constexpr int kPkPart = 8;
 
 struct PackedParams {
   void* out;                    // [T, Hq, D]

@@ -421,3 +421,24 @@ def test_one_weight_part(lib, dim):
                dict(weight_parts="x"), dict(weight_parts=-1)):
         with pytest.raises((ValueError, lib.PagedKVError)):
             lib.packed_attention_prefill(q, k, v, qs, 0.1, **kw)
+
+
+@pytest.mark.parametrize("dim,keys", [(64, 20000), (128, 9000), (128, 130000)])
+def test_sums_of_one_sign(lib, dim, keys):
+    """Values of one sign, so that O grows evenly while the tensor cores cut each of its sums.  A cut takes half a
+    step of the sum on average, and the steps are 2^-23 of their sum's binade: over a sum that grows from 0 they
+    average 1/3 to 3/8 of 2^-23 of its last size.  In the 8 key tiles that O is left in the tensor cores for there are 128
+    cuts (8 of 16 keys a tile, two weight parts): 128 2^-24 3/8 = 2.9e-6 of every output, however many keys there are.
+    The sums in float32 (156 to 1,016 tiles, 20 to 130 parts, both to nearest) add 2^-25 times the root of their number
+    over 3 at most, 0.6e-6.  The weights' parts are rounded to nearest and average out.  4e-6 leaves room for what is
+    cut of single products; twice as many sums, at 5.1e-6, do not pass."""
+    import torch
+    q, k, v = inputs(23, 130, keys, 2, 1, dim)
+    v = (1 + v.float().abs() / 8).bfloat16()
+    for causal in (True, False):
+        got = lib.packed_attention_prefill(q, k, v, torch.tensor([0, 130], dtype=torch.int32, device="cuda"), 0.1,
+                                           key_start=torch.tensor([0, keys], dtype=torch.int32, device="cuda"),
+                                           causal=causal)
+        for h in range(2):
+            want = long_reference(q[:, h], k[:, 0], v[:, 0], 0.1, causal)
+            assert ((got[:, h].double() - want).norm() / want.norm()).item() <= 4e-6
