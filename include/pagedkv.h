@@ -741,9 +741,11 @@ pkv_status rotary_turns(const double* inv_freq, int32_t n, uint64_t* turns);
  * the float32 one rounded.
  *   weight_parts : 0 or 2 - as said; 1 - one part (2^-9 of each weight, as a bf16 output's own
  *                  rounding) in half the product's time, for a bf16 output alone.
- * A key that a query does not see, but another one of its work tile (128 rows) does, has
- * weight 0 there; a V value of it that is not finite gives NaN.  Keys of other sequences and rows
- * outside every sequence have no influence, whatever they hold.  out overlaps no input.
+ * A key that a query does not see has weight 0, and no K value of it has an influence.  Queries are
+ * worked on in groups of 2 * floor(128 / G), counted from their sequence's first one, and keys in tiles of
+ * 128, counted likewise: a V value that is not finite may give NaN to the queries of a group one of
+ * which sees some key of its tile, and to no others.  Keys of other sequences and rows outside every sequence
+ * have no influence, whatever they hold.  out overlaps no input.
  * Supported: head_dim a multiple of 8 up to 128; G = num_q_heads / num_kv_heads <= 128; 16-byte
  * aligned q, k, v and out.  A bad start flags PKV_DEV_BAD_CONTEXT and skips its sequence. */
 typedef struct {

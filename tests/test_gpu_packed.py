@@ -442,3 +442,39 @@ def test_sums_of_one_sign(lib, dim, keys):
         for h in range(2):
             want = long_reference(q[:, h], k[:, 0], v[:, 0], 0.1, causal)
             assert ((got[:, h].double() - want).norm() / want.norm()).item() <= 4e-6
+
+
+@pytest.mark.parametrize("group,dim", [(8, 64), (3, 128), (1, 128), (100, 64)])
+@pytest.mark.parametrize("out_type", ["bf16", "f32"])
+def test_values_that_are_not_finite(lib, group, dim, out_type):
+    """A NaN or an infinity in V reaches the queries of those groups of 2 (128 / group) that see a key of its 128,
+    and one in K those that see it: no others, whatever order the tiles are worked on."""
+    import torch
+    lens, window, sinks = [20, 520, 33], 64, 3
+    q, k, v = inputs(group, sum(lens), sum(lens), group, 1, dim)
+    qs, dt = torch.from_numpy(starts(lens)).cuda(), torch.bfloat16 if out_type == "bf16" else torch.float32
+    i, per = np.arange(520), 2 * (128 // group)
+
+    def call(k, v, **kw):
+        return lib.packed_attention_prefill(q, k, v, qs, 0.1, out_dtype=dt, **kw)
+
+    for kw in ({}, dict(window=window), dict(window=window, sinks=sinks)):
+        sees = i <= i[:, None]
+        if kw:
+            sees &= (i > i[:, None] - window) | (i < kw.get("sinks", 0))
+        clean = call(k, v, **kw)
+        for at in (0, 100, 127, 128, 300, 519):
+            for bad in (float("nan"), float("inf")):
+                kb, vb = k.clone(), v.clone()
+                kb[20 + at] = bad
+                got = call(kb, v, **kw)
+                hit = torch.zeros(sum(lens), dtype=torch.bool, device="cuda")
+                hit[20:540] = torch.from_numpy(sees[:, at]).cuda()
+                assert torch.equal(got[~hit], clean[~hit]) and not torch.equal(got[hit], clean[hit])
+                vb[20 + at] = bad
+                got = call(k, vb, **kw)
+                tile = sees[:, at // 128 * 128:at // 128 * 128 + 128].any(1)
+                near = np.array([tile[n // per * per:n // per * per + per].any() for n in i])
+                assert not got[hit].isfinite().any()
+                hit[20:540] = torch.from_numpy(near).cuda()
+                assert torch.equal(got[~hit], clean[~hit])
