@@ -746,6 +746,9 @@ pkv_status rotary_turns(const double* inv_freq, int32_t n, uint64_t* turns);
  * 128, counted likewise: a V value that is not finite may give NaN to the queries of a group one of
  * which sees some key of its tile, and to no others.  Keys of other sequences and rows outside every sequence
  * have no influence, whatever they hold.  out overlaps no input.
+ * The tensor cores cut O's sums towards zero.  A float32 output is taken up every 1,024 keys and stays within
+ * 4e-6 of the norm of sums of one sign, however many keys there are; a bf16 one is not: 3e-4 of the norm over
+ * 130,000 keys, 2.3e-3 over a million (5.1e-3 for values of one sign), beside 1.7e-3 of its own rounding.
  * Supported: head_dim a multiple of 8 up to 128; G = num_q_heads / num_kv_heads <= 128; 16-byte
  * aligned q, k, v and out.  A bad start flags PKV_DEV_BAD_CONTEXT and skips its sequence. */
 typedef struct {

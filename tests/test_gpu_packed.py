@@ -478,3 +478,22 @@ def test_values_that_are_not_finite(lib, group, dim, out_type):
                 assert not got[hit].isfinite().any()
                 hit[20:540] = torch.from_numpy(near).cuda()
                 assert torch.equal(got[~hit], clean[~hit])
+
+
+@pytest.mark.parametrize("keys", [20000, 130000])
+def test_long_bf16(lib, keys):
+    """A bf16 output over long lists: its own rounding (2^-8 of a value at most) and the cut sums, which the tensor
+    cores keep to the end.  A key adds a sum of two parts; cut by half a step of a sum that averages half of the last
+    one, and of 16 products with two more bits each, keys / 16 4 2^-24 / 2 at most on average."""
+    import torch
+    q, k, v = inputs(24, 200, keys, 1, 1, 128)
+    for one_sign in (False, True):
+        if one_sign:
+            v = (1 + v.float().abs() / 8).bfloat16()
+        want = long_reference(q[:, 0], k[:, 0], v[:, 0], 0.1, True)
+        got = lib.packed_attention_prefill(q, k, v, torch.tensor([0, 200], dtype=torch.int32, device="cuda"), 0.1,
+                                           key_start=torch.tensor([0, keys], dtype=torch.int32, device="cuda"),
+                                           out_dtype=torch.bfloat16)
+        own = (want.bfloat16().double() - want).norm() / want.norm()
+        more = (got[:, 0].double() - want).norm() / want.norm()
+        assert more.item() <= own.item() + keys / 16 * 4 * 2.0 ** -25
