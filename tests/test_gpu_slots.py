@@ -194,3 +194,109 @@ def test_streams_and_arguments(lib):
                dict(free_next=torch.empty(1, dtype=torch.int32)), dict(row_per_sequence="x", query_start=dev([0] * 10))):
         with pytest.raises(ValueError):
             lib.slots_from_lengths(*args, **kw)
+
+
+def call_in_place(lib, tables, c, n, free, start, bs, T, nb, which, per_row=False):
+    """One call whose lengths, list start or both take the old ones' place, against the oracle."""
+    import torch
+    want = OS.slots(tables, c, n, free, start, bs, T, nb, per_row)
+    t, cd, fs, status = dev(tables), dev(c), dev([start]), torch.zeros(1, dtype=torch.int32, device="cuda")
+    kw = {}
+    if "lengths" in which:
+        kw["context_out"] = cd
+    if "start" in which:
+        kw["free_next"] = fs
+    got = lib.slots_from_lengths(t, cd, None if n is None else dev(n), dev(free), nb, bs, T, free_start=fs,
+                                 row_per_sequence=per_row, device_status=status, **kw)
+    assert int(status.item()) == sum(getattr(lib, FLAGS[f]) for f in want[6])
+    assert np.array_equal(t.cpu().numpy(), want[0])
+    assert np.array_equal(got.slot_mapping.cpu().numpy(), want[1])
+    assert np.array_equal(got.positions.cpu().numpy(), want[2])
+    if not per_row:
+        assert np.array_equal(got.query_start.cpu().numpy(), want[3])
+    assert np.array_equal(got.context_lens.cpu().numpy(), want[4])
+    assert got.free_start.tolist() == [want[5]]
+    assert cd.tolist() == (want[4] if "lengths" in which else np.asarray(c)).tolist()
+    assert fs.tolist() == [want[5] if "start" in which else start]
+    return want
+
+
+@pytest.mark.parametrize("which", [("lengths",), ("start",), ("lengths", "start")])
+@pytest.mark.parametrize("seqs,bs,ctx,new", [
+    (7, 16, 900, 1000), (40, 24, 300, 350), (64, 16, 2000, 2047), (1500, 16, 60, 4), (2500, 16, 90, 6),
+    (3100, 3, 40, 45)])
+def test_in_place_over_several_ctas(lib, which, seqs, bs, ctx, new):
+    """Prompts and chunks of 3,000 to 70,000 rows, which two, four or eight CTAs fill while the lengths and
+    the list's start that all of them read are written; up to four tiles of sequences; rows without a token."""
+    rng = np.random.default_rng(seqs)
+    tables, c, n, free, nb = batch(rng, seqs, bs, ctx, new)
+    T = int(n.sum())
+    assert T > 2048
+    for pad, start in ((0, 0), (5000, 3)):
+        want = call_in_place(lib, tables, c, n, free, start, bs, T + pad, nb, which)
+        assert not want[6] and (want[4] != c).any()
+
+
+@pytest.mark.parametrize("seqs", [2500, 9000, 20000])
+def test_decode_rows_in_place_over_several_ctas(lib, seqs):
+    rng = np.random.default_rng(seqs)
+    tables, c, n, free, nb = batch(rng, seqs, 16, 30, 1)
+    for T in (seqs, seqs + 99):
+        call_in_place(lib, tables, c, n, free, 0, 16, T, nb, ("lengths", "start"), per_row=True)
+    free = np.concatenate([free, nb + np.arange(seqs)])
+    call_in_place(lib, tables, c, None, free, 0, 16, seqs, nb + seqs, ("lengths", "start"), per_row=True)
+
+
+@pytest.mark.parametrize("seqs,new", [(60, 200), (1700, 8)])
+def test_all_or_nothing_in_place_over_several_ctas(lib, seqs, new):
+    """Too few blocks or rows: no CTA writes a table, the lengths and the list's start stay; bad sequences among good
+    ones; nothing to do."""
+    rng = np.random.default_rng(seqs)
+    tables, c, n, free, nb = batch(rng, seqs, 16, 90, new)
+    need, T = int(np.maximum(-(-(c + n) // 16) - -(-c // 16), 0).sum()), int(n.sum())
+    assert T > 4096
+    both = ("lengths", "start")
+    for f, start, rows, flag in ((free[:need - 1], 0, T, "free"), (free, len(free) - need + 1, T, "free"),
+                                 (free, -1, T, "free"), (free, 0, T - 1, "context")):
+        want = call_in_place(lib, tables, c, n, f, start, 16, rows, nb, both)
+        assert want[6] == {flag} and np.array_equal(want[4], c)
+    assert not call_in_place(lib, tables, c, n, free[:need], 0, 16, T, nb, both)[6]
+    assert not call_in_place(lib, tables, c, 0 * n, free[:0], 0, 16, 5000, nb, both)[6]
+    c2, n2 = c.copy(), n.copy()
+    c2[[3, seqs - 1]], n2[5] = (-1, 10 ** 9), -4
+    assert "context" in call_in_place(lib, tables, c2, n2, free, 0, 16, T, nb, both)[6]
+
+
+def test_captured_prompts_in_place(lib):
+    """A captured step of 9,000 rows, replayed with new lengths: every replay goes on from the last one."""
+    import torch
+    rng = np.random.default_rng(8)
+    seqs, T, bs = 90, 9000, 16
+    tables = np.full((seqs, 160), -1, dtype=np.int32)
+    free = rng.permutation(6000).astype(np.int32)
+    c, at = np.zeros(seqs, dtype=np.int32), 0
+    t, cd, fd, start, nd = dev(tables), dev(c), dev(free), dev([0]), dev(c)
+    kw = {"slot_mapping": torch.empty(T, dtype=torch.int64, device="cuda"),
+          "positions": torch.empty(T, dtype=torch.int32, device="cuda"),
+          "query_start": torch.empty(seqs + 1, dtype=torch.int32, device="cuda")}
+
+    def step():
+        lib.slots_from_lengths(t, cd, nd, fd, 6000, bs, T, free_start=start, context_out=cd, free_next=start, **kw)
+
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        step()                             # no new tokens: loads the kernel
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=side):
+        step()
+    for _ in range(12):
+        n = rng.integers(0, 100, seqs).astype(np.int32)
+        nd.copy_(dev(n))
+        g.replay()
+        torch.cuda.synchronize()
+        tables, slot, pos, qs, c, at, flags = OS.slots(tables, c, n, free, at, bs, T, 6000)
+        assert not flags
+        for name, x in (("slot_mapping", slot), ("positions", pos), ("query_start", qs)):
+            assert np.array_equal(kw[name].cpu().numpy(), x)
+        assert np.array_equal(t.cpu().numpy(), tables) and np.array_equal(cd.cpu().numpy(), c)
+        assert start.tolist() == [at]
