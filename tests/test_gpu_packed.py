@@ -497,3 +497,102 @@ def test_long_bf16(lib, keys):
         own = (want.bfloat16().double() - want).norm() / want.norm()
         more = (got[:, 0].double() - want).norm() / want.norm()
         assert more.item() <= own.item() + keys / 16 * 4 * 2.0 ** -25
+
+
+def gpu_reference(q, k, v, qs, ks, scale, causal=True, window=0, sinks=0):
+    """float64 on the GPU: (out, A = sum p |v|, the most of sum |q k| over visible keys), by sequence and head."""
+    import torch
+    out, mag = (torch.zeros(q.shape, dtype=torch.float64, device="cuda") for _ in range(2))
+    reach = torch.zeros(q.shape[:2], dtype=torch.float64, device="cuda")
+    group = q.shape[1] // k.shape[1]
+    for a, b, c0, c1 in zip(qs[:-1], qs[1:], ks[:-1], ks[1:]):
+        n, c = int(b - a), int(c1 - c0)
+        place = torch.arange(c - n, c, device="cuda")[:, None]
+        j = torch.arange(c, device="cuda")
+        sees = torch.ones((n, c), dtype=torch.bool, device="cuda")
+        if causal:
+            sees = j <= place
+            if window:
+                sees &= (j > place - window) | (j < sinks)
+        for h in range(q.shape[1]):
+            x, y, w = (z.double() for z in (q[a:b, h], k[c0:c1, h // group], v[c0:c1, h // group]))
+            z = (x @ y.t() * float(np.float32(scale))).masked_fill(~sees, -torch.inf)
+            p = torch.softmax(z, -1).nan_to_num(0.0)      # rows that see nothing
+            out[a:b, h], mag[a:b, h] = p @ w, p @ w.abs()
+            reach[a:b, h] = (x.abs() @ y.abs().t()).masked_fill(~sees, 0.0).amax(-1)
+    return out, mag, reach
+
+
+def check_parts(lib, q, k, v, lens, keys, scale, **kw):
+    """Every element of a float32 output of long lists, and the same call's again."""
+    import torch
+    qs, ks = starts(lens), starts(keys)
+    args = (q, k, v, torch.from_numpy(qs).cuda(), scale)
+    out = torch.full(q.shape, 77.0, device="cuda")
+    lib.packed_attention_prefill(*args, key_start=torch.from_numpy(ks).cuda(), out=out, **kw)
+    want, mag, reach = (x.cpu().numpy() for x in gpu_reference(q, k, v, qs, ks, scale, **kw))
+    # the bound's sums are a float32 step for each 16 keys: a list's parts are as exact as one list of 1,024 keys and a step
+    # for each part more
+    e = PC.attention_bound(BF16, None, want, mag, reach, scale, False, False, True, 1024 + max(keys) // 64)
+    y = out.double().cpu().numpy()
+    assert (np.abs(y - want) <= e).all(), (np.abs(y - want) / e).max()
+    again = lib.packed_attention_prefill(*args, key_start=torch.from_numpy(ks).cuda(), **kw)
+    assert torch.equal(out, again)
+    return out
+
+
+@pytest.mark.parametrize("keys", [1024, 1025, 1152, 2048, 2049, 2176, 3200, 4097])
+@pytest.mark.parametrize("causal", [True, False])
+def test_parts_that_end_at_a_tile(lib, keys, causal):
+    """Lists that fill parts of 8 key tiles, or one key or tile more; a pair whose first tile ends there and
+    whose second goes on."""
+    for n in (129, 256):
+        q, k, v = inputs(keys + n, n, keys, 2, 1, 64)
+        check_parts(lib, q, k, v, [n], [keys], 0.125, causal=causal)
+
+
+@pytest.mark.parametrize("group,hkv,dim", [(3, 2, 128), (8, 1, 64), (1, 2, 80), (40, 1, 128), (128, 1, 64)])
+@pytest.mark.parametrize("kw", [{}, {"window": 2500, "sinks": 200}, {"window": 1100}, {"causal": False}])
+def test_parts_of_grouped_heads(lib, group, hkv, dim, kw):
+    """Several parts to a list under grouped heads, windows (whose lists skip key tiles) and sinks of more than a tile;
+    sequences of one part beside them, and rows that see nothing."""
+    lens, keys = [70, 3, 130, 1, 40], [4300, 3, 2700, 1500, 10]
+    q, k, v = inputs(group, sum(lens), sum(keys), group * hkv, hkv, dim)
+    check_parts(lib, q, k, v, lens, keys, dim ** -0.5, **kw)
+
+
+@pytest.mark.parametrize("order", ["rising", "falling", "both"])
+@pytest.mark.parametrize("kw", [{}, {"causal": False}, {"window": 1500, "sinks": 129}])
+def test_parts_whose_references_move(lib, order, kw):
+    """Logits that grow or shrink by far more than 2^24 from part to part: what earlier parts left is scaled, or
+    what later ones add vanishes; rows of either kind beside rows whose logits stay."""
+    import torch
+    n, keys = 300, 4600
+    q, k, v = inputs(31, n, keys, 2, 1, 64)
+    step = 1 + (torch.arange(keys, device="cuda") // 512).double()
+    if order == "falling":
+        step = step.flip(0)
+    if order == "both":
+        step = torch.minimum(step, step.flip(0)) ** 2
+    k[:, 0, :32] = (k[:, 0, :32].double().abs() * step[:, None] / 2).bfloat16()
+    q[:, 0, :32] = q[:, 0, :32].abs()
+    q[:, 1, :32] *= 0.01                              # the other head's logits hardly move
+    q[1::3, 0, :32] *= -1                             # rows whose logits go the other way
+    check_parts(lib, q, k, v, [n], [keys], 1.0, **kw)
+
+
+def test_more_items_of_several_parts_than_ctas(lib):
+    """Items of two to five parts, three and more to a CTA, in sequences of all lengths."""
+    lens, ahead = [1500, 40, 700, 3, 260], [300, 2100, 1500, 4500, 0]
+    q, k, v = inputs(32, sum(lens), sum(lens) + sum(ahead), 32, 16, 64)
+    check_parts(lib, q, k, v, lens, [x + y for x, y in zip(lens, ahead)], 0.125)
+
+
+def test_a_first_part_that_is_masked_whole(lib):
+    """Sinks and a window far behind them: rows of an early position see keys of a later part alone, or of the first
+    one alone."""
+    lens, keys = [1300, 900], [1300, 4000]
+    q, k, v = inputs(33, sum(lens), sum(keys), 8, 1, 64)
+    for kw in (dict(window=1, sinks=1100), dict(window=1030, sinks=1), dict(window=1500, sinks=0),
+               dict(window=300, sinks=1030)):
+        check_parts(lib, q, k, v, lens, keys, 0.125, **kw)
