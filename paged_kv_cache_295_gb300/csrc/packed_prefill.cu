@@ -67,7 +67,7 @@ pkv_status refusal(const pkv_packed_prefill_args& a) {
   if (!a.q || !a.out || !a.query_start || (a.num_keys > 0 && (!a.k || !a.v))) return PKV_ERR_INVALID_ARG;
   if (!a.key_start && a.num_keys != a.num_tokens) return PKV_ERR_INVALID_ARG;
   if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.out) || !aligned4(a.query_start) ||
-      !aligned4(a.key_start))
+      !aligned4(a.key_start) || !aligned4(a.device_status))
     return PKV_ERR_INVALID_ARG;
 
   // from the first element to the last one

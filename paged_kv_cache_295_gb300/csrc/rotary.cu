@@ -471,7 +471,8 @@ extern "C" pkv_status rotary_and_cache(const pkv_rotary_args* args, pkv_stream_t
   for (const void* ptr : {a.q, a.k, a.v, static_cast<const void*>(a.q_out), static_cast<const void*>(a.k_out)})
     if (!aligned_to(ptr, es)) return PKV_ERR_INVALID_ARG;
   for (const void* ptr : {static_cast<const void*>(a.axis), static_cast<const void*>(a.positions),
-                          static_cast<const void*>(a.k_scale), static_cast<const void*>(a.v_scale)})
+                          static_cast<const void*>(a.k_scale), static_cast<const void*>(a.v_scale),
+                          static_cast<const void*>(a.device_status)})
     if (!aligned_to(ptr, 4)) return PKV_ERR_INVALID_ARG;
   if (!aligned_to(a.turns, 8) || !aligned_to(a.slot_mapping, 8)) return PKV_ERR_INVALID_ARG;
   if (cached && (!aligned_to(a.k_cache, 16) || !aligned_to(a.v_cache, 16))) return PKV_ERR_INVALID_ARG;

@@ -249,7 +249,7 @@ extern "C" pkv_status slots_from_lengths(
                           static_cast<const void*>(new_lens), static_cast<const void*>(free_blocks),
                           static_cast<const void*>(free_start), static_cast<const void*>(positions),
                           static_cast<const void*>(query_start), static_cast<const void*>(context_out),
-                          static_cast<const void*>(free_next)})
+                          static_cast<const void*>(free_next), static_cast<const void*>(device_status)})
     if (!aligned_to(ptr, 4)) return PKV_ERR_INVALID_ARG;
   if (!aligned_to(slot_mapping, 8)) return PKV_ERR_INVALID_ARG;
 

@@ -188,6 +188,13 @@ def test_packed_refusals(lib, kw, want):
     assert lib.library().packed_attention_prefill(None, None) == INVALID
 
 
+def test_status_words_off_their_boundary(lib):
+    """Four bytes that are flagged atomically: refused where they begin between two words."""
+    assert slots(lib, status=at(0xA02)) == INVALID
+    assert rotary(lib, **apart(device_status=at(0x36001))) == INVALID
+    assert packed(lib, device_status=at(0x60002)) == INVALID
+
+
 def test_packed_check(lib):
     """The check alone answers as the call does, without a launch: these arguments are taken."""
     a = dict(q=at(0), k=at(0x10000), v=at(0x20000), out=at(0x30000), query_start=at(0x100000), num_seqs=2,
