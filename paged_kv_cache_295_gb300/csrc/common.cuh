@@ -19,7 +19,9 @@ constexpr int kElemBytes[4] = {4, 2, 1, 1};
 
 inline int elem_bytes(int32_t dt) { return (dt >= 0 && dt <= 3) ? kElemBytes[dt] : 0; }
 
-inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool aligned_to(const void* p, unsigned bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+inline bool aligned4(const void* p) { return aligned_to(p, 4); }
+inline bool aligned16(const void* p) { return aligned_to(p, 16); }
 
 inline pkv_status cuda_status(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA; }
 

@@ -31,7 +31,6 @@ bool rows_map(CUtensorMap* m, const void* base, int dim, int heads, int64_t rows
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // A stride between rows or heads, where there is more than one of them.
 bool stride_ok(int64_t stride, int64_t count) {

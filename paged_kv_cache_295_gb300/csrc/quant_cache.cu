@@ -579,7 +579,6 @@ int ilog2(int x) {
   while ((1 << l) < x) ++l;
   return l;
 }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 }  // namespace
 }  // namespace pkv

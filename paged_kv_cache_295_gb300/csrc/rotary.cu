@@ -395,7 +395,6 @@ bool multiple(std::initializer_list<int64_t> xs, int64_t n) {
     if (x % n != 0) return false;
   return true;
 }
-bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 // Whether what a call writes overlaps something else that it reads or writes, but for rows turned in place.
 bool outputs_overlap(const pkv_rotary_args& a, bool cached, bool codes) {
@@ -473,9 +472,9 @@ extern "C" pkv_status rotary_and_cache(const pkv_rotary_args* args, pkv_stream_t
   for (const void* ptr : {static_cast<const void*>(a.axis), static_cast<const void*>(a.positions),
                           static_cast<const void*>(a.k_scale), static_cast<const void*>(a.v_scale),
                           static_cast<const void*>(a.device_status)})
-    if (!aligned_to(ptr, 4)) return PKV_ERR_INVALID_ARG;
+    if (!aligned4(ptr)) return PKV_ERR_INVALID_ARG;
   if (!aligned_to(a.turns, 8) || !aligned_to(a.slot_mapping, 8)) return PKV_ERR_INVALID_ARG;
-  if (cached && (!aligned_to(a.k_cache, 16) || !aligned_to(a.v_cache, 16))) return PKV_ERR_INVALID_ARG;
+  if (cached && (!aligned16(a.k_cache) || !aligned16(a.v_cache))) return PKV_ERR_INVALID_ARG;
   if (outputs_overlap(a, cached, kind >= 2)) return PKV_ERR_INVALID_ARG;
 
   RotaryParams p{};

@@ -223,7 +223,6 @@ __global__ void __launch_bounds__(kSlThreads, 1) slots_kernel(const __grid_const
   }
 }
 
-bool aligned_to(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 }  // namespace
 }  // namespace pkv
@@ -250,7 +249,7 @@ extern "C" pkv_status slots_from_lengths(
                           static_cast<const void*>(free_start), static_cast<const void*>(positions),
                           static_cast<const void*>(query_start), static_cast<const void*>(context_out),
                           static_cast<const void*>(free_next), static_cast<const void*>(device_status)})
-    if (!aligned_to(ptr, 4)) return PKV_ERR_INVALID_ARG;
+    if (!aligned4(ptr)) return PKV_ERR_INVALID_ARG;
   if (!aligned_to(slot_mapping, 8)) return PKV_ERR_INVALID_ARG;
 
   SlotsParams p{block_tables, context_lens, new_lens, free_blocks, free_start, slot_mapping,
