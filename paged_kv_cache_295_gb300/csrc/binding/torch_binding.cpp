@@ -625,7 +625,7 @@ PyObject* do_packed(PyObject* const* a, Py_ssize_t na) {
     refuse("k must have as many rows as q, or key_start be given");
   for (const auto& x : {std::make_pair(&q, "q"), std::make_pair(&k, "k"), std::make_pair(&v, "v")})
     for (int i = 0; i < 2; ++i)
-      if (x.first->size(i) > 1 && (x.first->stride(i) <= 0 || x.first->stride(i) % 8 != 0))
+      if (x.first->numel() > 0 && x.first->size(i) > 1 && (x.first->stride(i) <= 0 || x.first->stride(i) % 8 != 0))
         refuse(std::string(x.second) + " must have strides that are multiples of 8 elements");
   Tensor out = tensor(a[10], "out", true);
   const at::ScalarType type = out_type(a[11], out, at::kFloat);

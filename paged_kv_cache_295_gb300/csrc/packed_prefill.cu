@@ -58,9 +58,11 @@ pkv_status refusal(const pkv_packed_prefill_args& a) {
   if (a.head_dim > 128 || a.head_dim % 8 != 0 || G > kPkRows || a.num_seqs > (1 << 24) ||
       a.num_tokens > (1 << 30) || a.num_keys > (1 << 30) || a.num_q_heads > (1 << 16))
     return PKV_ERR_UNSUPPORTED;
-  if (!stride_ok(a.q_token_stride, a.num_tokens) || !stride_ok(a.q_head_stride, a.num_q_heads) ||
-      !stride_ok(a.k_token_stride, a.num_keys) || !stride_ok(a.k_head_stride, a.num_kv_heads) ||
-      !stride_ok(a.v_token_stride, a.num_keys) || !stride_ok(a.v_head_stride, a.num_kv_heads))
+  // of no rows the strides say nothing
+  if (a.num_tokens > 0 && (!stride_ok(a.q_token_stride, a.num_tokens) || !stride_ok(a.q_head_stride, a.num_q_heads)))
+    return PKV_ERR_INVALID_ARG;
+  if (a.num_keys > 0 && (!stride_ok(a.k_token_stride, a.num_keys) || !stride_ok(a.k_head_stride, a.num_kv_heads) ||
+                         !stride_ok(a.v_token_stride, a.num_keys) || !stride_ok(a.v_head_stride, a.num_kv_heads)))
     return PKV_ERR_INVALID_ARG;
   if (a.num_seqs == 0 || a.num_tokens == 0) return PKV_OK;
   if (!a.q || !a.out || !a.query_start || (a.num_keys > 0 && (!a.k || !a.v))) return PKV_ERR_INVALID_ARG;
@@ -117,14 +119,14 @@ extern "C" pkv_status packed_attention_prefill(const pkv_packed_prefill_args* ar
   p.test_stall_bytes = test_stall_bytes();
 
   CUtensorMap tq, tk, tv;
-  // without keys no key tile is read: any map will do
-  const void* k = a.num_keys > 0 ? a.k : a.q;
-  const void* v = a.num_keys > 0 ? a.v : a.q;
-  const int64_t keys = a.num_keys > 0 ? a.num_keys : 1;
+  auto keys_map = [&](CUtensorMap* m, const void* base, int64_t head_stride, int64_t token_stride) {
+    if (a.num_keys == 0)   // no key tile is read: any map will do
+      return rows_map(m, a.q, a.head_dim, a.num_kv_heads, 1, a.q_head_stride, 0, 1, kPkKeys);
+    return rows_map(m, base, a.head_dim, a.num_kv_heads, a.num_keys, head_stride, token_stride, 1, kPkKeys);
+  };
   if (!rows_map(&tq, a.q, a.head_dim, a.num_q_heads, a.num_tokens, a.q_head_stride, a.q_token_stride, G,
                 p.tile_tokens) ||
-      !rows_map(&tk, k, a.head_dim, a.num_kv_heads, keys, a.k_head_stride, a.k_token_stride, 1, kPkKeys) ||
-      !rows_map(&tv, v, a.head_dim, a.num_kv_heads, keys, a.v_head_stride, a.v_token_stride, 1, kPkKeys))
+      !keys_map(&tk, a.k, a.k_head_stride, a.k_token_stride) || !keys_map(&tv, a.v, a.v_head_stride, a.v_token_stride))
     return PKV_ERR_CUDA;
 
   const int64_t units = units_of(a);   // no more CTAs than items

@@ -596,3 +596,23 @@ def test_a_first_part_that_is_masked_whole(lib):
     for kw in (dict(window=1, sinks=1100), dict(window=1030, sinks=1), dict(window=1500, sinks=0),
                dict(window=300, sinks=1030)):
         check_parts(lib, q, k, v, lens, keys, 0.125, **kw)
+
+
+@pytest.mark.parametrize("out_type", ["bf16", "f32"])
+def test_strides_of_no_rows(lib, out_type):
+    """Rows of an empty tensor may have any strides: no tokens, and queries over no keys."""
+    import torch
+    i32 = dict(dtype=torch.int32, device="cuda")
+    dt = torch.bfloat16 if out_type == "bf16" else torch.float32
+    room = torch.empty(4096, dtype=torch.bfloat16, device="cuda")
+    for strides in ((0, 0, 0), (0, 0, 1), (5, 3, 1), (512, 64, 1)):
+        def none(heads):
+            return room.as_strided((0, heads, 64), strides)
+
+        for seqs in (0, 1, 3):
+            got = lib.packed_attention_prefill(none(4), none(2), none(2), torch.zeros(seqs + 1, **i32), 0.1, out_dtype=dt)
+            assert got.shape == (0, 4, 64) and got.dtype == dt
+        q = torch.ones((5, 4, 64), dtype=torch.bfloat16, device="cuda")
+        got = lib.packed_attention_prefill(q, none(2), none(2), torch.tensor([0, 2, 5], **i32), 0.1,
+                                           key_start=torch.zeros(3, **i32), out_dtype=dt)
+        assert got.shape == (5, 4, 64) and not got.any()
