@@ -731,6 +731,9 @@ pkv_status rotary_turns(const double* inv_freq, int32_t n, uint64_t* turns);
  *                  head * head_stride + d, strides multiples of 8 elements.
  *   query_start  : device [num_seqs + 1] int32, as in paged_attention_prefill.
  *   key_start    : the same for k and v; NULL: query_start (as many keys as queries).
+ *   context_lens : NULL, or device [num_seqs] int32: the tokens that each sequence has by now.  One with
+ *                  queries whose keys here are not all of them (it has a cached prefix) flags
+ *                  PKV_DEV_BAD_CONTEXT and is skipped, rather than attend to a part.
  *   causal       : 1 - query i of sequence s (of n queries and c keys) has position c - n + i and
  *                  sees keys 0 .. its position (none where that is negative); 0 - it sees all c.
  *   window, sinks : as in paged_attention_decode_window; need causal = 1.
@@ -768,6 +771,7 @@ typedef struct {
   int32_t q_dtype, kv_dtype, out_dtype;
   int32_t weight_parts;
   int32_t* device_status;
+  const int32_t* context_lens;
 } pkv_packed_prefill_args;
 
 pkv_status packed_attention_prefill(const pkv_packed_prefill_args* args, pkv_stream_t stream);

@@ -89,7 +89,7 @@ class _PackedPrefillArgs(C.Structure):
                 + [("scale", C.c_float)]
                 + [(n, C.c_int32) for n in ("causal", "window", "sinks", "q_dtype", "kv_dtype",
                                             "out_dtype", "weight_parts")]
-                + [("device_status", C.c_void_p)])
+                + [("device_status", C.c_void_p), ("context_lens", C.c_void_p)])
 
 
 _lib = None
@@ -842,7 +842,8 @@ def rotary_and_cache(q, k, v, positions, rotary, slot_mapping=None, k_cache=None
 
 
 def packed_attention_prefill(q, k, v, query_start, scale, key_start=None, causal=True, window=0,
-                             sinks=0, out=None, out_dtype=None, device_status=None, stream=None, weight_parts=2):
+                             sinks=0, out=None, out_dtype=None, device_status=None, stream=None, weight_parts=2,
+                             context_lens=None):
     """Attention over packed prompts: sequence ``s`` owns rows ``query_start[s] .. query_start[s + 1] - 1``
     (int32 ``[S + 1]`` on the device) of ``q`` ``[T, Hq, D]`` and, without ``key_start``, the same
     rows of ``k`` and ``v`` ``[N, Hkv, D]`` (bfloat16, D a multiple of 8 up to 128; parts of one
@@ -851,21 +852,25 @@ def packed_attention_prefill(q, k, v, query_start, scale, key_start=None, causal
     ``causal``: the queries are the last positions of their keys and see those up to their own;
     ``window`` and ``sinks`` as in ``paged_attention_prefill``.  A query that sees nothing gives 0.
     ``weight_parts``: bfloat16 parts that the weights enter the product with V as; a bfloat16 output may
-    take one, which is off by 2^-9 of each weight and saves half of the product's time."""
+    take one, which is off by 2^-9 of each weight and saves half of the product's time.
+    ``context_lens`` (int32 ``[S]``): a sequence with rows here that has other tokens than these flags
+    ``DEV_BAD_CONTEXT`` and gets nothing."""
     if stream is not None:
         with _on_stream(stream, q):
             return packed_attention_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks,
-                                            out, out_dtype, device_status, weight_parts=weight_parts)
-    return _packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks, weight_parts, out,
-                           out_dtype, device_status, True)
+                                            out, out_dtype, device_status, weight_parts=weight_parts,
+                                            context_lens=context_lens)
+    return _packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks, weight_parts,
+                           context_lens, out, out_dtype, device_status, True)
 
 
-def _packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks, weight_parts, out, out_dtype,
-                    device_status, launch):
+def _packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks, weight_parts, context_lens,
+                    out, out_dtype, device_status, launch):
     """``packed_attention_prefill`` on the current stream; without ``launch`` only its checks: returns the
     output that the call with these arguments would write."""
     return _done((_ext or _binding()).packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks,
-                                                     weight_parts, out, out_dtype, device_status, launch),
+                                                     weight_parts, context_lens, out, out_dtype, device_status,
+                                                     launch),
                  "packed_attention_prefill")
 
 

@@ -594,13 +594,13 @@ PyObject* do_rotary(PyObject* const* a, Py_ssize_t na) {
   return tuple_of(out);
 }
 
-// packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks, weight_parts, out,
-//                out_dtype, device_status, launch) -> out or status; without launch only the checks
+// packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks, weight_parts,
+//                context_lens, out, out_dtype, device_status, launch) -> out or status; without launch only the checks
 PyObject* do_packed(PyObject* const* a, Py_ssize_t na) {
-  arity(na, 14);
+  arity(na, 15);
   const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"),
                &qs = tensor(a[3], "query_start"), &ks = tensor(a[5], "key_start", true),
-               &st = status_word(a[12]);
+               &cl = tensor(a[10], "context_lens", true), &st = status_word(a[13]);
   if (q.dim() != 3 || k.dim() != 3) refuse("q, k and v must be [T, heads, dim]");
   if (qs.dim() != 1 || qs.size(0) < 1) refuse("query_start must be [S + 1]");
   const int64_t T = q.size(0), hq = q.size(1), dim = q.size(2), N = k.size(0), hkv = k.size(1), S = qs.size(0) - 1;
@@ -612,7 +612,7 @@ PyObject* do_packed(PyObject* const* a, Py_ssize_t na) {
   p.sinks = integer32(a[8], "sinks");
   p.weight_parts = integer32(a[9], "weight_parts");
   if (p.weight_parts < 1) refuse("weight_parts must be 1 or 2");
-  const bool launch = truth(a[13], "launch");
+  const bool launch = truth(a[14], "launch");
   const at::Device dev = cuda_device(q);
   const c10::cuda::CUDAGuard guard(dev);
   want_rows(q, "q", T, hq, dim, at::kBFloat16, dev);
@@ -627,8 +627,8 @@ PyObject* do_packed(PyObject* const* a, Py_ssize_t na) {
     for (int i = 0; i < 2; ++i)
       if (x.first->numel() > 0 && x.first->size(i) > 1 && (x.first->stride(i) <= 0 || x.first->stride(i) % 8 != 0))
         refuse(std::string(x.second) + " must have strides that are multiples of 8 elements");
-  Tensor out = tensor(a[10], "out", true);
-  const at::ScalarType type = out_type(a[11], out, at::kFloat);
+  Tensor out = tensor(a[11], "out", true);
+  const at::ScalarType type = out_type(a[12], out, at::kFloat);
   if (type != at::kFloat && type != at::kBFloat16) refuse("the output must be Float or BFloat16");
   if (!out.defined()) out = at::empty({T, hq, dim}, q.options().dtype(type));
   want(out, "out", {T, hq, dim}, {type});
@@ -639,6 +639,8 @@ PyObject* do_packed(PyObject* const* a, Py_ssize_t na) {
   p.v_token_stride = v.stride(0), p.v_head_stride = v.stride(1);
   p.query_start = ptr_as<int32_t>(qs, "query_start", dev);
   p.key_start = ptr_as<int32_t>(ks, "key_start", dev);
+  if (cl.defined()) want(cl, "context_lens", {S}, {at::kInt});
+  p.context_lens = ptr_as<int32_t>(cl, "context_lens", dev);
   p.num_seqs = count32(S, "query_start");
   p.num_tokens = count32(T, "q");
   p.num_keys = count32(N, "k");

@@ -68,7 +68,7 @@ pkv_status refusal(const pkv_packed_prefill_args& a) {
   if (!a.q || !a.out || !a.query_start || (a.num_keys > 0 && (!a.k || !a.v))) return PKV_ERR_INVALID_ARG;
   if (!a.key_start && a.num_keys != a.num_tokens) return PKV_ERR_INVALID_ARG;
   if (!aligned16(a.q) || !aligned16(a.k) || !aligned16(a.v) || !aligned16(a.out) || !aligned4(a.query_start) ||
-      !aligned4(a.key_start) || !aligned4(a.device_status))
+      !aligned4(a.key_start) || !aligned4(a.context_lens) || !aligned4(a.device_status))
     return PKV_ERR_INVALID_ARG;
 
   // from the first element to the last one
@@ -82,7 +82,8 @@ pkv_status refusal(const pkv_packed_prefill_args& a) {
       (a.num_keys > 0 &&
        (overlap(a.out, out_bytes, a.k, range(a.num_keys, a.num_kv_heads, a.k_token_stride, a.k_head_stride)) ||
         overlap(a.out, out_bytes, a.v, range(a.num_keys, a.num_kv_heads, a.v_token_stride, a.v_head_stride)))) ||
-      overlap(a.out, out_bytes, a.query_start, starts) || overlap(a.out, out_bytes, a.key_start, starts))
+      overlap(a.out, out_bytes, a.query_start, starts) || overlap(a.out, out_bytes, a.key_start, starts) ||
+      overlap(a.out, out_bytes, a.context_lens, starts - 4))
     return PKV_ERR_INVALID_ARG;
 
   // the items are counted in 32 bits
@@ -108,6 +109,7 @@ extern "C" pkv_status packed_attention_prefill(const pkv_packed_prefill_args* ar
   p.out = a.out;
   p.query_start = a.query_start;
   p.key_start = a.key_start ? a.key_start : a.query_start;
+  p.context_lens = a.context_lens;
   p.status = a.device_status;
   p.num_seqs = a.num_seqs, p.num_tokens = a.num_tokens, p.num_keys = a.num_keys;
   p.num_q_heads = a.num_q_heads, p.num_kv_heads = a.num_kv_heads, p.dim = a.head_dim;

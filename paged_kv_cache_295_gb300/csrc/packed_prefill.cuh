@@ -79,6 +79,7 @@ struct PackedParams {
   void* out;                    // [T, Hq, D]
   const int32_t* query_start;   // [S + 1]
   const int32_t* key_start;     // [S + 1]
+  const int32_t* context_lens;  // [S] or null
   int32_t* status;
   int32_t num_seqs, num_tokens, num_keys;
   int32_t num_q_heads, num_kv_heads, dim;
@@ -246,8 +247,10 @@ struct PkOrder {
       const int s = s0 + i;
       const int q0 = __ldg(p.query_start + s), q1 = __ldg(p.query_start + s + 1);
       const int k0 = __ldg(p.key_start + s), k1 = __ldg(p.key_start + s + 1);
+      const int ctx = p.context_lens ? __ldg(p.context_lens + s) : k1 - k0;
       int n = 0, lv = 0;
-      if (q0 < 0 || q1 < q0 || q1 > p.num_tokens || k0 < 0 || k1 < k0 || k1 > p.num_keys) {
+      if (q0 < 0 || q1 < q0 || q1 > p.num_tokens || k0 < 0 || k1 < k0 || k1 > p.num_keys ||
+          (q1 > q0 && ctx != k1 - k0)) {
         bad = true;
       } else {
         n = static_cast<int>((static_cast<int64_t>(q1) - q0 + per - 1) / per);

@@ -125,10 +125,12 @@ class PagedKVCache:
 
     def prompt(self, layer, q, k, v, positions, rotary, slots, window=0, sinks=0, out=None,
                out_dtype=None, device_status=None, stream=None, weight_parts=2):
-        """One layer of a step over whole prompts (sequences with nothing cached before): rotary
-        positions, the append, and causal attention over the packed rows.  ``slots`` as
-        ``self.slots`` gives them for this step; rows of the output behind the last sequence are not
-        written.  bfloat16 rows, head_dim a multiple of 8 up to 128."""
+        """One layer of a step over whole prompts: rotary positions, the append, and causal attention over the
+        packed rows.  ``slots`` as ``self.slots`` gives them for this step.  A sequence that had something
+        cached before flags ``DEV_BAD_CONTEXT`` and gets no attention (its rows are appended all the same): a
+        prompt's later chunks go through ``append_rotary`` and ``prefill``.  Rows of the output of such a
+        sequence and behind the last one are not written.  bfloat16 rows, head_dim a multiple of 8 up to 128.
+        With an 8-bit cache the prompt attends to its bfloat16 rows, the steps after it to the cache's codes."""
         if stream is not None:
             with _on_stream(stream, q):
                 return self.prompt(layer, q, k, v, positions, rotary, slots, window, sinks, out, out_dtype,
@@ -138,7 +140,8 @@ class PagedKVCache:
             raise ValueError("prompt takes bfloat16 rows and a head_dim that is a multiple of 8 up to 128")
         # what the attention refuses is known before the append: a refused prompt writes nothing
         turned = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k)]
-        args = (*turned, v, slots.query_start, self.scale, None, True, window, sinks, weight_parts)
+        args = (*turned, v, slots.query_start, self.scale, None, True, window, sinks, weight_parts,
+                slots.context_lens)
         out = _packed_prefill(*args, out, out_dtype, device_status, False)
         self.append_rotary(layer, q, k, v, positions, rotary, slots.slot_mapping, *turned,
                            device_status=device_status)

@@ -265,3 +265,32 @@ def test_every_refusal_of_a_prompt_comes_before_its_append(lib):
     assert torch.equal(out, torch.ones_like(out))     # every v is 1
     assert torch.equal(cache.v_cache(0).flatten(0, 1)[:T], v) and cache.k_cache(0).flatten(0, 1)[:T].any()
     assert call(out=over, **done) is over or torch.equal(over, out)
+
+
+@pytest.mark.parametrize("out_type", ["bfloat16", "float32"])
+def test_a_prompt_behind_a_cached_prefix_is_flagged(lib, out_type):
+    """A second chunk in prompt: its sequence has no attention rows and the status says so; a new sequence beside it
+    and one without tokens are as they should be."""
+    import torch
+    m = Model(lib, lib.BF16, 7)
+    cache, dt = m.cache, getattr(torch, out_type)
+    free, start, lens = dev(cache.pool.free_list()), dev([0]), dev([0, 0, 0, 0])
+    tables = torch.full((4, 20), -1, dtype=torch.int32, device="cuda")
+    for new, flagged in (([40, 0, 0, 9], []), ([0, 130, 0, 0], []), ([0, 5, 33, 1], [1, 3]), ([0, 0, 0, 0], [])):
+        T = sum(new)
+        x = m.step(T)
+        q, k, v = x[:, :HQ], x[:, HQ:HQ + HKV], x[:, HQ + HKV:]
+        sl = cache.slots(tables, lens, dev(new), free, T, free_start=start, context_out=lens, free_next=start)
+        status, out = dev([0]), torch.full((T, HQ, D), 5.0, dtype=dt, device="cuda")
+        cache.prompt(0, q, k, v, m.grid(sl.positions), m.rotary, sl, out=out, device_status=status)
+        assert int(status.item()) == (lib.DEV_BAD_CONTEXT if flagged else 0)
+        qr, kr = lib.rotary_and_cache(q, k, None, m.grid(sl.positions), m.rotary)
+        want = lib.packed_attention_prefill(qr, kr, v, sl.query_start, cache.scale, out_dtype=dt)
+        at = [0, *np.cumsum(new)]
+        for s in range(4):
+            rows = slice(at[s], at[s + 1])
+            assert torch.equal(out[rows], torch.full_like(out[rows], 5.0) if s in flagged else want[rows])
+    q, k, v = (torch.zeros((4, h, D), dtype=torch.bfloat16, device="cuda") for h in (HQ, HKV, HKV))
+    for bad in (dev([4]).long(), dev([4, 4]), torch.tensor([4], dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            lib.packed_attention_prefill(q, k, v, dev([0, 4]), 0.1, context_lens=bad)

@@ -215,10 +215,12 @@ def test_packed_check(lib):
     assert check(weight_parts=2, out_dtype=0) == OK and check(weight_parts=1, out_dtype=0) == UNSUPPORTED
     assert check(weight_parts=3) == INVALID and check(weight_parts=-1) == INVALID
     # as the C compiler lays the arguments out
-    assert lib._PackedPrefillArgs.device_status.offset == 152 and C.sizeof(lib._PackedPrefillArgs) == 160
+    assert lib._PackedPrefillArgs.device_status.offset == 152 and C.sizeof(lib._PackedPrefillArgs) == 168
     no = dict(q_token_stride=0, q_head_stride=0, k_token_stride=0, k_head_stride=0, v_token_stride=0, v_head_stride=3)
     assert check(num_tokens=0, num_keys=0, **no) == OK      # no rows: whatever their strides are
     assert check(key_start=at(0x110000), num_keys=0, k_head_stride=0, v_token_stride=-1, k=None, v=None) == OK
+    for n, status in ((0x60000, OK), (0x31000, OK), (0x60002, INVALID), (0x30FFC, INVALID), (0x2FFFC, INVALID)):
+        assert check(context_lens=at(n)) == status
     for kw in (dict(window=-1), dict(sinks=1), dict(out=at(0)), dict(v=at(8)), dict(num_keys=9),
                dict(v_token_stride=260), dict(window=4, causal=0)):
         assert check(**kw) == INVALID, kw
