@@ -294,3 +294,39 @@ def test_a_prompt_behind_a_cached_prefix_is_flagged(lib, out_type):
     for bad in (dev([4]).long(), dev([4, 4]), torch.tensor([4], dtype=torch.int32)):
         with pytest.raises(ValueError):
             lib.packed_attention_prefill(q, k, v, dev([0, 4]), 0.1, context_lens=bad)
+
+
+def test_a_captured_prompt(lib):
+    """Slots, rotary positions, append and attention of a step in one graph, replayed on other rows and lengths; the
+    replay writes what the same calls one by one do."""
+    import torch
+    m = Model(lib, lib.BF16, 9)
+    cache, T = m.cache, 300
+    x, new = m.step(T), dev([100, 3, 150])
+    free = dev(cache.pool.free_list())
+    tables, lens, start = torch.full((3, 20), -1, dtype=torch.int32, device="cuda"), dev([0, 0, 0]), dev([0])
+    out, status = torch.zeros((T, HQ, D), dtype=torch.bfloat16, device="cuda"), dev([0])
+
+    def step(stream=None):
+        sl = cache.slots(tables, lens, new, free, T, free_start=start, device_status=status)
+        cache.prompt(0, x[:, :HQ], x[:, HQ:HQ + HKV], x[:, HQ + HKV:], m.grid(sl.positions), m.rotary, sl, window=90,
+                     sinks=2, out=out, device_status=status, stream=stream)
+
+    step()
+    side, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=side):
+        step()
+    for lengths in ([100, 3, 150], [0, 299, 1], [1, 1, 1], [0, 0, 0], [60, 60, 60]):
+        x.copy_(m.step(T))
+        new.copy_(dev(lengths))
+        got = []
+        for run in (g.replay, step):
+            out.fill_(9.0)
+            cache.storage.zero_()
+            tables.fill_(-1)
+            run()
+            torch.cuda.synchronize()
+            got.append((out.clone(), cache.storage.clone(), tables.clone()))
+        assert int(status.item()) == 0 and all(torch.equal(a, b) for a, b in zip(*got))
+        assert (got[0][0][sum(lengths):] == 9.0).all() and not (got[0][0][:sum(lengths)] == 9.0).all(-1).any()
