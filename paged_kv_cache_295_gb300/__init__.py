@@ -860,18 +860,18 @@ def packed_attention_prefill(q, k, v, query_start, scale, key_start=None, causal
             return packed_attention_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks,
                                             out, out_dtype, device_status, weight_parts=weight_parts,
                                             context_lens=context_lens)
-    return _packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks, weight_parts,
-                           context_lens, out, out_dtype, device_status, True)
-
-
-def _packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks, weight_parts, context_lens,
-                    out, out_dtype, device_status, launch):
-    """``packed_attention_prefill`` on the current stream; without ``launch`` only its checks: returns the
-    output that the call with these arguments would write."""
     return _done((_ext or _binding()).packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks,
-                                                     weight_parts, context_lens, out, out_dtype, device_status,
-                                                     launch),
+                                                     weight_parts, context_lens, out, out_dtype, device_status),
                  "packed_attention_prefill")
+
+
+def _prompt(q, k, v, positions, rotary, slot_mapping, k_cache, v_cache, k_scale, v_scale, query_start, scale, window,
+            sinks, weight_parts, context_lens, out, out_dtype, device_status):
+    """``rotary_and_cache`` and causal ``packed_attention_prefill`` over its rows, both on the current stream, or a
+    refusal before either."""
+    return _done((_ext or _binding()).prompt(q, k, v, positions, rotary.plan, slot_mapping, k_cache, v_cache, k_scale,
+                                             v_scale, query_start, scale, None, True, window, sinks, weight_parts,
+                                             context_lens, out, out_dtype, device_status), "prompt")
 
 
 def copy_blocks(pool_tensor, pairs, device_status=None, stream=None):

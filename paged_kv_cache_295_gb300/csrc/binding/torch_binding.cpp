@@ -488,21 +488,27 @@ void want_rows(const Tensor& t, const char* name, int64_t rows, int64_t heads, i
     refuse(std::string(name) + " must not overlap itself");
 }
 
-// rotary_and_cache(q, k, v, positions, (turns, axis, rotary_dim, num_axes, adjacent, scale), slot_mapping,
-//                  k_cache, v_cache, k_scale, v_scale, q_out, k_out, keep_k, device_status)
-//   -> (q_out, k_out) or status
-PyObject* do_rotary(PyObject* const* a, Py_ssize_t na) {
-  arity(na, 14);
-  if (!PyTuple_Check(a[4]) || PyTuple_GET_SIZE(a[4]) != 6) refuse("rotary must be a Rotary's plan");
-  PyObject* const* plan = &PyTuple_GET_ITEM(a[4], 0);
-  const Tensor &q = tensor(a[0], "q", true), &k = tensor(a[1], "k"), &v = tensor(a[2], "v", true),
-               &pos = tensor(a[3], "positions"), &turns = tensor(plan[0], "turns"),
-               &axis = tensor(plan[1], "axis", true), &slots = tensor(a[5], "slot_mapping", true),
-               &kc = tensor(a[6], "k_cache", true), &vc = tensor(a[7], "v_cache", true),
-               &ks = tensor(a[8], "k_scale", true), &vs = tensor(a[9], "v_scale", true),
-               &st = status_word(a[13]);
-  Tensor out[2] = {tensor(a[10], "q_out", true), tensor(a[11], "k_out", true)};
-  const bool keep_k = truth(a[12], "keep_k"), cached = kc.defined();
+// What rotary_and_cache takes beside q, k, v and the outputs.
+struct RotaryTensors {
+  PyObject* const* plan;   // (turns, axis, rotary_dim, num_axes, adjacent, scale)
+  const Tensor &pos, &turns, &axis, &slots, &kc, &vc, &ks, &vs;
+  // positions, plan, slot_mapping, k_cache, v_cache, k_scale, v_scale
+  explicit RotaryTensors(PyObject* const* a)
+      : plan(items(a[1])), pos(tensor(a[0], "positions")), turns(tensor(plan[0], "turns")),
+        axis(tensor(plan[1], "axis", true)), slots(tensor(a[2], "slot_mapping", true)),
+        kc(tensor(a[3], "k_cache", true)), vc(tensor(a[4], "v_cache", true)), ks(tensor(a[5], "k_scale", true)),
+        vs(tensor(a[6], "v_scale", true)) {}
+  static PyObject* const* items(PyObject* plan) {
+    if (!PyTuple_Check(plan) || PyTuple_GET_SIZE(plan) != 6) refuse("rotary must be a Rotary's plan");
+    return &PyTuple_GET_ITEM(plan, 0);
+  }
+};
+
+// The call's arguments, checked; outputs that are not given are allocated on the current device.
+pkv_rotary_args rotary_args(const Tensor& q, const Tensor& k, const Tensor& v, const RotaryTensors& x, Tensor (&out)[2],
+                            bool keep_k, const Tensor& st) {
+  const auto &[plan, pos, turns, axis, slots, kc, vc, ks, vs] = x;
+  const bool cached = kc.defined();
   pkv_rotary_args p{};
   p.rotary_dim = integer32(plan[2], "rotary_dim");
   p.num_axes = integer32(plan[3], "num_axes");
@@ -514,7 +520,6 @@ PyObject* do_rotary(PyObject* const* a, Py_ssize_t na) {
   if (type != at::kFloat && type != at::kBFloat16) refuse("k must be Float or BFloat16, got " + show(k));
   if (hq > (1 << 20) || hkv > (1 << 20) || dim > (1 << 20)) refuse("too many heads or dims");
   const at::Device dev = cuda_device(k);
-  const c10::cuda::CUDAGuard guard(dev);
   want_rows(k, "k", T, hkv, dim, type, dev);
   if (q.defined()) {
     want_rows(q, "q", T, hq, dim, type, dev);
@@ -585,6 +590,21 @@ PyObject* do_rotary(PyObject* const* a, Py_ssize_t na) {
   p.axis = ptr_as<int32_t>(axis, "axis", dev);
   p.positions = ptr_as<int32_t>(pos, "positions", dev);
   p.device_status = ptr_as<int32_t>(st, "device_status", dev);
+  return p;
+}
+
+// rotary_and_cache(q, k, v, positions, plan, slot_mapping, k_cache, v_cache, k_scale, v_scale, q_out, k_out,
+//                  keep_k, device_status) -> (q_out, k_out) or status
+PyObject* do_rotary(PyObject* const* a, Py_ssize_t na) {
+  arity(na, 14);
+  const Tensor &q = tensor(a[0], "q", true), &k = tensor(a[1], "k"), &v = tensor(a[2], "v", true),
+               &st = status_word(a[13]);
+  const RotaryTensors x(a + 3);
+  Tensor out[2] = {tensor(a[10], "q_out", true), tensor(a[11], "k_out", true)};
+  const bool keep_k = truth(a[12], "keep_k");
+  const at::Device dev = cuda_device(k);
+  const c10::cuda::CUDAGuard guard(dev);
+  const pkv_rotary_args p = rotary_args(q, k, v, x, out, keep_k, st);
   const pkv_stream_t stream = stream_of(dev);
   pkv_status r;
   Py_BEGIN_ALLOW_THREADS
@@ -594,27 +614,24 @@ PyObject* do_rotary(PyObject* const* a, Py_ssize_t na) {
   return tuple_of(out);
 }
 
-// packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks, weight_parts,
-//                context_lens, out, out_dtype, device_status, launch) -> out or status; without launch only the checks
-PyObject* do_packed(PyObject* const* a, Py_ssize_t na) {
-  arity(na, 15);
-  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"),
-               &qs = tensor(a[3], "query_start"), &ks = tensor(a[5], "key_start", true),
-               &cl = tensor(a[10], "context_lens", true), &st = status_word(a[13]);
+// The arguments of packed_attention_prefill over these rows, checked; `a`: query_start, scale, key_start, causal,
+// window, sinks, weight_parts, context_lens, out, out_dtype, device_status.  `out` is allocated on the current
+// device where it is not given.
+pkv_packed_prefill_args packed_args(const Tensor& q, const Tensor& k, const Tensor& v, PyObject* const* a, Tensor& out) {
+  const Tensor &qs = tensor(a[0], "query_start"), &ks = tensor(a[2], "key_start", true),
+               &cl = tensor(a[7], "context_lens", true), &st = status_word(a[10]);
   if (q.dim() != 3 || k.dim() != 3) refuse("q, k and v must be [T, heads, dim]");
   if (qs.dim() != 1 || qs.size(0) < 1) refuse("query_start must be [S + 1]");
   const int64_t T = q.size(0), hq = q.size(1), dim = q.size(2), N = k.size(0), hkv = k.size(1), S = qs.size(0) - 1;
   if (hq > (1 << 20) || hkv > (1 << 20) || dim > (1 << 20)) refuse("too many heads or dims");
   pkv_packed_prefill_args p{};
-  p.scale = real(a[4], "scale");
-  p.causal = truth(a[6], "causal");
-  p.window = integer32(a[7], "window");
-  p.sinks = integer32(a[8], "sinks");
-  p.weight_parts = integer32(a[9], "weight_parts");
+  p.scale = real(a[1], "scale");
+  p.causal = truth(a[3], "causal");
+  p.window = integer32(a[4], "window");
+  p.sinks = integer32(a[5], "sinks");
+  p.weight_parts = integer32(a[6], "weight_parts");
   if (p.weight_parts < 1) refuse("weight_parts must be 1 or 2");
-  const bool launch = truth(a[14], "launch");
   const at::Device dev = cuda_device(q);
-  const c10::cuda::CUDAGuard guard(dev);
   want_rows(q, "q", T, hq, dim, at::kBFloat16, dev);
   want_rows(k, "k", N, hkv, dim, at::kBFloat16, dev);
   want_rows(v, "v", N, hkv, dim, at::kBFloat16, dev);
@@ -627,8 +644,8 @@ PyObject* do_packed(PyObject* const* a, Py_ssize_t na) {
     for (int i = 0; i < 2; ++i)
       if (x.first->numel() > 0 && x.first->size(i) > 1 && (x.first->stride(i) <= 0 || x.first->stride(i) % 8 != 0))
         refuse(std::string(x.second) + " must have strides that are multiples of 8 elements");
-  Tensor out = tensor(a[11], "out", true);
-  const at::ScalarType type = out_type(a[12], out, at::kFloat);
+  out = tensor(a[8], "out", true);
+  const at::ScalarType type = out_type(a[9], out, at::kFloat);
   if (type != at::kFloat && type != at::kBFloat16) refuse("the output must be Float or BFloat16");
   if (!out.defined()) out = at::empty({T, hq, dim}, q.options().dtype(type));
   want(out, "out", {T, hq, dim}, {type});
@@ -650,10 +667,45 @@ PyObject* do_packed(PyObject* const* a, Py_ssize_t na) {
   p.q_dtype = p.kv_dtype = PKV_BF16;
   p.out_dtype = code_of(type);
   p.device_status = ptr_as<int32_t>(st, "device_status", dev);
+  return p;
+}
+
+// packed_prefill(q, k, v, query_start, scale, key_start, causal, window, sinks, weight_parts, context_lens, out,
+//                out_dtype, device_status) -> out or status
+PyObject* do_packed(PyObject* const* a, Py_ssize_t na) {
+  arity(na, 14);
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+  const at::Device dev = cuda_device(q);
+  const c10::cuda::CUDAGuard guard(dev);
+  Tensor out;
+  const pkv_packed_prefill_args p = packed_args(q, k, v, a + 3, out);
   const pkv_stream_t stream = stream_of(dev);
   pkv_status r;
   Py_BEGIN_ALLOW_THREADS
-  r = launch ? packed_attention_prefill(&p, stream) : packed_attention_prefill_check(&p);
+  r = packed_attention_prefill(&p, stream);
+  Py_END_ALLOW_THREADS
+  if (r != PKV_OK) return status(r);
+  return THPVariable_Wrap(std::move(out));
+}
+
+// prompt(q, k, v, positions, plan, slot_mapping, k_cache, v_cache, k_scale, v_scale, query_start, ... as packed_prefill)
+//   -> out or status: rotary_and_cache, then packed_attention_prefill over the turned rows.  What the second
+// refuses is refused before the first writes anything.
+PyObject* do_prompt(PyObject* const* a, Py_ssize_t na) {
+  arity(na, 21);
+  const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v"), &st = status_word(a[20]);
+  const RotaryTensors x(a + 3);
+  const at::Device dev = cuda_device(k);
+  const c10::cuda::CUDAGuard guard(dev);
+  Tensor turned[2], out;
+  const pkv_rotary_args rp = rotary_args(q, k, v, x, turned, true, st);
+  const pkv_packed_prefill_args pp = packed_args(turned[0], turned[1], v, a + 10, out);
+  const pkv_stream_t stream = stream_of(dev);
+  pkv_status r;
+  Py_BEGIN_ALLOW_THREADS
+  r = packed_attention_prefill_check(&pp);
+  if (r == PKV_OK) r = rotary_and_cache(&rp, stream);
+  if (r == PKV_OK) r = packed_attention_prefill(&pp, stream);
   Py_END_ALLOW_THREADS
   if (r != PKV_OK) return status(r);
   return THPVariable_Wrap(std::move(out));
@@ -680,6 +732,7 @@ PyMethodDef kMethods[] = {
     {"slots_from_lengths", reinterpret_cast<PyCFunction>(entry<do_slots>), METH_FASTCALL, nullptr},
     {"rotary_and_cache", reinterpret_cast<PyCFunction>(entry<do_rotary>), METH_FASTCALL, nullptr},
     {"packed_prefill", reinterpret_cast<PyCFunction>(entry<do_packed>), METH_FASTCALL, nullptr},
+    {"prompt", reinterpret_cast<PyCFunction>(entry<do_prompt>), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_pkv_torch", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};

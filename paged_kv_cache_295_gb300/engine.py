@@ -14,7 +14,7 @@ from __future__ import annotations
 
 import numpy as np
 
-from . import (BF16, F32, FP8_E4M3, INT8, Pool, _on_stream, _packed_prefill, copy_blocks, gather_cache,
+from . import (BF16, F32, FP8_E4M3, INT8, Pool, _on_stream, _prompt, copy_blocks, gather_cache,
                paged_attention_decode, paged_attention_decode_append, paged_attention_prefill,
                quantize_and_cache, reshape_and_cache, rotary_and_cache, slots_from_lengths,
                swap_blocks, workspace_bytes)
@@ -114,14 +114,18 @@ class PagedKVCache:
                       keep_k=False, device_status=None, stream=None):
         """Rotary positions of q and k and the append of k and v in one pass
         (``rotary_and_cache``); returns ``(q, k)`` turned, k None unless ``keep_k``."""
+        k_cache, v_cache, ks, vs = self._rotary_cache(layer)
+        return rotary_and_cache(q, k, v, positions, rotary, slot_mapping, k_cache, v_cache, ks, vs, q_out=q_out,
+                                k_out=k_out, keep_k=keep_k, device_status=device_status, stream=stream)
+
+    def _rotary_cache(self, layer):
+        """A layer's caches and scales as ``rotary_and_cache`` takes them."""
         if self.scales is not None:
             raise ValueError("a cache with block scales: rotary_and_cache without a cache, then "
                              "append_rows")
         ks = None if self.k_scale is None else self.k_scale[layer]
         vs = None if self.v_scale is None else self.v_scale[layer]
-        return rotary_and_cache(q, k, v, positions, rotary, slot_mapping, self.k_cache(layer),
-                                self.v_cache(layer), ks, vs, q_out=q_out, k_out=k_out, keep_k=keep_k,
-                                device_status=device_status, stream=stream)
+        return self.k_cache(layer), self.v_cache(layer), ks, vs
 
     def prompt(self, layer, q, k, v, positions, rotary, slots, window=0, sinks=0, out=None,
                out_dtype=None, device_status=None, stream=None, weight_parts=2):
@@ -135,17 +139,11 @@ class PagedKVCache:
             with _on_stream(stream, q):
                 return self.prompt(layer, q, k, v, positions, rotary, slots, window, sinks, out, out_dtype,
                                    device_status, weight_parts=weight_parts)
-        torch = _torch()
-        if q.dtype != torch.bfloat16 or self.head_dim > 128 or self.head_dim % 8:
+        if q.dtype != _torch().bfloat16 or self.head_dim > 128 or self.head_dim % 8:
             raise ValueError("prompt takes bfloat16 rows and a head_dim that is a multiple of 8 up to 128")
-        # what the attention refuses is known before the append: a refused prompt writes nothing
-        turned = [torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k)]
-        args = (*turned, v, slots.query_start, self.scale, None, True, window, sinks, weight_parts,
-                slots.context_lens)
-        out = _packed_prefill(*args, out, out_dtype, device_status, False)
-        self.append_rotary(layer, q, k, v, positions, rotary, slots.slot_mapping, *turned,
-                           device_status=device_status)
-        return _packed_prefill(*args, out, out_dtype, device_status, True)
+        k_cache, v_cache, ks, vs = self._rotary_cache(layer)
+        return _prompt(q, k, v, positions, rotary, slots.slot_mapping, k_cache, v_cache, ks, vs, slots.query_start,
+                       self.scale, window, sinks, weight_parts, slots.context_lens, out, out_dtype, device_status)
 
     def gather(self, layer, block_tables, row_start, num_rows, max_rows, first_pos=None,
                out_dtype=None, k_out=None, v_out=None, device_status=None, stream=None):
