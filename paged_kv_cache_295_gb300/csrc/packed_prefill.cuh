@@ -30,23 +30,26 @@
 // Precision.  Scores, sums and O are float32, and the weights enter the product as two bf16 parts (2^-17 of
 // each at most): a bf16 output is the float32 one rounded.  A caller may ask for one part (2^-9 of each)
 // for a bf16 output: 1.2 to 1.4 times the error against 64 bits on normal values (2.0e-3 to 2.4e-3 of
-// the norm for 1.6e-3) and half the product's time.
+// the norm for 1.6e-3) and half the product's time.  A third part for float32 outputs has no room: the two
+// take all 128 columns of S.
 //
-// What bounds it.  At head_dim 128 the chain of a key tile: softmax 1,400 cycles, product and next scores
-// 770 of its 1,024 behind it, and about 450 until each sees that the other is done, with the other tile's
-// products in between: 2,600 cycles for a pair of tiles whose products need 2,048.  What it took to get
+// What bounds it.  At head_dim 128 with two weight parts the products: a pair of key tiles needs 3,072 cycles of
+// them and takes 3,660 (tensor pipe 84 % of active cycles).  With one part the chain of a key tile: softmax
+// 1,400 cycles, product and next scores 770 of its 1,024 behind it, and about 450 until each sees that the
+// other is done, with the other tile's products in between: 2,600 cycles for a pair whose products need
+// 2,048; without the exponentials it would be 6 % faster, without the maxima 4 %.  What it took to get
 // there: no mask code in tiles without one; a plain loop for the issuer (its general steps took 3,100
-// cycles a pair); references that move only on a vote; both halves' scores asked for together.  Without the
-// exponentials it would be 6 % faster, without the maxima 4 %.  Short lists wait for their first rows
+// cycles a pair); references that move only on a vote; both halves' scores asked for together.  Short lists wait for their first rows
 // (Q and K of the next item reach shared memory 2 to 3 us after they are asked for, as all CTAs ask at
-// once) and a cold CTA for its code.  Tried and left out: one issuer for each tile (both tiles' phases
+// once) and a cold CTA for its code.  Tried and left out, with one part: one issuer for each tile (both tiles' phases
 // fall together), with and without turns; prefetches of the next item to L2 (16 prompts of 512 tokens 77
 // -> 90 us); the order of items kept within sequences whose keys fit L2; lists of equal length for both tiles; the halves as a loop (20 % slower); Q before K.
 //
-// Measured: three prompts of 700 to 8,192 tokens, 32 heads on 8, causal 460 to 480 us (1,500 to 1,570
-// TFLOP/s; float32 output 706); 16 prompts of 512 tokens, 32 heads 65 us (float32 output 80); 11 images of 64 to 1,156 patches, 16 heads of 80, not
-// causal 46 to 47 us; nine chunks of up to 1,500 tokens behind 333 keys, 16 heads on 2 of 64, window 1,024,
-// float32 output 45 us; four prompts of up to 60 tokens 9.2 us.
+// Measured (bf16 output; with one weight part; float32 output): three prompts of 700 to 8,192 tokens, 32 heads
+// on 8, causal 585 to 655 us across GPUs, 460 to 506, 767 (1,100 to 1,230 TFLOP/s of q k and p v, the second part
+// of p not counted; 1,430 to 1,570 with one); 16 prompts of 512 tokens, 32 heads 74 us, 66, 81; 11 images of 64 to
+// 1,156 patches, 16 heads of 80, not causal 56 us, 47, 62; nine chunks of up to 1,500 tokens behind 333 keys, 16
+// heads on 2 of 64, window 1,024 44 us, 37, 48 to 52; four prompts of up to 60 tokens 9.7 us, 9.2, 10.3.
 //
 // Every wait is bounded (2 s) and gives up when another role has given up; copies in flight are then
 // waited for, and TMEM is released before the CTA exits.

@@ -15,7 +15,7 @@
 // barrier stands between the last read and the first write.
 //
 // Measured: 8 sequences of one token 3.6 us, 512 of them 4.2 us, 64 prompts and chunks of up to 2,047 tokens
-// (66,000 rows) 4.9 us.
+// (66,000 rows) 4.9 us, and 11 in place: a barrier spans one cluster, so that eight CTAs write what 32 do.
 #include "common.cuh"
 #include "ranges.cuh"
 
