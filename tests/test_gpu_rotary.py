@@ -382,3 +382,30 @@ def test_outputs_that_overlap_inputs(lib, dtype):
             lib.rotary_and_cache(q, k, v, pos, plan, slots, pool[0], pool[0])
         torch.cuda.synchronize()
         assert torch.equal(x, before) and torch.equal(pool, pool_before)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8", "int8"])
+def test_only_k_into_a_cache(lib, kv):
+    """Without q the caches and the turned k are what they are with it; one token of any token stride too."""
+    import torch
+    T, D, plan = 21, 80, lib.Rotary(40)
+    dt = {"bf16": torch.bfloat16, "fp8": torch.float8_e4m3fn, "int8": torch.int8}[kv]
+    x = torch.randn((T, 8, D), device="cuda").bfloat16()
+    q, k, v = x[:, :4], x[:, 4:6], x[:, 6:]
+    pos, slots = torch.arange(T, dtype=torch.int32, device="cuda") * 977, torch.randperm(32, device="cuda")[:T]
+    sc = {} if kv == "bf16" else {n: torch.tensor([0.02, 0.05], device="cuda") for n in ("k_scale", "v_scale")}
+
+    def call(q, k, v, pos, slots):
+        caches = [torch.zeros((2, 16, 2, D), device="cuda").to(dt) for _ in range(2)]
+        got = lib.rotary_and_cache(q, k, v, pos, plan, slots, *caches, keep_k=True, **sc)
+        return (*got, *(c.view(torch.uint8) for c in caches))
+
+    want = call(q, k, v, pos, slots)
+    got = call(None, k, v, pos, slots)
+    assert got[0] is None and all(torch.equal(a, b) for a, b in zip(got[1:], want[1:]))
+    for t in (0, 20):
+        a = call(q[t:t + 1], k[t:t + 1], v[t:t + 1], pos[t:t + 1], slots[t:t + 1])
+        far = [y[t:t + 1].as_strided((1, y.shape[1], D), (7, D, 1)) for y in (q, k, v)]
+        b = call(*far, pos[t:t + 1], slots[t:t + 1])
+        assert all(torch.equal(c, d) for c, d in zip(a, b))
+        assert torch.equal(a[0], want[0][t:t + 1]) and torch.equal(a[1], want[1][t:t + 1])
